@@ -287,6 +287,163 @@ typedef struct {
 } cg_chunk_plan_in;
 int cg_plan_chunk(const cg_chunk_plan_in* in, int32_t* quality_out, double* ratio_out);
 
+/* ---------------------------------------------------------------------------
+ * Paged caches: what happens to a decoded cache while requests are served on
+ * it.  A cache is a pair of pools as cg_decode_paged_async fills them, a block
+ * table per row (a row is one sequence), the rows' lengths and a reference
+ * count per page; all of it is device memory of the caller, and the calls work
+ * on it in stream order without looking at it from the host.
+ *
+ * A fresh cache has lens and refs all 0 and tables all -1.  Between calls: row r
+ * of length n holds pages in its first ceil(n / page_tokens) table entries and -1
+ * behind them; refs[p] counts the entries that name page p, 0 is a free page;
+ * the last page of a row is shared only when it is full.  The calls keep this.
+ * A context is decoded into a row by reserving its tokens there and passing the
+ * row's table to cg_decode_paged_async.
+ *
+ * status_dev, a caller-owned uint32 that the library never clears: bit 1 is set
+ * where a table entry that a call needs lies outside the pool (the tokens of
+ * that page are skipped), bit 2 where a request is refused (a row or page out
+ * of range or named twice, a row in a state that the call does not allow), bit
+ * 3 where the free pages do not suffice.  Whatever the device arrays hold, no
+ * call reads or writes outside the buffers it was given.
+ *
+ * The calls only enqueue on `stream` (a stream of the cache's device), allocate
+ * nothing and can be captured into a graph.  They change the cache in place:
+ * calls on one cache run in one stream or are ordered by events, and two calls
+ * that may run at the same time need two workspaces.
+ * Errors: CG_E_INVAL before any GPU work for a NULL pointer or a number out of
+ * range, CG_E_CAPACITY for a workspace that is too small, CG_E_HIP. */
+typedef struct {
+  int32_t device;               /* HIP device of every pointer of the call */
+  int32_t layers, channels;     /* 1 .. 4096, 1 .. 65536 */
+  int32_t page_tokens;          /* a power of two in [1, 65536]; a page of one layer is below
+                                   4 GiB */
+  int32_t num_pages;            /* 1 .. 2^24 */
+  int32_t n_rows;               /* 1 .. 65536 */
+  int32_t max_blocks;           /* table entries of a row; max_blocks x page_tokens <= 2^30 */
+  int32_t reserved;             /* 0 */
+  void *k_pool_dev, *v_pool_dev; /* fp16 [layers][num_pages][page_tokens][channels]; a layer
+                                    may be larger than 4 GiB */
+  int32_t* tables_dev;          /* [n_rows][max_blocks] */
+  int32_t* lens_dev;            /* [n_rows] */
+  int32_t* refs_dev;            /* [num_pages] */
+  uint32_t* status_dev;
+} cg_paged_cache;
+
+/* Bytes of workspace (16-byte aligned) that one reserve, fork or compact call on
+ * this cache needs.  Host only. */
+int cg_pages_workspace(const cg_paged_cache* cache, size_t* bytes);
+
+/* Copies page src[i] to page dst[i] in every layer of both pools, i < n (device
+ * int32 arrays); tables and counts are not touched.  A pair whose dst is also
+ * another pair's dst, or whose src is any pair's dst, is not copied (bit 2): the
+ * result does not depend on an order. n = 0 is allowed. */
+int cg_pages_copy_async(const cg_paged_cache* cache, int32_t n, const int32_t* src_dev,
+                        const int32_t* dst_dev, void* stream);
+
+/* Makes room for new tokens: request i adds starts[i+1] - starts[i] of the
+ * n_tokens tokens to row rows[i] (device int32 arrays of n and n + 1 entries,
+ * starts ascending within 0 .. n_tokens <= 2^21; rows distinct, n <= n_rows).  The rows
+ * get the free pages of the lowest numbers, dealt out in the order of the
+ * requests and of their blocks, with refs 1; lens grows.  slots_dev (n_tokens
+ * int64, may be NULL) receives where each token goes: page x page_tokens + row
+ * of the page.  A request whose row would pass max_blocks, or whose row is bad or
+ * repeated, is refused (bit 2); one whose pages, with those of the requests
+ * before it, are more than the free ones is left out (bit 3).  Its row does
+ * not change and its tokens' slots are -1, as are those of tokens of no request. */
+int cg_pages_reserve_async(const cg_paged_cache* cache, int32_t n, const int32_t* rows_dev,
+                           const int32_t* starts_dev, int32_t n_tokens, int64_t* slots_dev,
+                           void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/* Writes the K and V of new tokens to their slots in layers layer0 .. layer0 +
+ * n_layers - 1 (a model writes each layer as it gets there, or all at once).
+ * k_new_dev, v_new_dev: fp16, token t of layer layer0 + l at element
+ * l x layer_stride + t x token_stride, channels contiguous (token_stride >=
+ * channels: K and V may be slices of a wider projection).  A slot of -1 is
+ * skipped, any other outside the pool too (bit 1).  Two tokens with one slot
+ * overwrite each other. */
+int cg_pages_write_async(const cg_paged_cache* cache, int32_t layer0, int32_t n_layers,
+                         int32_t n_tokens, const int64_t* slots_dev, const void* k_new_dev,
+                         const void* v_new_dev, int64_t token_stride, int64_t layer_stride,
+                         void* stream);
+
+/* Row children[i] becomes a continuation of row parents[i], i < n (device int32
+ * arrays): it gets the parent's length and full pages, whose counts grow by one,
+ * and a page of its own (lowest free number, in the order of the list) with a
+ * copy of the rows in use of a last page that is not full, in every layer.
+ * A parent may be named often.  Refused (bit 2): a child that is not empty, is
+ * named twice or is also a parent in this list.  A fork whose page, with those of
+ * the forks before it, is more than the free ones is left out (bit 3).  Its
+ * child stays empty. */
+int cg_pages_fork_async(const cg_paged_cache* cache, int32_t n, const int32_t* parents_dev,
+                        const int32_t* children_dev, void* workspace_dev, size_t workspace_bytes,
+                        void* stream);
+
+/* Empties rows rows[i], i < n (device int32): the counts of their pages drop by
+ * one (a page is free at 0), their entries become -1 and their lengths 0.  A
+ * row named twice is freed once (bit 2); an empty row is fine. */
+int cg_pages_free_async(const cg_paged_cache* cache, int32_t n, const int32_t* rows_dev,
+                        void* stream);
+
+/* Packs the pages in use into the lowest numbers: with M of them, the j-th page
+ * in use at or past M (ascending) moves to the j-th free page below M, in every
+ * layer, and tables and counts follow; no other page moves, and the
+ * contents of pages that became free stay.  n_live_dev (device int32, may be NULL)
+ * receives M: pages M .. num_pages - 1 are free then. */
+int cg_pages_compact_async(const cg_paged_cache* cache, int32_t* n_live_dev,
+                           void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/* Attention of new tokens over a paged cache, in which the sequences of a group
+ * share a prefix that is read once for all of them.
+ *
+ * Sequence s is row rows[s] of the cache (rows_dev NULL: row s).  Its queries are
+ * tokens q_starts[s] .. q_starts[s+1] - 1 of q, the last of the row (their K and V
+ * are already in the cache): with n the row's length and m queries, query j sees
+ * tokens 0 .. n - m + j.  Query heads h of n_heads share the channels of kv head
+ * h / (n_heads / kv_heads), kv_heads = channels / head_dim.
+ *   out = sum_t p_t v_t,  p = softmax_t(scale q . k_t),  lse = log sum_t exp(scale q . k_t)
+ * with scores, sums and lse in binary32 and the weights p rounded to binary16
+ * for the product with v.  What a masked or missing token holds (also NaN
+ * or infinity) has no influence.  A query that sees nothing, or only scores of
+ * -infinity, gets zeros and lse = -infinity.
+ *
+ * Group g: sequences group_starts[g] .. group_starts[g+1] - 1, whose first
+ * prefix_lens[g] tokens are the same, as forks of one row have them; they are read
+ * through the row of the group's first sequence.  Every sequence of the group
+ * that has queries must be at least prefix_lens[g] + m long; one that is not gets
+ * zeros, lse = -infinity and bit 2.  Sequences in no group, and n_groups = 0
+ * (pointers may be NULL), are computed by themselves.
+ *
+ * Rows of out and lse that no sequence has queries for are left as they were.
+ * Tokens of pages outside the pool are left out (bit 1). */
+typedef struct {
+  int32_t layer;                /* 0 .. layers - 1 */
+  int32_t n_heads, head_dim;    /* head_dim a multiple of 8 up to 256 that divides channels;
+                                   n_heads a multiple of kv_heads, at most 1024 */
+  float scale;                  /* finite */
+  int32_t n_seqs, n_q, n_groups; /* 0 .. n_rows, 0 .. 2^20 (rows of q), 0 .. n_seqs */
+  int32_t max_q, max_prefix, max_len; /* what to size the launch for, >= 0: queries of a
+                                   sequence, longest shared prefix, longest row.  Other
+                                   lengths are computed as correctly, if less fast */
+  const int32_t* rows_dev;      /* [n_seqs] or NULL */
+  const int32_t* q_starts_dev;  /* [n_seqs + 1], ascending within 0 .. n_q */
+  const int32_t* group_starts_dev; /* [n_groups + 1], ascending within 0 .. n_seqs */
+  const int32_t* prefix_lens_dev;  /* [n_groups] */
+  const void* q_dev;            /* fp16 [n_q][n_heads][head_dim], q_stride elements a token */
+  void* out_dev;                /* the same with out_stride */
+  float* lse_dev;               /* [n_q][n_heads] or NULL */
+  int64_t q_stride, out_stride; /* multiples of 8, >= n_heads x head_dim */
+} cg_attention;
+
+/* Bytes of workspace (16-byte aligned) that this call needs: it depends on the
+ * cache's and the call's numbers, not on pointers or device values.  Host only. */
+int cg_attention_workspace(const cg_paged_cache* cache, const cg_attention* call, size_t* bytes);
+
+/* CG_E_INVAL also for pools, q or out that are not 16-byte aligned. */
+int cg_attention_prefix_async(const cg_paged_cache* cache, const cg_attention* call,
+                              void* workspace_dev, size_t workspace_bytes, void* stream);
+
 /* For long-running processes: frees the device memory the library keeps
  * between calls, on every device it has used — the table-build and encode
  * workspaces (and their pinned host words), and the blocks its per-device

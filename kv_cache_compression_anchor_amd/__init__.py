@@ -3,7 +3,11 @@ declared in include/cachegen.h) and its thin Python binding."""
 from ._binding import (CG_GROUP_CHANNEL, CG_GROUP_GLOBAL, CG_GROUP_LAYER,  # noqa: F401
                        CG_GROUP_LAYER_CHANNEL, CG_E_CAPACITY, CG_E_CORRUPT, CG_E_HIP, CG_E_INVAL, CG_E_MISMATCH,  # noqa: F401
                        CG_E_NOMEM, CG_OK, CG_Q_H, CG_Q_L, CG_Q_M, EXPORTS, LIB_PATH, CgError,
-                       Tables, cg_build_tables, cg_build_tables_grouped, cg_chunk_info, cg_chunk_info_parse, cg_decode,
+                       PagedCache, Tables, cg_attention, cg_attention_prefix_async,
+                       cg_attention_workspace, cg_paged_cache, cg_pages_compact_async,
+                       cg_pages_copy_async, cg_pages_fork_async, cg_pages_free_async,
+                       cg_pages_reserve_async, cg_pages_workspace, cg_pages_write_async,
+                       cg_build_tables, cg_build_tables_grouped, cg_chunk_info, cg_chunk_info_parse, cg_decode,
                        cg_decode_async, cg_decode_paged_async, cg_decode_streamed, cg_encode,
                        cg_encode_batch, cg_encode_batch_noalloc,
                        cg_encode_bound,
@@ -13,4 +17,4 @@ from ._binding import (CG_GROUP_CHANNEL, CG_GROUP_GLOBAL, CG_GROUP_LAYER,  # noq
                        make_params)
 
 __all__ = [n for n in dir() if n.startswith("cg_") or n.startswith("CG_")] + [
-    "CgError", "Tables", "lib", "make_params", "EXPORTS", "LIB_PATH"]
+    "CgError", "PagedCache", "Tables", "lib", "make_params", "EXPORTS", "LIB_PATH"]

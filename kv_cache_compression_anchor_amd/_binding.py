@@ -24,7 +24,10 @@ _NAMES = {0: "CG_OK", -1: "CG_E_INVAL", -2: "CG_E_NOMEM", -3: "CG_E_HIP", -4: "C
 EXPORTS = ["cg_build_tables", "cg_build_tables_grouped", "cg_tables_free", "cg_tables_serialize",
            "cg_tables_deserialize", "cg_tables_id", "cg_tables_params", "cg_num_chunks", "cg_encode_bound", "cg_encode",
            "cg_encode_batch", "cg_encode_batch_noalloc", "cg_chunk_info_parse", "cg_decode", "cg_decode_async", "cg_decode_paged_async",
-           "cg_decode_streamed",
+           "cg_decode_streamed", "cg_pages_workspace", "cg_pages_copy_async",
+           "cg_pages_reserve_async", "cg_pages_write_async", "cg_pages_fork_async",
+           "cg_pages_free_async", "cg_pages_compact_async", "cg_attention_workspace",
+           "cg_attention_prefix_async",
            "cg_plan_chunk", "cg_release_cached", "cg_last_error"]
 
 
@@ -53,6 +56,25 @@ class cg_chunk_info(C.Structure):
                 ("group_tokens", C.c_int32), ("n_groups", C.c_int32), ("quality", C.c_int32),
                 ("payload_words", C.c_uint32), ("version", C.c_uint32),
                 ("tables_id", C.c_uint64), ("blob_bytes", C.c_uint64)]
+
+
+class cg_paged_cache(C.Structure):
+    _fields_ = [("device", C.c_int32), ("layers", C.c_int32), ("channels", C.c_int32),
+                ("page_tokens", C.c_int32), ("num_pages", C.c_int32), ("n_rows", C.c_int32),
+                ("max_blocks", C.c_int32), ("reserved", C.c_int32),
+                ("k_pool_dev", C.c_void_p), ("v_pool_dev", C.c_void_p),
+                ("tables_dev", C.c_void_p), ("lens_dev", C.c_void_p), ("refs_dev", C.c_void_p),
+                ("status_dev", C.c_void_p)]
+
+
+class cg_attention(C.Structure):
+    _fields_ = [("layer", C.c_int32), ("n_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("scale", C.c_float), ("n_seqs", C.c_int32), ("n_q", C.c_int32),
+                ("n_groups", C.c_int32), ("max_q", C.c_int32), ("max_prefix", C.c_int32),
+                ("max_len", C.c_int32), ("rows_dev", C.c_void_p), ("q_starts_dev", C.c_void_p),
+                ("group_starts_dev", C.c_void_p), ("prefix_lens_dev", C.c_void_p),
+                ("q_dev", C.c_void_p), ("out_dev", C.c_void_p), ("lse_dev", C.c_void_p),
+                ("q_stride", C.c_int64), ("out_stride", C.c_int64)]
 
 
 _lib = None
@@ -89,6 +111,15 @@ def lib():
                                           C.c_int64, I32, P, C.c_int64, P, P]),
             "cg_decode_streamed": (I, [P, I32, C.POINTER(P), C.POINTER(cg_chunk_info), P, P, P,
                                        SZ, P, P, P]),
+            "cg_pages_workspace": (I, [P, C.POINTER(SZ)]),
+            "cg_pages_copy_async": (I, [P, I32, P, P, P]),
+            "cg_pages_reserve_async": (I, [P, I32, P, P, I32, P, P, SZ, P]),
+            "cg_pages_write_async": (I, [P, I32, I32, I32, P, P, P, C.c_int64, C.c_int64, P]),
+            "cg_pages_fork_async": (I, [P, I32, P, P, P, SZ, P]),
+            "cg_pages_free_async": (I, [P, I32, P, P]),
+            "cg_pages_compact_async": (I, [P, P, P, SZ, P]),
+            "cg_attention_workspace": (I, [P, P, C.POINTER(SZ)]),
+            "cg_attention_prefix_async": (I, [P, P, P, SZ, P]),
             "cg_plan_chunk": (I, [C.POINTER(cg_chunk_plan_in), C.POINTER(I32),
                                   C.POINTER(C.c_double)]),
             "cg_release_cached": (I, []),
@@ -360,6 +391,184 @@ def cg_decode_streamed(t: Tables, host_blobs, infos, k_out, v_out, staging, stat
                                     _dev_ptr(staging, torch.uint8, "staging"), staging.numel(),
                                     _dev_ptr(status, torch.int32, "status"),
                                     _stream(copy_stream), _stream(compute_stream)))
+
+
+def _rows3(t, dtype, device, last, what):
+    """(stride of axis 0, stride of axis 1) of a 3-d device tensor whose last axis
+    is contiguous, as the library counts them: an axis of one element, whose stride
+    a view leaves at anything, gets the one it would have if contiguous."""
+    if (t.dim() != 3 or t.dtype != dtype or t.device != device or t.shape[2] != last
+            or (t.stride(2) != 1 and last > 1 and t.numel())):
+        raise ValueError(f"{what} must be {dtype} [.., .., {last}] on the cache's device, its last "
+                         "axis contiguous")
+    s1 = t.stride(1) if t.shape[1] > 1 else last
+    return (t.stride(0) if t.shape[0] > 1 else s1 * t.shape[1]), s1
+
+
+class PagedCache:
+    """A paged cache over caller-owned device tensors of one device: fp16 pools
+    [layers, num_pages, page_tokens, channels], int32 tables [rows, max_blocks],
+    int32 lens [rows], int32 refs [num_pages], int32 status [1].  Keeps the
+    tensors and the struct that the cg_pages_* and cg_attention_* calls take."""
+
+    def __init__(self, k_pool, v_pool, tables, lens, refs, status):
+        import torch
+        if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
+            raise ValueError("pools must both be [layers, num_pages, page_tokens, channels]")
+        if tables.dim() != 2 or lens.numel() != tables.shape[0]:
+            raise ValueError("tables must be [rows, max_blocks] and lens [rows]")
+        if refs.numel() != k_pool.shape[1]:
+            raise ValueError("refs must be [num_pages]")
+        if status.numel() < 1:
+            raise ValueError("status must be one int32")
+        self.device = k_pool.device
+        self.tensors = (k_pool, v_pool, tables, lens, refs, status)
+        s = cg_paged_cache()
+        for name, t, dtype in (("k_pool", k_pool, torch.float16), ("v_pool", v_pool, torch.float16),
+                               ("tables", tables, torch.int32), ("lens", lens, torch.int32),
+                               ("refs", refs, torch.int32), ("status", status, torch.int32)):
+            if t.device != self.device:
+                raise ValueError("the tensors of a cache must be on one device")
+            setattr(s, name + "_dev", _dev_ptr(t, dtype, name))
+        s.device = self.device.index
+        s.layers, s.num_pages, s.page_tokens, s.channels = k_pool.shape
+        s.n_rows, s.max_blocks = tables.shape
+        self.struct = s
+        self.ref = C.byref(s)
+
+    def _ptr(self, t, dtype, what, numel=None):
+        """Device address of a tensor of a call on this cache (None: NULL)."""
+        if t is None:
+            return None
+        if (t.dtype != dtype or t.device != self.device or not t.is_contiguous()
+                or (numel is not None and t.numel() != numel)):
+            raise ValueError(f"{what} must be contiguous {dtype} on the cache's device"
+                             + (f" with {numel} elements" if numel is not None else ""))
+        return t.data_ptr()
+
+    def _stream(self, stream):
+        if stream is None:
+            import torch
+            return torch.cuda.current_stream(self.device).cuda_stream
+        return _stream(stream)
+
+    def _ws(self, ws):
+        import torch
+        return self._ptr(ws, torch.uint8, "workspace"), ws.numel()
+
+
+def cg_pages_workspace(cache: PagedCache) -> int:
+    n = C.c_size_t(0)
+    _check(lib().cg_pages_workspace(cache.ref, C.byref(n)))
+    return n.value
+
+
+def cg_pages_copy_async(cache: PagedCache, src, dst, stream=None):
+    """Copies page src[i] to page dst[i] in every layer (int32 device tensors)."""
+    import torch
+    n = src.numel()
+    _check(lib().cg_pages_copy_async(cache.ref, n, cache._ptr(src, torch.int32, "src"),
+                                     cache._ptr(dst, torch.int32, "dst", n),
+                                     cache._stream(stream)))
+
+
+def cg_pages_reserve_async(cache: PagedCache, rows, starts, slots, workspace, n_tokens=None,
+                           stream=None):
+    """Room for tokens starts[i] .. starts[i+1]-1 in row rows[i]; slots (int64, one
+    per token) receives where they go.  slots None: n_tokens says how many there are."""
+    import torch
+    n = rows.numel()
+    if n_tokens is None:
+        n_tokens = slots.numel()
+    ws, nws = cache._ws(workspace)
+    _check(lib().cg_pages_reserve_async(cache.ref, n, cache._ptr(rows, torch.int32, "rows"),
+                                        cache._ptr(starts, torch.int32, "starts", n + 1), n_tokens,
+                                        cache._ptr(slots, torch.int64, "slots", n_tokens),
+                                        ws, nws, cache._stream(stream)))
+
+
+def cg_pages_write_async(cache: PagedCache, layer0, slots, k_new, v_new, stream=None):
+    """Writes k_new / v_new (fp16 [layers, tokens, channels], channels contiguous,
+    both with the same strides) to `slots` in layers layer0 .."""
+    import torch
+    ch = cache.struct.channels
+    ls, ts = _rows3(k_new, torch.float16, cache.device, ch, "k_new")
+    if k_new.shape != v_new.shape or (ls, ts) != _rows3(v_new, torch.float16, cache.device, ch,
+                                                        "v_new"):
+        raise ValueError("k_new and v_new must have the same shape and strides")
+    layers, n, _ = k_new.shape
+    _check(lib().cg_pages_write_async(cache.ref, layer0, layers, n,
+                                      cache._ptr(slots, torch.int64, "slots", n), k_new.data_ptr(),
+                                      v_new.data_ptr(), ts, ls, cache._stream(stream)))
+
+
+def cg_pages_fork_async(cache: PagedCache, parents, children, workspace, stream=None):
+    """Row children[i] continues row parents[i]: full pages shared, the rows in
+    use of a last page that is not full copied."""
+    import torch
+    n = parents.numel()
+    ws, nws = cache._ws(workspace)
+    _check(lib().cg_pages_fork_async(cache.ref, n, cache._ptr(parents, torch.int32, "parents"),
+                                     cache._ptr(children, torch.int32, "children", n), ws, nws,
+                                     cache._stream(stream)))
+
+
+def cg_pages_free_async(cache: PagedCache, rows, stream=None):
+    """Empties rows; pages that no other row names become free."""
+    import torch
+    _check(lib().cg_pages_free_async(cache.ref, rows.numel(), cache._ptr(rows, torch.int32, "rows"),
+                                     cache._stream(stream)))
+
+
+def cg_pages_compact_async(cache: PagedCache, workspace, n_live=None, stream=None):
+    """Packs the pages in use into the lowest numbers; n_live (int32 [1]) receives
+    how many there are."""
+    import torch
+    ws, nws = cache._ws(workspace)
+    _check(lib().cg_pages_compact_async(cache.ref, cache._ptr(n_live, torch.int32, "n_live", 1),
+                                        ws, nws, cache._stream(stream)))
+
+
+def cg_attention_workspace(cache: PagedCache, n_q, n_heads, head_dim, n_seqs, n_groups, max_q,
+                           max_prefix, max_len) -> int:
+    """Bytes of workspace of a cg_attention_prefix_async call of these numbers."""
+    a = cg_attention()
+    a.n_q, a.n_heads, a.head_dim, a.n_seqs, a.n_groups = n_q, n_heads, head_dim, n_seqs, n_groups
+    a.max_q, a.max_prefix, a.max_len = max_q, max_prefix, max_len
+    n = C.c_size_t(0)
+    _check(lib().cg_attention_workspace(cache.ref, C.byref(a), C.byref(n)))
+    return n.value
+
+
+def cg_attention_prefix_async(cache: PagedCache, layer, q, out, scale, rows, q_starts, group_starts,
+                              prefix_lens, max_q, max_prefix, max_len, workspace, lse=None,
+                              stream=None):
+    """Attention of q (fp16 [tokens, heads, head_dim]) over layer `layer` of the
+    cache into out (the same shape) and lse (fp32 [tokens, heads], may be None).
+    rows None: sequence s is row s.  group_starts / prefix_lens None: no shared
+    prefixes.  q and out may have a longer stride between tokens."""
+    import torch
+    n_q, heads, dim = q.shape
+    q_stride, s1 = _rows3(q, torch.float16, cache.device, dim, "q")
+    out_stride, s2 = _rows3(out, torch.float16, cache.device, dim, "out")
+    if out.shape != q.shape or (n_q and (s1 != dim or s2 != dim)):
+        raise ValueError("out must have the shape of q, the heads of both contiguous")
+    n = q_starts.numel() - 1
+    groups = 0 if group_starts is None else group_starts.numel() - 1
+    a = cg_attention()
+    a.layer, a.n_heads, a.head_dim, a.scale = layer, heads, dim, scale
+    a.n_seqs, a.n_q, a.n_groups = n, n_q, groups
+    a.max_q, a.max_prefix, a.max_len = max_q, max_prefix, max_len
+    i32 = torch.int32
+    a.rows_dev = cache._ptr(rows, i32, "rows", n)
+    a.q_starts_dev = cache._ptr(q_starts, i32, "q_starts")
+    a.group_starts_dev = cache._ptr(group_starts, i32, "group_starts")
+    a.prefix_lens_dev = cache._ptr(prefix_lens, i32, "prefix_lens", groups)
+    a.q_dev, a.out_dev = q.data_ptr(), out.data_ptr()
+    a.lse_dev = cache._ptr(lse, torch.float32, "lse", n_q * heads)
+    a.q_stride, a.out_stride = q_stride, out_stride
+    ws, nws = cache._ws(workspace)
+    _check(lib().cg_attention_prefix_async(cache.ref, C.byref(a), ws, nws, cache._stream(stream)))
 
 
 def cg_release_cached():

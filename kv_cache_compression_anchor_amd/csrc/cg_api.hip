@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "cg_build.h"
+#include "cg_hostapi.h"
 
 using namespace cg;
 
@@ -26,29 +27,6 @@ struct cg_tables {
 };
 
 namespace {
-
-int hip_fail(hipError_t e, const char* what) {
-  return fail(CG_E_HIP, std::string(what) + ": " + hipGetErrorString(e));
-}
-
-#define HIP_TRY(expr, what)               \
-  do {                                    \
-    hipError_t e_ = (expr);               \
-    if (e_ != hipSuccess) return hip_fail(e_, what); \
-  } while (0)
-
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) prev = -1;
-    if (prev != dev) ok = hipSetDevice(dev) == hipSuccess;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
 
 void init_dev_tables(DevTables& t, const cg_params& p) {
   t.L = p.layers;

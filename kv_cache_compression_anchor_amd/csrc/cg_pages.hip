@@ -1,0 +1,677 @@
+// Pages of a cache: copying, reserving and writing new tokens, forking, freeing,
+// compacting (include/cachegen.h, "Paged caches").
+//
+// Two kinds of work.  Bookkeeping (who gets which page) is a handful of prefix
+// sums over the requests and over refs; each call does it in one workgroup of
+// 1,024 threads, so that one launch suffices and page numbers do not depend on
+// scheduling.  Moving K and V is a plain copy bound by HBM; it is cut into
+// pieces of kPieceUnits units spread over the chip.
+#include <algorithm>
+
+#include "cg_hostapi.h"
+#include "cg_internal.h"
+#include "cg_paged.h"
+
+namespace cg {
+namespace {
+
+constexpr int kThreads = 1024;            // of a bookkeeping workgroup
+constexpr int kWaves = kThreads / 64;
+constexpr int kScanPages = 16 * kThreads; // pages of refs looked at per scan step
+constexpr int kCopyThreads = 256;
+constexpr int kPieceUnits = 2048;         // units a copying workgroup moves per piece
+constexpr uint32_t kBadPage = 2u, kRefused = 4u, kNoPages = 8u;  // status bits
+
+struct Cache {  // the device side's view of cg_paged_cache
+  int L, C, P, shift, N, R, B;
+  char *k, *v;
+  int32_t *tables, *lens, *refs;
+  uint32_t* status;
+};
+
+// ---------------------------------------------------------------------------
+// Prefix sums of a bookkeeping workgroup
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
+__device__ __forceinline__ int below(uint64_t mask) {  // set bits below this lane
+  return __popcll(mask & ((1ull << lane_id()) - 1));
+}
+
+struct ScanLds {
+  int64_t wave[kWaves];
+};
+
+// exclusive sum of one value per thread; *total receives the sum
+__device__ int64_t block_scan(int64_t x, ScanLds& s, int64_t* total) {
+  int64_t inc = x;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t y = __shfl_up(inc, d);
+    if (lane_id() >= d) inc += y;
+  }
+  __syncthreads();  // s is free again
+  if (lane_id() == 63) s.wave[threadIdx.x >> 6] = inc;
+  __syncthreads();
+  int64_t base = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; w++) {
+    const int64_t t = s.wave[w];
+    if (w < (int)(threadIdx.x >> 6)) base += t;
+    all += t;
+  }
+  *total = all;
+  return base + inc - x;
+}
+
+// Calls f(page, rank) for every page in [from, to) that is free (kFree) or in use
+// (!kFree), rank in ascending order, until `limit` were found; returns how many
+// there are up to where it stopped.  A wave looks at 1,024 consecutive pages per
+// step: 16 coalesced loads in flight, one ballot each.
+template <bool kFree, class F>
+__device__ int scan_pages(const int32_t* refs, int from, int to, int limit, ScanLds& s, F f) {
+  int found = 0;
+  for (int base = from; base < to && found < limit; base += kScanPages) {
+    const int p0 = base + (threadIdx.x >> 6) * 1024 + lane_id();
+    uint64_t hit[16];
+    int n = 0;
+    int32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      const int p = p0 + 64 * i;
+      r[i] = p < to ? refs[p] : (kFree ? 1 : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      hit[i] = __ballot(kFree ? r[i] == 0 : r[i] > 0);
+      n += __popcll(hit[i]);
+    }
+    int64_t all;
+    const int at = (int)block_scan(lane_id() == 0 ? n : 0, s, &all);
+    int rank = found + __shfl(at, 0);
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      if ((hit[i] >> lane_id()) & 1) f(p0 + 64 * i, rank + below(hit[i]));
+      rank += __popcll(hit[i]);
+    }
+    found += (int)all;
+  }
+  return found;
+}
+
+// One bit per row of the cache (n_rows <= 65536).
+constexpr int kRowWords = 65536 / 32;
+__device__ __forceinline__ void clear_bits(uint32_t* b, int rows) {
+  for (int i = threadIdx.x; i < (rows + 31) / 32; i += kThreads) b[i] = 0;
+}
+__device__ __forceinline__ bool test_bit(const uint32_t* b, int i) { return (b[i >> 5] >> (i & 31)) & 1; }
+__device__ __forceinline__ bool set_bit(uint32_t* b, int i) {  // whether it was set before
+  return (atomicOr(&b[i >> 5], 1u << (i & 31)) >> (i & 31)) & 1;
+}
+
+__device__ __forceinline__ bool row_ok(const Cache& c, int r) { return r >= 0 && r < c.R; }
+__device__ __forceinline__ bool page_ok(const Cache& c, int p) { return p >= 0 && p < c.N; }
+__device__ __forceinline__ bool len_ok(const Cache& c, int64_t n) {
+  return n >= 0 && n <= (int64_t)c.B << c.shift;
+}
+__device__ __forceinline__ int blocks_of(const Cache& c, int64_t n) {
+  return (int)((n + c.P - 1) >> c.shift);
+}
+__device__ __forceinline__ int32_t& entry(const Cache& c, int row, int b) {
+  return c.tables[(int64_t)row * c.B + b];
+}
+
+// largest i in [0, n) with a[i] <= x, or -1
+__device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {
+  int lo = -1, hi = n;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (a[m] <= x) lo = m; else hi = m;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------------------
+// Moving rows of pages
+// ---------------------------------------------------------------------------
+// Piece `piece` of the copy of the first `units` units (of sizeof(U) bytes) of
+// page src to page dst in all layers of both pools; the units of the
+// (kv, layer)s are numbered through.  Four loads are in flight per thread.
+template <class U>
+__device__ __forceinline__ void copy_piece(const Cache& c, int src, int dst, uint32_t units,
+                                           int64_t piece) {
+  const int64_t all = (int64_t)2 * c.L * units;
+  const int64_t first = piece * kPieceUnits;
+  const int64_t page_bytes = (int64_t)c.P * c.C * 2;
+  const uint32_t n = (uint32_t)(all - first < kPieceUnits ? all - first : kPieceUnits);
+  const uint32_t sl0 = (uint32_t)(first / units), u0 = (uint32_t)(first % units);
+  for (uint32_t i = threadIdx.x; i < n; i += 4 * kCopyThreads) {
+    U x[4];
+    int64_t off[4];
+    char* base[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const uint32_t e = i + j * kCopyThreads;
+      if (e < n) {
+        const uint32_t sl = sl0 + (u0 + e) / units, u = (u0 + e) % units;
+        base[j] = sl < (uint32_t)c.L ? c.k : c.v;
+        const int64_t l = sl < (uint32_t)c.L ? sl : sl - c.L;
+        off[j] = l * c.N * page_bytes + (int64_t)u * sizeof(U);
+        x[j] = *(const U*)(base[j] + off[j] + src * page_bytes);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      if (i + j * kCopyThreads < n) *(U*)(base[j] + off[j] + dst * page_bytes) = x[j];
+  }
+}
+
+__host__ __device__ __forceinline__ int64_t pieces_of(int L, int64_t units) {
+  return (2 * (int64_t)L * units + kPieceUnits - 1) / kPieceUnits;
+}
+
+// Pair i is copied unless its dst is named twice or its src is a dst: every
+// workgroup looks through the lists for its own pair, n / 256 pairs a thread,
+// which needs no workspace and no second launch.
+template <class U>
+__global__ __launch_bounds__(kCopyThreads) void k_pages_copy(Cache c, int n, const int32_t* src,
+                                                             const int32_t* dst, int64_t pieces) {
+  for (int64_t w = blockIdx.x; w < n * pieces; w += gridDim.x) {
+    const int i = (int)(w / pieces);
+    const int s = src[i], d = dst[i];
+    bool clash = false;
+    for (int j = threadIdx.x; j < n; j += kCopyThreads) {
+      const int o = dst[j];
+      clash |= o == s || (o == d && j != i);
+    }
+    clash = __syncthreads_or(clash);
+    if (!page_ok(c, s) || !page_ok(c, d)) {
+      if (threadIdx.x == 0) atomicOr(c.status, kBadPage);
+    } else if (clash) {
+      if (threadIdx.x == 0) atomicOr(c.status, kRefused);
+    } else {
+      copy_piece<U>(c, s, d, (uint32_t)((int64_t)c.P * c.C * 2 / sizeof(U)), w % pieces);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Reserve
+// ---------------------------------------------------------------------------
+// Slots of tokens [t0, t1): the request by binary search in starts, the page
+// from the row's table.  Runs behind the tables' and lens' update.
+__device__ void fill_slots(const Cache& c, int n, const int32_t* rows, const int32_t* starts,
+                           const int32_t* ok, int64_t* slots, int t0, int t1, int step) {
+  for (int t = t0; t < t1; t += step) {
+    int64_t slot = -1;
+    const int i = last_at_most(starts, n, t);
+    if (i >= 0 && t < starts[i + 1] && ok[i]) {
+      const int row = rows[i];
+      const int64_t pos = (int64_t)c.lens[row] - (starts[i + 1] - t);
+      const int page = entry(c, row, (int)(pos >> c.shift));
+      if (page_ok(c, page))
+        slot = ((int64_t)page << c.shift) + (pos & (c.P - 1));
+      else
+        atomicOr(c.status, kBadPage);
+    }
+    slots[t] = slot;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_reserve(Cache c, int n, const int32_t* rows,
+                                                      const int32_t* starts, int n_tokens,
+                                                      int64_t* slots, int32_t* cum, int32_t* ok,
+                                                      int32_t* list) {
+  __shared__ ScanLds s;
+  __shared__ uint32_t seen[kRowWords], twice[kRowWords];
+  clear_bits(seen, c.R);
+  clear_bits(twice, c.R);
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads)
+    if (row_ok(c, rows[i]) && set_bit(seen, rows[i])) set_bit(twice, rows[i]);
+  __syncthreads();
+  // what each request needs, and where its pages start in the dealt list
+  constexpr int64_t kMany = 1 << 30;  // sums are cut there: no pool has so many pages
+  int64_t sum = 0;
+  for (int base = 0; base < n; base += kThreads) {
+    const int i = base + threadIdx.x;
+    int need = 0, good = 0;
+    if (i < n) {
+      const int row = rows[i], a = starts[i], b = starts[i + 1];
+      if (row_ok(c, row) && !test_bit(twice, row) && a >= 0 && a <= b && b <= n_tokens) {
+        const int64_t len = c.lens[row];
+        if (len_ok(c, len) && len_ok(c, len + (b - a))) {
+          good = 1;
+          need = blocks_of(c, len + (b - a)) - blocks_of(c, len);
+        }
+      }
+      if (!good) atomicOr(c.status, kRefused);
+    }
+    int64_t all;
+    const int64_t at = sum + block_scan(need, s, &all);
+    if (i < n) {
+      cum[i] = (int)(at < kMany ? at : kMany);
+      ok[i] = good;
+    }
+    sum += all;
+  }
+  const int total = (int)(sum < kMany ? sum : kMany);
+  if (threadIdx.x == 0) cum[n] = total;
+  __syncthreads();
+  const int found = total ? scan_pages<true>(c.refs, 0, c.N, total, s,
+                                             [&](int page, int rank) {
+                                               if (rank < total) list[rank] = page;
+                                             })
+                          : 0;
+  const int have = min(found, total);
+  __syncthreads();
+  for (int r = threadIdx.x; r < have; r += kThreads) {
+    const int i = last_at_most(cum, n, r);  // the last of equal ones: the request that needs pages
+    if (cum[i + 1] <= have) {
+      const int row = rows[i];
+      entry(c, row, blocks_of(c, c.lens[row]) + (r - cum[i])) = list[r];
+      c.refs[list[r]] = 1;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    if (!ok[i]) continue;
+    if (cum[i + 1] > cum[i] && cum[i + 1] > have) {
+      ok[i] = 0;
+      atomicOr(c.status, kNoPages);
+    } else {
+      c.lens[rows[i]] += starts[i + 1] - starts[i];
+    }
+  }
+  if (!slots) return;
+  __syncthreads();
+  fill_slots(c, n, rows, starts, ok, slots, threadIdx.x, n_tokens, kThreads);
+}
+
+// ---------------------------------------------------------------------------
+// Write
+// ---------------------------------------------------------------------------
+// A workgroup writes `tile` tokens of one (kv, layer): a token's row is `units`
+// units, contiguous on both sides.
+template <class U>
+__global__ __launch_bounds__(kCopyThreads) void k_write(Cache c, int layer0, int n_layers,
+                                                        int n_tokens, const int64_t* slots,
+                                                        const char* k_new, const char* v_new,
+                                                        int64_t token_bytes, int64_t layer_bytes,
+                                                        uint32_t units, int tile) {
+  const int sl = blockIdx.y, l = sl < n_layers ? sl : sl - n_layers;
+  const char* from = (sl < n_layers ? k_new : v_new) + l * layer_bytes;
+  const int64_t row_bytes = (int64_t)c.C * 2;
+  char* to = (sl < n_layers ? c.k : c.v) + (int64_t)(layer0 + l) * c.N * c.P * row_bytes;
+  const int64_t t0 = (int64_t)blockIdx.x * tile;
+  const uint32_t nt = (uint32_t)(n_tokens - t0 < tile ? n_tokens - t0 : tile);
+  const int64_t cap = (int64_t)c.N << c.shift;
+  for (uint32_t e = threadIdx.x; e < nt * units; e += kCopyThreads) {
+    const uint32_t t = e / units, u = e % units;
+    const int64_t slot = slots[t0 + t];
+    if (slot >= 0 && slot < cap)
+      *(U*)(to + slot * row_bytes + (int64_t)u * sizeof(U)) =
+          *(const U*)(from + (t0 + t) * token_bytes + (int64_t)u * sizeof(U));
+    else if (slot != -1 && u == 0)
+      atomicOr(c.status, kBadPage);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Fork
+// ---------------------------------------------------------------------------
+// aux[3 i ..]: the parent's partly filled page, the child's page, rows in use
+__global__ __launch_bounds__(kThreads) void k_fork_plan(Cache c, int n, const int32_t* parents,
+                                                        const int32_t* children, int32_t* ok,
+                                                        int32_t* cum, int32_t* aux,
+                                                        int32_t* list) {
+  __shared__ ScanLds s;
+  __shared__ uint32_t kids[kRowWords], twice[kRowWords], olds[kRowWords];
+  clear_bits(kids, c.R);
+  clear_bits(twice, c.R);
+  clear_bits(olds, c.R);
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    if (row_ok(c, children[i]) && set_bit(kids, children[i])) set_bit(twice, children[i]);
+    if (row_ok(c, parents[i])) set_bit(olds, parents[i]);
+  }
+  __syncthreads();
+  int total = 0;
+  for (int base = 0; base < n; base += kThreads) {
+    const int i = base + threadIdx.x;
+    int need = 0, good = 0;
+    if (i < n) {
+      const int par = parents[i], kid = children[i];
+      int part = 0, last = -1;
+      if (row_ok(c, par) && row_ok(c, kid) && !test_bit(twice, kid) && !test_bit(olds, kid) &&
+          c.lens[kid] == 0 && len_ok(c, c.lens[par])) {
+        const int len = c.lens[par];
+        good = 1;
+        part = len & (c.P - 1);
+        if (part) {
+          last = entry(c, par, blocks_of(c, len) - 1);
+          need = 1;
+          if (!page_ok(c, last)) {
+            good = need = 0;
+            atomicOr(c.status, kBadPage);
+          }
+        }
+      } else {
+        atomicOr(c.status, kRefused);
+      }
+      aux[3 * i] = last;
+      aux[3 * i + 2] = part;
+    }
+    int64_t all;
+    const int64_t at = block_scan(need, s, &all);
+    if (i < n) {
+      cum[i] = total + (int)at;
+      ok[i] = good | need << 1;
+    }
+    total += (int)all;
+  }
+  const int found = total ? scan_pages<true>(c.refs, 0, c.N, total, s,
+                                             [&](int page, int rank) {
+                                               if (rank < total) list[rank] = page;
+                                             })
+                          : 0;
+  const int have = min(found, total);
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    if (!(ok[i] & 1)) continue;
+    if ((ok[i] & 2) && cum[i] >= have) {
+      ok[i] = 0;
+      atomicOr(c.status, kNoPages);
+      continue;
+    }
+    if (ok[i] & 2) {
+      aux[3 * i + 1] = list[cum[i]];
+      c.refs[list[cum[i]]] = 1;
+    }
+    c.lens[children[i]] = c.lens[parents[i]];
+  }
+}
+
+// blockIdx.y 0: the child's table row and the counts; others: pieces of the copy
+template <class U>
+__global__ __launch_bounds__(kCopyThreads) void k_fork_copy(Cache c, const int32_t* parents,
+                                                            const int32_t* children,
+                                                            const int32_t* ok, const int32_t* aux) {
+  const int i = blockIdx.x;
+  if (!(ok[i] & 1)) return;
+  const int part = aux[3 * i + 2], to = aux[3 * i + 1];
+  if (blockIdx.y == 0) {
+    const int par = parents[i], kid = children[i];
+    const int nblk = blocks_of(c, c.lens[par]);
+    for (int b = threadIdx.x; b < nblk; b += kCopyThreads) {
+      const bool own = part && b == nblk - 1;
+      const int p = entry(c, par, b);
+      entry(c, kid, b) = own ? to : p;
+      if (own) continue;
+      if (page_ok(c, p))
+        atomicAdd(&c.refs[p], 1);
+      else
+        atomicOr(c.status, kBadPage);
+    }
+    return;
+  }
+  if (!part) return;
+  const uint32_t units = (uint32_t)((int64_t)part * c.C * 2 / sizeof(U));
+  const int64_t pieces = pieces_of(c.L, units);
+  for (int64_t w = blockIdx.y - 1; w < pieces; w += gridDim.y - 1)
+    copy_piece<U>(c, aux[3 * i], to, units, w);
+}
+
+// ---------------------------------------------------------------------------
+// Free
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kCopyThreads) void k_free(Cache c, int n, const int32_t* rows) {
+  const int i = blockIdx.x, row = rows[i];
+  bool again = false;
+  for (int j = threadIdx.x; j < i; j += kCopyThreads) again |= rows[j] == row;
+  again = __syncthreads_or(again);
+  if (again || !row_ok(c, row) || !len_ok(c, c.lens[row])) {
+    if (threadIdx.x == 0) atomicOr(c.status, kRefused);
+    return;
+  }
+  const int nblk = blocks_of(c, c.lens[row]);
+  for (int b = threadIdx.x; b < nblk; b += kCopyThreads) {
+    const int p = entry(c, row, b);
+    entry(c, row, b) = -1;
+    if (!page_ok(c, p)) {
+      atomicOr(c.status, kBadPage);
+    } else if (atomicSub(&c.refs[p], 1) <= 0) {  // counts that were wrong before stay at 0
+      atomicAdd(&c.refs[p], 1);
+      atomicOr(c.status, kRefused);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) c.lens[row] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// Compact
+// ---------------------------------------------------------------------------
+// ws[0] moves; from[j], to[j]: the j-th move; where[p - M]: move of page p
+__global__ __launch_bounds__(kThreads) void k_compact_plan(Cache c, int32_t* live_out, int32_t* ws,
+                                                           int32_t* to, int32_t* from) {
+  __shared__ ScanLds s;
+  const int live = scan_pages<false>(c.refs, 0, c.N, c.N, s, [](int, int) {});
+  const int frees =
+      scan_pages<true>(c.refs, 0, live, c.N, s, [&](int page, int rank) { to[rank] = page; });
+  const int above = scan_pages<false>(c.refs, live, c.N, c.N, s,
+                                      [&](int page, int rank) { from[rank] = page; });
+  // as many as each other unless some count is negative
+  const int moves = min(frees, above);
+  if (frees != above && threadIdx.x == 0) atomicOr(c.status, kRefused);
+  __syncthreads();
+  for (int j = threadIdx.x; j < moves; j += kThreads) {
+    c.refs[to[j]] = c.refs[from[j]];
+    c.refs[from[j]] = 0;
+  }
+  if (threadIdx.x == 0) {
+    ws[0] = moves;
+    if (live_out) *live_out = live;
+  }
+}
+
+// Tables follow (an entry's move by binary search in the ascending `from`), then
+// the pages are copied; both spread over a fixed grid, as the host does not know
+// how many there are.
+template <class U>
+__global__ __launch_bounds__(kCopyThreads) void k_compact_move(Cache c, const int32_t* ws,
+                                                               const int32_t* to,
+                                                               const int32_t* from,
+                                                               int64_t pieces) {
+  const int moves = ws[0];
+  if (moves == 0) return;
+  const int first = from[0];
+  for (int row = blockIdx.x; row < c.R; row += gridDim.x) {
+    const int64_t len = c.lens[row];
+    if (!len_ok(c, len)) continue;
+    const int nblk = blocks_of(c, len);
+    for (int b = threadIdx.x; b < nblk; b += kCopyThreads) {
+      const int p = entry(c, row, b);
+      if (p < first) continue;
+      const int j = last_at_most(from, moves, p);
+      if (from[j] == p) entry(c, row, b) = to[j];
+    }
+  }
+  const uint32_t units = (uint32_t)((int64_t)c.P * c.C * 2 / sizeof(U));
+  for (int64_t w = blockIdx.x; w < moves * pieces; w += gridDim.x) {
+    const int j = (int)(w / pieces);
+    copy_piece<U>(c, from[j], to[j], units, w % pieces);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+Cache view(const cg_paged_cache& c) {
+  return {c.layers, c.channels, c.page_tokens, __builtin_ctz((unsigned)c.page_tokens),
+          c.num_pages, c.n_rows, c.max_blocks, (char*)c.k_pool_dev, (char*)c.v_pool_dev,
+          c.tables_dev, c.lens_dev, c.refs_dev, c.status_dev};
+}
+
+// The widest unit that every address and size is a multiple of: 16 bytes in any
+// model's shape, 4 or 2 for odd channel counts or views of a buffer.
+int unit_of(uint64_t bits) { return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2; }
+uint64_t pool_bits(const cg_paged_cache& c) { return (uintptr_t)c.k_pool_dev | (uintptr_t)c.v_pool_dev; }
+
+#define BY_UNIT(unit, call)                        \
+  do {                                             \
+    if ((unit) == 16) { using U = uint4; call; }   \
+    else if ((unit) == 4) { using U = uint32_t; call; } \
+    else { using U = uint16_t; call; }             \
+  } while (0)
+
+int launched(const char* what) {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? CG_OK : hip_fail(e, what);
+}
+
+int check_workspace(const cg_paged_cache* c, const void* ws, size_t bytes) {
+  if (!ws || (uintptr_t)ws % 16) return fail(CG_E_INVAL, "workspace NULL or not 16-byte aligned");
+  if (bytes < 4 * pages_ws(*c).words) return fail(CG_E_CAPACITY, "workspace too small");
+  return CG_OK;
+}
+
+constexpr int64_t kMaxGrid = 1 << 20;
+
+}  // namespace
+}  // namespace cg
+
+using namespace cg;
+
+extern "C" {
+
+int cg_pages_workspace(const cg_paged_cache* c, size_t* bytes) {
+  if (int rc = check_paged_cache(c)) return rc;
+  if (!bytes) return fail(CG_E_INVAL, "bytes is NULL");
+  *bytes = 4 * pages_ws(*c).words;
+  return CG_OK;
+}
+
+int cg_pages_copy_async(const cg_paged_cache* c, int32_t n, const int32_t* src_dev,
+                        const int32_t* dst_dev, void* stream) {
+  if (int rc = check_paged_cache(c)) return rc;
+  if (n < 0 || n > c->num_pages) return fail(CG_E_INVAL, "n must be in 0..num_pages");
+  if (n == 0) return CG_OK;
+  if (!src_dev || !dst_dev) return fail(CG_E_INVAL, "NULL list");
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
+  const int64_t page = (int64_t)c->page_tokens * c->channels * 2;
+  const int unit = unit_of((uint64_t)page | pool_bits(*c));
+  const int64_t pieces = pieces_of(c->layers, page / unit);
+  const int grid = (int)std::min(n * pieces, kMaxGrid);
+  BY_UNIT(unit, (k_pages_copy<U><<<grid, kCopyThreads, 0, (hipStream_t)stream>>>(
+                    view(*c), n, src_dev, dst_dev, pieces)));
+  return launched("page copy");
+}
+
+int cg_pages_reserve_async(const cg_paged_cache* c, int32_t n, const int32_t* rows_dev,
+                           const int32_t* starts_dev, int32_t n_tokens, int64_t* slots_dev,
+                           void* workspace_dev, size_t workspace_bytes, void* stream) {
+  if (int rc = check_paged_cache(c)) return rc;
+  if (n < 0 || n > c->n_rows || n_tokens < 0 || n_tokens > kMaxTokens)
+    return fail(CG_E_INVAL, "n must be in 0..n_rows and n_tokens in 0..2^21");
+  if (n == 0 && (n_tokens == 0 || !slots_dev)) return CG_OK;
+  if (n > 0 && (!rows_dev || !starts_dev)) return fail(CG_E_INVAL, "NULL list");
+  if (int rc = check_workspace(c, workspace_dev, workspace_bytes)) return rc;
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
+  const PagesWs w = pages_ws(*c);
+  int32_t* ws = (int32_t*)workspace_dev;
+  k_reserve<<<1, kThreads, 0, (hipStream_t)stream>>>(view(*c), n, rows_dev, starts_dev, n_tokens,
+                                                     slots_dev, ws + w.cum, ws + w.ok, ws + w.list);
+  return launched("reserve");
+}
+
+int cg_pages_write_async(const cg_paged_cache* c, int32_t layer0, int32_t n_layers,
+                         int32_t n_tokens, const int64_t* slots_dev, const void* k_new_dev,
+                         const void* v_new_dev, int64_t token_stride, int64_t layer_stride,
+                         void* stream) {
+  if (int rc = check_paged_cache(c)) return rc;
+  if (layer0 < 0 || n_layers < 0 || layer0 > c->layers - n_layers)
+    return fail(CG_E_INVAL, "layers out of range");
+  if (n_tokens < 0 || n_tokens > kMaxTokens)
+    return fail(CG_E_INVAL, "n_tokens must be in 0..2^21");
+  const int64_t most = (int64_t)1 << 40;
+  if (token_stride < c->channels || token_stride > most || layer_stride < 0 || layer_stride > most)
+    return fail(CG_E_INVAL, "token_stride must be at least channels, layer_stride not negative");
+  if (n_layers == 0 || n_tokens == 0) return CG_OK;
+  if (!slots_dev || !k_new_dev || !v_new_dev) return fail(CG_E_INVAL, "NULL argument");
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
+  const int64_t row = (int64_t)c->channels * 2;
+  const int unit = unit_of((uint64_t)row | pool_bits(*c) | (uintptr_t)k_new_dev |
+                           (uintptr_t)v_new_dev | (uint64_t)(2 * token_stride) |
+                           (uint64_t)(n_layers > 1 ? 2 * layer_stride : 0));
+  const uint32_t units = (uint32_t)(row / unit);
+  const int tile = (int)std::max<int64_t>(1, kPieceUnits / units);
+  const dim3 grid((unsigned)((n_tokens + tile - 1) / tile), 2 * n_layers);
+  BY_UNIT(unit, (k_write<U><<<grid, kCopyThreads, 0, (hipStream_t)stream>>>(
+                    view(*c), layer0, n_layers, n_tokens, slots_dev, (const char*)k_new_dev,
+                    (const char*)v_new_dev, 2 * token_stride, 2 * layer_stride, units, tile)));
+  return launched("page write");
+}
+
+int cg_pages_fork_async(const cg_paged_cache* c, int32_t n, const int32_t* parents_dev,
+                        const int32_t* children_dev, void* workspace_dev, size_t workspace_bytes,
+                        void* stream) {
+  if (int rc = check_paged_cache(c)) return rc;
+  if (n < 0 || n > c->n_rows) return fail(CG_E_INVAL, "n must be in 0..n_rows");
+  if (n == 0) return CG_OK;
+  if (!parents_dev || !children_dev) return fail(CG_E_INVAL, "NULL list");
+  if (int rc = check_workspace(c, workspace_dev, workspace_bytes)) return rc;
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
+  const PagesWs w = pages_ws(*c);
+  int32_t* ws = (int32_t*)workspace_dev;
+  hipStream_t st = (hipStream_t)stream;
+  k_fork_plan<<<1, kThreads, 0, st>>>(view(*c), n, parents_dev, children_dev, ws + w.ok,
+                                      ws + w.cum, ws + w.aux, ws + w.list);
+  if (int rc = launched("fork")) return rc;
+  // the copy's rows are known on the device only: pieces for a full page, the
+  // surplus workgroups return at once
+  const int64_t row = (int64_t)c->channels * 2;
+  const int unit = unit_of((uint64_t)row | pool_bits(*c));
+  const int64_t pieces = pieces_of(c->layers, (c->page_tokens - 1) * row / unit);
+  const dim3 grid(n, (unsigned)(1 + std::min<int64_t>(pieces, std::max<int64_t>(1, 32768 / n))));
+  BY_UNIT(unit, (k_fork_copy<U><<<grid, kCopyThreads, 0, st>>>(view(*c), parents_dev, children_dev,
+                                                               ws + w.ok, ws + w.aux)));
+  return launched("fork");
+}
+
+int cg_pages_free_async(const cg_paged_cache* c, int32_t n, const int32_t* rows_dev,
+                        void* stream) {
+  if (int rc = check_paged_cache(c)) return rc;
+  if (n < 0 || n > c->n_rows) return fail(CG_E_INVAL, "n must be in 0..n_rows");
+  if (n == 0) return CG_OK;
+  if (!rows_dev) return fail(CG_E_INVAL, "NULL list");
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
+  k_free<<<n, kCopyThreads, 0, (hipStream_t)stream>>>(view(*c), n, rows_dev);
+  return launched("free");
+}
+
+int cg_pages_compact_async(const cg_paged_cache* c, int32_t* n_live_dev, void* workspace_dev,
+                           size_t workspace_bytes, void* stream) {
+  if (int rc = check_paged_cache(c)) return rc;
+  if (int rc = check_workspace(c, workspace_dev, workspace_bytes)) return rc;
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
+  const PagesWs w = pages_ws(*c);
+  int32_t* ws = (int32_t*)workspace_dev;
+  hipStream_t st = (hipStream_t)stream;
+  k_compact_plan<<<1, kThreads, 0, st>>>(view(*c), n_live_dev, ws, ws + w.list, ws + w.list2);
+  if (int rc = launched("compact")) return rc;
+  const int64_t page = (int64_t)c->page_tokens * c->channels * 2;
+  const int unit = unit_of((uint64_t)page | pool_bits(*c));
+  const int64_t pieces = pieces_of(c->layers, page / unit);
+  const int grid = (int)std::min<int64_t>(2048, std::max<int64_t>(c->n_rows, c->num_pages / 2 * pieces));
+  BY_UNIT(unit, (k_compact_move<U><<<grid, kCopyThreads, 0, st>>>(view(*c), ws, ws + w.list,
+                                                                  ws + w.list2, pieces)));
+  return launched("compact");
+}
+
+}  // extern "C"

@@ -1,0 +1,423 @@
+"""The attention over a paged cache against the oracle's binary64 one.
+
+Bound of one output, in exact arithmetic of the stated roundings (u = 2^-11 is
+binary16's half step, e = 2^-24 binary32's): the weights are rounded to binary16
+(relative u, and absolutely 2^-25 of the largest weight below binary16's normal
+range), scores are binary32 sums of d products of size at most S = max scale
+sum |q k|, so that a weight is off by a factor exp(+-D), D = e (d + 16) (S + 1)
+with the exponential's own error, binary32 sums over n tokens add e (n + 64), and
+the result is rounded once: u |out| + 2^-25.  With A = sum p |v|:
+    |out - o| <= u |o| + (u + 4 D + 2 e (n + 64)) A + n 2^-25 max|v| / l + 2^-25
+    |lse - x| <= 2 D + e (n + 64) + 4 e |x|
+(l = sum exp(s - max) >= 1)."""
+import numpy as np
+import pytest
+
+from oracle import paged_cache as pc
+from tests import gpu_util as gu
+from tests.test_gpu_pages import Pair
+
+pytestmark = pytest.mark.gpu
+
+U, E = 2.0 ** -11, 2.0 ** -24
+
+
+def build(rng, L, C, P, prefixes, tails, spare=3, spread=1.0):
+    """A cache in which group g's sequences continue a prefix of prefixes[g] tokens
+    by tails[g][i] tokens, made with the page operators of the oracle."""
+    seqs = [(g, n) for g, t in enumerate(tails) for n in t]
+    R = len(seqs)
+    longest = max(prefixes[g] + n for g, n in seqs)
+    pages = sum(-(-(prefixes[g] + n) // P) + 1 for g, n in seqs) + spare
+    c = pc.empty(L, pages, P, C, R + 2, -(-longest // P) + 2)
+    order = rng.permutation(R + 2)[:R]
+    first, rows = {}, []
+
+    def add(row, n):
+        st, slots = pc.reserve(c, [row], [0, n], n)
+        assert st == 0
+        k, v = ((spread * rng.standard_normal((L, n, C))).astype(np.float16) for _ in range(2))
+        pc.write(c, 0, slots, k, v)
+
+    for (g, _), row in zip(seqs, order):
+        if g not in first:
+            first[g] = row
+            add(row, prefixes[g])
+        else:
+            assert pc.fork(c, [first[g]], [row]) == 0
+        rows.append(row)
+    for (g, n), row in zip(seqs, rows):
+        if n:
+            add(row, n)
+    return c, rows
+
+
+def gpu_attention(x, layer, q, scale, rows, q_starts, group_starts, prefix_lens, hints=None, lse=True,
+                  out=None, stream=None):
+    cg, t = x.cg, x.t
+    n_q, H, d = q.shape
+    lens = x.o.lens
+    hints = hints or (max(1, int(np.max(np.diff(q_starts), initial=0))),
+                      int(np.max(prefix_lens, initial=0)) if prefix_lens is not None else 0,
+                      int(np.max(lens)))
+    hints = tuple(max(0, h) for h in hints)
+    groups = 0 if group_starts is None else len(group_starts) - 1
+    ws = t.full((cg.cg_attention_workspace(x.cache, n_q, H, d, len(q_starts) - 1, groups, *hints),), 0xFF,
+                dtype=t.uint8, device="cuda")
+    qd = gu.to_dev(q)
+    if out is None:
+        out = t.full((n_q, H, d), 123.0, dtype=t.float16, device="cuda")
+    ld = t.full((n_q, H), 321.0, dtype=t.float32, device="cuda") if lse else None
+    opt = lambda v: None if v is None else x.i32(v)  # noqa: E731
+    cg.cg_attention_prefix_async(x.cache, layer, qd, out, scale, opt(rows), x.i32(q_starts),
+                                 opt(group_starts), opt(prefix_lens), *hints, ws, lse=ld, stream=stream)
+    t.cuda.synchronize()
+    st = int(x.status.item())
+    x.status.zero_()
+    return st, out.cpu().numpy(), None if ld is None else ld.cpu().numpy()
+
+
+def compare(got, want, q):
+    (st, out, lse), (ost, recs) = got, want
+    assert st == ost, (st, ost)
+    n_q, H, d = q.shape
+    for j in range(n_q):
+        if j not in recs:  # no sequence's query
+            assert (out[j] == 123.0).all() and (lse is None or (lse[j] == 321.0).all()), j
+            continue
+        for h, r in enumerate(recs[j]):
+            if r["lse"] == -np.inf:
+                assert (out[j, h] == 0).all(), (j, h)
+                assert lse is None or lse[j, h] == -np.inf
+                continue
+            n = r["tokens"]
+            D = E * (d + 16) * (r["size"] + 1)
+            tol = (U * np.abs(r["out"]) + (U + 4 * D + 2 * E * (n + 64)) * r["mean_abs"]
+                   + n * 2.0 ** -25 * r["vmax"] / r["l"] + 2.0 ** -25)
+            off = np.abs(out[j, h].astype(np.float64) - r["out"])
+            assert (off <= tol).all(), (j, h, n, float((off / tol).max()))
+            if lse is not None:
+                assert abs(lse[j, h] - r["lse"]) <= 2 * D + E * (n + 64) + 4 * E * abs(r["lse"]), (j, h)
+
+
+def check(x, layer, q, scale, rows, q_starts, group_starts=None, prefix_lens=None, **kw):
+    got = gpu_attention(x, layer, q, scale, rows, q_starts, group_starts, prefix_lens, **kw)
+    want = pc.attention(x.o, layer, q, scale, rows, q_starts, group_starts, prefix_lens)
+    compare(got, want, q)
+    return got
+
+
+def queries(rng, n, H, d):
+    return rng.standard_normal((n, H, d)).astype(np.float16)
+
+
+def starts_of(counts):
+    return np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+
+
+def group_starts_of(tails):
+    return starts_of([len(t) for t in tails])
+
+
+# heads: kv heads, query heads per kv head, head dimension
+@pytest.mark.parametrize("kv,G,d", [(2, 1, 64), (1, 4, 128), (3, 7, 80), (2, 8, 128), (1, 2, 256), (1, 1, 8),
+                                    (2, 5, 40), (1, 3, 192), (4, 17, 64), (1, 70, 128)])
+@pytest.mark.parametrize("P", [1, 16, 128])
+def test_heads_and_pages(kv, G, d, P):
+    rng = np.random.default_rng(kv * 10007 + G * 101 + d + P)
+    tails = [[1, 5, 40], [2, 33]]
+    c, rows = build(rng, 2, kv * d, P, [50, 37], tails)
+    x = Pair(c)
+    q = queries(rng, 5, kv * G, d)
+    check(x, 1, q, d ** -0.5, rows, np.arange(6), group_starts_of(tails), [50, 37])
+    check(x, 0, q, d ** -0.5, rows, np.arange(6))
+
+
+@pytest.mark.parametrize("prefix", [1, 15, 16, 63, 64, 65, 127, 128, 200, 257, 1000])
+@pytest.mark.parametrize("tail", [[1], [1, 2, 3], [16, 17, 64, 65, 300]])
+def test_lengths(prefix, tail):
+    rng = np.random.default_rng(prefix * 31 + len(tail))
+    c, rows = build(rng, 1, 128, 16, [prefix], [tail])
+    x = Pair(c)
+    q = queries(rng, len(tail), 4, 64)
+    check(x, 0, q, 0.125, rows, np.arange(len(tail) + 1), [0, len(tail)], [prefix])
+    # the same by themselves, and with part of the prefix shared
+    check(x, 0, q, 0.125, rows, np.arange(len(tail) + 1))
+    check(x, 0, q, 0.125, rows, np.arange(len(tail) + 1), [0, len(tail)], [prefix - prefix // 3])
+
+
+@pytest.mark.parametrize("counts", [[1, 1, 1], [4, 0, 2], [0, 0, 1], [9, 30, 17], [64, 65, 1], [130, 3, 0]])
+@pytest.mark.parametrize("G", [1, 4])
+def test_several_queries(counts, G):
+    """Drafts and prompts: a sequence's queries see one token more each."""
+    rng = np.random.default_rng(sum(counts) * 10 + G)
+    tails = [[max(1, counts[0]) + 3, max(1, counts[1])], [max(1, counts[2]) + 70]]
+    c, rows = build(rng, 1, 256, 8, [45, 20], tails)
+    x = Pair(c)
+    q = queries(rng, sum(counts) + 3, 2 * G, 128)  # three rows behind the last sequence
+    check(x, 0, q, 0.09, rows, starts_of(counts), group_starts_of(tails), [45, 20])
+    check(x, 0, q, 0.09, rows, starts_of(counts))
+
+
+def test_wrong_hints_change_nothing():
+    rng = np.random.default_rng(3)
+    tails = [[5, 300, 40], [1, 2]]
+    c, rows = build(rng, 1, 128, 16, [700, 90], tails)
+    x = Pair(c)
+    counts = [5, 70, 1, 1, 2]
+    q = queries(rng, sum(counts), 4, 64)
+    for hints in ((0, 0, 0), (1, 1, 1), (1, 100000, 200000), (5000, 700, 1000), (70, 10, 1 << 30),
+                  (1 << 20, 1 << 30, 1 << 30)):
+        check(x, 0, q, 0.125, rows, starts_of(counts), group_starts_of(tails), [700, 90], hints=hints)
+
+
+def test_many_sequences():
+    """Groups of one, an uneven batch, more groups than a wavefront has lanes."""
+    rng = np.random.default_rng(4)
+    tails = [[int(rng.integers(1, 40)) for _ in range(rng.integers(1, 4))] for _ in range(80)]
+    prefixes = [int(rng.integers(1, 50)) for _ in tails]
+    c, rows = build(rng, 1, 64, 8, prefixes, tails)
+    x = Pair(c)
+    n = len(rows)
+    q = queries(rng, n, 2, 64)
+    check(x, 0, q, 0.125, rows, np.arange(n + 1), group_starts_of(tails), prefixes)
+    # some sequences in no group
+    gs = group_starts_of(tails)
+    check(x, 0, q, 0.125, rows, np.arange(n + 1), gs[10:41], prefixes[10:40])
+
+
+def test_group_of_many():
+    """More rows than one tile of the shared part: 70 sequences of 4 heads, ragged queries."""
+    rng = np.random.default_rng(14)
+    tails = [[int(n) for n in rng.integers(3, 30, 70)]]
+    c, rows = build(rng, 1, 128, 16, [333], tails)
+    x = Pair(c)
+    counts = rng.integers(0, 4, 70)
+    q = queries(rng, int(counts.sum()), 8, 64)
+    check(x, 0, q, 0.125, rows, starts_of(counts), [0, 70], [333])
+
+
+def test_rows_default_and_empty_rows():
+    rng = np.random.default_rng(5)
+    x = Pair(pc.empty(1, 30, 16, 64, 4, 6))
+    x.new(rng, [0, 2], [20, 3])
+    q = queries(rng, 8, 1, 64)
+    # rows 1 and 3 are empty: their queries see nothing; row 2 has more queries than tokens
+    check(x, 0, q, 0.125, None, [0, 1, 2, 7, 8])
+    check(x, 0, q, 0.125, [1], [0, 8])
+
+
+def test_refused_sequences():
+    rng = np.random.default_rng(6)
+    tails = [[4, 1, 9], [3]]
+    c, rows = build(rng, 1, 64, 8, [30, 12], tails)
+    x = Pair(c)
+    q = queries(rng, 9, 2, 64)
+    qs, gs = [0, 2, 4, 7, 9], [0, 3, 4]
+    # the second sequence's two queries start before token 30 + 1
+    st, out, _ = check(x, 0, q, 0.125, rows, qs, gs, [30, 12])
+    assert st == pc.REFUSED and (out[2:4] == 0).all()
+    check(x, 0, q, 0.125, rows, qs, gs, [29, 12])
+    check(x, 0, q, 0.125, rows, qs, gs, [33, 16])     # longer than the rows
+    check(x, 0, q, 0.125, rows, qs, gs, [-1, 1 << 30])
+    check(x, 0, q, 0.125, [rows[0], -1, 1 << 20, rows[3]], qs, gs, [29, 12])
+    check(x, 0, q, 0.125, rows, qs, [0, 0, 4], [29, 12])  # an empty group
+
+
+def test_malformed_lists_stay_in_bounds():
+    """Starts that descend or leave the batch: no value is promised, but nothing
+    outside the outputs is touched and the call comes back."""
+    rng = np.random.default_rng(7)
+    c, rows = build(rng, 1, 64, 8, [30], [[4, 6, 9]])
+    x = Pair(c)
+    q = queries(rng, 6, 2, 64)
+    t = x.t
+    for qs in ([0, 4, 2, 6], [-5, 1, 2, 3], [0, 1, 2, 60], [3, 3, 3, 3], [9, 9, 9, 9], [5, 4, 3, 2]):
+        for gs, pl in (([0, 3], [25]), ([-4, 3], [25]), ([2, 1], [25]), ([0, 50], [25]), ([1, 9], [1 << 30])):
+            big = t.full((8, 2, 64), 55.0, dtype=t.float16, device="cuda")
+            gpu_attention(x, 0, q, 0.125, rows, qs, gs, pl, hints=(2, 30, 40), out=big[1:7])
+            assert (big[0] == 55.0).all() and (big[7] == 55.0).all()
+
+
+def test_pages_outside_the_pool():
+    rng = np.random.default_rng(8)
+    tails = [[4, 40, 9]]
+    c, rows = build(rng, 1, 64, 8, [30], tails)
+    c.tables[rows[0], 1], c.tables[rows[1], 5], c.tables[rows[2], 4] = -1, c.N, 1 << 30
+    x = Pair(c)
+    q = queries(rng, 3, 2, 64)
+    st, _, _ = check(x, 0, q, 0.125, rows, np.arange(4), [0, 3], [24])
+    assert st == pc.BAD_PAGE
+    # a row with no page at all
+    c.tables[rows[1], :] = -1
+    check(Pair(c), 0, q, 0.125, rows, np.arange(4))
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_masked_places_have_no_influence(bad):
+    """NaN and infinities behind the rows' ends, in free pages, and in tokens that
+    later queries of the same sequence see but earlier ones do not."""
+    rng = np.random.default_rng(9)
+    tails = [[7, 20, 33]]
+    counts = [5, 3, 2]
+    c, rows = build(rng, 1, 128, 16, [50], tails)
+    want = c.copy()
+    used = np.zeros((c.N, c.P), bool)
+    for r in rows:
+        tt = np.arange(c.lens[r])
+        used[c.tables[r, tt // c.P], tt % c.P] = True
+    for x in (c.k, c.v):
+        x[0][~used] = bad
+    q = queries(rng, 10, 2, 128)
+    check(Pair(c), 0, q, 0.09, rows, starts_of(counts), [0, 3], [50])
+    # the last token of each sequence: only its last query sees it
+    for r in rows:
+        n = int(c.lens[r]) - 1
+        c.v[0, c.tables[r, n // c.P], n % c.P, ::3] = bad
+        c.k[0, c.tables[r, n // c.P], n % c.P, 5] = bad
+    for groups in (([0, 3], [50]), (None, None)):
+        st, out, lse = gpu_attention(Pair(c), 0, q, 0.09, rows, starts_of(counts), *groups)
+        _, recs = pc.attention(want, 0, q, 0.09, rows, starts_of(counts), *groups)
+        early = [j for s in range(3) for j in range(sum(counts[:s]), sum(counts[:s + 1]) - 1)]
+        for j in range(10):
+            if j not in early:
+                recs.pop(j)
+                out[j], lse[j] = 123.0, 321.0
+        compare((st, out, lse), (0, recs), q)
+
+
+def test_infinite_scores():
+    """Scores of -infinity weigh nothing; a row of nothing else gives zeros; NaN in a
+    visible token is an output of NaN."""
+    rng = np.random.default_rng(10)
+    c, rows = build(rng, 1, 64, 16, [40], [[3, 5, 6]])
+    q = np.abs(queries(rng, 3, 1, 64))
+    for t in range(0, 40, 2):  # every other token of the prefix
+        c.k[0, c.tables[rows[0], t // 16], t % 16, :] = -np.inf
+    x = Pair(c)
+    st, out, lse = gpu_attention(x, 0, q, 0.125, rows, np.arange(4), [0, 3], [40])
+    _, recs = pc.attention(c, 0, q, 0.125, rows, np.arange(4), [0, 3], [40])
+    for j in range(3):
+        for r in recs[j]:
+            r["size"] = 30.0  # the finite scores' size
+    compare((st, out, lse), (0, recs), q)
+    c.k[:] = -np.inf
+    st, out, lse = gpu_attention(Pair(c), 0, q, 0.125, rows, np.arange(4), [0, 3], [40])
+    assert (out == 0).all() and (lse == -np.inf).all()
+    c, rows = build(rng, 1, 64, 16, [40], [[3, 5, 6]])
+    c.k[0, c.tables[rows[1], 44 // 16], 44 % 16, 3] = np.nan  # the second sequence's last token
+    st, out, lse = gpu_attention(Pair(c), 0, q, 0.125, rows, np.arange(4), [0, 3], [40])
+    assert np.isnan(out[1]).all() and np.isnan(lse[1]).all()
+    assert np.isfinite(out[[0, 2]]).all()
+
+
+def test_large_scores_and_spread():
+    """Peaked weights (one token takes all) and scores whose exponentials overflow
+    without the maximum."""
+    rng = np.random.default_rng(11)
+    c, rows = build(rng, 1, 128, 16, [300], [[9, 40]], spread=3.0)
+    x = Pair(c)
+    q = 8 * queries(rng, 2, 4, 64)
+    for scale in (0.125, 4.0, -1.0, 0.0, 1e-6):
+        check(x, 0, q, scale, rows, np.arange(3), [0, 2], [300])
+
+
+def test_strides_and_no_lse():
+    """q as a slice of a wider projection, out inside a wider buffer."""
+    rng = np.random.default_rng(12)
+    c, rows = build(rng, 1, 128, 16, [70], [[5, 12, 1]])
+    x = Pair(c)
+    t, H, d = x.t, 4, 64
+    wide = gu.to_dev(rng.standard_normal((3, 2 * H * d + 24)).astype(np.float16))
+    qd = wide[:, 8:8 + H * d].view(3, H, d)
+    buf = t.full((3, 2 * H * d), 9.0, dtype=t.float16, device="cuda")
+    out = buf[:, H * d:].view(3, H, d)
+    ws = t.empty(x.cg.cg_attention_workspace(x.cache, 3, H, d, 3, 1, 1, 70, 82), dtype=t.uint8, device="cuda")
+    x.cg.cg_attention_prefix_async(x.cache, 0, qd, out, 0.125, x.i32(rows), x.i32([0, 1, 2, 3]), x.i32([0, 3]),
+                                   x.i32([70]), 1, 70, 82, ws)
+    t.cuda.synchronize()
+    q = qd.cpu().numpy()
+    want = pc.attention(c, 0, q, 0.125, rows, [0, 1, 2, 3], [0, 3], [70])
+    compare((0, out.cpu().numpy(), None), want, q)
+    assert (buf[:, :H * d] == 9.0).all()
+    with pytest.raises(ValueError):
+        x.cg.cg_attention_prefix_async(x.cache, 0, qd.float(), out, 0.125, None, x.i32([0, 1]), None, None, 1, 0,
+                                       82, ws)
+    with pytest.raises(x.cg.CgError):
+        x.cg.cg_attention_prefix_async(x.cache, 0, qd, out, 0.125, x.i32(rows), x.i32([0, 1, 2, 3]), x.i32([0, 3]),
+                                       x.i32([70]), 1, 70, 82, ws[:16 * ((ws.numel() - 1) // 16)])
+
+
+def test_streams_and_repeats():
+    """The same bits each time, on the default and another stream."""
+    rng = np.random.default_rng(13)
+    tails = [[30, 1, 500], [2, 64]]
+    c, rows = build(rng, 1, 256, 16, [900, 65], tails)
+    x = Pair(c)
+    q = queries(rng, 5, 8, 64)
+    args = (0, q, 0.125, rows, np.arange(6), group_starts_of(tails), [900, 65])
+    st, out, lse = check(x, *args)
+    side = x.t.cuda.Stream()
+    x.t.cuda.synchronize()
+    for s in (None, side, None, side):
+        st, o, l = gpu_attention(x, *args, stream=s)
+        assert st == 0 and gu.same_bits(o, out) and np.array_equal(l, lse)
+
+
+def test_captured_decode_loop():
+    """Reserve, write and attend in one graph: every replay is a decoding step,
+    compared with the oracle, with eager work between the replays."""
+    rng = np.random.default_rng(15)
+    tails = [[3, 14, 30]]
+    c, rows = build(rng, 2, 128, 16, [100], tails, spare=10)
+    x = Pair(c)
+    t, cg = x.t, x.cg
+    H, d = 4, 64
+    r, qs, gs, pl = x.i32(rows), x.i32([0, 1, 2, 3]), x.i32([0, 3]), x.i32([100])
+    slots = t.empty(3, dtype=t.int64, device="cuda")
+    kd, vd = (t.zeros((2, 3, 128), dtype=t.float16, device="cuda") for _ in range(2))
+    qd, out = (t.zeros((3, H, d), dtype=t.float16, device="cuda") for _ in range(2))
+    lse = t.zeros((3, H), dtype=t.float32, device="cuda")
+    ws = t.empty(cg.cg_attention_workspace(x.cache, 3, H, d, 3, 1, 1, 100, 160), dtype=t.uint8, device="cuda")
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        cg.cg_pages_reserve_async(x.cache, r, qs, slots, x.ws)
+        cg.cg_pages_write_async(x.cache, 0, slots, kd, vd)
+        cg.cg_attention_prefix_async(x.cache, 1, qd, out, 0.125, r, qs, gs, pl, 1, 100, 160, ws, lse=lse)
+    for step in range(8):
+        k, v = (rng.standard_normal((2, 3, 128)).astype(np.float16) for _ in range(2))
+        q = queries(rng, 3, H, d)
+        for dst, src in ((kd, k), (vd, v), (qd, q)):
+            dst.copy_(gu.to_dev(src))
+        graph.replay()
+        t.cuda.synchronize()
+        st, want = pc.reserve(c, rows, [0, 1, 2, 3], 3)
+        pc.write(c, 0, want, k, v)
+        got = (int(x.status.item()), out.cpu().numpy(), lse.cpu().numpy())
+        compare(got, pc.attention(c, 1, q, 0.125, rows, [0, 1, 2, 3], [0, 3], [100]), q)
+        if step % 3 == 1:  # eager, in between
+            check(x, 0, q, 0.125, rows, [0, 1, 2, 3], [0, 3], [100])
+
+
+def test_pool_past_four_gib():
+    import kv_cache_compression_anchor_amd as cg
+    t = gu.torch()
+    N, P, C = 70000, 32, 1024
+    k, v = (t.empty((1, N, P, C), dtype=t.float16, device="cuda") for _ in range(2))
+    k[0, N - 6:], v[0, N - 6:] = t.randn((6, P, C), device="cuda").half(), t.randn((6, P, C), device="cuda").half()
+    tables = t.full((2, 6), -1, dtype=t.int32, device="cuda")
+    tables[0], tables[1] = t.arange(N - 6, N), t.arange(N - 6, N)
+    lens = t.tensor([180, 170], dtype=t.int32, device="cuda")
+    refs, status = t.ones(N, dtype=t.int32, device="cuda"), t.zeros(1, dtype=t.int32, device="cuda")
+    cache = cg.PagedCache(k, v, tables, lens, refs, status)
+    host = pc.Cache(k[:, N - 6:].cpu().numpy(), v[:, N - 6:].cpu().numpy(),
+                    np.tile(np.arange(6, dtype=np.int32), (2, 1)), lens.cpu().numpy(), np.ones(6, np.int32))
+    q = queries(np.random.default_rng(16), 2, 8, 128)
+    ws = t.empty(cg.cg_attention_workspace(cache, 2, 8, 128, 2, 1, 1, 100, 180), dtype=t.uint8, device="cuda")
+    out, lse = gu.to_dev(np.zeros_like(q)), t.zeros((2, 8), dtype=t.float32, device="cuda")
+    i32 = lambda x: t.tensor(x, dtype=t.int32, device="cuda")  # noqa: E731
+    cg.cg_attention_prefix_async(cache, 0, gu.to_dev(q), out, 0.088, None, i32([0, 1, 2]), i32([0, 2]), i32([100]),
+                                 1, 100, 180, ws, lse=lse)
+    t.cuda.synchronize()
+    want = pc.attention(host, 0, q, 0.088, None, [0, 1, 2], [0, 2], [100])
+    compare((int(status.item()), out.cpu().numpy(), lse.cpu().numpy()), want, q)

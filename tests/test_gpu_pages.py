@@ -1,0 +1,322 @@
+"""GPU parity of the page operators with the oracle: the whole state (tables,
+lengths, counts, slots, every pool byte) equal after each call, for page and
+channel sizes that take each copy width, repeated and bad requests, empty and
+full caches, exhausted pools, strided new tokens, another stream and a captured
+graph."""
+import numpy as np
+import pytest
+
+from oracle import paged_cache as pc
+from tests import gpu_util as gu
+
+pytestmark = pytest.mark.gpu
+
+
+class Pair:
+    """The same cache on the device and in the oracle."""
+
+    def __init__(self, host):
+        import kv_cache_compression_anchor_amd as cg
+        t = gu.torch()
+        self.cg, self.t, self.o = cg, t, host
+        self.k, self.v = gu.to_dev(host.k), gu.to_dev(host.v)
+        self.tables, self.lens, self.refs = (gu.to_dev(x) for x in (host.tables, host.lens, host.refs))
+        self.status = t.zeros(1, dtype=t.int32, device="cuda")
+        self.cache = cg.PagedCache(self.k, self.v, self.tables, self.lens, self.refs, self.status)
+        self.ws = t.full((cg.cg_pages_workspace(self.cache),), 0xA5, dtype=t.uint8, device="cuda")
+
+    def i32(self, x):
+        return gu.to_dev(np.asarray(x, np.int32))
+
+    def check(self, status, what):
+        self.t.cuda.synchronize()
+        assert int(self.status.item()) == status, (what, int(self.status.item()), status)
+        self.status.zero_()
+        for name in ("tables", "lens", "refs"):
+            assert np.array_equal(getattr(self, name).cpu().numpy(), getattr(self.o, name)), (what, name)
+        assert gu.same_bits(self.k.cpu().numpy(), self.o.k), (what, "k")
+        assert gu.same_bits(self.v.cpu().numpy(), self.o.v), (what, "v")
+
+    def reserve(self, rows, starts, n_tokens, what="reserve"):
+        slots = self.t.full((n_tokens,), 77, dtype=self.t.int64, device="cuda")
+        self.cg.cg_pages_reserve_async(self.cache, self.i32(rows), self.i32(starts), slots, self.ws)
+        st, want = pc.reserve(self.o, rows, starts, n_tokens)
+        self.check(st, what)
+        assert np.array_equal(slots.cpu().numpy(), want), what
+        return slots, want
+
+    def write(self, layer0, slots, want, k, v, what="write"):
+        self.cg.cg_pages_write_async(self.cache, layer0, slots, gu.to_dev(k), gu.to_dev(v))
+        self.check(pc.write(self.o, layer0, want, k, v), what)
+
+    def new(self, rng, rows, counts):
+        starts = np.concatenate([[0], np.cumsum(counts)])
+        slots, want = self.reserve(rows, starts, int(starts[-1]))
+        L, n, C = self.o.k.shape[0], int(starts[-1]), self.o.k.shape[3]
+        k, v = (rng.standard_normal((L, n, C)).astype(np.float16) for _ in range(2))
+        self.write(0, slots, want, k, v)
+
+    def fork(self, parents, children, what="fork"):
+        self.cg.cg_pages_fork_async(self.cache, self.i32(parents), self.i32(children), self.ws)
+        self.check(pc.fork(self.o, parents, children), what)
+
+    def free(self, rows, what="free"):
+        self.cg.cg_pages_free_async(self.cache, self.i32(rows))
+        self.check(pc.free(self.o, rows), what)
+
+    def copy(self, src, dst, what="copy"):
+        self.cg.cg_pages_copy_async(self.cache, self.i32(src), self.i32(dst))
+        self.check(pc.copy(self.o, src, dst), what)
+
+    def compact(self, what="compact"):
+        live = self.t.full((1,), -5, dtype=self.t.int32, device="cuda")
+        self.cg.cg_pages_compact_async(self.cache, self.ws, live)
+        st, want = pc.compact(self.o)
+        self.check(st, what)
+        assert int(live.item()) == want
+
+
+def randomised(c, rng):
+    """Pool contents that no two pages share."""
+    for x in (c.k, c.v):
+        x[:] = rng.integers(0, 1 << 16, x.shape, dtype=np.uint16).view(np.float16)
+    return c
+
+
+# channels 128 and 1000: 16-byte units; 138: 4-byte rows; 65: 2-byte rows
+@pytest.mark.parametrize("P,C", [(1, 128), (1, 65), (4, 138), (16, 128), (16, 65), (64, 1000)])
+def test_random_sequences(P, C):
+    rng = np.random.default_rng(P * 1000 + C)
+    R, L = 11, 3
+    c = randomised(pc.empty(L, 500 // P + 14, P, C, R, 250 // P + 2), rng)
+    x = Pair(c)
+    for step in range(60):
+        kind = rng.integers(5)
+        if kind == 0 or step < 3:
+            rows = rng.permutation(R)[:rng.integers(1, 6)]
+            x.new(rng, rows, rng.integers(0, 24, len(rows)))
+        elif kind == 1:
+            n = rng.integers(1, 5)
+            x.fork(rng.integers(0, R, n), rng.permutation(R)[:n])
+        elif kind == 2:
+            x.free(rng.permutation(R)[:rng.integers(1, 4)])
+        elif kind == 3:
+            x.compact()
+        else:  # contents only, free pages or not
+            n = rng.integers(1, c.N // 2)
+            pages = rng.permutation(c.N)
+            x.copy(pages[:n], pages[n:2 * n])
+
+
+def test_repeated_and_bad_requests():
+    rng = np.random.default_rng(5)
+    x = Pair(randomised(pc.empty(2, 40, 4, 64, 8, 6), rng))
+    x.new(rng, [0, 1, 2], [5, 8, 24])
+    x.reserve([3, 3, 0], [0, 2, 4, 7], 7, "a row twice")
+    x.reserve([-1, 8, 1 << 30, 4], [0, 1, 2, 3, 4], 4, "rows out of range")
+    x.reserve([2, 3], [0, 1, 2], 2, "a full row")
+    x.reserve([3, 4], [0, 3, 2], 3, "starts that descend")
+    x.reserve([3, 4], [0, 3, 9], 8, "starts past the tokens")
+    x.reserve([5, 6], [2, 4, 4], 6, "tokens of no request")
+    x.fork([0, 1, 0], [3, 3, 6], "a child twice, and one that holds tokens")
+    x.fork([0, 3], [7, 0], "a child that is a parent")
+    x.fork([-1, 0, 9], [7, 8, 7], "rows out of range")
+    x.free([1, 1, -3, 8, 7], "twice, out of range, empty")
+    x.copy([0, 1, 2, 3], [30, 30, 31, 2], "a dst twice, a src that is a dst")
+    x.copy([0, -1, 40, 5], [32, 33, 34, 40], "pages out of range")
+    x.copy([5], [5], "a page onto itself")
+    x.compact()
+
+
+def test_exhausted_pool():
+    rng = np.random.default_rng(6)
+    x = Pair(randomised(pc.empty(1, 10, 4, 64, 9, 6), rng))
+    x.new(rng, [0, 1, 2, 3], [10, 9, 17, 0])   # 3 + 3 pages; 5 do not fit; none needed
+    x.fork([0, 1, 0, 1, 0], [4, 5, 6, 7, 8])   # four partly filled pages, then none
+    x.reserve([0, 1], [0, 1, 2], 2, "room in the last pages")
+    x.free([0])
+    x.free([4, 5])
+    x.compact()
+    x.new(rng, [0], [9])
+
+
+def test_garbage_state_is_bounded():
+    """Entries, lengths and counts that no call leaves behind: flagged, in bounds."""
+    rng = np.random.default_rng(7)
+    x = Pair(randomised(pc.empty(1, 30, 4, 64, 6, 5), rng))
+    x.new(rng, [0, 1, 2, 3], [10, 9, 17, 6])
+    x.o.tables[0, 1], x.o.tables[1, 2], x.o.tables[2, 0] = 30, -7, 1 << 30
+    x.o.lens[3], x.o.lens[4] = 21, -1
+    x.tables.copy_(gu.to_dev(x.o.tables))
+    x.lens.copy_(gu.to_dev(x.o.lens))
+    x.reserve([1, 3, 4], [0, 2, 3, 4], 4, "reserve")
+    x.fork([0, 1, 3, 4], [5, 5, 5, 5], "children repeated")
+    x.fork([1], [5], "a last page outside the pool")
+    x.fork([2], [5], "a full page outside the pool")
+    x.compact()
+    x.free([0, 1, 2, 3, 4, 5], "free")
+    x.o.refs[5], x.o.refs[29] = -3, 4
+    x.refs.copy_(gu.to_dev(x.o.refs))
+    # a negative count is neither free nor in use: fewer free pages than moves
+    x.o.refs[:5] = -1
+    x.refs.copy_(gu.to_dev(x.o.refs))
+    x.t.cuda.synchronize()
+    live = x.t.zeros(1, dtype=x.t.int32, device="cuda")
+    x.cg.cg_pages_compact_async(x.cache, x.ws, live)
+    x.t.cuda.synchronize()
+    assert int(x.status.item()) == pc.REFUSED and int(live.item()) == (x.o.refs > 0).sum()
+
+
+def test_nothing_to_do():
+    x = Pair(pc.empty(1, 4, 4, 64, 3, 4))
+    for call in (lambda: x.reserve([], [0], 0), lambda: x.fork([], []), lambda: x.free([]),
+                 lambda: x.copy([], []), x.compact):
+        call()
+    # tokens but no request: every slot is -1
+    x.reserve([], [0], 5)
+    # no slots wanted
+    x.cg.cg_pages_reserve_async(x.cache, x.i32([1]), x.i32([0, 6]), None, x.ws, n_tokens=6)
+    x.check(pc.reserve(x.o, [1], [0, 6], 6)[0], "no slots")
+
+
+def test_many_rows_and_pages():
+    """More requests than a workgroup has threads, more pages than one scan step."""
+    rng = np.random.default_rng(8)
+    R = 2500
+    x = Pair(randomised(pc.empty(1, 40000, 2, 8, 2 * R, 40), rng))
+    x.new(rng, rng.permutation(R), rng.integers(0, 21, R))
+    x.fork(rng.integers(0, R, R), R + rng.permutation(R))
+    x.free(rng.permutation(2 * R)[:R + 77])
+    x.compact()
+    x.copy(*np.split(rng.permutation(40000)[:6000], 2))
+    # the highest pages in use: moves from past the first scan steps
+    x.o.refs[39990:] = 1
+    x.refs.copy_(gu.to_dev(x.o.refs))
+    x.compact()
+
+
+def test_write_layers_and_strides():
+    """Layer ranges, K and V as slices of a wider projection, slots outside the pool."""
+    rng = np.random.default_rng(9)
+    t = gu.torch()
+    for C in (64, 65):
+        x = Pair(randomised(pc.empty(4, 20, 8, C, 2, 10), rng))
+        slots, want = x.reserve([1, 0], [0, 33, 40], 40)
+        both = rng.standard_normal((2, 40, 3 * C + 5)).astype(np.float16)
+        dev = gu.to_dev(both)
+        k, v = both[:, :, C:2 * C], both[:, :, 2 * C:3 * C]
+        x.cg.cg_pages_write_async(x.cache, 1, slots, dev[:, :, C:2 * C], dev[:, :, 2 * C:3 * C])
+        x.check(pc.write(x.o, 1, want, k, v), "slices")
+        one = rng.standard_normal((1, 40, C)).astype(np.float16)
+        x.write(3, slots, want, one, -one)
+        bad = want.copy()
+        bad[3], bad[9], bad[17], bad[20] = -1, -2, 160, 1 << 40
+        x.write(0, t.from_numpy(bad).cuda(), bad, one, -one)
+        # a single token
+        x.write(2, slots[5:6], want[5:6], one[:, :1], -one[:, :1])
+
+
+def test_another_stream():
+    rng = np.random.default_rng(10)
+    x = Pair(randomised(pc.empty(2, 64, 4, 64, 6, 12), rng))
+    side = x.t.cuda.Stream()
+    k, v = (rng.standard_normal((2, 20, 64)).astype(np.float16) for _ in range(2))
+    kd, vd, slots = gu.to_dev(k), gu.to_dev(v), x.t.empty(20, dtype=x.t.int64, device="cuda")
+    lists = [x.i32(y) for y in ([0, 1], [0, 13, 20], [0, 1], [2, 3], [0, 1])]
+    x.t.cuda.synchronize()
+    cg, c = x.cg, x.cache
+    cg.cg_pages_reserve_async(c, lists[0], lists[1], slots, x.ws, stream=side)
+    cg.cg_pages_write_async(c, 0, slots, kd, vd, stream=side)
+    cg.cg_pages_fork_async(c, lists[2], lists[3], x.ws, stream=side)
+    cg.cg_pages_free_async(c, lists[4], stream=side)
+    cg.cg_pages_compact_async(c, x.ws, stream=side)
+    side.synchronize()
+    st, want = pc.reserve(x.o, [0, 1], [0, 13, 20], 20)
+    st |= pc.write(x.o, 0, want, k, v) | pc.fork(x.o, [0, 1], [2, 3]) | pc.free(x.o, [0, 1])
+    st |= pc.compact(x.o)[0]
+    x.check(st, "side stream")
+
+
+def test_captured_step():
+    """A decoding step in a graph: each replay adds a token to every row, with eager
+    calls and synchronisations between the replays."""
+    rng = np.random.default_rng(11)
+    x = Pair(randomised(pc.empty(2, 64, 4, 64, 5, 12), rng))
+    x.new(rng, [0, 2, 4], [3, 4, 9])
+    t, cg, c = x.t, x.cg, x.cache
+    rows, starts = x.i32([4, 0, 2]), x.i32([0, 1, 2, 3])
+    slots = t.empty(3, dtype=t.int64, device="cuda")
+    kd, vd = t.zeros((2, 3, 64), dtype=t.float16, device="cuda"), t.zeros((2, 3, 64), dtype=t.float16, device="cuda")
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        cg.cg_pages_reserve_async(c, rows, starts, slots, x.ws)
+        cg.cg_pages_write_async(c, 0, slots, kd, vd)
+    for step in range(6):
+        k, v = (rng.standard_normal((2, 3, 64)).astype(np.float16) for _ in range(2))
+        kd.copy_(gu.to_dev(k))
+        vd.copy_(gu.to_dev(v))
+        graph.replay()
+        st, want = pc.reserve(x.o, [4, 0, 2], [0, 1, 2, 3], 3)
+        st |= pc.write(x.o, 0, want, k, v)
+        x.check(st, ("replay", step))
+        assert np.array_equal(slots.cpu().numpy(), want)
+        if step == 2:
+            x.fork([0], [1])
+        if step == 3:
+            x.free([2])
+            x.compact()
+
+
+def test_pool_past_four_gib():
+    """Offsets past 32 bits inside one layer's pool."""
+    import kv_cache_compression_anchor_amd as cg
+    t = gu.torch()
+    N, P, C = 70000, 32, 1024
+    k, v = (t.empty((1, N, P, C), dtype=t.float16, device="cuda") for _ in range(2))
+    tables, lens = (t.full((3, 8), -1, dtype=t.int32, device="cuda"),
+                    t.zeros(3, dtype=t.int32, device="cuda"))
+    refs = t.ones(N, dtype=t.int32, device="cuda")
+    refs[N - 6:] = 0
+    status = t.zeros(1, dtype=t.int32, device="cuda")
+    c = cg.PagedCache(k, v, tables, lens, refs, status)
+    ws = t.empty(cg.cg_pages_workspace(c), dtype=t.uint8, device="cuda")
+    new = t.randn((1, 100, C), device="cuda").half()
+    slots = t.empty(100, dtype=t.int64, device="cuda")
+    i32 = lambda x: t.tensor(x, dtype=t.int32, device="cuda")  # noqa: E731
+    cg.cg_pages_reserve_async(c, i32([0]), i32([0, 100]), slots, ws)
+    cg.cg_pages_write_async(c, 0, slots, new, -new)
+    assert tables[0, :4].tolist() == [N - 6, N - 5, N - 4, N - 3]
+    assert slots.tolist() == [(N - 6) * P + i for i in range(100)]
+    assert t.equal(k[0, N - 6:N - 2].reshape(-1, C)[:100], new[0])
+    cg.cg_pages_fork_async(c, i32([0]), i32([1]), ws)
+    assert tables[1, :4].tolist() == [N - 6, N - 5, N - 4, N - 2]
+    assert t.equal(v[0, N - 2, :4], -new[0, 96:])
+    cg.cg_pages_copy_async(c, i32([N - 6]), i32([3]))
+    assert t.equal(k[0, 3], new[0, :32])
+    refs[7] = 0
+    cg.cg_pages_compact_async(c, ws)
+    assert tables[0, :4].tolist() == [N - 6, N - 5, N - 4, N - 3] and tables[1, 3].item() == 7
+    assert t.equal(v[0, 7, :4], -new[0, 96:]) and int(refs[7]) == 1 and int(refs[N - 2]) == 0
+    assert int(status.item()) == 0
+
+
+def test_binding_refuses_wrong_tensors():
+    x = Pair(pc.empty(1, 8, 4, 64, 3, 4))
+    cg, t, c = x.cg, x.t, x.cache
+    i64 = t.zeros(2, dtype=t.int64, device="cuda")
+    ok = x.i32([0, 1])
+    for call in (lambda: cg.PagedCache(x.k, x.v[:, :4], x.tables, x.lens, x.refs, x.status),
+                 lambda: cg.PagedCache(x.k, x.v, x.tables, x.lens[:2], x.refs, x.status),
+                 lambda: cg.PagedCache(x.k, x.v, x.tables, x.lens, x.refs[:4], x.status),
+                 lambda: cg.PagedCache(x.k.cpu(), x.v, x.tables, x.lens, x.refs, x.status),
+                 lambda: cg.PagedCache(x.k.float(), x.v.float(), x.tables, x.lens, x.refs, x.status),
+                 lambda: cg.cg_pages_copy_async(c, i64, i64),
+                 lambda: cg.cg_pages_copy_async(c, ok, ok[:1]),
+                 lambda: cg.cg_pages_copy_async(c, ok.cpu(), ok.cpu()),
+                 lambda: cg.cg_pages_reserve_async(c, ok, ok, i64, x.ws),
+                 lambda: cg.cg_pages_fork_async(c, ok, ok[:1], x.ws),
+                 lambda: cg.cg_pages_write_async(c, 0, i64, x.k[0, 0, :2], x.k[0, 0, :2])):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    with pytest.raises(cg.CgError):
+        cg.cg_pages_fork_async(c, ok, ok, x.ws[:64])
