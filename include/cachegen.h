@@ -410,9 +410,10 @@ int cg_pages_compact_async(const cg_paged_cache* cache, int32_t* n_live_dev,
  *
  * Group g: sequences group_starts[g] .. group_starts[g+1] - 1, whose first
  * prefix_lens[g] tokens are the same, as forks of one row have them; they are read
- * through the row of the group's first sequence.  Every sequence of the group
- * that has queries must be at least prefix_lens[g] + m long; one that is not gets
- * zeros, lse = -infinity and bit 2.  Sequences in no group, and n_groups = 0
+ * through the row of the group's first sequence, which must be as long (whether or
+ * not it has queries); if it is not, the group is refused.  Every sequence of the
+ * group that has queries must be at least prefix_lens[g] + m long; one that is not
+ * is refused.  A refused sequence gets zeros, lse = -infinity and bit 2.  Sequences in no group, and n_groups = 0
  * (pointers may be NULL), are computed by themselves.
  *
  * Rows of out and lse that no sequence has queries for are left as they were.

@@ -11,12 +11,30 @@ namespace {
 
 constexpr uint32_t kBadPage = 2u, kRefused = 4u;  // status bits
 
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) s4 lds_s4;
+
+constexpr int kTile = 32;        // tokens of a tile: the depth of one 16x16x32 product
+constexpr int kWaves = 4;        // of a workgroup
+constexpr int kThreads = 64 * kWaves;
+constexpr int kListPages = 1024; // table entries staged at a time
+constexpr int kMinTiles = 8;     // tiles of a split, at least
+// Weights are 2^(score - m) with m at most kSlack above what the running maximum
+// was when it was last raised, and kLift below it: up to 2^14, and binary16's
+// normal range reaches down to 2^-20 of the largest.
+constexpr float kSlack = 8.0f, kLift = 6.0f;
+
 struct Attn {
   int C, P, shift, N, R, B;
-  const uint16_t *k, *v;  // the layer's pools
+  const char *k, *v;  // the layer's pools
   const int32_t *tables, *lens;
   uint32_t* status;
-  int H, G, d;  // query heads, heads per kv head, head dimension
+  int H, G, d, kv;  // query heads, heads per kv head, head dimension, kv heads
   float scale;
   int n_seqs, n_q, n_groups;
   const int32_t *rows, *q_starts, *group_starts, *prefix_lens;
@@ -24,103 +42,684 @@ struct Attn {
   uint16_t* out;
   float* lse;
   int64_t q_stride, out_stride;
+  // the launch: splits of a prefix and of a sequence's rest, row tiles that have
+  // workgroups of their own (there may be more)
+  int pre_splits, rest_splits, pre_tiles, rest_tiles, pre_groups;
+  float* part;  // [pre_splits + rest_splits][n_q][H][d] sums, not divided
+  float* ml;    // the same with [2]: reference exponent m, sum of weights l
 };
 
-// largest i in [0, n) with a[i] <= x, or -1
+// Largest i in [0, n) with a[i] <= x, or -1, a ascending; every lane of the wave
+// gets it.  64 samples a step: one round of loads up to n = 64, two up to 4,096.
 __device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {
-  int lo = -1, hi = n;
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (a[m] <= x) lo = m; else hi = m;
+  const int lane = threadIdx.x & 63;
+  int lo = 0, len = n;  // the answer is in [lo - 1, lo + len - 1]
+  while (len > 0) {
+    const int step = (len + 63) >> 6;
+    const int i = lane * step;
+    const uint64_t hit = __ballot(i < len && a[lo + (i < len ? i : 0)] <= x);
+    const int n_hit = __popcll(hit);
+    if (n_hit == 0) return lo - 1;
+    const int at = (n_hit - 1) * step;  // a[lo + at] <= x, and not the next sample
+    len = min(step, len - at) - 1;
+    lo += at + 1;
   }
-  return lo;
+  return lo - 1;
+}
+
+__device__ __forceinline__ int row_of(const Attn& a, int s) { return a.rows ? a.rows[s] : s; }
+__device__ __forceinline__ bool len_ok(const Attn& a, int64_t n) {
+  return n >= 0 && n <= (int64_t)a.B << a.shift;
 }
 
 struct Seq {
-  bool ok;              // its row, length and prefix fit together
-  int row, pre_row;     // rows of the tables that the rest and the prefix are read through
-  int len, pre, q0, m;  // tokens, those of the prefix, first query, queries
+  bool ok;           // its row, length, queries and prefix fit together
+  int row, len, pre; // table row, tokens, those of the shared prefix
+  int q0, m;         // first query, queries
 };
 
-__device__ __forceinline__ int row_of(const Attn& a, int s) { return a.rows ? a.rows[s] : s; }
-
+// Sequence s; all of it is uniform over the wave.
 __device__ __forceinline__ Seq sequence(const Attn& a, int s) {
   Seq q;
   q.row = row_of(a, s);
   q.q0 = a.q_starts[s];
-  q.m = a.q_starts[s + 1] - q.q0;
+  const int end = a.q_starts[s + 1];
   q.pre = 0;
-  q.pre_row = q.row;
   const bool in = q.row >= 0 && q.row < a.R;
   q.len = in ? a.lens[q.row] : 0;
-  q.ok = in && q.len >= 0 && q.len <= (int64_t)a.B << a.shift && q.q0 >= 0 &&
-         a.q_starts[s + 1] <= a.n_q;
+  q.ok = in && len_ok(a, q.len) && q.q0 >= 0 && end <= a.n_q;
+  q.m = q.ok ? end - q.q0 : 0;
   if (a.n_groups) {
     const int g = last_at_most(a.group_starts, a.n_groups, s);
     if (g >= 0 && s < a.group_starts[g + 1]) {
-      q.pre = a.prefix_lens[g];
-      q.pre_row = row_of(a, a.group_starts[g] < 0 ? 0 : a.group_starts[g]);
-      q.ok = q.ok && q.pre_row >= 0 && q.pre_row < a.R && q.pre >= 0 &&
-             (q.pre == 0 || (int64_t)q.pre + q.m <= q.len);
+      const int pre = a.prefix_lens[g];
+      if (pre != 0) {
+        const int first = row_of(a, max(a.group_starts[g], 0));
+        q.ok = q.ok && pre > 0 && first >= 0 && first < a.R && a.lens[first] >= pre &&
+               len_ok(a, a.lens[first]) && (int64_t)pre + q.m <= q.len;
+        q.pre = pre;
+      }
     }
   }
   return q;
 }
 
-// One workgroup per (query token, head): 256 tokens at a time, a thread scores
-// one token, then a thread sums one channel.
-__global__ __launch_bounds__(256) void k_attention(Attn a) {
-  __shared__ float qs[256], p[256], red[256];
-  __shared__ int64_t at[256];
-  const int qi = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, kvh = h / a.G;
-  const int s = last_at_most(a.q_starts, a.n_seqs, qi);
-  if (s < 0 || qi >= a.q_starts[s + 1]) return;
-  const Seq q = sequence(a, s);
-  if (tid < a.d)
-    qs[tid] = half_bits_to_float(a.q[qi * a.q_stride + h * a.d + tid]) * a.scale;
-  int lim = q.len - q.m + (qi - q.q0) + 1;
-  if (!q.ok) {
-    lim = 0;
-    if (tid == 0) atomicOr(a.status, kRefused);
+// Tokens [lo, hi) in tiles that start at multiples of kTile, dealt to `splits`
+// workgroups in turn of at least kMinTiles each.
+struct Split {
+  int tile0, tiles, per, used;
+};
+__device__ __forceinline__ Split split_of(int lo, int hi, int splits) {
+  Split s;
+  s.tile0 = lo / kTile;
+  s.tiles = hi > lo ? (hi + kTile - 1) / kTile - s.tile0 : 0;
+  s.per = max(kMinTiles, (s.tiles + splits - 1) / splits);
+  s.used = (s.tiles + s.per - 1) / s.per;
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+// Tiles of K and V in LDS
+// ---------------------------------------------------------------------------
+// A tile is kTile rows of DP halves, in 16-byte chunks; chunk c of row r lies at
+// position c ^ swizzle(r), so that the 16 rows that a product's operand reads at
+// one chunk fall into 16 different positions of the 256 bytes of all banks.
+template <int DP>
+struct Geo {
+  static constexpr int NC = DP / 8;       // chunks of a row
+  static constexpr int RPI = 64 / NC;     // rows that one load of a wave brings
+  static constexpr int NI = kTile / RPI;  // loads of a tile
+  static constexpr int BYTES = kTile * DP * 2;
+};
+template <int DP>
+__device__ __forceinline__ int swizzle(int row) {
+  return DP == 64 ? (row >> 1) & 7 : row & 15;
+}
+
+// LDS <- global, 16 bytes a lane: lane i's bytes land at lds + 16 i.  No register
+// receives them, and the compiler does not count them: wait_loads<n>() waits
+// until at most n of the wave's newest are on their way.
+__device__ __forceinline__ void load_lds(uint32_t lds, const char* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base)
+               : "memory");
+}
+__device__ __forceinline__ void load_lds(uint32_t lds, const char* addr) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds), "v"(addr)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// This thread's lane, as a value that the compiler does not know: what a rare path
+// computes from it is not kept in registers through the loop around it.
+__device__ __forceinline__ int rare_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+struct Source {           // where a workgroup's tokens come from
+  const int32_t* list;    // LDS: pages of blocks block0 .. of the table row, -1 if bad
+  int block0, lo, hi;     // tokens outside [lo, hi) do not exist for it
+  int shift, pmask, nc;   // of the page; chunks of a head's row in use
+  uint32_t page_bytes, row_bytes;
+};
+
+// Page of token t0 + lane (lanes 0..31), -1 where there is none.
+__device__ __forceinline__ int tile_pages(const Source& s, int t0) {
+  const int t = t0 + (threadIdx.x & 31);
+  return t >= s.lo && t < s.hi ? s.list[(t >> s.shift) - s.block0] : -1;
+}
+
+// Issues the loads of the tile at t0 of a pool (pointing at the kv head's channels)
+// to LDS address lds.  full: every token exists.  If the rows of a load also lie in
+// one page and the head fills the tile's width, its address is scalar but for a
+// lane's fixed offset.  Otherwise rows of tokens that do not exist, and chunks
+// behind the head's, keep what they held.  A full tile is NI loads either way.
+template <int DP>
+__device__ __forceinline__ void load_tile(const Source& s, const char* pool, uint32_t lds, int t0,
+                                          int pages, bool full) {
+  using Ge = Geo<DP>;
+  if (full && s.pmask >= Ge::RPI - 1 && s.nc == Ge::NC) {
+    const int lane = threadIdx.x & 63, lrow = lane / Ge::NC, lc = lane % Ge::NC;
+#pragma unroll
+    for (int i = 0; i < Ge::NI; i++) {
+      const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(pages, i * Ge::RPI);
+      const char* base = pool + (uint64_t)page * s.page_bytes +
+                         (uint64_t)(uint32_t)((t0 + i * Ge::RPI) & s.pmask) * s.row_bytes;
+      load_lds(lds + i * 1024, base,
+               lrow * s.row_bytes + (lc ^ swizzle<DP>(i * Ge::RPI + lrow)) * 16);
+    }
+  } else {
+    const int lane = rare_lane(), lrow = lane / Ge::NC, lc = lane % Ge::NC;
+#pragma unroll 1
+    for (int i = 0; i < Ge::NI; i++) {
+      const int row = i * Ge::RPI + lrow;
+      const int page = __shfl(pages, row);
+      const int c = lc ^ swizzle<DP>(row);
+      const char* addr = pool + (uint64_t)(uint32_t)max(page, 0) * s.page_bytes +
+                         (uint64_t)(uint32_t)((t0 + row) & s.pmask) * s.row_bytes + c * 16;
+      if (c < s.nc && page >= 0) load_lds(lds + i * 1024, addr);
+    }
   }
-  float m = -__builtin_inff(), l = 0.0f, o = 0.0f;
-  for (int base = 0; base < lim; base += 256) {
-    const int t = base + tid;
-    float x = -__builtin_inff();
-    int64_t where = -1;
-    if (t < lim) {
-      const int page = a.tables[(int64_t)(t < q.pre ? q.pre_row : q.row) * a.B + (t >> a.shift)];
-      if (page >= 0 && page < a.N)
-        where = (((int64_t)page << a.shift) + (t & (a.P - 1))) * a.C + kvh * a.d;
-      else
-        atomicOr(a.status, kBadPage);
+}
+
+// Before the values of a tile that not every query sees whole: rows of tokens that
+// do not exist become zeros (their weights are zero, but what an earlier tile left
+// there might be no number).  Returns whether the tile holds a value that is no
+// finite number.
+template <int DP>
+__device__ __forceinline__ bool prepare_values(char* tile, int pages) {
+  using Ge = Geo<DP>;
+  const int lane = rare_lane();
+  bool odd = false;
+#pragma unroll 1
+  for (int i = 0; i < Ge::NI; i++) {
+    uint4* at = (uint4*)(tile + i * 1024 + lane * 16);
+    if (__shfl(pages, i * Ge::RPI + lane / Ge::NC) < 0) {
+      *at = uint4{0, 0, 0, 0};
+    } else {
+      const uint4 x = *at;
+      for (uint32_t y : {x.x, x.y, x.z, x.w})
+        odd |= (y & 0x7C00u) == 0x7C00u || (y & 0x7C000000u) == 0x7C000000u;
     }
-    __syncthreads();  // qs is written; p, at and red of the last step are read
-    if (where >= 0) {
-      x = 0.0f;
-      for (int i = 0; i < a.d; i++) x += qs[i] * half_bits_to_float(a.k[where + i]);
+  }
+  wait_lds();
+  return __any(odd);
+}
+
+// ---------------------------------------------------------------------------
+// One wave's part: 16 RT query rows against its tiles
+// ---------------------------------------------------------------------------
+// Scores are computed transposed, S^T = K Q^T, so that a lane holds scores of one
+// query (its column, lane & 15) for tokens 4 (lane >> 4) .. + 3 of each half tile.
+// That is the layout in which O^T = V^T P^T takes P as its second operand, if
+// the depth of that product runs over the tokens in the same order, which V's
+// transposing reads choose freely: P never leaves its registers.
+template <int DP, int RT>
+struct Wave {
+  static constexpr int KS = DP / 32, NB = DP / 16;
+  h8 q[RT][KS];
+  f4 o[RT][NB];
+  float m[RT], mu[RT], l[RT];  // reference exponent (-inf: none yet), the one in use, sum
+  int lim[RT];                 // tokens that the lane's query sees
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+      m[r] = -__builtin_inff();
+      mu[r] = 0.0f;
+      l[r] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NB; b++) o[r][b] = f4{0, 0, 0, 0};
     }
-    red[tid] = x;
-    at[tid] = where;
-    for (int w = 128; w; w >>= 1) {
+  }
+
+  __device__ __forceinline__ void scores(const char* kt, f4 (&s)[RT][2]) {
+    const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int r = 0; r < RT; r++) s[r][0] = s[r][1] = f4{0, 0, 0, 0};
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++) {
+        const int row = sub * 16 + n;
+        const h8 a = *(const h8*)(kt + row * (DP * 2) + (((ks * 4 + g) ^ swizzle<DP>(row)) * 16));
+#pragma unroll
+        for (int r = 0; r < RT; r++)
+          s[r][sub] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][ks], s[r][sub], 0, 0, 0);
+      }
+  }
+
+  // Scores of tokens that do not exist, or that a query does not see, become -inf.
+  __device__ __forceinline__ void mask(f4 (&s)[RT][2], int t0, int pages) {
+    const int g = rare_lane() >> 4;
+#pragma unroll
+    for (int sub = 0; sub < 2; sub++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int tok = sub * 16 + 4 * g + i;
+        const int t = __shfl(pages, tok) >= 0 ? t0 + tok : 0x7FFFFFFF;
+#pragma unroll
+        for (int r = 0; r < RT; r++) s[r][sub][i] = t < lim[r] ? s[r][sub][i] : -__builtin_inff();
+      }
+  }
+
+  // Scores to weights.  m is raised only where a score passes it by kSlack, so
+  // most tiles need neither the maximum over the lanes nor a rescaling of o.
+  __device__ __forceinline__ void weights(f4 (&s)[RT][2], float c, h8 (&p)[RT]) {
+    float mx[RT];
+    bool raise = false;
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+      mx[r] = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
+                    fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
+      raise |= mx[r] * c > m[r] + (kSlack + kLift);
+    }
+    if (__any(raise)) {
+#pragma unroll
+      for (int r = 0; r < RT; r++) {
+        float x = mx[r];
+        x = fmaxf(x, __shfl_xor(x, 16));
+        x = fmaxf(x, __shfl_xor(x, 32));
+        const float nm = fmaxf(m[r], x * c - kLift);
+        const float f = nm == m[r] ? 1.0f : __builtin_amdgcn_exp2f(m[r] - nm);
+        m[r] = nm;
+        mu[r] = nm == -__builtin_inff() ? 0.0f : nm;
+        l[r] *= f;
+#pragma unroll
+        for (int b = 0; b < NB; b++) o[r][b] *= f;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; e++)
+        w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][e >> 2][e & 3], c, -mu[r]));
+      l[r] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+#pragma unroll
+      for (int e = 0; e < 8; e++) p[r][e] = (_Float16)w[e];  // rounded to nearest
+    }
+  }
+
+  // o += V^T P^T
+  __device__ __forceinline__ void values(const char* vt, const h8 (&p)[RT]) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
+    const int row = 4 * g + (j >> 2), in = (j & 1) * 8, half = (j & 3) >> 1;
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+      union { s4 x[2]; h8 a; } u;
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++) {
+        const int rr = sub * 16 + row;
+        u.x[sub] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s4*)(vt + rr * (DP * 2) + (((2 * b + half) ^ swizzle<DP>(rr)) * 16) + in));
+      }
+#pragma unroll
+      for (int r = 0; r < RT; r++)
+        o[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(u.a, p[r], o[r][b], 0, 0, 0);
+    }
+  }
+
+  // The same one token at a time, and only to the queries that see it: for tiles in
+  // which a value that is no finite number would meet zero weights.
+  __device__ __forceinline__ void values_one_by_one(const char* vt, const h8 (&p)[RT], int t0) {
+    const int lane = rare_lane(), g = lane >> 4;
+#pragma unroll 1
+    for (int tok = 0; tok < kTile; tok++) {
+      const int e0 = (tok >> 4) * 4 + (tok & 3), g0 = (tok >> 2) & 3;
+      float x[RT];  // the weight of the lane's queries; 0 and not seen are not the same
+      bool sees[RT];
+#pragma unroll
+      for (int r = 0; r < RT; r++) {
+        const uint4 w = __builtin_bit_cast(uint4, p[r]);
+        const uint32_t lo = e0 & 2 ? w.y : w.x, hi = e0 & 2 ? w.w : w.z;
+        const uint32_t two = __shfl(e0 & 4 ? hi : lo, g0 * 16 + (lane & 15));
+        x[r] = half_bits_to_float((uint16_t)(two >> (16 * (e0 & 1))));
+        sees[r] = t0 + tok < lim[r];
+      }
+#pragma unroll
+      for (int b = 0; b < NB; b++) {
+        const int c = 2 * b + (g >> 1);
+        const h4 v = *(const h4*)(vt + tok * (DP * 2) + ((c ^ swizzle<DP>(tok)) * 16) + (g & 1) * 8);
+#pragma unroll
+        for (int r = 0; r < RT; r++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) o[r][b][i] += sees[r] ? x[r] * (float)v[i] : 0.0f;
+        asm volatile("" ::: "memory");  // one block's values in registers at a time
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// One workgroup: a tile of rows against a split of the tokens
+// ---------------------------------------------------------------------------
+struct Item {
+  int head;                 // kv head
+  int q0, rows;             // first query; rows = queries x heads of the kv head
+  int lo, hi;               // tokens
+  int lim0;                 // tokens that the first query sees (each later one 1 more)
+  int trow;                 // table row
+  int splits, split, slot0; // of the tokens; first partial of this kind
+  int row_tile, row_tiles;  // this workgroup's first row tile and its stride
+};
+
+template <int DP>
+struct Shared {
+  // each wave's tile of K and of V; then the sums of the waves
+  __attribute__((aligned(1024))) char tile[kWaves][2][Geo<DP>::BYTES];
+  int32_t list[kListPages];
+  float m[kWaves][64], l[kWaves][64], scale[kWaves][64];
+};
+
+// The waves take the split's tiles in turn and share nothing until the end.  Each
+// has room for one tile of K and one of V: the next K is on its way while the
+// weights and the values are computed, the next V while the scores are.
+template <int DP, int RT>
+__device__ __forceinline__ void run_rows(const Attn& a, const Item& it, Shared<DP>& sh) {
+  using Ge = Geo<DP>;
+  using W = Wave<DP, RT>;
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Split sp = split_of(it.lo, it.hi, it.splits);
+  if (it.split >= sp.used) return;
+  const int first = sp.tile0 + it.split * sp.per;
+  const int last = min(first + sp.per, sp.tile0 + sp.tiles);  // tiles [first, last)
+  const uint32_t row_bytes = (uint32_t)a.C * 2;
+  Source src{sh.list, 0, it.lo, it.hi, a.shift, a.P - 1, a.d / 8, row_bytes * (uint32_t)a.P, row_bytes};
+  const char *kp = a.k + it.head * a.d * 2, *vp = a.v + it.head * a.d * 2;
+  char *kt = sh.tile[wave][0], *vt = sh.tile[wave][1];
+  const uint32_t klds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char*)kt);
+  const uint32_t vlds = klds + Ge::BYTES;
+  // negated queries stand for a negative scale, queries of 0 for a scale of 0, so
+  // that the largest product has the largest score and c is positive
+  const float c = a.scale == 0 ? 1.0f : fminf(fabsf(a.scale) * 1.44269504088896341f, 3.4e38f);
+  const uint32_t keep = a.scale == 0 ? 0 : 0xFFFFFFFFu, flip = a.scale < 0 ? 0x80008000u : 0;
+  const int row_tiles = (it.rows + 16 * RT - 1) / (16 * RT);
+  // tiles whose pages the list holds, wherever in a page they begin
+  const int list_tiles = (int)((int64_t)(kListPages - 1) * a.P / kTile) - 1;
+
+  for (int rt = it.row_tile; rt < row_tiles; rt += it.row_tiles) {
+    W w;
+    w.clear();
+    int min_lim = it.hi, max_lim = it.lo;
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+      const int row = rt * 16 * RT + r * 16 + n;
+      const bool in = row < it.rows;
+      const int qi = in ? row / a.G : 0, h = it.head * a.G + (in ? row % a.G : 0);
+      const uint16_t* src_q = a.q + (it.q0 + qi) * a.q_stride + (int64_t)h * a.d;
+#pragma unroll
+      for (int ks = 0; ks < W::KS; ks++) {
+        const int ch = ks * 4 + g;
+        uint4 z = in && ch < src.nc ? *(const uint4*)(src_q + ch * 8) : uint4{0, 0, 0, 0};
+        z = uint4{(z.x & keep) ^ flip, (z.y & keep) ^ flip, (z.z & keep) ^ flip, (z.w & keep) ^ flip};
+        w.q[r][ks] = __builtin_bit_cast(h8, z);
+      }
+      w.lim[r] = in ? min(it.hi, it.lim0 + qi) : it.hi;
+      min_lim = min(min_lim, w.lim[r]);
+      if (in) max_lim = max(max_lim, w.lim[r]);
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+      min_lim = min(min_lim, __shfl_xor(min_lim, x));
+      max_lim = max(max_lim, __shfl_xor(max_lim, x));
+    }
+    min_lim = __builtin_amdgcn_readfirstlane(min_lim);
+    max_lim = __builtin_amdgcn_readfirstlane(max_lim);
+    const int end = min(last, (max_lim + kTile - 1) / kTile);  // later tiles: nobody sees them
+    if (a.d < DP) {  // the chunks behind the head's row stay zero
       __syncthreads();
-      if (tid < w) red[tid] = fmaxf(red[tid], red[tid + w]);
+      for (int i = tid; i < (int)sizeof(sh.tile) / 16; i += kThreads)
+        ((uint4*)sh.tile)[i] = uint4{0, 0, 0, 0};
     }
-    __syncthreads();
-    const float nm = fmaxf(m, red[0]);
-    const float keep = nm == -__builtin_inff() ? 1.0f : __expf(m - nm);
-    p[tid] = x == -__builtin_inff() ? 0.0f : __expf(x - nm);
-    __syncthreads();
-    l *= keep;
-    o *= keep;
-    m = nm;
-    for (int i = 0; i < 256; i++) {
-      l += p[i];
-      if (tid < a.d && at[i] >= 0) o += p[i] * half_bits_to_float(a.v[at[i] + tid]);
+    for (int base = first; base < end; base += list_tiles) {
+      const int stop = min(base + list_tiles, end);
+      // pages of the tokens of tiles [base, stop)
+      const int b0 = max(base * kTile, it.lo) >> a.shift;
+      const int b1 = (min(stop * kTile, it.hi) - 1) >> a.shift;
+      __syncthreads();  // the list and the tiles are free
+      bool bad = false;
+      for (int i = tid; i <= b1 - b0; i += kThreads) {
+        const int page = a.tables[(int64_t)it.trow * a.B + b0 + i];
+        const bool ok = page >= 0 && page < a.N;
+        sh.list[i] = ok ? page : -1;
+        bad |= !ok;
+      }
+      bad = __syncthreads_or(bad);
+      if (bad && tid == 0) atomicOr(a.status, kBadPage);
+      src.block0 = b0;
+      // one round more than there are tiles: the first only starts the loads
+      int tile = base + wave - kWaves, pages = -1;
+      bool have = false, is_full = false;
+      while (have || tile + kWaves < stop) {
+        const int t0 = tile * kTile, next = tile + kWaves;
+        const bool more = next < stop;
+        const bool next_full = more && !bad && next * kTile >= it.lo && (next + 1) * kTile <= min_lim;
+        const int next_pages = more ? tile_pages(src, next * kTile) : -1;
+        f4 s[RT][2];
+        if (have) {
+          if (is_full) wait_loads<Ge::NI>(); else wait_loads<0>();
+          w.scores(kt, s);
+          wait_lds();
+        }
+        if (more) load_tile<DP>(src, kp, klds, next * kTile, next_pages, next_full);
+        if (have) {
+          h8 p[RT];
+          if (!is_full) w.mask(s, t0, pages);
+          w.weights(s, c, p);
+          if (is_full && next_full) wait_loads<Ge::NI>(); else wait_loads<0>();
+          if (!is_full && prepare_values<DP>(vt, pages)) w.values_one_by_one(vt, p, t0);
+          else w.values(vt, p);
+          wait_lds();
+        }
+        if (more) load_tile<DP>(src, vp, vlds, next * kTile, next_pages, next_full);
+        tile = next;
+        pages = next_pages;
+        is_full = next_full;
+        have = more;
+      }
     }
+    // the waves' sums together, against the largest reference exponent
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+      float l = w.l[r];
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      if (g == 0) {
+        sh.m[wave][r * 16 + n] = w.m[r];
+        sh.l[wave][r * 16 + n] = l;
+      }
+    }
+    __syncthreads();  // all waves are done with their tiles
+    if (tid < 16 * RT) {
+      float m = -__builtin_inff(), l = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kWaves; x++) m = fmaxf(m, sh.m[x][tid]);
+#pragma unroll
+      for (int x = 0; x < kWaves; x++) {
+        // a wave without a reference has weighed nothing, or only what is no number
+        const float mx = sh.m[x][tid];
+        const float f = mx == m ? 1.0f : mx == -__builtin_inff() && sh.l[x][tid] != 0.0f
+                            ? 1.0f : __builtin_amdgcn_exp2f(mx - m);
+        sh.scale[x][tid] = f;
+        l += f * sh.l[x][tid];
+      }
+      const int row = rt * 16 * RT + tid;
+      if (row < it.rows) {
+        const int64_t at = ((int64_t)(it.slot0 + it.split) * a.n_q + it.q0 + row / a.G) * a.H +
+                           it.head * a.G + row % a.G;
+        a.ml[2 * at] = m;
+        a.ml[2 * at + 1] = l;
+      }
+    }
+    constexpr int kRounds = RT > 2 ? RT / 2 : 1;      // as the tiles' room allows
+    constexpr int kBlocks = W::NB / kRounds;          // 16-channel blocks a round
+    constexpr int kQuads = kBlocks * 4;               // 4-channel groups of a row and round
+    static_assert(sizeof(sh.tile) >= (size_t)kWaves * 16 * RT * kQuads * 16, "room for the sums");
+    f4* sums = (f4*)sh.tile;                          // [wave][row][quad], quads rotated by row
+#pragma unroll
+    for (int round = 0; round < kRounds; round++) {
+      __syncthreads();  // scale is written; the last round is read
+#pragma unroll
+      for (int r = 0; r < RT; r++)
+#pragma unroll
+        for (int b = 0; b < kBlocks; b++)
+          sums[(wave * 16 * RT + r * 16 + n) * kQuads + ((b * 4 + g + r * 16 + n) & (kQuads - 1))] =
+              w.o[r][round * kBlocks + b];
+      __syncthreads();
+#pragma unroll 1
+      for (int i = tid; i < 16 * RT * kQuads; i += kThreads) {
+        const int row = i / kQuads, quad = i % kQuads;
+        const int ch = round * kBlocks * 16 + quad * 4, gr = rt * 16 * RT + row;
+        if (gr >= it.rows || ch >= a.d) continue;
+        f4 x{0, 0, 0, 0};
+#pragma unroll
+        for (int y = 0; y < kWaves; y++)
+          x += sh.scale[y][row] * sums[(y * 16 * RT + row) * kQuads + ((quad + row) & (kQuads - 1))];
+        const int64_t at = ((int64_t)(it.slot0 + it.split) * a.n_q + it.q0 + gr / a.G) * a.H +
+                           it.head * a.G + gr % a.G;
+        *(f4*)(a.part + at * a.d + ch) = x;
+      }
+    }
+    __syncthreads();  // m, l and scale are free
   }
-  if (tid < a.d) a.out[qi * a.out_stride + h * a.d + tid] = float_to_half_bits(l == 0 ? 0.0f : o / l);
-  if (tid == 0 && a.lse) a.lse[(int64_t)qi * a.H + h] = l == 0 ? -__builtin_inff() : m + __logf(l);
+}
+
+// The w-th item of the launch: first (group, split, row tile, kv head), kv heads
+// fastest, for the shared prefixes, then the same per sequence for what lies behind
+// them.  False: nothing to do.
+__device__ __forceinline__ bool item_of(const Attn& a, int w, Item& it) {
+  it.head = w % a.kv;
+  w /= a.kv;
+  const int pre_items = a.pre_groups * a.pre_splits * a.pre_tiles;
+  if (w < pre_items) {
+    it.row_tile = w % a.pre_tiles;
+    w /= a.pre_tiles;
+    it.split = w % a.pre_splits;
+    const int grp = w / a.pre_splits;
+    const int s0 = a.group_starts[grp], s1 = a.group_starts[grp + 1];
+    it.lo = 0;
+    it.hi = a.prefix_lens[grp];
+    if (s0 < 0 || s1 <= s0 || s1 > a.n_seqs || it.hi <= 0) return false;
+    it.trow = row_of(a, s0);
+    if (it.trow < 0 || it.trow >= a.R || !len_ok(a, a.lens[it.trow]) || a.lens[it.trow] < it.hi)
+      return false;
+    it.q0 = a.q_starts[s0];
+    const int q1 = a.q_starts[s1];
+    if (it.q0 < 0 || q1 <= it.q0 || q1 > a.n_q) return false;
+    it.rows = (q1 - it.q0) * a.G;
+    it.lim0 = it.hi;
+    it.splits = a.pre_splits;
+    it.slot0 = 0;
+    it.row_tiles = a.pre_tiles;
+    return true;
+  }
+  w -= pre_items;
+  it.row_tile = w % a.rest_tiles;
+  w /= a.rest_tiles;
+  it.split = w % a.rest_splits;
+  const Seq q = sequence(a, w / a.rest_splits);
+  if (!q.ok || q.m <= 0) return false;
+  it.lo = q.pre;
+  it.hi = q.len;
+  it.trow = q.row;
+  it.q0 = q.q0;
+  it.rows = q.m * a.G;
+  it.lim0 = q.len - q.m + 1;
+  it.splits = a.rest_splits;
+  it.slot0 = a.pre_splits;
+  it.row_tiles = a.rest_tiles;
+  return true;
+}
+
+template <int DP, int RT>
+__global__ __launch_bounds__(kThreads, DP == 256 || RT == 4 ? 1 : 2) void k_attention(Attn a, int first,
+                                                                                      int end) {
+  __shared__ Shared<DP> sh;
+  for (int w = first + blockIdx.x; w < end; w += gridDim.x) {
+    Item it;
+    if (item_of(a, w, it)) run_rows<DP, RT>(a, it, sh);
+  }
+}
+
+// Joins the partial sums of a query's heads: a workgroup per query, d / 4 lanes a head.
+__global__ __launch_bounds__(kThreads) void k_join(Attn a) {
+  const int qi = blockIdx.x;
+  const int s = last_at_most(a.q_starts, a.n_seqs, qi);
+  if (s < 0 || qi < a.q_starts[s] || qi >= a.q_starts[s + 1]) return;
+  const Seq q = sequence(a, s);
+  if (!q.ok && threadIdx.x == 0) atomicOr(a.status, kRefused);
+  const int pre = q.ok ? split_of(0, q.pre, a.pre_splits).used : 0;
+  const int rest = q.ok ? split_of(q.pre, q.len, a.rest_splits).used : 0;
+  const int quads = a.d / 4;
+  for (int i = threadIdx.x; i < a.H * quads; i += kThreads) {
+    const int h = i / quads, ch = (i % quads) * 4;
+    float m = -__builtin_inff(), l = 0.0f;
+    f4 o{0, 0, 0, 0};
+    for (int x = 0; x < pre + rest; x++) {
+      const int slot = x < pre ? x : a.pre_splits + x - pre;
+      const int64_t at = ((int64_t)slot * a.n_q + qi) * a.H + h;
+      const float mx = a.ml[2 * at], lx = a.ml[2 * at + 1];
+      if (lx == 0.0f) continue;  // weighed nothing
+      const f4 ox = *(const f4*)(a.part + at * a.d + ch);
+      const float nm = fmaxf(m, mx);
+      const float f = m == nm ? 1.0f : __builtin_amdgcn_exp2f(m - nm);
+      const float fx = mx == nm ? 1.0f : __builtin_amdgcn_exp2f(mx - nm);
+      o = o * f + ox * fx;
+      l = l * f + lx * fx;
+      m = nm;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    ushort4 r;
+    r.x = float_to_half_bits(o[0] * inv);
+    r.y = float_to_half_bits(o[1] * inv);
+    r.z = float_to_half_bits(o[2] * inv);
+    r.w = float_to_half_bits(o[3] * inv);
+    *(ushort4*)(a.out + qi * a.out_stride + (int64_t)h * a.d + ch) = r;
+    if (ch == 0 && a.lse)
+      a.lse[(int64_t)qi * a.H + h] = l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945309f;
+  }
+}
+
+// How many splits and row tiles the launch has, from the call's numbers alone.
+struct Plan {
+  int dp, pre_splits, rest_splits, pre_tiles, rest_tiles, pre_r, rest_r, pre_groups;
+  size_t words;
+};
+
+int rows_per_wave(int64_t rows, int dp) {  // in 16-row tiles
+  return rows <= 16 ? 1 : rows <= 32 || dp == 256 ? 2 : 4;
+}
+
+// items first .. end - 1 of the launch's list
+void launch(int dp, int r, const Attn& a, int64_t first, int64_t end, hipStream_t st) {
+  if (end <= first) return;
+  const int grid = (int)std::min<int64_t>(end - first, 1 << 22);
+#define GO(DP, RT) k_attention<DP, RT><<<grid, kThreads, 0, st>>>(a, (int)first, (int)end)
+  if (dp == 64) { if (r == 1) GO(64, 1); else if (r == 2) GO(64, 2); else GO(64, 4); }
+  else if (dp == 128) { if (r == 1) GO(128, 1); else if (r == 2) GO(128, 2); else GO(128, 4); }
+  else { if (r == 1) GO(256, 1); else GO(256, 2); }
+#undef GO
+}
+
+Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
+  Plan p;
+  const int kv = c.channels / x.head_dim, G = x.n_heads / kv;
+  p.dp = x.head_dim <= 64 ? 64 : x.head_dim <= 128 ? 128 : 256;
+  // row tiles with workgroups of their own: few enough that an item's number, over
+  // all heads, sequences and splits, fits 31 bits
+  auto most = [&](int64_t items) { return std::max<int64_t>(1, (1 << 22) / std::max<int64_t>(1, items)); };
+  const int64_t rows = (int64_t)std::max(1, std::min(x.max_q, x.n_q)) * G;
+  p.rest_r = rows_per_wave(rows, p.dp);
+  p.rest_tiles = (int)std::min(most((int64_t)x.n_seqs * kv), (rows + 16 * p.rest_r - 1) / (16 * p.rest_r));
+  const bool shared = x.n_groups > 0 && x.max_prefix > 0;
+  p.pre_groups = x.n_groups;
+  // rows of an average group
+  const int64_t pre_rows = std::max<int64_t>(1, x.n_groups ? (x.n_q + x.n_groups - 1) / x.n_groups : 1) * G;
+  p.pre_r = rows_per_wave(pre_rows, p.dp);
+  p.pre_tiles = (int)std::min(most((int64_t)x.n_groups * kv), (pre_rows + 16 * p.pre_r - 1) / (16 * p.pre_r));
+  // enough workgroups for two on each of 256 compute units, but splits of
+  // 256 tokens at least
+  auto splits = [&](int64_t items, int64_t tokens) {
+    const int64_t want = (512 + items - 1) / std::max<int64_t>(1, items);
+    const int64_t room = std::max<int64_t>(1, tokens / (kMinTiles * kTile));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, room), 64));
+  };
+  p.pre_splits = x.n_groups ? splits((int64_t)x.n_groups * kv * p.pre_tiles, shared ? x.max_prefix : 0) : 0;
+  p.rest_splits = splits((int64_t)std::max(1, x.n_seqs) * kv * p.rest_tiles,
+                         std::max(0, x.max_len - (shared ? x.max_prefix : 0)));
+  p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + 4;
+  return p;
 }
 
 Attn view(const cg_paged_cache& c, const cg_attention& x) {
@@ -131,15 +730,16 @@ Attn view(const cg_paged_cache& c, const cg_attention& x) {
   a.N = c.num_pages;
   a.R = c.n_rows;
   a.B = c.max_blocks;
-  const int64_t layer = (int64_t)x.layer * c.num_pages * c.page_tokens * c.channels;
-  a.k = (const uint16_t*)c.k_pool_dev + layer;
-  a.v = (const uint16_t*)c.v_pool_dev + layer;
+  const int64_t layer = (int64_t)x.layer * c.num_pages * c.page_tokens * c.channels * 2;
+  a.k = (const char*)c.k_pool_dev + layer;
+  a.v = (const char*)c.v_pool_dev + layer;
   a.tables = c.tables_dev;
   a.lens = c.lens_dev;
   a.status = c.status_dev;
   a.H = x.n_heads;
   a.d = x.head_dim;
-  a.G = x.n_heads / (c.channels / x.head_dim);
+  a.kv = c.channels / x.head_dim;
+  a.G = x.n_heads / a.kv;
   a.scale = x.scale;
   a.n_seqs = x.n_seqs;
   a.n_q = x.n_q;
@@ -166,7 +766,7 @@ extern "C" {
 int cg_attention_workspace(const cg_paged_cache* c, const cg_attention* a, size_t* bytes) {
   if (int rc = check_attention(c, a)) return rc;
   if (!bytes) return fail(CG_E_INVAL, "bytes is NULL");
-  *bytes = 16;
+  *bytes = 4 * plan_of(*c, *a).words;
   return CG_OK;
 }
 
@@ -191,7 +791,25 @@ int cg_attention_prefix_async(const cg_paged_cache* c, const cg_attention* a, vo
   if (workspace_bytes < need) return fail(CG_E_CAPACITY, "workspace too small");
   DeviceGuard dg(c->device);
   if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
-  k_attention<<<dim3(a->n_q, a->n_heads), 256, 0, (hipStream_t)stream>>>(view(*c, *a));
+  const Plan p = plan_of(*c, *a);
+  Attn v = view(*c, *a);
+  v.pre_splits = p.pre_splits;
+  v.rest_splits = p.rest_splits;
+  v.pre_tiles = p.pre_tiles;
+  v.rest_tiles = p.rest_tiles;
+  v.pre_groups = p.pre_groups;
+  v.part = (float*)workspace_dev;
+  v.ml = v.part + (size_t)(p.pre_splits + p.rest_splits) * a->n_q * a->n_heads * a->head_dim;
+  const int64_t pre = (int64_t)p.pre_groups * p.pre_splits * p.pre_tiles * v.kv;
+  const int64_t rest = (int64_t)a->n_seqs * p.rest_splits * p.rest_tiles * v.kv;
+  hipStream_t st = (hipStream_t)stream;
+  if (p.pre_r == p.rest_r) {
+    launch(p.dp, p.pre_r, v, 0, pre + rest, st);
+  } else {
+    launch(p.dp, p.pre_r, v, 0, pre, st);
+    launch(p.dp, p.rest_r, v, pre, pre + rest, st);
+  }
+  k_join<<<a->n_q, kThreads, 0, st>>>(v);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? CG_OK : hip_fail(e, "attention");
 }

@@ -213,7 +213,8 @@ def attention(c: Cache, layer, q, scale, rows, q_starts, group_starts=None, pref
                 pre = int(prefix_lens[g])
                 f = int(group_starts[g])
                 first = f if rows is None else int(rows[f])
-        if pre < 0 or (pre > 0 and pre + b - a > n):
+        if pre < 0 or (pre > 0 and (pre + b - a > n or not row_ok(c, first) or not len_ok(c, c.lens[first])
+                                    or c.lens[first] < pre)):
             ok = False
         if not ok:
             status |= REFUSED
