@@ -44,7 +44,7 @@ struct Attn {
   int64_t q_stride, out_stride;
   // the launch: splits of a prefix and of a sequence's rest, row tiles that have
   // workgroups of their own (there may be more)
-  int pre_splits, rest_splits, pre_tiles, rest_tiles, pre_groups;
+  int pre_splits, rest_splits, pre_tiles, rest_tiles, pre_groups, join;
   float* part;  // [pre_splits + rest_splits][n_q][H][d] sums, not divided
   float* ml;    // the same with [2]: reference exponent m, sum of weights l
 };
@@ -178,19 +178,21 @@ __device__ __forceinline__ int tile_pages(const Source& s, int t0) {
   return t >= s.lo && t < s.hi ? s.list[(t >> s.shift) - s.block0] : -1;
 }
 
-// Issues the loads of the tile at t0 of a pool (pointing at the kv head's channels)
-// to LDS address lds.  full: every token exists.  If the rows of a load also lie in
-// one page and the head fills the tile's width, its address is scalar but for a
-// lane's fixed offset.  Otherwise rows of tokens that do not exist, and chunks
-// behind the head's, keep what they held.  A full tile is NI loads either way.
-template <int DP>
+// Issues loads i0 .. i0 + N - 1 of the NI of the tile at t0 of a pool (pointing at the
+// kv head's channels) to the tile at LDS address lds.  Always N loads, so that
+// wait_loads() can count them: for tokens that do not exist some row of the pool is
+// read instead.  full: every token exists; if the rows of a load also lie in one
+// page and the head fills the tile's width, its address is scalar but for a lane's
+// fixed offset.  Chunks behind the head's keep what they held.
+template <int DP, int N>
 __device__ __forceinline__ void load_tile(const Source& s, const char* pool, uint32_t lds, int t0,
-                                          int pages, bool full) {
+                                          int pages, bool full, int i0 = 0) {
   using Ge = Geo<DP>;
   if (full && s.pmask >= Ge::RPI - 1 && s.nc == Ge::NC) {
     const int lane = threadIdx.x & 63, lrow = lane / Ge::NC, lc = lane % Ge::NC;
 #pragma unroll
-    for (int i = 0; i < Ge::NI; i++) {
+    for (int j = 0; j < N; j++) {
+      const int i = i0 + j;
       const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(pages, i * Ge::RPI);
       const char* base = pool + (uint64_t)page * s.page_bytes +
                          (uint64_t)(uint32_t)((t0 + i * Ge::RPI) & s.pmask) * s.row_bytes;
@@ -200,13 +202,13 @@ __device__ __forceinline__ void load_tile(const Source& s, const char* pool, uin
   } else {
     const int lane = rare_lane(), lrow = lane / Ge::NC, lc = lane % Ge::NC;
 #pragma unroll 1
-    for (int i = 0; i < Ge::NI; i++) {
+    for (int i = i0; i < i0 + N; i++) {
       const int row = i * Ge::RPI + lrow;
       const int page = __shfl(pages, row);
       const int c = lc ^ swizzle<DP>(row);
       const char* addr = pool + (uint64_t)(uint32_t)max(page, 0) * s.page_bytes +
                          (uint64_t)(uint32_t)((t0 + row) & s.pmask) * s.row_bytes + c * 16;
-      if (c < s.nc && page >= 0) load_lds(lds + i * 1024, addr);
+      if (c < s.nc) load_lds(lds + i * 1024, addr);
     }
   }
 }
@@ -235,6 +237,16 @@ __device__ __forceinline__ bool prepare_values(char* tile, int pages) {
   return __any(odd);
 }
 
+struct Item {
+  int head;                 // kv head
+  int q0, rows;             // first query; rows = queries x heads of the kv head
+  int lo, hi;               // tokens
+  int lim0;                 // tokens that the first query sees (each later one 1 more)
+  int trow;                 // table row
+  int splits, split, slot0; // of the tokens; first partial of this kind
+  int row_tile, row_tiles;  // this workgroup's first row tile and its stride
+};
+
 // ---------------------------------------------------------------------------
 // One wave's part: 16 RT query rows against its tiles
 // ---------------------------------------------------------------------------
@@ -259,6 +271,30 @@ struct Wave {
       l[r] = 0.0f;
 #pragma unroll
       for (int b = 0; b < NB; b++) o[r][b] = f4{0, 0, 0, 0};
+    }
+  }
+
+  // Queries of rows row0 .. row0 + 16 RT - 1 (row = query x heads of the kv head +
+  // head); rows past the item's are zeros that see everything.
+  __device__ __forceinline__ void load_queries(const Attn& a, const Item& it, int row0) {
+    const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    // negated queries stand for a negative scale, queries of 0 for a scale of 0, so
+    // that the largest product has the largest score
+    const uint32_t keep = a.scale == 0 ? 0 : 0xFFFFFFFFu, flip = a.scale < 0 ? 0x80008000u : 0;
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+      const int row = row0 + r * 16 + n;
+      const bool in = row < it.rows;
+      const int qi = in ? row / a.G : 0, h = it.head * a.G + (in ? row % a.G : 0);
+      const uint16_t* from = a.q + (it.q0 + qi) * a.q_stride + (int64_t)h * a.d;
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++) {
+        const int ch = ks * 4 + g;
+        uint4 z = in && ch < a.d / 8 ? *(const uint4*)(from + ch * 8) : uint4{0, 0, 0, 0};
+        z = uint4{(z.x & keep) ^ flip, (z.y & keep) ^ flip, (z.z & keep) ^ flip, (z.w & keep) ^ flip};
+        q[r][ks] = __builtin_bit_cast(h8, z);
+      }
+      lim[r] = in ? min(it.hi, it.lim0 + qi) : it.hi;
     }
   }
 
@@ -383,129 +419,147 @@ struct Wave {
 // ---------------------------------------------------------------------------
 // One workgroup: a tile of rows against a split of the tokens
 // ---------------------------------------------------------------------------
-struct Item {
-  int head;                 // kv head
-  int q0, rows;             // first query; rows = queries x heads of the kv head
-  int lo, hi;               // tokens
-  int lim0;                 // tokens that the first query sees (each later one 1 more)
-  int trow;                 // table row
-  int splits, split, slot0; // of the tokens; first partial of this kind
-  int row_tile, row_tiles;  // this workgroup's first row tile and its stride
-};
+constexpr int kStages = 4;  // of the ring of tiles that the waves share
 
 template <int DP>
 struct Shared {
-  // each wave's tile of K and of V; then the sums of the waves
-  __attribute__((aligned(1024))) char tile[kWaves][2][Geo<DP>::BYTES];
+  // each wave's tile of K and of V, or a ring of tiles of both; then the sums of the waves
+  __attribute__((aligned(1024))) char tile[kStages][2][Geo<DP>::BYTES];
   int32_t list[kListPages];
   float m[kWaves][64], l[kWaves][64], scale[kWaves][64];
 };
+static_assert(kStages == kWaves, "one layout for both uses");
 
-// The waves take the split's tiles in turn and share nothing until the end.  Each
-// has room for one tile of K and one of V: the next K is on its way while the
-// weights and the values are computed, the next V while the scores are.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char*)(char*)p);
+}
+
+// What both ways of working share: the split's tiles, the pages of a stretch of them.
+template <int DP>
+struct Tokens {
+  Source src;
+  const char *kp, *vp;
+  int first, last;  // tiles
+  int list_tiles;   // tiles whose pages the list holds, wherever in a page they begin
+  bool bad;         // a page of the present stretch is outside the pool
+
+  __device__ __forceinline__ bool start(const Attn& a, const Item& it, Shared<DP>& sh) {
+    const Split sp = split_of(it.lo, it.hi, it.splits);
+    if (it.split >= sp.used) return false;
+    first = sp.tile0 + it.split * sp.per;
+    last = min(first + sp.per, sp.tile0 + sp.tiles);
+    const uint32_t row_bytes = (uint32_t)a.C * 2;
+    src = Source{sh.list, 0, it.lo, it.hi, a.shift, a.P - 1, a.d / 8, row_bytes * (uint32_t)a.P, row_bytes};
+    kp = a.k + it.head * a.d * 2;
+    vp = a.v + it.head * a.d * 2;
+    list_tiles = (int)((int64_t)(kListPages - 1) * a.P / kTile) - 1;
+    return true;
+  }
+  // the chunks behind the head's row stay zero
+  __device__ __forceinline__ void clear_tiles(const Attn& a, Shared<DP>& sh) {
+    if (a.d == DP) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < (int)sizeof(sh.tile) / 16; i += kThreads)
+      ((uint4*)sh.tile)[i] = uint4{0, 0, 0, 0};
+  }
+  // pages of the tokens of tiles [base, stop)
+  __device__ __forceinline__ void stretch(const Attn& a, const Item& it, Shared<DP>& sh, int base,
+                                          int stop) {
+    const int b0 = max(base * kTile, it.lo) >> a.shift;
+    const int b1 = (min(stop * kTile, it.hi) - 1) >> a.shift;
+    __syncthreads();  // the list and the tiles are free
+    bad = false;
+    for (int i = threadIdx.x; i <= b1 - b0; i += kThreads) {
+      const int page = a.tables[(int64_t)it.trow * a.B + b0 + i];
+      const bool ok = page >= 0 && page < a.N;
+      sh.list[i] = ok ? page : -1;
+      bad |= !ok;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) atomicOr(a.status, kBadPage);
+    src.block0 = b0;
+  }
+  __device__ __forceinline__ bool full(int tile) const {  // every token of the tile exists
+    return !bad && tile * kTile >= src.lo && (tile + 1) * kTile <= src.hi;
+  }
+};
+
+// The exponent's scale: scores are c (q . k) in units of log 2.
+__device__ __forceinline__ float log2_scale(const Attn& a) {
+  return a.scale == 0 ? 1.0f : fminf(fabsf(a.scale) * 1.44269504088896341f, 3.4e38f);
+}
+// tokens that the query of a row sees
+__device__ __forceinline__ int row_lim(const Attn& a, const Item& it, int row) {
+  return min(it.hi, it.lim0 + min(row, it.rows - 1) / a.G);
+}
+__device__ __forceinline__ int64_t part_at(const Attn& a, const Item& it, int row) {
+  return ((int64_t)(it.slot0 + it.split) * a.n_q + it.q0 + row / a.G) * a.H + it.head * a.G + row % a.G;
+}
+
+// One tile whose K and V have landed: weights from the scores, then the values.
+// all: every query of the wave sees the whole tile.
 template <int DP, int RT>
-__device__ __forceinline__ void run_rows(const Attn& a, const Item& it, Shared<DP>& sh) {
+__device__ __forceinline__ void finish_tile(Wave<DP, RT>& w, f4 (&s)[RT][2], h8 (&p)[RT], char* vt,
+                                            int t0, int pages, bool all) {
+  if (!all && prepare_values<DP>(vt, pages)) w.values_one_by_one(vt, p, t0);
+  else w.values(vt, p);
+}
+
+// Few rows: every wave holds all 16 RT of a row tile and takes the split's token
+// tiles in turn; the waves share nothing until the end.  Each has room for one tile
+// of K and one of V: the next K is on its way while the weights and the values are
+// computed, the next V while the scores are.
+template <int DP, int RT>
+__device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<DP>& sh) {
   using Ge = Geo<DP>;
   using W = Wave<DP, RT>;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Split sp = split_of(it.lo, it.hi, it.splits);
-  if (it.split >= sp.used) return;
-  const int first = sp.tile0 + it.split * sp.per;
-  const int last = min(first + sp.per, sp.tile0 + sp.tiles);  // tiles [first, last)
-  const uint32_t row_bytes = (uint32_t)a.C * 2;
-  Source src{sh.list, 0, it.lo, it.hi, a.shift, a.P - 1, a.d / 8, row_bytes * (uint32_t)a.P, row_bytes};
-  const char *kp = a.k + it.head * a.d * 2, *vp = a.v + it.head * a.d * 2;
+  Tokens<DP> tk;
+  if (!tk.start(a, it, sh)) return;
   char *kt = sh.tile[wave][0], *vt = sh.tile[wave][1];
-  const uint32_t klds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char*)kt);
-  const uint32_t vlds = klds + Ge::BYTES;
-  // negated queries stand for a negative scale, queries of 0 for a scale of 0, so
-  // that the largest product has the largest score and c is positive
-  const float c = a.scale == 0 ? 1.0f : fminf(fabsf(a.scale) * 1.44269504088896341f, 3.4e38f);
-  const uint32_t keep = a.scale == 0 ? 0 : 0xFFFFFFFFu, flip = a.scale < 0 ? 0x80008000u : 0;
+  const uint32_t klds = lds_address(kt), vlds = klds + Ge::BYTES;
+  const float c = log2_scale(a);
   const int row_tiles = (it.rows + 16 * RT - 1) / (16 * RT);
-  // tiles whose pages the list holds, wherever in a page they begin
-  const int list_tiles = (int)((int64_t)(kListPages - 1) * a.P / kTile) - 1;
 
   for (int rt = it.row_tile; rt < row_tiles; rt += it.row_tiles) {
     W w;
     w.clear();
-    int min_lim = it.hi, max_lim = it.lo;
-#pragma unroll
-    for (int r = 0; r < RT; r++) {
-      const int row = rt * 16 * RT + r * 16 + n;
-      const bool in = row < it.rows;
-      const int qi = in ? row / a.G : 0, h = it.head * a.G + (in ? row % a.G : 0);
-      const uint16_t* src_q = a.q + (it.q0 + qi) * a.q_stride + (int64_t)h * a.d;
-#pragma unroll
-      for (int ks = 0; ks < W::KS; ks++) {
-        const int ch = ks * 4 + g;
-        uint4 z = in && ch < src.nc ? *(const uint4*)(src_q + ch * 8) : uint4{0, 0, 0, 0};
-        z = uint4{(z.x & keep) ^ flip, (z.y & keep) ^ flip, (z.z & keep) ^ flip, (z.w & keep) ^ flip};
-        w.q[r][ks] = __builtin_bit_cast(h8, z);
-      }
-      w.lim[r] = in ? min(it.hi, it.lim0 + qi) : it.hi;
-      min_lim = min(min_lim, w.lim[r]);
-      if (in) max_lim = max(max_lim, w.lim[r]);
-    }
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) {
-      min_lim = min(min_lim, __shfl_xor(min_lim, x));
-      max_lim = max(max_lim, __shfl_xor(max_lim, x));
-    }
-    min_lim = __builtin_amdgcn_readfirstlane(min_lim);
-    max_lim = __builtin_amdgcn_readfirstlane(max_lim);
-    const int end = min(last, (max_lim + kTile - 1) / kTile);  // later tiles: nobody sees them
-    if (a.d < DP) {  // the chunks behind the head's row stay zero
-      __syncthreads();
-      for (int i = tid; i < (int)sizeof(sh.tile) / 16; i += kThreads)
-        ((uint4*)sh.tile)[i] = uint4{0, 0, 0, 0};
-    }
-    for (int base = first; base < end; base += list_tiles) {
-      const int stop = min(base + list_tiles, end);
-      // pages of the tokens of tiles [base, stop)
-      const int b0 = max(base * kTile, it.lo) >> a.shift;
-      const int b1 = (min(stop * kTile, it.hi) - 1) >> a.shift;
-      __syncthreads();  // the list and the tiles are free
-      bool bad = false;
-      for (int i = tid; i <= b1 - b0; i += kThreads) {
-        const int page = a.tables[(int64_t)it.trow * a.B + b0 + i];
-        const bool ok = page >= 0 && page < a.N;
-        sh.list[i] = ok ? page : -1;
-        bad |= !ok;
-      }
-      bad = __syncthreads_or(bad);
-      if (bad && tid == 0) atomicOr(a.status, kBadPage);
-      src.block0 = b0;
+    w.load_queries(a, it, rt * 16 * RT);
+    const int min_lim = row_lim(a, it, rt * 16 * RT);
+    const int max_lim = row_lim(a, it, (rt + 1) * 16 * RT - 1);
+    const int end = min(tk.last, (max_lim + kTile - 1) / kTile);  // later tiles: nobody sees them
+    tk.clear_tiles(a, sh);
+    for (int base = tk.first; base < end; base += tk.list_tiles) {
+      const int stop = min(base + tk.list_tiles, end);
+      tk.stretch(a, it, sh, base, stop);
       // one round more than there are tiles: the first only starts the loads
       int tile = base + wave - kWaves, pages = -1;
-      bool have = false, is_full = false;
+      bool have = false, all = false;
       while (have || tile + kWaves < stop) {
         const int t0 = tile * kTile, next = tile + kWaves;
         const bool more = next < stop;
-        const bool next_full = more && !bad && next * kTile >= it.lo && (next + 1) * kTile <= min_lim;
-        const int next_pages = more ? tile_pages(src, next * kTile) : -1;
+        const bool full = more && tk.full(next);
+        const int next_pages = more ? tile_pages(tk.src, next * kTile) : -1;
         f4 s[RT][2];
         if (have) {
-          if (is_full) wait_loads<Ge::NI>(); else wait_loads<0>();
+          wait_loads<Ge::NI>();
           w.scores(kt, s);
           wait_lds();
         }
-        if (more) load_tile<DP>(src, kp, klds, next * kTile, next_pages, next_full);
+        if (more) load_tile<DP, Ge::NI>(tk.src, tk.kp, klds, next * kTile, next_pages, full);
         if (have) {
           h8 p[RT];
-          if (!is_full) w.mask(s, t0, pages);
+          if (!all) w.mask(s, t0, pages);
           w.weights(s, c, p);
-          if (is_full && next_full) wait_loads<Ge::NI>(); else wait_loads<0>();
-          if (!is_full && prepare_values<DP>(vt, pages)) w.values_one_by_one(vt, p, t0);
-          else w.values(vt, p);
+          if (more) wait_loads<Ge::NI>(); else wait_loads<0>();
+          finish_tile<DP, RT>(w, s, p, vt, t0, pages, all);
           wait_lds();
         }
-        if (more) load_tile<DP>(src, vp, vlds, next * kTile, next_pages, next_full);
+        if (more) load_tile<DP, Ge::NI>(tk.src, tk.vp, vlds, next * kTile, next_pages, full);
         tile = next;
         pages = next_pages;
-        is_full = next_full;
+        all = full && (next + 1) * kTile <= min_lim;
         have = more;
       }
     }
@@ -536,8 +590,7 @@ __device__ __forceinline__ void run_rows(const Attn& a, const Item& it, Shared<D
       }
       const int row = rt * 16 * RT + tid;
       if (row < it.rows) {
-        const int64_t at = ((int64_t)(it.slot0 + it.split) * a.n_q + it.q0 + row / a.G) * a.H +
-                           it.head * a.G + row % a.G;
+        const int64_t at = part_at(a, it, row);
         a.ml[2 * at] = m;
         a.ml[2 * at + 1] = l;
       }
@@ -566,12 +619,90 @@ __device__ __forceinline__ void run_rows(const Attn& a, const Item& it, Shared<D
 #pragma unroll
         for (int y = 0; y < kWaves; y++)
           x += sh.scale[y][row] * sums[(y * 16 * RT + row) * kQuads + ((quad + row) & (kQuads - 1))];
-        const int64_t at = ((int64_t)(it.slot0 + it.split) * a.n_q + it.q0 + gr / a.G) * a.H +
-                           it.head * a.G + gr % a.G;
-        *(f4*)(a.part + at * a.d + ch) = x;
+        *(f4*)(a.part + part_at(a, it, gr) * a.d + ch) = x;
       }
     }
     __syncthreads();  // m, l and scale are free
+  }
+}
+
+// Many rows: a wave holds 16 RT of the tile's 64 RT rows, all waves read the same
+// token tiles from a ring; each loads a quarter of a tile, kStages - 1 tiles ahead,
+// and one barrier a tile both publishes it and frees the slot that is filled next.
+template <int DP, int RT>
+__device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<DP>& sh) {
+  using Ge = Geo<DP>;
+  using W = Wave<DP, RT>;
+  constexpr int kMine = Ge::NI / kWaves;  // loads of a wave for K, and for V
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Tokens<DP> tk;
+  if (!tk.start(a, it, sh)) return;
+  const uint32_t lds = lds_address(sh.tile);
+  const float c = log2_scale(a);
+  const int tile_rows = 16 * RT * kWaves, row_tiles = (it.rows + tile_rows - 1) / tile_rows;
+
+  for (int rt = it.row_tile; rt < row_tiles; rt += it.row_tiles) {
+    const int row0 = rt * tile_rows + wave * 16 * RT;
+    W w;
+    w.clear();
+    w.load_queries(a, it, row0);
+    const int min_lim = row_lim(a, it, row0);
+    const int max_lim = row_lim(a, it, (rt + 1) * tile_rows - 1);
+    const int end = min(tk.last, (max_lim + kTile - 1) / kTile);
+    tk.clear_tiles(a, sh);
+    for (int base = tk.first; base < end; base += tk.list_tiles) {
+      const int stop = min(base + tk.list_tiles, end);
+      tk.stretch(a, it, sh, base, stop);
+      // the first kStages - 1 rounds only start loads
+      for (int tile = base - (kStages - 1); tile < stop; tile++) {
+        const int next = tile + kStages - 1;
+        if (tile >= base) {
+          const int left = stop - 1 - tile;  // tiles behind this one whose loads are under way
+          if (left >= 2) wait_loads<4 * kMine>();
+          else if (left == 1) wait_loads<2 * kMine>();
+          else wait_loads<0>();
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        }
+        if (next < stop) {
+          const int slot = (next - base) & (kStages - 1);
+          const uint32_t to = lds + slot * 2 * Ge::BYTES;
+          const int next_pages = tile_pages(tk.src, next * kTile);
+          const bool full = tk.full(next);
+          load_tile<DP, kMine>(tk.src, tk.kp, to, next * kTile, next_pages, full, wave * kMine);
+          load_tile<DP, kMine>(tk.src, tk.vp, to + Ge::BYTES, next * kTile, next_pages, full, wave * kMine);
+        }
+        if (tile >= base) {
+          const int slot = (tile - base) & (kStages - 1), t0 = tile * kTile;
+          const bool all = tk.full(tile) && t0 + kTile <= min_lim;
+          const int pages = all ? 0 : tile_pages(tk.src, t0);
+          f4 s[RT][2];
+          h8 p[RT];
+          w.scores(sh.tile[slot][0], s);
+          if (!all) w.mask(s, t0, pages);
+          w.weights(s, c, p);
+          finish_tile<DP, RT>(w, s, p, sh.tile[slot][1], t0, pages, all);
+          wait_lds();  // read before the barrier that frees the slot
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+      float l = w.l[r];
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      const int row = row0 + r * 16 + n;
+      if (row >= it.rows) continue;
+      const int64_t at = part_at(a, it, row);
+      if (g == 0) {
+        a.ml[2 * at] = w.m[r];
+        a.ml[2 * at + 1] = l;
+      }
+#pragma unroll
+      for (int b = 0; b < W::NB; b++)
+        if (b * 16 + g * 4 < a.d) *(f4*)(a.part + at * a.d + b * 16 + g * 4) = w.o[r][b];
+    }
   }
 }
 
@@ -622,74 +753,106 @@ __device__ __forceinline__ bool item_of(const Attn& a, int w, Item& it) {
   return true;
 }
 
-template <int DP, int RT>
-__global__ __launch_bounds__(kThreads, DP == 256 || RT == 4 ? 1 : 2) void k_attention(Attn a, int first,
-                                                                                      int end) {
+template <int DP, int RT, bool kRing>
+__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void k_attention(Attn a, int first, int end) {
   __shared__ Shared<DP> sh;
   for (int w = first + blockIdx.x; w < end; w += gridDim.x) {
     Item it;
-    if (item_of(a, w, it)) run_rows<DP, RT>(a, it, sh);
+    if (!item_of(a, w, it)) continue;
+    if (kRing) run_ring<DP, RT>(a, it, sh);
+    else run_split<DP, RT>(a, it, sh);
   }
 }
 
-// Joins the partial sums of a query's heads: a workgroup per query, d / 4 lanes a head.
+// Joins the partial sums of one query's heads.  A head takes d / 4 lanes by a.join
+// parts, which add up every join-th split each: with many splits it is the number of
+// loads under way that counts.
 __global__ __launch_bounds__(kThreads) void k_join(Attn a) {
-  const int qi = blockIdx.x;
+  __shared__ f4 sums[kThreads];
+  __shared__ float ls[kThreads];
+  const int qi = blockIdx.x, tid = threadIdx.x;
   const int s = last_at_most(a.q_starts, a.n_seqs, qi);
   if (s < 0 || qi < a.q_starts[s] || qi >= a.q_starts[s + 1]) return;
   const Seq q = sequence(a, s);
-  if (!q.ok && threadIdx.x == 0) atomicOr(a.status, kRefused);
+  if (!q.ok && tid == 0) atomicOr(a.status, kRefused);
   const int pre = q.ok ? split_of(0, q.pre, a.pre_splits).used : 0;
-  const int rest = q.ok ? split_of(q.pre, q.len, a.rest_splits).used : 0;
-  const int quads = a.d / 4;
-  for (int i = threadIdx.x; i < a.H * quads; i += kThreads) {
-    const int h = i / quads, ch = (i % quads) * 4;
-    float m = -__builtin_inff(), l = 0.0f;
-    f4 o{0, 0, 0, 0};
-    for (int x = 0; x < pre + rest; x++) {
-      const int slot = x < pre ? x : a.pre_splits + x - pre;
-      const int64_t at = ((int64_t)slot * a.n_q + qi) * a.H + h;
-      const float mx = a.ml[2 * at], lx = a.ml[2 * at + 1];
-      if (lx == 0.0f) continue;  // weighed nothing
-      const f4 ox = *(const f4*)(a.part + at * a.d + ch);
-      const float nm = fmaxf(m, mx);
-      const float f = m == nm ? 1.0f : __builtin_amdgcn_exp2f(m - nm);
-      const float fx = mx == nm ? 1.0f : __builtin_amdgcn_exp2f(mx - nm);
-      o = o * f + ox * fx;
-      l = l * f + lx * fx;
-      m = nm;
+  const int used = pre + (q.ok ? split_of(q.pre, q.len, a.rest_splits).used : 0);
+  const int quads = a.d / 4, unit = tid / quads, quad = tid % quads;
+  const int heads = kThreads / quads / a.join;  // of a workgroup
+  const int part = unit % a.join, hl = unit / a.join, h = blockIdx.y * heads + hl;
+  const bool in = hl < heads && h < a.H;
+  const int64_t slot_step = (int64_t)a.n_q * a.H, at0 = (int64_t)qi * a.H + h;
+  auto at = [&](int x) { return at0 + slot_step * (x < pre ? x : a.pre_splits + x - pre); };
+  // splits that weighed nothing have l = 0 and no reference exponent
+  float m = -__builtin_inff(), l = 0.0f;
+  f4 o{0, 0, 0, 0};
+  if (in) {
+#pragma unroll 8
+    for (int x = 0; x < used; x++) m = fmaxf(m, a.ml[2 * at(x)]);
+#pragma unroll 4
+    for (int x = part; x < used; x += a.join) {
+      const float mx = a.ml[2 * at(x)], lx = a.ml[2 * at(x) + 1];
+      const f4 ox = *(const f4*)(a.part + at(x) * a.d + quad * 4);
+      const float f = mx == m ? 1.0f : __builtin_amdgcn_exp2f(mx - m);
+      // nothing weighed: what the split left in o is not looked at; no number stays one
+      if (lx != 0.0f) {
+        o += ox * (mx == -__builtin_inff() ? 1.0f : f);
+        l += lx * (mx == -__builtin_inff() ? 1.0f : f);
+      }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    ushort4 r;
-    r.x = float_to_half_bits(o[0] * inv);
-    r.y = float_to_half_bits(o[1] * inv);
-    r.z = float_to_half_bits(o[2] * inv);
-    r.w = float_to_half_bits(o[3] * inv);
-    *(ushort4*)(a.out + qi * a.out_stride + (int64_t)h * a.d + ch) = r;
-    if (ch == 0 && a.lse)
-      a.lse[(int64_t)qi * a.H + h] = l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945309f;
   }
+  if (a.join > 1) {
+    sums[tid] = o;
+    ls[tid] = l;
+    __syncthreads();
+    if (!in || part) return;
+    for (int x = 1; x < a.join; x++) {
+      o += sums[tid + x * quads];
+      l += ls[tid + x * quads];
+    }
+  } else if (!in) {
+    return;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  ushort4 r;
+  r.x = float_to_half_bits(o[0] * inv);
+  r.y = float_to_half_bits(o[1] * inv);
+  r.z = float_to_half_bits(o[2] * inv);
+  r.w = float_to_half_bits(o[3] * inv);
+  *(ushort4*)(a.out + qi * a.out_stride + (int64_t)h * a.d + quad * 4) = r;
+  if (quad == 0 && a.lse)
+    a.lse[(int64_t)qi * a.H + h] = l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945309f;
 }
 
 // How many splits and row tiles the launch has, from the call's numbers alone.
 struct Plan {
-  int dp, pre_splits, rest_splits, pre_tiles, rest_tiles, pre_r, rest_r, pre_groups;
+  int dp, pre_splits, rest_splits, pre_tiles, rest_tiles, pre_mode, rest_mode, pre_groups;
   size_t words;
 };
 
-int rows_per_wave(int64_t rows, int dp) {  // in 16-row tiles
-  return rows <= 16 ? 1 : rows <= 32 || dp == 256 ? 2 : 4;
-}
+// How a launch's waves hold rows: all of 16 or 32, or a quarter each of 64 or 128.
+enum { kRows16 = 0, kRows32 = 1, kRows64 = 2, kRows128 = 3 };
+int rows_of(int mode) { return 16 << mode; }
 
 // items first .. end - 1 of the launch's list
-void launch(int dp, int r, const Attn& a, int64_t first, int64_t end, hipStream_t st) {
+void launch(int dp, int mode, const Attn& a, int64_t first, int64_t end, hipStream_t st) {
   if (end <= first) return;
   const int grid = (int)std::min<int64_t>(end - first, 1 << 22);
-#define GO(DP, RT) k_attention<DP, RT><<<grid, kThreads, 0, st>>>(a, (int)first, (int)end)
-  if (dp == 64) { if (r == 1) GO(64, 1); else if (r == 2) GO(64, 2); else GO(64, 4); }
-  else if (dp == 128) { if (r == 1) GO(128, 1); else if (r == 2) GO(128, 2); else GO(128, 4); }
-  else { if (r == 1) GO(256, 1); else GO(256, 2); }
+#define GO(DP, RT, RING) k_attention<DP, RT, RING><<<grid, kThreads, 0, st>>>(a, (int)first, (int)end)
+#define BY_MODE(DP)                            \
+  if (mode == kRows16) GO(DP, 1, false);       \
+  else if (mode == kRows32) GO(DP, 2, false);  \
+  else if (mode == kRows64) GO(DP, 1, true);   \
+  else GO(DP, 2, true)
+  if (dp == 64) { BY_MODE(64); }
+  else if (dp == 128) { BY_MODE(128); }
+  else { BY_MODE(256); }
+#undef BY_MODE
 #undef GO
+}
+
+int mode_of(int64_t rows) {
+  return rows <= 16 ? kRows16 : rows <= 32 ? kRows32 : rows <= 64 ? kRows64 : kRows128;
 }
 
 Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
@@ -700,14 +863,16 @@ Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
   // all heads, sequences and splits, fits 31 bits
   auto most = [&](int64_t items) { return std::max<int64_t>(1, (1 << 22) / std::max<int64_t>(1, items)); };
   const int64_t rows = (int64_t)std::max(1, std::min(x.max_q, x.n_q)) * G;
-  p.rest_r = rows_per_wave(rows, p.dp);
-  p.rest_tiles = (int)std::min(most((int64_t)x.n_seqs * kv), (rows + 16 * p.rest_r - 1) / (16 * p.rest_r));
+  p.rest_mode = mode_of(rows);
+  const int rest_rows = rows_of(p.rest_mode);
+  p.rest_tiles = (int)std::min(most((int64_t)x.n_seqs * kv), (rows + rest_rows - 1) / rest_rows);
   const bool shared = x.n_groups > 0 && x.max_prefix > 0;
   p.pre_groups = x.n_groups;
   // rows of an average group
   const int64_t pre_rows = std::max<int64_t>(1, x.n_groups ? (x.n_q + x.n_groups - 1) / x.n_groups : 1) * G;
-  p.pre_r = rows_per_wave(pre_rows, p.dp);
-  p.pre_tiles = (int)std::min(most((int64_t)x.n_groups * kv), (pre_rows + 16 * p.pre_r - 1) / (16 * p.pre_r));
+  p.pre_mode = mode_of(pre_rows);
+  const int pre_tile = rows_of(p.pre_mode);
+  p.pre_tiles = (int)std::min(most((int64_t)x.n_groups * kv), (pre_rows + pre_tile - 1) / pre_tile);
   // enough workgroups for two on each of 256 compute units, but splits of
   // 256 tokens at least
   auto splits = [&](int64_t items, int64_t tokens) {
@@ -803,13 +968,16 @@ int cg_attention_prefix_async(const cg_paged_cache* c, const cg_attention* a, vo
   const int64_t pre = (int64_t)p.pre_groups * p.pre_splits * p.pre_tiles * v.kv;
   const int64_t rest = (int64_t)a->n_seqs * p.rest_splits * p.rest_tiles * v.kv;
   hipStream_t st = (hipStream_t)stream;
-  if (p.pre_r == p.rest_r) {
-    launch(p.dp, p.pre_r, v, 0, pre + rest, st);
+  if (p.pre_mode == p.rest_mode) {
+    launch(p.dp, p.pre_mode, v, 0, pre + rest, st);
   } else {
-    launch(p.dp, p.pre_r, v, 0, pre, st);
-    launch(p.dp, p.rest_r, v, pre, pre + rest, st);
+    launch(p.dp, p.pre_mode, v, 0, pre, st);
+    launch(p.dp, p.rest_mode, v, pre, pre + rest, st);
   }
-  k_join<<<a->n_q, kThreads, 0, st>>>(v);
+  const int total = p.pre_splits + p.rest_splits;
+  v.join = std::min(total <= 2 ? 1 : total <= 8 ? 2 : 8, kThreads / (v.d / 4));
+  const int heads = kThreads / (v.d / 4) / v.join;
+  k_join<<<dim3(a->n_q, (v.H + heads - 1) / heads), kThreads, 0, st>>>(v);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? CG_OK : hip_fail(e, "attention");
 }
