@@ -213,25 +213,33 @@ __device__ __forceinline__ void load_tile(const Source& s, const char* pool, uin
   }
 }
 
-// Before the values of a tile that not every query sees whole: rows of tokens that
-// do not exist become zeros (their weights are zero, but what an earlier tile left
-// there might be no number).  Returns whether the tile holds a value that is no
-// finite number.
+// Before the values of a tile of which some token does not exist or some query does
+// not see some token: a value there that is no finite number must not meet the
+// zero weight of such a query.  Rows of tokens that do not exist (which hold
+// anything) become zeros, and so does every value that is no finite number; returns
+// whether there was one: add_odd_values() gives it to the queries that see it.
 template <int DP>
-__device__ __forceinline__ bool prepare_values(char* tile, int pages) {
+__device__ __forceinline__ bool clean_values(char* tile, int pages) {
   using Ge = Geo<DP>;
   const int lane = rare_lane();
   bool odd = false;
 #pragma unroll 1
   for (int i = 0; i < Ge::NI; i++) {
     uint4* at = (uint4*)(tile + i * 1024 + lane * 16);
+    uint4 x = *at;
     if (__shfl(pages, i * Ge::RPI + lane / Ge::NC) < 0) {
-      *at = uint4{0, 0, 0, 0};
+      x = uint4{0, 0, 0, 0};
     } else {
-      const uint4 x = *at;
-      for (uint32_t y : {x.x, x.y, x.z, x.w})
-        odd |= (y & 0x7C00u) == 0x7C00u || (y & 0x7C000000u) == 0x7C000000u;
+      uint32_t* y = &x.x;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const uint32_t keep = ((y[j] & 0x7C00u) == 0x7C00u ? 0 : 0xFFFFu) |
+                              ((y[j] & 0x7C000000u) == 0x7C000000u ? 0 : 0xFFFF0000u);
+        odd |= keep != 0xFFFFFFFFu;
+        y[j] &= keep;
+      }
     }
+    *at = x;
   }
   wait_lds();
   return __any(odd);
@@ -255,6 +263,12 @@ struct Item {
 // That is the layout in which O^T = V^T P^T takes P as its second operand, if
 // the depth of that product runs over the tokens in the same order, which V's
 // transposing reads choose freely: P never leaves its registers.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 template <int DP, int RT>
 struct Wave {
   static constexpr int KS = DP / 32, NB = DP / 16;
@@ -335,8 +349,8 @@ struct Wave {
     bool raise = false;
 #pragma unroll
     for (int r = 0; r < RT; r++) {
-      mx[r] = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
-                    fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
+      mx[r] = max3(max3(s[r][0][0], s[r][0][1], s[r][0][2]),
+                   max3(s[r][0][3], s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]));
       raise |= mx[r] * c > m[r] + (kSlack + kLift);
     }
     if (__any(raise)) {
@@ -384,36 +398,6 @@ struct Wave {
         o[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(u.a, p[r], o[r][b], 0, 0, 0);
     }
   }
-
-  // The same one token at a time, and only to the queries that see it: for tiles in
-  // which a value that is no finite number would meet zero weights.
-  __device__ __forceinline__ void values_one_by_one(const char* vt, const h8 (&p)[RT], int t0) {
-    const int lane = rare_lane(), g = lane >> 4;
-#pragma unroll 1
-    for (int tok = 0; tok < kTile; tok++) {
-      const int e0 = (tok >> 4) * 4 + (tok & 3), g0 = (tok >> 2) & 3;
-      float x[RT];  // the weight of the lane's queries; 0 and not seen are not the same
-      bool sees[RT];
-#pragma unroll
-      for (int r = 0; r < RT; r++) {
-        const uint4 w = __builtin_bit_cast(uint4, p[r]);
-        const uint32_t lo = e0 & 2 ? w.y : w.x, hi = e0 & 2 ? w.w : w.z;
-        const uint32_t two = __shfl(e0 & 4 ? hi : lo, g0 * 16 + (lane & 15));
-        x[r] = half_bits_to_float((uint16_t)(two >> (16 * (e0 & 1))));
-        sees[r] = t0 + tok < lim[r];
-      }
-#pragma unroll
-      for (int b = 0; b < NB; b++) {
-        const int c = 2 * b + (g >> 1);
-        const h4 v = *(const h4*)(vt + tok * (DP * 2) + ((c ^ swizzle<DP>(tok)) * 16) + (g & 1) * 8);
-#pragma unroll
-        for (int r = 0; r < RT; r++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) o[r][b][i] += sees[r] ? x[r] * (float)v[i] : 0.0f;
-        asm volatile("" ::: "memory");  // one block's values in registers at a time
-      }
-    }
-  }
 };
 
 // ---------------------------------------------------------------------------
@@ -427,6 +411,7 @@ struct Shared {
   __attribute__((aligned(1024))) char tile[kStages][2][Geo<DP>::BYTES];
   int32_t list[kListPages];
   float m[kWaves][64], l[kWaves][64], scale[kWaves][64];
+  uint32_t odd;  // clean_values() found something
 };
 static_assert(kStages == kWaves, "one layout for both uses");
 
@@ -496,13 +481,29 @@ __device__ __forceinline__ int64_t part_at(const Attn& a, const Item& it, int ro
   return ((int64_t)(it.slot0 + it.split) * a.n_q + it.q0 + row / a.G) * a.H + it.head * a.G + row % a.G;
 }
 
-// One tile whose K and V have landed: weights from the scores, then the values.
-// all: every query of the wave sees the whole tile.
-template <int DP, int RT>
-__device__ __forceinline__ void finish_tile(Wave<DP, RT>& w, f4 (&s)[RT][2], h8 (&p)[RT], char* vt,
-                                            int t0, int pages, bool all) {
-  if (!all && prepare_values<DP>(vt, pages)) w.values_one_by_one(vt, p, t0);
-  else w.values(vt, p);
+// After the sums of rows [row0, row1) are stored: what clean_values() took out of
+// tiles [first, end), for the rows that see it (a sum with such a value is an
+// infinity or no number whatever the weight, and stays so where the value was
+// counted already).  Rare, and slow.
+template <int DP>
+__device__ __forceinline__ void add_odd_values(const Attn& a, const Item& it, const Tokens<DP>& tk,
+                                               int first, int end, int row0, int row1) {
+  const int tid = kThreads - 1 - threadIdx.x;  // nothing here is worth sharing with the loops above
+#pragma unroll 1
+  for (int t = max(first * kTile, it.lo); t < min(end * kTile, it.hi); t++) {
+    const int page = a.tables[(int64_t)it.trow * a.B + (t >> a.shift)];
+    if (page < 0 || page >= a.N) continue;
+    const char* v = tk.vp + (uint64_t)(uint32_t)page * tk.src.page_bytes +
+                    (uint64_t)(uint32_t)(t & tk.src.pmask) * tk.src.row_bytes;
+#pragma unroll 1
+    for (int ch = tid; ch < a.d; ch += kThreads) {
+      const float x = half_bits_to_float(((const uint16_t*)v)[ch]);
+      if (x - x == 0.0f) continue;
+#pragma unroll 1
+      for (int row = row0; row < row1; row++)
+        if (t < row_lim(a, it, row)) a.part[part_at(a, it, row) * a.d + ch] += x;
+    }
+  }
 }
 
 // Few rows: every wave holds all 16 RT of a row tile and takes the split's token
@@ -530,37 +531,46 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
     const int max_lim = row_lim(a, it, (rt + 1) * 16 * RT - 1);
     const int end = min(tk.last, (max_lim + kTile - 1) / kTile);  // later tiles: nobody sees them
     tk.clear_tiles(a, sh);
+    if (threadIdx.x == 0) sh.odd = 0;
     for (int base = tk.first; base < end; base += tk.list_tiles) {
       const int stop = min(base + tk.list_tiles, end);
       tk.stretch(a, it, sh, base, stop);
-      // one round more than there are tiles: the first only starts the loads
-      int tile = base + wave - kWaves, pages = -1;
-      bool have = false, all = false;
-      while (have || tile + kWaves < stop) {
-        const int t0 = tile * kTile, next = tile + kWaves;
-        const bool more = next < stop;
-        const bool full = more && tk.full(next);
-        const int next_pages = more ? tile_pages(tk.src, next * kTile) : -1;
-        f4 s[RT][2];
-        if (have) {
-          wait_loads<Ge::NI>();
-          w.scores(kt, s);
-          wait_lds();
-        }
-        if (more) load_tile<DP, Ge::NI>(tk.src, tk.kp, klds, next * kTile, next_pages, full);
-        if (have) {
-          h8 p[RT];
-          if (!all) w.mask(s, t0, pages);
-          w.weights(s, c, p);
-          if (more) wait_loads<Ge::NI>(); else wait_loads<0>();
-          finish_tile<DP, RT>(w, s, p, vt, t0, pages, all);
-          wait_lds();
-        }
-        if (more) load_tile<DP, Ge::NI>(tk.src, tk.vp, vlds, next * kTile, next_pages, full);
+      // the tile in hand, its pages, whether its queries see all of it; the next one
+      int tile = base + wave, pages = -1, next, next_pages = -1;
+      bool all = false, more = false, full = false;
+      auto look = [&](int nt) {
+        next = nt;
+        more = nt < stop;
+        full = more && tk.full(nt);
+        next_pages = more ? tile_pages(tk.src, nt * kTile) : -1;
+      };
+      auto load_k = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, tk.kp, klds, next * kTile, next_pages, full); };
+      auto load_v = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, tk.vp, vlds, next * kTile, next_pages, full); };
+      auto step = [&] {
         tile = next;
         pages = next_pages;
         all = full && (next + 1) * kTile <= min_lim;
-        have = more;
+      };
+      look(tile);
+      load_k();
+      load_v();
+      step();
+      while (tile < stop) {
+        f4 s[RT][2];
+        h8 p[RT];
+        look(tile + kWaves);
+        wait_loads<Ge::NI>();
+        w.scores(kt, s);
+        wait_lds();
+        load_k();
+        if (!all) w.mask(s, tile * kTile, pages);
+        w.weights(s, c, p);
+        if (more) wait_loads<Ge::NI>(); else wait_loads<0>();
+        if (!all && clean_values<DP>(vt, pages)) sh.odd = 1;
+        w.values(vt, p);
+        wait_lds();
+        load_v();
+        step();
       }
     }
     // the waves' sums together, against the largest reference exponent
@@ -623,6 +633,8 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
       }
     }
     __syncthreads();  // m, l and scale are free
+    if (sh.odd) add_odd_values(a, it, tk, tk.first, end, rt * 16 * RT, min(it.rows, (rt + 1) * 16 * RT));
+    __syncthreads();
   }
 }
 
@@ -647,44 +659,45 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
     W w;
     w.clear();
     w.load_queries(a, it, row0);
-    const int min_lim = row_lim(a, it, row0);
+    const int min_lim = row_lim(a, it, rt * tile_rows);
     const int max_lim = row_lim(a, it, (rt + 1) * tile_rows - 1);
     const int end = min(tk.last, (max_lim + kTile - 1) / kTile);
     tk.clear_tiles(a, sh);
+    if (threadIdx.x == 0) sh.odd = 0;
     for (int base = tk.first; base < end; base += tk.list_tiles) {
       const int stop = min(base + tk.list_tiles, end);
       tk.stretch(a, it, sh, base, stop);
-      // the first kStages - 1 rounds only start loads
-      for (int tile = base - (kStages - 1); tile < stop; tile++) {
-        const int next = tile + kStages - 1;
-        if (tile >= base) {
-          const int left = stop - 1 - tile;  // tiles behind this one whose loads are under way
-          if (left >= 2) wait_loads<4 * kMine>();
-          else if (left == 1) wait_loads<2 * kMine>();
-          else wait_loads<0>();
-          __builtin_amdgcn_s_barrier();
-          asm volatile("" ::: "memory");
-        }
-        if (next < stop) {
-          const int slot = (next - base) & (kStages - 1);
-          const uint32_t to = lds + slot * 2 * Ge::BYTES;
-          const int next_pages = tile_pages(tk.src, next * kTile);
-          const bool full = tk.full(next);
-          load_tile<DP, kMine>(tk.src, tk.kp, to, next * kTile, next_pages, full, wave * kMine);
-          load_tile<DP, kMine>(tk.src, tk.vp, to + Ge::BYTES, next * kTile, next_pages, full, wave * kMine);
-        }
-        if (tile >= base) {
-          const int slot = (tile - base) & (kStages - 1), t0 = tile * kTile;
-          const bool all = tk.full(tile) && t0 + kTile <= min_lim;
-          const int pages = all ? 0 : tile_pages(tk.src, t0);
-          f4 s[RT][2];
-          h8 p[RT];
-          w.scores(sh.tile[slot][0], s);
-          if (!all) w.mask(s, t0, pages);
-          w.weights(s, c, p);
-          finish_tile<DP, RT>(w, s, p, sh.tile[slot][1], t0, pages, all);
-          wait_lds();  // read before the barrier that frees the slot
-        }
+      auto load = [&](int next) {
+        if (next >= stop) return;
+        const uint32_t to = lds + ((next - base) & (kStages - 1)) * 2 * Ge::BYTES;
+        const int pages = tile_pages(tk.src, next * kTile);
+        const bool full = tk.full(next);
+        load_tile<DP, kMine>(tk.src, tk.kp, to, next * kTile, pages, full, wave * kMine);
+        load_tile<DP, kMine>(tk.src, tk.vp, to + Ge::BYTES, next * kTile, pages, full, wave * kMine);
+      };
+      auto publish = [&](int tile) {  // all of the tile is there, the slot before it free
+        const int left = stop - 1 - tile;  // tiles behind this one whose loads are under way
+        if (left >= 2) wait_loads<4 * kMine>();
+        else if (left == 1) wait_loads<2 * kMine>();
+        else wait_loads<0>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        load(tile + kStages - 1);
+      };
+      for (int i = 0; i < kStages - 1; i++) load(base + i);
+      for (int tile = base; tile < stop; tile++) {
+        char* slot = sh.tile[(tile - base) & (kStages - 1)][0];
+        f4 s[RT][2];
+        h8 p[RT];
+        publish(tile);
+        w.scores(slot, s);
+        const bool all = tk.full(tile) && (tile + 1) * kTile <= min_lim;  // the same for all waves
+        const int pages = all ? 0 : tile_pages(tk.src, tile * kTile);
+        if (!all) w.mask(s, tile * kTile, pages);
+        w.weights(s, c, p);
+        if (!all && clean_values<DP>(slot + Ge::BYTES, pages)) sh.odd = 1;
+        w.values(slot + Ge::BYTES, p);
+        wait_lds();  // read before the barrier that frees the slot
       }
     }
 #pragma unroll
@@ -703,6 +716,9 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
       for (int b = 0; b < W::NB; b++)
         if (b * 16 + g * 4 < a.d) *(f4*)(a.part + at * a.d + b * 16 + g * 4) = w.o[r][b];
     }
+    __syncthreads();
+    if (sh.odd) add_odd_values(a, it, tk, tk.first, end, rt * tile_rows, min(it.rows, (rt + 1) * tile_rows));
+    __syncthreads();
   }
 }
 
