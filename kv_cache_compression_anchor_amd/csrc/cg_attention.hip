@@ -312,20 +312,28 @@ struct Wave {
     }
   }
 
+  // All of a tile's operands are read before the first product: one wait for LDS
+  // instead of one per product (left to itself the compiler saves the registers).
   __device__ __forceinline__ void scores(const char* kt, f4 (&s)[RT][2]) {
     const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int r = 0; r < RT; r++) s[r][0] = s[r][1] = f4{0, 0, 0, 0};
+    h8 k[KS][2];
 #pragma unroll
     for (int ks = 0; ks < KS; ks++)
 #pragma unroll
       for (int sub = 0; sub < 2; sub++) {
         const int row = sub * 16 + n;
-        const h8 a = *(const h8*)(kt + row * (DP * 2) + (((ks * 4 + g) ^ swizzle<DP>(row)) * 16));
+        k[ks][sub] = *(const h8*)(kt + row * (DP * 2) + (((ks * 4 + g) ^ swizzle<DP>(row)) * 16));
+      }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int r = 0; r < RT; r++) s[r][0] = s[r][1] = f4{0, 0, 0, 0};
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++)
 #pragma unroll
         for (int r = 0; r < RT; r++)
-          s[r][sub] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][ks], s[r][sub], 0, 0, 0);
-      }
+          s[r][sub] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[ks][sub], q[r][ks], s[r][sub], 0, 0, 0);
   }
 
   // Scores of tokens that do not exist, or that a query does not see, become -inf.
@@ -380,8 +388,8 @@ struct Wave {
     }
   }
 
-  // o += V^T P^T
-  __device__ __forceinline__ void values(const char* vt, const h8 (&p)[RT]) {
+  // V^T of a tile, 16 channels by all its tokens a block
+  __device__ __forceinline__ void read_values(const char* vt, h8 (&v)[NB]) {
     const int lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
     const int row = 4 * g + (j >> 2), in = (j & 1) * 8, half = (j & 3) >> 1;
 #pragma unroll
@@ -393,10 +401,17 @@ struct Wave {
         u.x[sub] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (lds_s4*)(vt + rr * (DP * 2) + (((2 * b + half) ^ swizzle<DP>(rr)) * 16) + in));
       }
+      v[b] = u.a;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // o += V^T P^T
+  __device__ __forceinline__ void add_values(const h8 (&v)[NB], const h8 (&p)[RT]) {
+#pragma unroll
+    for (int b = 0; b < NB; b++)
 #pragma unroll
       for (int r = 0; r < RT; r++)
-        o[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(u.a, p[r], o[r][b], 0, 0, 0);
-    }
+        o[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[b], p[r], o[r][b], 0, 0, 0);
   }
 };
 
@@ -567,9 +582,11 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
         w.weights(s, c, p);
         if (more) wait_loads<Ge::NI>(); else wait_loads<0>();
         if (!all && clean_values<DP>(vt, pages)) sh.odd = 1;
-        w.values(vt, p);
+        h8 v[W::NB];
+        w.read_values(vt, v);
         wait_lds();
         load_v();
+        w.add_values(v, p);
         step();
       }
     }
@@ -693,10 +710,14 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
         w.scores(slot, s);
         const bool all = tk.full(tile) && (tile + 1) * kTile <= min_lim;  // the same for all waves
         const int pages = all ? 0 : tile_pages(tk.src, tile * kTile);
-        if (!all) w.mask(s, tile * kTile, pages);
+        if (!all) {
+          w.mask(s, tile * kTile, pages);
+          if (clean_values<DP>(slot + Ge::BYTES, pages)) sh.odd = 1;
+        }
+        h8 v[W::NB];
+        w.read_values(slot + Ge::BYTES, v);  // on their way while the weights are computed
         w.weights(s, c, p);
-        if (!all && clean_values<DP>(slot + Ge::BYTES, pages)) sh.odd = 1;
-        w.values(slot + Ge::BYTES, p);
+        w.add_values(v, p);
         wait_lds();  // read before the barrier that frees the slot
       }
     }
