@@ -1,6 +1,7 @@
 // Attention of new tokens over a paged cache whose groups of sequences share a
 // prefix (include/cachegen.h, cg_attention_prefix_async).
 #include <algorithm>
+#include <type_traits>
 
 #include "cg_hostapi.h"
 #include "cg_internal.h"
@@ -20,10 +21,10 @@ typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s4 lds_s4;
 
 constexpr int kTile = 32;        // tokens of a tile: the depth of one 16x16x32 product
-constexpr int kWaves = 4;        // of a workgroup
-constexpr int kThreads = 64 * kWaves;
-constexpr int kListPages = 1024; // table entries staged at a time
-constexpr int kMinTiles = 8;     // tiles of a split, at least
+constexpr int kThreads = 256;    // of a joining workgroup
+// Tiles of a split, at least: of the shared prefixes, whose partial sums are many rows
+// each (64 requests on a 9K context: 54 us with 16 splits, 65 with 32), and of the rest.
+constexpr int kPreTiles = 16, kRestTiles = 8;
 // Weights are 2^(score - m) with m at most kSlack above what the running maximum
 // was when it was last raised, and kLift below it: up to 2^14, and binary16's
 // normal range reaches down to 2^-20 of the largest.
@@ -105,15 +106,15 @@ __device__ __forceinline__ Seq sequence(const Attn& a, int s) {
 }
 
 // Tokens [lo, hi) in tiles that start at multiples of kTile, dealt to `splits`
-// workgroups in turn of at least kMinTiles each.
+// workgroups in turn, at least `least` each.
 struct Split {
   int tile0, tiles, per, used;
 };
-__device__ __forceinline__ Split split_of(int lo, int hi, int splits) {
+__device__ __forceinline__ Split split_of(int lo, int hi, int splits, int least) {
   Split s;
   s.tile0 = lo / kTile;
   s.tiles = hi > lo ? (hi + kTile - 1) / kTile - s.tile0 : 0;
-  s.per = max(kMinTiles, (s.tiles + splits - 1) / splits);
+  s.per = max(least, (s.tiles + splits - 1) / splits);
   s.used = (s.tiles + s.per - 1) / s.per;
   return s;
 }
@@ -172,43 +173,48 @@ struct Source {           // where a workgroup's tokens come from
   uint32_t page_bytes, row_bytes;
 };
 
-// Page of token t0 + lane (lanes 0..31), -1 where there is none.
-__device__ __forceinline__ int tile_pages(const Source& s, int t0) {
+// Lane i (mod 32) knows token t0 + i of a tile: its page, -1 if it does not exist, and
+// where its row begins in a layer's pool (of some row, if it does not exist).
+struct TileAt {
+  int page;
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ TileAt tile_at(const Source& s, int t0) {
   const int t = t0 + (threadIdx.x & 31);
-  return t >= s.lo && t < s.hi ? s.list[(t >> s.shift) - s.block0] : -1;
+  TileAt at;
+  at.page = t >= s.lo && t < s.hi ? s.list[(t >> s.shift) - s.block0] : -1;
+  const uint64_t off = (uint64_t)(uint32_t)max(at.page, 0) * s.page_bytes +
+                       (uint64_t)(uint32_t)(t & s.pmask) * s.row_bytes;
+  at.lo = (uint32_t)off;
+  at.hi = (uint32_t)(off >> 32);
+  return at;
 }
 
-// Issues loads i0 .. i0 + N - 1 of the NI of the tile at t0 of a pool (pointing at the
-// kv head's channels) to the tile at LDS address lds.  Always N loads, so that
-// wait_loads() can count them: for tokens that do not exist some row of the pool is
-// read instead.  full: every token exists; if the rows of a load also lie in one
-// page and the head fills the tile's width, its address is scalar but for a lane's
-// fixed offset.  Chunks behind the head's keep what they held.
+// Issues loads i0 .. i0 + N - 1 of the NI of a tile of a pool (pointing at the kv
+// head's channels) to the tile at LDS address lds.  Always N loads, so that
+// wait_loads() can count them.  If the rows of a load lie in one page and the head
+// fills the tile's width, its address is scalar but for a lane's fixed offset.
+// Chunks behind the head's keep what they held.
 template <int DP, int N>
-__device__ __forceinline__ void load_tile(const Source& s, const char* pool, uint32_t lds, int t0,
-                                          int pages, bool full, int i0 = 0) {
+__device__ __forceinline__ void load_tile(const Source& s, const char* pool, uint32_t lds, const TileAt& at,
+                                          bool full, int i0 = 0) {
   using Ge = Geo<DP>;
   if (full && s.pmask >= Ge::RPI - 1 && s.nc == Ge::NC) {
     const int lane = threadIdx.x & 63, lrow = lane / Ge::NC, lc = lane % Ge::NC;
 #pragma unroll
     for (int j = 0; j < N; j++) {
       const int i = i0 + j;
-      const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(pages, i * Ge::RPI);
-      const char* base = pool + (uint64_t)page * s.page_bytes +
-                         (uint64_t)(uint32_t)((t0 + i * Ge::RPI) & s.pmask) * s.row_bytes;
-      load_lds(lds + i * 1024, base,
-               lrow * s.row_bytes + (lc ^ swizzle<DP>(i * Ge::RPI + lrow)) * 16);
+      const uint64_t off = (uint64_t)(uint32_t)__builtin_amdgcn_readlane(at.hi, i * Ge::RPI) << 32 |
+                           (uint32_t)__builtin_amdgcn_readlane(at.lo, i * Ge::RPI);
+      load_lds(lds + i * 1024, pool + off, lrow * s.row_bytes + (lc ^ swizzle<DP>(i * Ge::RPI + lrow)) * 16);
     }
   } else {
     const int lane = rare_lane(), lrow = lane / Ge::NC, lc = lane % Ge::NC;
 #pragma unroll 1
     for (int i = i0; i < i0 + N; i++) {
-      const int row = i * Ge::RPI + lrow;
-      const int page = __shfl(pages, row);
-      const int c = lc ^ swizzle<DP>(row);
-      const char* addr = pool + (uint64_t)(uint32_t)max(page, 0) * s.page_bytes +
-                         (uint64_t)(uint32_t)((t0 + row) & s.pmask) * s.row_bytes + c * 16;
-      if (c < s.nc) load_lds(lds + i * 1024, addr);
+      const int row = i * Ge::RPI + lrow, c = lc ^ swizzle<DP>(row);
+      const uint64_t off = (uint64_t)(uint32_t)__shfl(at.hi, row) << 32 | (uint32_t)__shfl(at.lo, row);
+      if (c < s.nc) load_lds(lds + i * 1024, pool + off + c * 16);
     }
   }
 }
@@ -251,9 +257,15 @@ struct Item {
   int lo, hi;               // tokens
   int lim0;                 // tokens that the first query sees (each later one 1 more)
   int trow;                 // table row
-  int splits, split, slot0; // of the tokens; first partial of this kind
+  int splits, split, least; // of the tokens; tiles of one at least
+  int slot0;                // first partial of this kind
   int row_tile, row_tiles;  // this workgroup's first row tile and its stride
 };
+
+// tokens that the query of a row sees
+__device__ __forceinline__ int row_lim(const Attn& a, const Item& it, int row) {
+  return min(it.hi, it.lim0 + min(row, it.rows - 1) / a.G);
+}
 
 // ---------------------------------------------------------------------------
 // One wave's part: 16 RT query rows against its tiles
@@ -263,6 +275,26 @@ struct Item {
 // That is the layout in which O^T = V^T P^T takes P as its second operand, if
 // the depth of that product runs over the tokens in the same order, which V's
 // transposing reads choose freely: P never leaves its registers.
+// Byte offsets of a lane's operands in a tile.  For the scores: row lane & 15, chunk
+// 4 ks + lane / 16, which is at k ^ 64 ks.  For the values: the 8 bytes that its group
+// of 16 lanes transposes, block b at v ^ 32 b.  Rows 16 further on have the same
+// swizzle, so the second half of a tile is an immediate.
+template <int DP>
+struct Places {
+  int k, v;
+  __device__ __forceinline__ Places() {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, row = 4 * g + (n >> 2);
+    k = n * (DP * 2) + (g ^ swizzle<DP>(n)) * 16;
+    v = row * (DP * 2) + (((n & 3) >> 1) ^ swizzle<DP>(row)) * 16 + (n & 1) * 8;
+  }
+  // the same, not to be kept for every block in registers through the loop
+  __device__ __forceinline__ Places fresh() const {
+    Places p = *this;
+    asm volatile("" : "+v"(p.k), "+v"(p.v));
+    return p;
+  }
+};
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
@@ -274,14 +306,12 @@ struct Wave {
   static constexpr int KS = DP / 32, NB = DP / 16;
   h8 q[RT][KS];
   f4 o[RT][NB];
-  float m[RT], mu[RT], l[RT];  // reference exponent (-inf: none yet), the one in use, sum
-  int lim[RT];                 // tokens that the lane's query sees
+  float m[RT], l[RT];          // reference exponent (-inf: none yet), sum
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int r = 0; r < RT; r++) {
       m[r] = -__builtin_inff();
-      mu[r] = 0.0f;
       l[r] = 0.0f;
 #pragma unroll
       for (int b = 0; b < NB; b++) o[r][b] = f4{0, 0, 0, 0};
@@ -308,37 +338,43 @@ struct Wave {
         z = uint4{(z.x & keep) ^ flip, (z.y & keep) ^ flip, (z.z & keep) ^ flip, (z.w & keep) ^ flip};
         q[r][ks] = __builtin_bit_cast(h8, z);
       }
-      lim[r] = in ? min(it.hi, it.lim0 + qi) : it.hi;
     }
   }
 
-  // All of a tile's operands are read before the first product: one wait for LDS
-  // instead of one per product (left to itself the compiler saves the registers).
-  __device__ __forceinline__ void scores(const char* kt, f4 (&s)[RT][2]) {
-    const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    h8 k[KS][2];
-#pragma unroll
-    for (int ks = 0; ks < KS; ks++)
-#pragma unroll
-      for (int sub = 0; sub < 2; sub++) {
-        const int row = sub * 16 + n;
-        k[ks][sub] = *(const h8*)(kt + row * (DP * 2) + (((ks * 4 + g) ^ swizzle<DP>(row)) * 16));
-      }
-    __builtin_amdgcn_sched_barrier(0);
+  // LDS operands are read in batches before the products that use them: one wait
+  // for LDS instead of one per product (left to itself the compiler saves the
+  // registers).
+  static constexpr int KB = KS < 2 ? KS : 2, VB = NB < 4 ? NB : 4;  // of a batch
+  __device__ __forceinline__ void scores(const char* kt, const Places<DP>& at, f4 (&s)[RT][2]) {
 #pragma unroll
     for (int r = 0; r < RT; r++) s[r][0] = s[r][1] = f4{0, 0, 0, 0};
 #pragma unroll
-    for (int ks = 0; ks < KS; ks++)
+    for (int x = 0; x < KS; x += KB) {
+      h8 k[KB][2];
 #pragma unroll
-      for (int sub = 0; sub < 2; sub++)
+      for (int y = 0; y < KB; y++)
 #pragma unroll
-        for (int r = 0; r < RT; r++)
-          s[r][sub] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[ks][sub], q[r][ks], s[r][sub], 0, 0, 0);
+        for (int sub = 0; sub < 2; sub++)
+          k[y][sub] = *(const h8*)(kt + (at.k ^ ((x + y) * 64)) + sub * 16 * DP * 2);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int y = 0; y < KB; y++)
+#pragma unroll
+        for (int sub = 0; sub < 2; sub++)
+#pragma unroll
+          for (int r = 0; r < RT; r++)
+            s[r][sub] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[y][sub], q[r][x + y], s[r][sub], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
   // Scores of tokens that do not exist, or that a query does not see, become -inf.
-  __device__ __forceinline__ void mask(f4 (&s)[RT][2], int t0, int pages) {
-    const int g = rare_lane() >> 4;
+  __device__ __forceinline__ void mask(const Attn& a, const Item& it, int row0, f4 (&s)[RT][2], int t0,
+                                       int pages) {
+    const int lane = rare_lane(), g = lane >> 4;
+    int lim[RT];
+#pragma unroll
+    for (int r = 0; r < RT; r++) lim[r] = row_lim(a, it, row0 + r * 16 + (lane & 15));
 #pragma unroll
     for (int sub = 0; sub < 2; sub++)
 #pragma unroll
@@ -350,10 +386,10 @@ struct Wave {
       }
   }
 
-  // Scores to weights.  m is raised only where a score passes it by kSlack, so
-  // most tiles need neither the maximum over the lanes nor a rescaling of o.
-  __device__ __forceinline__ void weights(f4 (&s)[RT][2], float c, h8 (&p)[RT]) {
-    float mx[RT];
+  // The reference exponents of a tile's weights.  m is raised only where a score
+  // passes it by kSlack, so most tiles need neither the maximum over the lanes nor a
+  // rescaling of o.  peaks() finds the lane's largest scores and whether one does.
+  __device__ __forceinline__ bool peaks(const f4 (&s)[RT][2], float c, float (&mx)[RT]) const {
     bool raise = false;
 #pragma unroll
     for (int r = 0; r < RT; r++) {
@@ -361,6 +397,9 @@ struct Wave {
                    max3(s[r][0][3], s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]));
       raise |= mx[r] * c > m[r] + (kSlack + kLift);
     }
+    return raise;
+  }
+  __device__ __forceinline__ void reference(bool raise, const float (&mx)[RT], float c) {
     if (__any(raise)) {
 #pragma unroll
       for (int r = 0; r < RT; r++) {
@@ -370,81 +409,81 @@ struct Wave {
         const float nm = fmaxf(m[r], x * c - kLift);
         const float f = nm == m[r] ? 1.0f : __builtin_amdgcn_exp2f(m[r] - nm);
         m[r] = nm;
-        mu[r] = nm == -__builtin_inff() ? 0.0f : nm;
         l[r] *= f;
 #pragma unroll
         for (int b = 0; b < NB; b++) o[r][b] *= f;
       }
     }
+  }
+  // Scores to weights, which are summed before they are rounded.
+  __device__ __forceinline__ void weights(const f4 (&s)[RT][2], float c, h8 (&p)[RT]) {
 #pragma unroll
     for (int r = 0; r < RT; r++) {
       float w[8];
+      const float mu = m[r] == -__builtin_inff() ? 0.0f : m[r];
 #pragma unroll
       for (int e = 0; e < 8; e++)
-        w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][e >> 2][e & 3], c, -mu[r]));
+        w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][e >> 2][e & 3], c, -mu));
       l[r] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
 #pragma unroll
       for (int e = 0; e < 8; e++) p[r][e] = (_Float16)w[e];  // rounded to nearest
     }
   }
 
-  // V^T of a tile, 16 channels by all its tokens a block
-  __device__ __forceinline__ void read_values(const char* vt, h8 (&v)[NB]) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
-    const int row = 4 * g + (j >> 2), in = (j & 1) * 8, half = (j & 3) >> 1;
-#pragma unroll
-    for (int b = 0; b < NB; b++) {
-      union { s4 x[2]; h8 a; } u;
-#pragma unroll
-      for (int sub = 0; sub < 2; sub++) {
-        const int rr = sub * 16 + row;
-        u.x[sub] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s4*)(vt + rr * (DP * 2) + (((2 * b + half) ^ swizzle<DP>(rr)) * 16) + in));
-      }
-      v[b] = u.a;
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  }
   // o += V^T P^T
-  __device__ __forceinline__ void add_values(const h8 (&v)[NB], const h8 (&p)[RT]) {
+  __device__ __forceinline__ void values(const char* vt, const Places<DP>& at, const h8 (&p)[RT]) {
 #pragma unroll
-    for (int b = 0; b < NB; b++)
+    for (int x = 0; x < NB; x += VB) {
+      h8 v[VB];
 #pragma unroll
-      for (int r = 0; r < RT; r++)
-        o[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[b], p[r], o[r][b], 0, 0, 0);
+      for (int y = 0; y < VB; y++) {
+        union { s4 x[2]; h8 a; } u;
+#pragma unroll
+        for (int sub = 0; sub < 2; sub++)
+          u.x[sub] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_s4*)(vt + (at.v ^ ((x + y) * 32)) + sub * 16 * DP * 2));
+        v[y] = u.a;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int y = 0; y < VB; y++)
+#pragma unroll
+        for (int r = 0; r < RT; r++)
+          o[r][x + y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[y], p[r], o[r][x + y], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 };
 
 // ---------------------------------------------------------------------------
 // One workgroup: a tile of rows against a split of the tokens
 // ---------------------------------------------------------------------------
-constexpr int kStages = 4;  // of the ring of tiles that the waves share
-
-template <int DP>
+// NW waves of a workgroup; TILES tiles of K and V: one for each wave, or a ring
+template <int DP, int NW, int TILES>
 struct Shared {
-  // each wave's tile of K and of V, or a ring of tiles of both; then the sums of the waves
-  __attribute__((aligned(1024))) char tile[kStages][2][Geo<DP>::BYTES];
-  int32_t list[kListPages];
-  float m[kWaves][64], l[kWaves][64], scale[kWaves][64];
+  static constexpr int kList = 512;  // table entries staged at a time
+  __attribute__((aligned(1024))) char tile[TILES][2][Geo<DP>::BYTES];  // then the sums of the waves
+  int32_t list[kList];
+  float m[NW][32], l[NW][32], scale[NW][32];
   uint32_t odd;  // clean_values() found something
 };
-static_assert(kStages == kWaves, "one layout for both uses");
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char*)(char*)p);
 }
 
 // What both ways of working share: the split's tiles, the pages of a stretch of them.
-template <int DP>
+template <int DP, class Sh>
 struct Tokens {
+  static constexpr int kThreads = sizeof(Sh::m) / 128 * 64;
   Source src;
   const char *kp, *vp;
   int first, last;  // tiles
   int list_tiles;   // tiles whose pages the list holds, wherever in a page they begin
   bool bad;         // a page of the present stretch is outside the pool
 
-  __device__ __forceinline__ bool start(const Attn& a, const Item& it, Shared<DP>& sh) {
-    const Split sp = split_of(it.lo, it.hi, it.splits);
+  __device__ __forceinline__ bool start(const Attn& a, const Item& it, Sh& sh) {
+    const Split sp = split_of(it.lo, it.hi, it.splits, it.least);
     if (it.split >= sp.used) return false;
     first = sp.tile0 + it.split * sp.per;
     last = min(first + sp.per, sp.tile0 + sp.tiles);
@@ -452,18 +491,18 @@ struct Tokens {
     src = Source{sh.list, 0, it.lo, it.hi, a.shift, a.P - 1, a.d / 8, row_bytes * (uint32_t)a.P, row_bytes};
     kp = a.k + it.head * a.d * 2;
     vp = a.v + it.head * a.d * 2;
-    list_tiles = (int)((int64_t)(kListPages - 1) * a.P / kTile) - 1;
+    list_tiles = (int)((int64_t)(Sh::kList - 1) * a.P / kTile) - 1;
     return true;
   }
   // the chunks behind the head's row stay zero
-  __device__ __forceinline__ void clear_tiles(const Attn& a, Shared<DP>& sh) {
+  __device__ __forceinline__ void clear_tiles(const Attn& a, Sh& sh) {
     if (a.d == DP) return;
     __syncthreads();
     for (int i = threadIdx.x; i < (int)sizeof(sh.tile) / 16; i += kThreads)
       ((uint4*)sh.tile)[i] = uint4{0, 0, 0, 0};
   }
   // pages of the tokens of tiles [base, stop)
-  __device__ __forceinline__ void stretch(const Attn& a, const Item& it, Shared<DP>& sh, int base,
+  __device__ __forceinline__ void stretch(const Attn& a, const Item& it, Sh& sh, int base,
                                           int stop) {
     const int b0 = max(base * kTile, it.lo) >> a.shift;
     const int b1 = (min(stop * kTile, it.hi) - 1) >> a.shift;
@@ -488,10 +527,6 @@ struct Tokens {
 __device__ __forceinline__ float log2_scale(const Attn& a) {
   return a.scale == 0 ? 1.0f : fminf(fabsf(a.scale) * 1.44269504088896341f, 3.4e38f);
 }
-// tokens that the query of a row sees
-__device__ __forceinline__ int row_lim(const Attn& a, const Item& it, int row) {
-  return min(it.hi, it.lim0 + min(row, it.rows - 1) / a.G);
-}
 __device__ __forceinline__ int64_t part_at(const Attn& a, const Item& it, int row) {
   return ((int64_t)(it.slot0 + it.split) * a.n_q + it.q0 + row / a.G) * a.H + it.head * a.G + row % a.G;
 }
@@ -500,9 +535,9 @@ __device__ __forceinline__ int64_t part_at(const Attn& a, const Item& it, int ro
 // tiles [first, end), for the rows that see it (a sum with such a value is an
 // infinity or no number whatever the weight, and stays so where the value was
 // counted already).  Rare, and slow.
-template <int DP>
-__device__ __forceinline__ void add_odd_values(const Attn& a, const Item& it, const Tokens<DP>& tk,
-                                               int first, int end, int row0, int row1) {
+template <int kThreads, class Tk>
+__device__ __forceinline__ void add_odd_values(const Attn& a, const Item& it, const Tk& tk, int first, int end,
+                                               int row0, int row1) {
   const int tid = kThreads - 1 - threadIdx.x;  // nothing here is worth sharing with the loops above
 #pragma unroll 1
   for (int t = max(first * kTile, it.lo); t < min(end * kTile, it.hi); t++) {
@@ -525,14 +560,16 @@ __device__ __forceinline__ void add_odd_values(const Attn& a, const Item& it, co
 // tiles in turn; the waves share nothing until the end.  Each has room for one tile
 // of K and one of V: the next K is on its way while the weights and the values are
 // computed, the next V while the scores are.
-template <int DP, int RT>
-__device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<DP>& sh) {
+template <int DP, int RT, int kWaves>
+__device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<DP, kWaves, kWaves>& sh) {
+  constexpr int kThreads = 64 * kWaves;
   using Ge = Geo<DP>;
   using W = Wave<DP, RT>;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  Tokens<DP> tk;
+  Tokens<DP, Shared<DP, kWaves, kWaves>> tk;
   if (!tk.start(a, it, sh)) return;
+  const Places<DP> at_lane;
   char *kt = sh.tile[wave][0], *vt = sh.tile[wave][1];
   const uint32_t klds = lds_address(kt), vlds = klds + Ge::BYTES;
   const float c = log2_scale(a);
@@ -550,20 +587,22 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
     for (int base = tk.first; base < end; base += tk.list_tiles) {
       const int stop = min(base + tk.list_tiles, end);
       tk.stretch(a, it, sh, base, stop);
-      // the tile in hand, its pages, whether its queries see all of it; the next one
-      int tile = base + wave, pages = -1, next, next_pages = -1;
+      // the tile in hand, where its tokens are, whether its queries see all of it; the
+      // next one
+      int tile = base + wave, next;
+      TileAt at{-1, 0, 0}, next_at{-1, 0, 0};
       bool all = false, more = false, full = false;
       auto look = [&](int nt) {
         next = nt;
         more = nt < stop;
         full = more && tk.full(nt);
-        next_pages = more ? tile_pages(tk.src, nt * kTile) : -1;
+        if (more) next_at = tile_at(tk.src, nt * kTile);
       };
-      auto load_k = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, tk.kp, klds, next * kTile, next_pages, full); };
-      auto load_v = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, tk.vp, vlds, next * kTile, next_pages, full); };
+      auto load_k = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, tk.kp, klds, next_at, full); };
+      auto load_v = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, tk.vp, vlds, next_at, full); };
       auto step = [&] {
         tile = next;
-        pages = next_pages;
+        at = next_at;
         all = full && (next + 1) * kTile <= min_lim;
       };
       look(tile);
@@ -575,18 +614,19 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
         h8 p[RT];
         look(tile + kWaves);
         wait_loads<Ge::NI>();
-        w.scores(kt, s);
+        w.scores(kt, at_lane.fresh(), s);
         wait_lds();
         load_k();
-        if (!all) w.mask(s, tile * kTile, pages);
+        if (!all) w.mask(a, it, rt * 16 * RT, s, tile * kTile, at.page);
+        float mx[RT];
+        const bool raise = w.peaks(s, c, mx);
+        w.reference(raise, mx, c);
         w.weights(s, c, p);
         if (more) wait_loads<Ge::NI>(); else wait_loads<0>();
-        if (!all && clean_values<DP>(vt, pages)) sh.odd = 1;
-        h8 v[W::NB];
-        w.read_values(vt, v);
+        if (!all && clean_values<DP>(vt, at.page)) sh.odd = 1;
+        w.values(vt, at_lane.fresh(), p);
         wait_lds();
         load_v();
-        w.add_values(v, p);
         step();
       }
     }
@@ -650,23 +690,29 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
       }
     }
     __syncthreads();  // m, l and scale are free
-    if (sh.odd) add_odd_values(a, it, tk, tk.first, end, rt * 16 * RT, min(it.rows, (rt + 1) * 16 * RT));
+    if (sh.odd) add_odd_values<kThreads>(a, it, tk, tk.first, end, rt * 16 * RT, min(it.rows, (rt + 1) * 16 * RT));
     __syncthreads();
   }
 }
 
-// Many rows: a wave holds 16 RT of the tile's 64 RT rows, all waves read the same
-// token tiles from a ring; each loads a quarter of a tile, kStages - 1 tiles ahead,
-// and one barrier a tile both publishes it and frees the slot that is filled next.
-template <int DP, int RT>
-__device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<DP>& sh) {
+// Many rows: a wave holds 16 RT of the 16 RT kWaves rows, all waves read the same token
+// tiles from a ring; each loads its part of a tile, kStages - 2 tiles ahead, and one
+// barrier a tile both publishes it and frees the slot that is filled next.
+template <int DP, int RT, int kWaves, int kStages>
+__device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<DP, kWaves, kStages>& sh) {
+  constexpr int kThreads = 64 * kWaves;
   using Ge = Geo<DP>;
   using W = Wave<DP, RT>;
-  constexpr int kMine = Ge::NI / kWaves;  // loads of a wave for K, and for V
+  // a wave's loads of a tile: of K, and of V; with few a tile, half the waves K, half V
+  constexpr bool kHalf = Ge::NI < kWaves;
+  constexpr int kMine = kHalf ? 2 * Ge::NI / kWaves : Ge::NI / kWaves;
+  constexpr int kLoads = kHalf ? kMine : 2 * kMine;
+  static_assert(kMine >= 1 && kStages >= 2 && kStages <= 4, "");
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  Tokens<DP> tk;
+  Tokens<DP, Shared<DP, kWaves, kStages>> tk;
   if (!tk.start(a, it, sh)) return;
+  const Places<DP> at_lane;
   const uint32_t lds = lds_address(sh.tile);
   const float c = log2_scale(a);
   const int tile_rows = 16 * RT * kWaves, row_tiles = (it.rows + tile_rows - 1) / tile_rows;
@@ -684,41 +730,56 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
     for (int base = tk.first; base < end; base += tk.list_tiles) {
       const int stop = min(base + tk.list_tiles, end);
       tk.stretch(a, it, sh, base, stop);
-      auto load = [&](int next) {
-        if (next >= stop) return;
-        const uint32_t to = lds + ((next - base) & (kStages - 1)) * 2 * Ge::BYTES;
-        const int pages = tile_pages(tk.src, next * kTile);
-        const bool full = tk.full(next);
-        load_tile<DP, kMine>(tk.src, tk.kp, to, next * kTile, pages, full, wave * kMine);
-        load_tile<DP, kMine>(tk.src, tk.vp, to + Ge::BYTES, next * kTile, pages, full, wave * kMine);
+      auto load = [&](int tile) {
+        if (tile >= stop) return;
+        const TileAt at = tile_at(tk.src, tile * kTile);
+        const bool full = tk.full(tile);
+        const uint32_t to = lds + (uint32_t)(tile - base) % kStages * (2 * Ge::BYTES);
+        if constexpr (kHalf) {
+          const bool v = wave >= kWaves / 2;
+          load_tile<DP, kMine>(tk.src, v ? tk.vp : tk.kp, to + (v ? Ge::BYTES : 0), at, full,
+                               (wave & (kWaves / 2 - 1)) * kMine);
+        } else {
+          load_tile<DP, kMine>(tk.src, tk.kp, to, at, full, wave * kMine);
+          load_tile<DP, kMine>(tk.src, tk.vp, to + Ge::BYTES, at, full, wave * kMine);
+        }
       };
-      auto publish = [&](int tile) {  // all of the tile is there, the slot before it free
-        const int left = stop - 1 - tile;  // tiles behind this one whose loads are under way
-        if (left >= 2) wait_loads<4 * kMine>();
-        else if (left == 1) wait_loads<2 * kMine>();
+      // The tile is there for all waves, and none reads the slot of the one before it any
+      // more, which takes the tile kStages - 1 ahead of it.
+      auto publish = [&](int tile) {
+        wait_lds();
+        if (tile + kStages - 1 <= stop) wait_loads<(kStages - 2) * kLoads>();
         else wait_loads<0>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         load(tile + kStages - 1);
       };
-      for (int i = 0; i < kStages - 1; i++) load(base + i);
-      for (int tile = base; tile < stop; tile++) {
-        char* slot = sh.tile[(tile - base) & (kStages - 1)][0];
+      auto step = [&](auto slot_c, int tile) {
+        char* kt = sh.tile[decltype(slot_c)::value][0];
+        char* vt = kt + Ge::BYTES;
         f4 s[RT][2];
         h8 p[RT];
+        float mx[RT];
         publish(tile);
-        w.scores(slot, s);
+        w.scores(kt, at_lane.fresh(), s);
         const bool all = tk.full(tile) && (tile + 1) * kTile <= min_lim;  // the same for all waves
-        const int pages = all ? 0 : tile_pages(tk.src, tile * kTile);
         if (!all) {
-          w.mask(s, tile * kTile, pages);
-          if (clean_values<DP>(slot + Ge::BYTES, pages)) sh.odd = 1;
+          const int pages = tile_at(tk.src, tile * kTile).page;
+          w.mask(a, it, row0, s, tile * kTile, pages);
+          if (clean_values<DP>(vt, pages)) sh.odd = 1;
         }
-        h8 v[W::NB];
-        w.read_values(slot + Ge::BYTES, v);  // on their way while the weights are computed
+        const bool raise = w.peaks(s, c, mx);
+        w.reference(raise, mx, c);
         w.weights(s, c, p);
-        w.add_values(v, p);
-        wait_lds();  // read before the barrier that frees the slot
+        w.values(vt, at_lane.fresh(), p);
+      };
+      for (int i = 0; i < kStages - 1; i++) load(base + i);
+      // unrolled by the ring's slots, so that LDS offsets are immediates
+      for (int tile = base; tile < stop; tile += kStages) {
+        step(std::integral_constant<int, 0>(), tile);
+        if (tile + 1 < stop) step(std::integral_constant<int, 1>(), tile + 1);
+        if (kStages > 2 && tile + 2 < stop) step(std::integral_constant<int, 2 % kStages>(), tile + 2);
+        if (kStages > 3 && tile + 3 < stop) step(std::integral_constant<int, 3 % kStages>(), tile + 3);
       }
     }
 #pragma unroll
@@ -738,7 +799,7 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
         if (b * 16 + g * 4 < a.d) *(f4*)(a.part + at * a.d + b * 16 + g * 4) = w.o[r][b];
     }
     __syncthreads();
-    if (sh.odd) add_odd_values(a, it, tk, tk.first, end, rt * tile_rows, min(it.rows, (rt + 1) * tile_rows));
+    if (sh.odd) add_odd_values<kThreads>(a, it, tk, tk.first, end, rt * tile_rows, min(it.rows, (rt + 1) * tile_rows));
     __syncthreads();
   }
 }
@@ -768,6 +829,7 @@ __device__ __forceinline__ bool item_of(const Attn& a, int w, Item& it) {
     it.rows = (q1 - it.q0) * a.G;
     it.lim0 = it.hi;
     it.splits = a.pre_splits;
+    it.least = kPreTiles;
     it.slot0 = 0;
     it.row_tiles = a.pre_tiles;
     return true;
@@ -785,19 +847,36 @@ __device__ __forceinline__ bool item_of(const Attn& a, int w, Item& it) {
   it.rows = q.m * a.G;
   it.lim0 = q.len - q.m + 1;
   it.splits = a.rest_splits;
+  it.least = kRestTiles;
   it.slot0 = a.pre_splits;
   it.row_tiles = a.rest_tiles;
   return true;
 }
 
-template <int DP, int RT, bool kRing>
-__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void k_attention(Attn a, int first, int end) {
-  __shared__ Shared<DP> sh;
+// How an item's workgroup holds rows: all of 16 or 32 in each of four waves, which
+// deal out the tokens; or 16 or 32 in each, and the waves deal out the rows.
+enum { kRows16 = 0, kRows32 = 1, kRows64 = 2, kRows128 = 3 };
+__host__ __device__ constexpr int rows_of(int mode) { return 16 << mode; }
+constexpr int kBlock = 256, kTiles = 4;
+// workgroups on a compute unit, as LDS and registers allow
+__host__ __device__ constexpr int resident(int dp) { return dp == 256 ? 1 : 2; }
+
+template <int DP, int MODE>
+__device__ __forceinline__ void run_item(const Attn& a, const Item& it, Shared<DP, 4, kTiles>& sh) {
+  if constexpr (MODE <= kRows32) run_split<DP, 1 + MODE, 4>(a, it, sh);
+  else run_ring<DP, MODE == kRows128 ? 2 : 1, 4, kTiles>(a, it, sh);
+}
+
+// Items of the shared prefixes and of the rest in one launch: the former keep the
+// matrix cores busy, the latter HBM.
+template <int DP, int PRE, int REST>
+__global__ __launch_bounds__(kBlock, resident(DP)) void k_attention(Attn a, int first, int end) {
+  __shared__ Shared<DP, 4, kTiles> sh;
   for (int w = first + blockIdx.x; w < end; w += gridDim.x) {
     Item it;
     if (!item_of(a, w, it)) continue;
-    if (kRing) run_ring<DP, RT>(a, it, sh);
-    else run_split<DP, RT>(a, it, sh);
+    if (PRE == REST || it.slot0 == 0) run_item<DP, PRE>(a, it, sh);
+    else run_item<DP, REST>(a, it, sh);
   }
 }
 
@@ -812,8 +891,8 @@ __global__ __launch_bounds__(kThreads) void k_join(Attn a) {
   if (s < 0 || qi < a.q_starts[s] || qi >= a.q_starts[s + 1]) return;
   const Seq q = sequence(a, s);
   if (!q.ok && tid == 0) atomicOr(a.status, kRefused);
-  const int pre = q.ok ? split_of(0, q.pre, a.pre_splits).used : 0;
-  const int used = pre + (q.ok ? split_of(q.pre, q.len, a.rest_splits).used : 0);
+  const int pre = q.ok ? split_of(0, q.pre, a.pre_splits, kPreTiles).used : 0;
+  const int used = pre + (q.ok ? split_of(q.pre, q.len, a.rest_splits, kRestTiles).used : 0);
   const int quads = a.d / 4, unit = tid / quads, quad = tid % quads;
   const int heads = kThreads / quads / a.join;  // of a workgroup
   const int part = unit % a.join, hl = unit / a.join, h = blockIdx.y * heads + hl;
@@ -867,29 +946,35 @@ struct Plan {
   size_t words;
 };
 
-// How a launch's waves hold rows: all of 16 or 32, or a quarter each of 64 or 128.
-enum { kRows16 = 0, kRows32 = 1, kRows64 = 2, kRows128 = 3 };
-int rows_of(int mode) { return 16 << mode; }
-
-// items first .. end - 1 of the launch's list
-void launch(int dp, int mode, const Attn& a, int64_t first, int64_t end, hipStream_t st) {
-  if (end <= first) return;
+// Items first .. end - 1 of the launch's list, if there is a kernel for both kinds.
+template <int DP>
+bool launch(int pre, int rest, const Attn& a, int64_t first, int64_t end, hipStream_t st) {
+  if (end <= first) return true;
   const int grid = (int)std::min<int64_t>(end - first, 1 << 22);
-#define GO(DP, RT, RING) k_attention<DP, RT, RING><<<grid, kThreads, 0, st>>>(a, (int)first, (int)end)
-#define BY_MODE(DP)                            \
-  if (mode == kRows16) GO(DP, 1, false);       \
-  else if (mode == kRows32) GO(DP, 2, false);  \
-  else if (mode == kRows64) GO(DP, 1, true);   \
-  else GO(DP, 2, true)
-  if (dp == 64) { BY_MODE(64); }
-  else if (dp == 128) { BY_MODE(128); }
-  else { BY_MODE(256); }
-#undef BY_MODE
+#define GO(PRE, REST)                                                                    \
+  if (pre == PRE && rest == REST) {                                                      \
+    k_attention<DP, PRE, REST><<<grid, kBlock, 0, st>>>(a, (int)first, (int)end);        \
+    return true;                                                                         \
+  }
+  GO(kRows16, kRows16) GO(kRows64, kRows64) GO(kRows64, kRows16)
+  if constexpr (DP <= 128) {
+    GO(kRows32, kRows32) GO(kRows128, kRows128) GO(kRows32, kRows16) GO(kRows128, kRows16)
+    GO(kRows64, kRows32) GO(kRows128, kRows32)
+  }
 #undef GO
+  return false;
+}
+bool launch(int dp, int pre, int rest, const Attn& a, int64_t first, int64_t end, hipStream_t st) {
+  return dp == 64 ? launch<64>(pre, rest, a, first, end, st)
+         : dp == 128 ? launch<128>(pre, rest, a, first, end, st) : launch<256>(pre, rest, a, first, end, st);
 }
 
-int mode_of(int64_t rows) {
-  return rows <= 16 ? kRows16 : rows <= 32 ? kRows32 : rows <= 64 ? kRows64 : kRows128;
+// The smallest that holds `rows`.  Waves of 32 rows of 256 channels would not fit
+// their registers.
+int mode_of(int64_t rows, int dp) {
+  if (rows <= 16) return kRows16;
+  if (dp == 256) return kRows64;
+  return rows <= 32 ? kRows32 : rows <= 64 ? kRows64 : kRows128;
 }
 
 Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
@@ -900,26 +985,26 @@ Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
   // all heads, sequences and splits, fits 31 bits
   auto most = [&](int64_t items) { return std::max<int64_t>(1, (1 << 22) / std::max<int64_t>(1, items)); };
   const int64_t rows = (int64_t)std::max(1, std::min(x.max_q, x.n_q)) * G;
-  p.rest_mode = mode_of(rows);
+  p.rest_mode = mode_of(rows, p.dp);
   const int rest_rows = rows_of(p.rest_mode);
   p.rest_tiles = (int)std::min(most((int64_t)x.n_seqs * kv), (rows + rest_rows - 1) / rest_rows);
   const bool shared = x.n_groups > 0 && x.max_prefix > 0;
   p.pre_groups = x.n_groups;
   // rows of an average group
   const int64_t pre_rows = std::max<int64_t>(1, x.n_groups ? (x.n_q + x.n_groups - 1) / x.n_groups : 1) * G;
-  p.pre_mode = mode_of(pre_rows);
+  p.pre_mode = mode_of(pre_rows, p.dp);
   const int pre_tile = rows_of(p.pre_mode);
   p.pre_tiles = (int)std::min(most((int64_t)x.n_groups * kv), (pre_rows + pre_tile - 1) / pre_tile);
-  // enough workgroups for two on each of 256 compute units, but splits of
-  // 256 tokens at least
-  auto splits = [&](int64_t items, int64_t tokens) {
-    const int64_t want = (512 + items - 1) / std::max<int64_t>(1, items);
-    const int64_t room = std::max<int64_t>(1, tokens / (kMinTiles * kTile));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, room), 64));
+  // As many workgroups as are resident at once on 256 compute units (a second round
+  // of a few would cost as much as the first), but no shorter splits than split_of() makes.
+  auto splits = [&](int64_t items, int64_t tokens, int least) {
+    const int64_t slots = 256 * resident(p.dp);
+    const int64_t room = std::max<int64_t>(1, tokens / (least * kTile));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({slots / std::max<int64_t>(1, items), room, 64}));
   };
-  p.pre_splits = x.n_groups ? splits((int64_t)x.n_groups * kv * p.pre_tiles, shared ? x.max_prefix : 0) : 0;
+  p.pre_splits = x.n_groups ? splits((int64_t)x.n_groups * kv * p.pre_tiles, shared ? x.max_prefix : 0, kPreTiles) : 0;
   p.rest_splits = splits((int64_t)std::max(1, x.n_seqs) * kv * p.rest_tiles,
-                         std::max(0, x.max_len - (shared ? x.max_prefix : 0)));
+                         std::max(0, x.max_len - (shared ? x.max_prefix : 0)), kRestTiles);
   p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + 4;
   return p;
 }
@@ -1005,11 +1090,10 @@ int cg_attention_prefix_async(const cg_paged_cache* c, const cg_attention* a, vo
   const int64_t pre = (int64_t)p.pre_groups * p.pre_splits * p.pre_tiles * v.kv;
   const int64_t rest = (int64_t)a->n_seqs * p.rest_splits * p.rest_tiles * v.kv;
   hipStream_t st = (hipStream_t)stream;
-  if (p.pre_mode == p.rest_mode) {
-    launch(p.dp, p.pre_mode, v, 0, pre + rest, st);
-  } else {
-    launch(p.dp, p.pre_mode, v, 0, pre, st);
-    launch(p.dp, p.rest_mode, v, pre, pre + rest, st);
+  const int only = pre ? p.pre_mode : p.rest_mode;
+  if (!launch(p.dp, only, p.rest_mode, v, 0, pre + rest, st)) {  // unusual pairs: one after the other
+    launch(p.dp, p.pre_mode, p.pre_mode, v, 0, pre, st);
+    launch(p.dp, p.rest_mode, p.rest_mode, v, pre, pre + rest, st);
   }
   const int total = p.pre_splits + p.rest_splits;
   v.join = std::min(total <= 2 ? 1 : total <= 8 ? 2 : 8, kThreads / (v.d / 4));
