@@ -400,7 +400,7 @@ struct Wave {
     return raise;
   }
   __device__ __forceinline__ void reference(bool raise, const float (&mx)[RT], float c) {
-    if (__any(raise)) {
+    if (__builtin_expect(__any(raise), 0)) {
 #pragma unroll
       for (int r = 0; r < RT; r++) {
         float x = mx[r];
@@ -703,11 +703,8 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
   constexpr int kThreads = 64 * kWaves;
   using Ge = Geo<DP>;
   using W = Wave<DP, RT>;
-  // a wave's loads of a tile: of K, and of V; with few a tile, half the waves K, half V
-  constexpr bool kHalf = Ge::NI < kWaves;
-  constexpr int kMine = kHalf ? 2 * Ge::NI / kWaves : Ge::NI / kWaves;
-  constexpr int kLoads = kHalf ? kMine : 2 * kMine;
-  static_assert(kMine >= 1 && kStages >= 2 && kStages <= 4, "");
+  constexpr int kMine = Ge::NI / kWaves;  // a wave's loads of a tile of K, and of V
+  static_assert(kMine >= 1 && kStages == 4, "");
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Tokens<DP, Shared<DP, kWaves, kStages>> tk;
@@ -730,37 +727,87 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
     for (int base = tk.first; base < end; base += tk.list_tiles) {
       const int stop = min(base + tk.list_tiles, end);
       tk.stretch(a, it, sh, base, stop);
+      char* ring = sh.tile[0][0];
+      auto slot_of = [&](int tile) { return (tile - base) & (kStages - 1); };
       auto load = [&](int tile) {
         if (tile >= stop) return;
         const TileAt at = tile_at(tk.src, tile * kTile);
-        const bool full = tk.full(tile);
-        const uint32_t to = lds + (uint32_t)(tile - base) % kStages * (2 * Ge::BYTES);
-        if constexpr (kHalf) {
-          const bool v = wave >= kWaves / 2;
-          load_tile<DP, kMine>(tk.src, v ? tk.vp : tk.kp, to + (v ? Ge::BYTES : 0), at, full,
-                               (wave & (kWaves / 2 - 1)) * kMine);
-        } else {
-          load_tile<DP, kMine>(tk.src, tk.kp, to, at, full, wave * kMine);
-          load_tile<DP, kMine>(tk.src, tk.vp, to + Ge::BYTES, at, full, wave * kMine);
-        }
+        const uint32_t to = lds + slot_of(tile) * (2 * Ge::BYTES);
+        load_tile<DP, kMine>(tk.src, tk.kp, to, at, tk.full(tile), wave * kMine);
+        load_tile<DP, kMine>(tk.src, tk.vp, to + Ge::BYTES, at, tk.full(tile), wave * kMine);
       };
-      // The tile is there for all waves, and none reads the slot of the one before it any
-      // more, which takes the tile kStages - 1 ahead of it.
-      auto publish = [&](int tile) {
-        wait_lds();
-        if (tile + kStages - 1 <= stop) wait_loads<(kStages - 2) * kLoads>();
-        else wait_loads<0>();
+      // Behind the barrier the tile is there for all waves, and none reads the slot of
+      // the one before it any more, which takes the tile kStages - 1 ahead.
+      auto publish = [&] {
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        load(tile + kStages - 1);
       };
-      auto step = [&](auto slot_c, int tile) {
-        char* kt = sh.tile[decltype(slot_c)::value][0];
+      for (int i = 0; i < kStages - 1; i++) load(base + i);
+
+      // Tiles of which every query sees all, and the tiles loaded meanwhile too, in
+      // rounds of the ring's slots: no branch but one, LDS offsets are immediates, and
+      // a wave's 8 rows of a tile lie in one page, whose number is read a tile ahead.
+      // (A wave that finds its way through the conditions below instead spends a third
+      // of its time on them and on addresses: 165 us against 128 for 32 requests on 81920
+      // tokens.)
+      int tile = base;
+      const int seen = tk.bad || base * kTile < it.lo ? base : min(stop, min_lim / kTile);
+      if (tk.src.pmask >= 7 && tk.src.nc == Ge::NC && tile + 2 * kStages - 1 <= seen) {
+        const int last_page = ((min(stop * kTile, it.hi) - 1) >> tk.src.shift) - tk.src.block0;
+        auto page_of = [&](int tl) {
+          return sh.list[min(((tl * kTile + wave * 8) >> tk.src.shift) - tk.src.block0, last_page)];
+        };
+        const int lrow = lane / Ge::NC, lc = lane % Ge::NC;
+        uint32_t at_row[kMine];
+#pragma unroll
+        for (int j = 0; j < kMine; j++)
+          at_row[j] = (j * Ge::RPI + lrow) * tk.src.row_bytes +
+                      (lc ^ swizzle<DP>((wave * kMine + j) * Ge::RPI + lrow)) * 16;
+        int page = page_of(tile + kStages - 1);
+        auto step = [&](auto slot_c) {
+          constexpr int kSlot = decltype(slot_c)::value;
+          char* kt = ring + kSlot * 2 * Ge::BYTES;
+          const uint32_t to = lds + ((kSlot + kStages - 1) & (kStages - 1)) * 2 * Ge::BYTES + wave * kMine * 1024;
+          f4 s[RT][2];
+          h8 p[RT];
+          float mx[RT];
+          wait_lds();
+          wait_loads<(kStages - 2) * 2 * kMine>();
+          publish();
+          w.scores(kt, at_lane.fresh(), s);
+          const int next = tile + kStages - 1;
+          const uint64_t off =
+              (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(page) * tk.src.page_bytes +
+              (uint64_t)((uint32_t)((next * kTile + wave * 8) & tk.src.pmask) * tk.src.row_bytes);
+#pragma unroll
+          for (int j = 0; j < kMine; j++) load_lds(to + j * 1024, tk.kp + off, at_row[j]);
+#pragma unroll
+          for (int j = 0; j < kMine; j++) load_lds(to + Ge::BYTES + j * 1024, tk.vp + off, at_row[j]);
+          page = page_of(next + 1);
+          const bool raise = w.peaks(s, c, mx);
+          w.reference(raise, mx, c);
+          w.weights(s, c, p);
+          w.values(kt + Ge::BYTES, at_lane.fresh(), p);
+          tile++;
+        };
+        do {
+          step(std::integral_constant<int, 0>());
+          step(std::integral_constant<int, 1>());
+          step(std::integral_constant<int, 2>());
+          step(std::integral_constant<int, 3>());
+        } while (tile + 2 * kStages - 1 <= seen);
+      }
+      for (; tile < stop; tile++) {
+        char* kt = ring + slot_of(tile) * (2 * Ge::BYTES);
         char* vt = kt + Ge::BYTES;
         f4 s[RT][2];
         h8 p[RT];
         float mx[RT];
-        publish(tile);
+        wait_lds();
+        if (tile + kStages - 1 <= stop) wait_loads<(kStages - 2) * 2 * kMine>();
+        else wait_loads<0>();
+        publish();
+        load(tile + kStages - 1);
         w.scores(kt, at_lane.fresh(), s);
         const bool all = tk.full(tile) && (tile + 1) * kTile <= min_lim;  // the same for all waves
         if (!all) {
@@ -772,14 +819,6 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
         w.reference(raise, mx, c);
         w.weights(s, c, p);
         w.values(vt, at_lane.fresh(), p);
-      };
-      for (int i = 0; i < kStages - 1; i++) load(base + i);
-      // unrolled by the ring's slots, so that LDS offsets are immediates
-      for (int tile = base; tile < stop; tile += kStages) {
-        step(std::integral_constant<int, 0>(), tile);
-        if (tile + 1 < stop) step(std::integral_constant<int, 1>(), tile + 1);
-        if (kStages > 2 && tile + 2 < stop) step(std::integral_constant<int, 2 % kStages>(), tile + 2);
-        if (kStages > 3 && tile + 3 < stop) step(std::integral_constant<int, 3 % kStages>(), tile + 3);
       }
     }
 #pragma unroll
@@ -997,14 +1036,22 @@ Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
   p.pre_tiles = (int)std::min(most((int64_t)x.n_groups * kv), (pre_rows + pre_tile - 1) / pre_tile);
   // As many workgroups as are resident at once on 256 compute units (a second round
   // of a few would cost as much as the first), but no shorter splits than split_of() makes.
-  auto splits = [&](int64_t items, int64_t tokens, int least) {
-    const int64_t slots = 256 * resident(p.dp);
+  auto splits = [&](int64_t items, int64_t tokens, int64_t slots, int least) {
     const int64_t room = std::max<int64_t>(1, tokens / (least * kTile));
     return (int)std::max<int64_t>(1, std::min<int64_t>({slots / std::max<int64_t>(1, items), room, 64}));
   };
-  p.pre_splits = x.n_groups ? splits((int64_t)x.n_groups * kv * p.pre_tiles, shared ? x.max_prefix : 0, kPreTiles) : 0;
+  const int64_t slots = 256 * resident(p.dp);
+  if (x.n_groups) {
+    // the prefixes of a batch take half of the slots, and leave the others to the rest,
+    // unless they are long
+    const int64_t items = (int64_t)x.n_groups * kv * p.pre_tiles, tokens = shared ? x.max_prefix : 0;
+    p.pre_splits = splits(items, tokens, slots, 2 * kPreTiles);
+    if (items * p.pre_splits < slots * 3 / 4) p.pre_splits = splits(items, tokens, slots / 2, kPreTiles);
+  } else {
+    p.pre_splits = 0;
+  }
   p.rest_splits = splits((int64_t)std::max(1, x.n_seqs) * kv * p.rest_tiles,
-                         std::max(0, x.max_len - (shared ? x.max_prefix : 0)), kRestTiles);
+                         std::max(0, x.max_len - (shared ? x.max_prefix : 0)), slots, kRestTiles);
   p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + 4;
   return p;
 }
