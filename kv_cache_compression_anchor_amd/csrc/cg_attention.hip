@@ -345,7 +345,9 @@ struct Wave {
   // for LDS instead of one per product (left to itself the compiler saves the
   // registers).
   static constexpr int KB = KS < 2 ? KS : 2, VB = NB < 4 ? NB : 4;  // of a batch
-  __device__ __forceinline__ void scores(const char* kt, const Places<DP>& at, f4 (&s)[RT][2]) {
+  // between(): called once half of the products are under way.
+  template <class F>
+  __device__ __forceinline__ void scores(const char* kt, const Places<DP>& at, f4 (&s)[RT][2], F between) {
 #pragma unroll
     for (int r = 0; r < RT; r++) s[r][0] = s[r][1] = f4{0, 0, 0, 0};
 #pragma unroll
@@ -365,6 +367,7 @@ struct Wave {
           for (int r = 0; r < RT; r++)
             s[r][sub] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[y][sub], q[r][x + y], s[r][sub], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
+      if (x == 0) between();
     }
   }
 
@@ -431,7 +434,8 @@ struct Wave {
   }
 
   // o += V^T P^T
-  __device__ __forceinline__ void values(const char* vt, const Places<DP>& at, const h8 (&p)[RT]) {
+  template <class F>
+  __device__ __forceinline__ void values(const char* vt, const Places<DP>& at, const h8 (&p)[RT], F between) {
 #pragma unroll
     for (int x = 0; x < NB; x += VB) {
       h8 v[VB];
@@ -451,6 +455,7 @@ struct Wave {
         for (int r = 0; r < RT; r++)
           o[r][x + y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[y], p[r], o[r][x + y], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
+      if (x == 0) between();
     }
   }
 };
@@ -614,7 +619,7 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
         h8 p[RT];
         look(tile + kWaves);
         wait_loads<Ge::NI>();
-        w.scores(kt, at_lane.fresh(), s);
+        w.scores(kt, at_lane.fresh(), s, [] {});
         wait_lds();
         load_k();
         if (!all) w.mask(a, it, rt * 16 * RT, s, tile * kTile, at.page);
@@ -624,7 +629,7 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
         w.weights(s, c, p);
         if (more) wait_loads<Ge::NI>(); else wait_loads<0>();
         if (!all && clean_values<DP>(vt, at.page)) sh.odd = 1;
-        w.values(vt, at_lane.fresh(), p);
+        w.values(vt, at_lane.fresh(), p, [] {});
         wait_lds();
         load_v();
         step();
@@ -774,20 +779,29 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
           wait_lds();
           wait_loads<(kStages - 2) * 2 * kMine>();
           publish();
-          w.scores(kt, at_lane.fresh(), s);
           const int next = tile + kStages - 1;
           const uint64_t off =
               (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(page) * tk.src.page_bytes +
               (uint64_t)((uint32_t)((next * kTile + wave * 8) & tk.src.pmask) * tk.src.row_bytes);
+          // A wave's loads are spread over the step: issued at once by all waves they
+          // queue for hundreds of cycles, and the waves with them.
+          auto load = [&](int i) {
+            if (i < kMine) load_lds(to + i * 1024, tk.kp + off, at_row[i < kMine ? i : 0]);
+            else load_lds(to + Ge::BYTES + (i - kMine) * 1024, tk.vp + off, at_row[i < kMine ? 0 : i - kMine]);
+          };
+          constexpr int kQuarter = kMine >= 2 ? kMine / 2 : 1;
+          auto some = [&](int from) {
 #pragma unroll
-          for (int j = 0; j < kMine; j++) load_lds(to + j * 1024, tk.kp + off, at_row[j]);
-#pragma unroll
-          for (int j = 0; j < kMine; j++) load_lds(to + Ge::BYTES + j * 1024, tk.vp + off, at_row[j]);
+            for (int i = from * kQuarter; i < (from + 1) * kQuarter && i < 2 * kMine; i++) load(i);
+          };
+          w.scores(kt, at_lane.fresh(), s, [&] { some(0); });
+          some(1);
           page = page_of(next + 1);
           const bool raise = w.peaks(s, c, mx);
           w.reference(raise, mx, c);
           w.weights(s, c, p);
-          w.values(kt + Ge::BYTES, at_lane.fresh(), p);
+          some(2);
+          w.values(kt + Ge::BYTES, at_lane.fresh(), p, [&] { some(3); });
           tile++;
         };
         do {
@@ -808,7 +822,7 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
         else wait_loads<0>();
         publish();
         load(tile + kStages - 1);
-        w.scores(kt, at_lane.fresh(), s);
+        w.scores(kt, at_lane.fresh(), s, [] {});
         const bool all = tk.full(tile) && (tile + 1) * kTile <= min_lim;  // the same for all waves
         if (!all) {
           const int pages = tile_at(tk.src, tile * kTile).page;
@@ -818,7 +832,7 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
         const bool raise = w.peaks(s, c, mx);
         w.reference(raise, mx, c);
         w.weights(s, c, p);
-        w.values(vt, at_lane.fresh(), p);
+        w.values(vt, at_lane.fresh(), p, [] {});
       }
     }
 #pragma unroll
