@@ -48,6 +48,9 @@ struct Attn {
   int pre_splits, rest_splits, pre_tiles, rest_tiles, pre_groups, join;
   float* part;  // [pre_splits + rest_splits][n_q][H][d] sums, not divided
   float* ml;    // the same with [2]: reference exponent m, sum of weights l
+  // [n_q]: splits of the prefix and (in the upper half) of the rest that the query's
+  // sums are in, -1 if its sequence is refused; of queries that have a sequence
+  int32_t* used;
 };
 
 // Largest i in [0, n) with a[i] <= x, or -1, a ascending; every lane of the wave
@@ -77,32 +80,49 @@ struct Seq {
   bool ok;           // its row, length, queries and prefix fit together
   int row, len, pre; // table row, tokens, those of the shared prefix
   int q0, m;         // first query, queries
+  int first;         // the group's first sequence, -1 if it has no prefix
 };
 
-// Sequence s; all of it is uniform over the wave.
+// Sequence s; all of it is uniform over the wave.  Loads that do not need one
+// another are issued together, the groups' (up to 63) by the lanes: what a workgroup
+// does before its first token is a chain of latencies.
 __device__ __forceinline__ Seq sequence(const Attn& a, int s) {
   Seq q;
   q.row = row_of(a, s);
   q.q0 = a.q_starts[s];
   const int end = a.q_starts[s + 1];
-  q.pre = 0;
+  int g = -1, start = 0, next = 0, pre = 0;
+  if (a.n_groups > 0 && a.n_groups < 64) {
+    const int lane = threadIdx.x & 63;
+    const int gs = a.group_starts[min(lane, a.n_groups)];
+    const int pl = a.prefix_lens[min(lane, a.n_groups - 1)];
+    g = __popcll(__ballot(lane < a.n_groups && gs <= s)) - 1;
+    start = __builtin_amdgcn_readlane(gs, max(g, 0));
+    next = __builtin_amdgcn_readlane(gs, g + 1);
+    pre = __builtin_amdgcn_readlane(pl, max(g, 0));
+  } else if (a.n_groups) {
+    g = last_at_most(a.group_starts, a.n_groups, s);
+    start = a.group_starts[max(g, 0)];
+    next = a.group_starts[g + 1];
+    pre = a.prefix_lens[max(g, 0)];
+  }
   const bool in = q.row >= 0 && q.row < a.R;
-  q.len = in ? a.lens[q.row] : 0;
+  q.len = a.lens[in ? q.row : 0];
   q.ok = in && len_ok(a, q.len) && q.q0 >= 0 && end <= a.n_q;
-  q.m = q.ok ? end - q.q0 : 0;
-  if (a.n_groups) {
-    const int g = last_at_most(a.group_starts, a.n_groups, s);
-    if (g >= 0 && s < a.group_starts[g + 1]) {
-      const int pre = a.prefix_lens[g];
-      if (pre != 0) {
-        const int first = row_of(a, max(a.group_starts[g], 0));
-        q.ok = q.ok && pre > 0 && first >= 0 && first < a.R && a.lens[first] >= pre &&
-               len_ok(a, a.lens[first]) && (int64_t)pre + q.m <= q.len;
-        q.pre = pre;
-      }
-    }
+  q.m = end - q.q0;
+  q.pre = 0;
+  q.first = -1;
+  if (g >= 0 && s < next && pre != 0) {
+    q.pre = pre;
+    q.first = min(max(start, 0), a.n_seqs - 1);
+    q.ok = q.ok && pre > 0 && (int64_t)pre + q.m <= q.len;
   }
   return q;
+}
+
+// Whether row `row` can lend its first `pre` tokens.
+__device__ __forceinline__ bool lends(const Attn& a, int row, int pre) {
+  return row >= 0 && row < a.R && a.lens[row] >= pre && len_ok(a, a.lens[row]);
 }
 
 // Tokens [lo, hi) in tiles that start at multiples of kTile, dealt to `splits`
@@ -260,6 +280,10 @@ struct Item {
   int splits, split, least; // of the tokens; tiles of one at least
   int slot0;                // first partial of this kind
   int row_tile, row_tiles;  // this workgroup's first row tile and its stride
+  // of a sequence's rest: whether this item says where its queries' sums are, and what
+  // that takes
+  bool says, ok;
+  int pre, first, q_end;
 };
 
 // tokens that the query of a row sees
@@ -322,9 +346,6 @@ struct Wave {
   // head); rows past the item's are zeros that see everything.
   __device__ __forceinline__ void load_queries(const Attn& a, const Item& it, int row0) {
     const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    // negated queries stand for a negative scale, queries of 0 for a scale of 0, so
-    // that the largest product has the largest score
-    const uint32_t keep = a.scale == 0 ? 0 : 0xFFFFFFFFu, flip = a.scale < 0 ? 0x80008000u : 0;
 #pragma unroll
     for (int r = 0; r < RT; r++) {
       const int row = row0 + r * 16 + n;
@@ -334,18 +355,28 @@ struct Wave {
 #pragma unroll
       for (int ks = 0; ks < KS; ks++) {
         const int ch = ks * 4 + g;
-        uint4 z = in && ch < a.d / 8 ? *(const uint4*)(from + ch * 8) : uint4{0, 0, 0, 0};
-        z = uint4{(z.x & keep) ^ flip, (z.y & keep) ^ flip, (z.z & keep) ^ flip, (z.w & keep) ^ flip};
-        q[r][ks] = __builtin_bit_cast(h8, z);
+        q[r][ks] = __builtin_bit_cast(h8, in && ch < a.d / 8 ? *(const uint4*)(from + ch * 8) : uint4{0, 0, 0, 0});
       }
+    }
+    // negated queries stand for a negative scale, queries of 0 for a scale of 0, so
+    // that the largest product has the largest score and the exponent's scale is positive
+    if (a.scale <= 0) {
+      const uint32_t keep = a.scale == 0 ? 0 : 0xFFFFFFFFu, flip = a.scale < 0 ? 0x80008000u : 0;
+#pragma unroll
+      for (int r = 0; r < RT; r++)
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++) {
+          uint4 z = __builtin_bit_cast(uint4, q[r][ks]);
+          z = uint4{(z.x & keep) ^ flip, (z.y & keep) ^ flip, (z.z & keep) ^ flip, (z.w & keep) ^ flip};
+          q[r][ks] = __builtin_bit_cast(h8, z);
+        }
     }
   }
 
   // LDS operands are read in batches before the products that use them: one wait
   // for LDS instead of one per product (left to itself the compiler saves the
-  // registers).
+  // registers).  between(): called once the first batch's products are under way.
   static constexpr int KB = KS < 2 ? KS : 2, VB = NB < 4 ? NB : 4;  // of a batch
-  // between(): called once half of the products are under way.
   template <class F>
   __device__ __forceinline__ void scores(const char* kt, const Places<DP>& at, f4 (&s)[RT][2], F between) {
 #pragma unroll
@@ -868,6 +899,7 @@ __device__ __forceinline__ bool item_of(const Attn& a, int w, Item& it) {
     it.row_tile = w % a.pre_tiles;
     w /= a.pre_tiles;
     it.split = w % a.pre_splits;
+    it.says = false;
     const int grp = w / a.pre_splits;
     const int s0 = a.group_starts[grp], s1 = a.group_starts[grp + 1];
     it.lo = 0;
@@ -892,7 +924,11 @@ __device__ __forceinline__ bool item_of(const Attn& a, int w, Item& it) {
   w /= a.rest_tiles;
   it.split = w % a.rest_splits;
   const Seq q = sequence(a, w / a.rest_splits);
-  if (!q.ok || q.m <= 0) return false;
+  it.says = it.head == 0 && it.split == 0 && it.row_tile == 0;
+  it.ok = q.ok;
+  it.pre = q.pre;
+  it.first = q.first;
+  it.q_end = a.q_starts[w / a.rest_splits + 1];
   it.lo = q.pre;
   it.hi = q.len;
   it.trow = q.row;
@@ -903,7 +939,17 @@ __device__ __forceinline__ bool item_of(const Attn& a, int w, Item& it) {
   it.least = kRestTiles;
   it.slot0 = a.pre_splits;
   it.row_tiles = a.rest_tiles;
-  return true;
+  return q.ok && q.m > 0;
+}
+
+// For the join: where the sums of a sequence's queries are.
+__device__ __forceinline__ void say_used(const Attn& a, const Item& it) {
+  const bool ok = it.ok && (it.first < 0 || lends(a, row_of(a, it.first), it.pre));
+  const int used = ok ? split_of(0, it.pre, a.pre_splits, kPreTiles).used |
+                            split_of(it.pre, it.hi, a.rest_splits, kRestTiles).used << 16
+                      : -1;
+  for (int i = max(it.q0, 0) + (int)threadIdx.x; i < min(it.q_end, a.n_q); i += blockDim.x) a.used[i] = used;
+  if (!ok && threadIdx.x == 0 && it.q0 < it.q_end) atomicOr(a.status, kRefused);
 }
 
 // How an item's workgroup holds rows: all of 16 or 32 in each of four waves, which
@@ -927,9 +973,12 @@ __global__ __launch_bounds__(kBlock, resident(DP)) void k_attention(Attn a, int 
   __shared__ Shared<DP, 4, kTiles> sh;
   for (int w = first + blockIdx.x; w < end; w += gridDim.x) {
     Item it;
-    if (!item_of(a, w, it)) continue;
-    if (PRE == REST || it.slot0 == 0) run_item<DP, PRE>(a, it, sh);
-    else run_item<DP, REST>(a, it, sh);
+    const bool go = item_of(a, w, it);
+    if (go) {
+      if (PRE == REST || it.slot0 == 0) run_item<DP, PRE>(a, it, sh);
+      else run_item<DP, REST>(a, it, sh);
+    }
+    if (it.says) say_used(a, it);
   }
 }
 
@@ -940,12 +989,10 @@ __global__ __launch_bounds__(kThreads) void k_join(Attn a) {
   __shared__ f4 sums[kThreads];
   __shared__ float ls[kThreads];
   const int qi = blockIdx.x, tid = threadIdx.x;
-  const int s = last_at_most(a.q_starts, a.n_seqs, qi);
-  if (s < 0 || qi < a.q_starts[s] || qi >= a.q_starts[s + 1]) return;
-  const Seq q = sequence(a, s);
-  if (!q.ok && tid == 0) atomicOr(a.status, kRefused);
-  const int pre = q.ok ? split_of(0, q.pre, a.pre_splits, kPreTiles).used : 0;
-  const int used = pre + (q.ok ? split_of(q.pre, q.len, a.rest_splits, kRestTiles).used : 0);
+  const int from = a.q_starts[0], to = a.q_starts[a.n_seqs], said = a.used[qi];
+  if (qi < from || qi >= to) return;  // no sequence's query
+  const int pre = said < 0 ? 0 : min(said & 0xFFFF, a.pre_splits);
+  const int used = said < 0 ? 0 : pre + min(said >> 16, a.rest_splits);
   const int quads = a.d / 4, unit = tid / quads, quad = tid % quads;
   const int heads = kThreads / quads / a.join;  // of a workgroup
   const int part = unit % a.join, hl = unit / a.join, h = blockIdx.y * heads + hl;
@@ -1066,7 +1113,7 @@ Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
   }
   p.rest_splits = splits((int64_t)std::max(1, x.n_seqs) * kv * p.rest_tiles,
                          std::max(0, x.max_len - (shared ? x.max_prefix : 0)), slots, kRestTiles);
-  p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + 4;
+  p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + x.n_q + 4;
   return p;
 }
 
@@ -1148,6 +1195,7 @@ int cg_attention_prefix_async(const cg_paged_cache* c, const cg_attention* a, vo
   v.pre_groups = p.pre_groups;
   v.part = (float*)workspace_dev;
   v.ml = v.part + (size_t)(p.pre_splits + p.rest_splits) * a->n_q * a->n_heads * a->head_dim;
+  v.used = (int32_t*)(v.ml + (size_t)2 * (p.pre_splits + p.rest_splits) * a->n_q * a->n_heads);
   const int64_t pre = (int64_t)p.pre_groups * p.pre_splits * p.pre_tiles * v.kv;
   const int64_t rest = (int64_t)a->n_seqs * p.rest_splits * p.rest_tiles * v.kv;
   hipStream_t st = (hipStream_t)stream;
