@@ -53,6 +53,14 @@ struct Attn {
   int32_t* used;
 };
 
+// The same for kernels in which one item has all of its queries' tokens (the
+// prefix's, unshared, and then the rest's), writes the outputs itself and nothing is
+// joined.  Their own kernels: the tests for it cost the others 5%.
+template <bool kDirect>
+struct Call : Attn {
+  static constexpr bool direct = kDirect;
+};
+
 // Largest i in [0, n) with a[i] <= x, or -1, a ascending; every lane of the wave
 // gets it.  64 samples a step: one round of loads up to n = 64, two up to 4,096.
 __device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {
@@ -284,7 +292,40 @@ struct Item {
   // that takes
   bool says, ok;
   int pre, first, q_end;
+  int lender;               // direct: table row that the first `pre` tokens are read through
 };
+
+__device__ __forceinline__ int64_t part_at(const Attn& a, const Item& it, int row) {
+  return ((int64_t)(it.slot0 + it.split) * a.n_q + it.q0 + row / a.G) * a.H + it.head * a.G + row % a.G;
+}
+
+// The two stretches of tokens of a direct item, or an item's only one.
+template <class A>
+__device__ __forceinline__ int ranges_of(const A& a, const Item& it) { return a.direct && it.pre > 0 ? 2 : 1; }
+__device__ __forceinline__ Item range_of(const Item& it, int ranges, int i) {
+  Item r = it;
+  if (ranges == 2 && i == 0) {
+    r.lo = 0;
+    r.hi = it.pre;
+    r.trow = it.lender;
+  }
+  return r;
+}
+__device__ __forceinline__ uint16_t* out_at(const Attn& a, const Item& it, int row) {
+  return a.out + (it.q0 + row / a.G) * a.out_stride + (int64_t)(it.head * a.G + row % a.G) * a.d;
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945309f;
+}
+__device__ __forceinline__ void store_out(uint16_t* to, f4 x) {  // 4 channels
+  ushort4 r;
+  r.x = float_to_half_bits(x[0]);
+  r.y = float_to_half_bits(x[1]);
+  r.z = float_to_half_bits(x[2]);
+  r.w = float_to_half_bits(x[3]);
+  *(ushort4*)to = r;
+}
+
 
 // tokens that the query of a row sees
 __device__ __forceinline__ int row_lim(const Attn& a, const Item& it, int row) {
@@ -557,54 +598,68 @@ struct Tokens {
   __device__ __forceinline__ bool full(int tile) const {  // every token of the tile exists
     return !bad && tile * kTile >= src.lo && (tile + 1) * kTile <= src.hi;
   }
+  // tiles behind this one nobody up to row `row` sees
+  __device__ __forceinline__ int seen_end(const Attn& a, const Item& it, int row) const {
+    return min(last, (row_lim(a, it, row) + kTile - 1) / kTile);
+  }
+  // After the sums of rows [row0, row1) are stored: what clean_values() took out, for the
+  // rows that see it (a sum with such a value is an infinity or no number whatever
+  // the weight, and stays so where the value was counted already).  Rare, and slow.
+  template <int kThreads, class A>
+  __device__ __forceinline__ void add_odd(const A& a, const Item& it, Sh& sh, int ranges, int row0, int row1) {
+    const int tid = kThreads - 1 - threadIdx.x;  // nothing here is worth sharing with the loops above
+    row1 = min(row1, it.rows);
+#pragma unroll 1
+    for (int range = 0; range < ranges; range++) {
+      const Item cur = range_of(it, ranges, range);
+      if (!start(a, cur, sh)) continue;
+      const int end = min(seen_end(a, cur, row1 - 1) * kTile, cur.hi);
+#pragma unroll 1
+      for (int t = max(first * kTile, cur.lo); t < end; t++) {
+        const int page = a.tables[(int64_t)cur.trow * a.B + (t >> a.shift)];
+        if (page < 0 || page >= a.N) continue;
+        const char* v = vp + (uint64_t)(uint32_t)page * src.page_bytes +
+                        (uint64_t)(uint32_t)(t & src.pmask) * src.row_bytes;
+#pragma unroll 1
+        for (int ch = tid; ch < a.d; ch += kThreads) {
+          const float x = half_bits_to_float(((const uint16_t*)v)[ch]);
+          if (x - x == 0.0f) continue;
+#pragma unroll 1
+          for (int row = row0; row < row1; row++) {
+            if (t >= row_lim(a, cur, row)) continue;
+            if (a.direct) {
+              uint16_t* to = out_at(a, it, row) + ch;
+              *to = float_to_half_bits(half_bits_to_float(*to) + x);
+            } else {
+              a.part[part_at(a, it, row) * a.d + ch] += x;
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
 };
 
 // The exponent's scale: scores are c (q . k) in units of log 2.
 __device__ __forceinline__ float log2_scale(const Attn& a) {
   return a.scale == 0 ? 1.0f : fminf(fabsf(a.scale) * 1.44269504088896341f, 3.4e38f);
 }
-__device__ __forceinline__ int64_t part_at(const Attn& a, const Item& it, int row) {
-  return ((int64_t)(it.slot0 + it.split) * a.n_q + it.q0 + row / a.G) * a.H + it.head * a.G + row % a.G;
-}
-
-// After the sums of rows [row0, row1) are stored: what clean_values() took out of
-// tiles [first, end), for the rows that see it (a sum with such a value is an
-// infinity or no number whatever the weight, and stays so where the value was
-// counted already).  Rare, and slow.
-template <int kThreads, class Tk>
-__device__ __forceinline__ void add_odd_values(const Attn& a, const Item& it, const Tk& tk, int first, int end,
-                                               int row0, int row1) {
-  const int tid = kThreads - 1 - threadIdx.x;  // nothing here is worth sharing with the loops above
-#pragma unroll 1
-  for (int t = max(first * kTile, it.lo); t < min(end * kTile, it.hi); t++) {
-    const int page = a.tables[(int64_t)it.trow * a.B + (t >> a.shift)];
-    if (page < 0 || page >= a.N) continue;
-    const char* v = tk.vp + (uint64_t)(uint32_t)page * tk.src.page_bytes +
-                    (uint64_t)(uint32_t)(t & tk.src.pmask) * tk.src.row_bytes;
-#pragma unroll 1
-    for (int ch = tid; ch < a.d; ch += kThreads) {
-      const float x = half_bits_to_float(((const uint16_t*)v)[ch]);
-      if (x - x == 0.0f) continue;
-#pragma unroll 1
-      for (int row = row0; row < row1; row++)
-        if (t < row_lim(a, it, row)) a.part[part_at(a, it, row) * a.d + ch] += x;
-    }
-  }
-}
 
 // Few rows: every wave holds all 16 RT of a row tile and takes the split's token
 // tiles in turn; the waves share nothing until the end.  Each has room for one tile
 // of K and one of V: the next K is on its way while the weights and the values are
 // computed, the next V while the scores are.
-template <int DP, int RT, int kWaves>
-__device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<DP, kWaves, kWaves>& sh) {
+template <int DP, int RT, int kWaves, class A>
+__device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP, kWaves, kWaves>& sh) {
   constexpr int kThreads = 64 * kWaves;
   using Ge = Geo<DP>;
   using W = Wave<DP, RT>;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   Tokens<DP, Shared<DP, kWaves, kWaves>> tk;
-  if (!tk.start(a, it, sh)) return;
+  if (!a.direct && !tk.start(a, it, sh)) return;
+  const int ranges = ranges_of(a, it);
   const Places<DP> at_lane;
   char *kt = sh.tile[wave][0], *vt = sh.tile[wave][1];
   const uint32_t klds = lds_address(kt), vlds = klds + Ge::BYTES;
@@ -615,14 +670,17 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
     W w;
     w.clear();
     w.load_queries(a, it, rt * 16 * RT);
-    const int min_lim = row_lim(a, it, rt * 16 * RT);
-    const int max_lim = row_lim(a, it, (rt + 1) * 16 * RT - 1);
-    const int end = min(tk.last, (max_lim + kTile - 1) / kTile);  // later tiles: nobody sees them
     tk.clear_tiles(a, sh);
     if (threadIdx.x == 0) sh.odd = 0;
+#pragma unroll 1
+    for (int range = 0; range < ranges; range++) {
+    const Item cur = range_of(it, ranges, range);
+    if (a.direct && !tk.start(a, cur, sh)) continue;
+    const int min_lim = row_lim(a, cur, rt * 16 * RT);
+    const int end = tk.seen_end(a, cur, (rt + 1) * 16 * RT - 1);
     for (int base = tk.first; base < end; base += tk.list_tiles) {
       const int stop = min(base + tk.list_tiles, end);
-      tk.stretch(a, it, sh, base, stop);
+      tk.stretch(a, cur, sh, base, stop);
       // the tile in hand, where its tokens are, whether its queries see all of it; the
       // next one
       int tile = base + wave, next;
@@ -653,7 +711,7 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
         w.scores(kt, at_lane.fresh(), s, [] {});
         wait_lds();
         load_k();
-        if (!all) w.mask(a, it, rt * 16 * RT, s, tile * kTile, at.page);
+        if (!all) w.mask(a, cur, rt * 16 * RT, s, tile * kTile, at.page);
         float mx[RT];
         const bool raise = w.peaks(s, c, mx);
         w.reference(raise, mx, c);
@@ -665,6 +723,7 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
         load_v();
         step();
       }
+    }
     }
     // the waves' sums together, against the largest reference exponent
 #pragma unroll
@@ -692,7 +751,11 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
         l += f * sh.l[x][tid];
       }
       const int row = rt * 16 * RT + tid;
-      if (row < it.rows) {
+      if (a.direct) {
+        sh.l[0][tid] = l == 0.0f ? 0.0f : 1.0f / l;
+        if (row < it.rows && a.lse)
+          a.lse[(int64_t)(it.q0 + row / a.G) * a.H + it.head * a.G + row % a.G] = lse_of(m, l);
+      } else if (row < it.rows) {
         const int64_t at = part_at(a, it, row);
         a.ml[2 * at] = m;
         a.ml[2 * at + 1] = l;
@@ -722,11 +785,12 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
 #pragma unroll
         for (int y = 0; y < kWaves; y++)
           x += sh.scale[y][row] * sums[(y * 16 * RT + row) * kQuads + ((quad + row) & (kQuads - 1))];
-        *(f4*)(a.part + part_at(a, it, gr) * a.d + ch) = x;
+        if (a.direct) store_out(out_at(a, it, gr) + ch, x * sh.l[0][row]);
+        else *(f4*)(a.part + part_at(a, it, gr) * a.d + ch) = x;
       }
     }
     __syncthreads();  // m, l and scale are free
-    if (sh.odd) add_odd_values<kThreads>(a, it, tk, tk.first, end, rt * 16 * RT, min(it.rows, (rt + 1) * 16 * RT));
+    if (sh.odd) tk.template add_odd<kThreads>(a, it, sh, ranges, rt * 16 * RT, (rt + 1) * 16 * RT);
     __syncthreads();
   }
 }
@@ -734,8 +798,8 @@ __device__ __forceinline__ void run_split(const Attn& a, const Item& it, Shared<
 // Many rows: a wave holds 16 RT of the 16 RT kWaves rows, all waves read the same token
 // tiles from a ring; each loads its part of a tile, kStages - 2 tiles ahead, and one
 // barrier a tile both publishes it and frees the slot that is filled next.
-template <int DP, int RT, int kWaves, int kStages>
-__device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<DP, kWaves, kStages>& sh) {
+template <int DP, int RT, int kWaves, int kStages, class A>
+__device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, kWaves, kStages>& sh) {
   constexpr int kThreads = 64 * kWaves;
   using Ge = Geo<DP>;
   using W = Wave<DP, RT>;
@@ -744,7 +808,8 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Tokens<DP, Shared<DP, kWaves, kStages>> tk;
-  if (!tk.start(a, it, sh)) return;
+  if (!a.direct && !tk.start(a, it, sh)) return;
+  const int ranges = ranges_of(a, it);
   const Places<DP> at_lane;
   const uint32_t lds = lds_address(sh.tile);
   const float c = log2_scale(a);
@@ -755,14 +820,17 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
     W w;
     w.clear();
     w.load_queries(a, it, row0);
-    const int min_lim = row_lim(a, it, rt * tile_rows);
-    const int max_lim = row_lim(a, it, (rt + 1) * tile_rows - 1);
-    const int end = min(tk.last, (max_lim + kTile - 1) / kTile);
     tk.clear_tiles(a, sh);
     if (threadIdx.x == 0) sh.odd = 0;
+#pragma unroll 1
+    for (int range = 0; range < ranges; range++) {
+    const Item cur = range_of(it, ranges, range);
+    if (a.direct && !tk.start(a, cur, sh)) continue;
+    const int min_lim = row_lim(a, cur, rt * tile_rows);
+    const int end = tk.seen_end(a, cur, (rt + 1) * tile_rows - 1);
     for (int base = tk.first; base < end; base += tk.list_tiles) {
       const int stop = min(base + tk.list_tiles, end);
-      tk.stretch(a, it, sh, base, stop);
+      tk.stretch(a, cur, sh, base, stop);
       char* ring = sh.tile[0][0];
       auto slot_of = [&](int tile) { return (tile - base) & (kStages - 1); };
       auto load = [&](int tile) {
@@ -787,9 +855,9 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
       // of its time on them and on addresses: 165 us against 128 for 32 requests on 81920
       // tokens.)
       int tile = base;
-      const int seen = tk.bad || base * kTile < it.lo ? base : min(stop, min_lim / kTile);
+      const int seen = tk.bad || base * kTile < cur.lo ? base : min(stop, min_lim / kTile);
       if (tk.src.pmask >= 7 && tk.src.nc == Ge::NC && tile + 2 * kStages - 1 <= seen) {
-        const int last_page = ((min(stop * kTile, it.hi) - 1) >> tk.src.shift) - tk.src.block0;
+        const int last_page = ((min(stop * kTile, cur.hi) - 1) >> tk.src.shift) - tk.src.block0;
         auto page_of = [&](int tl) {
           return sh.list[min(((tl * kTile + wave * 8) >> tk.src.shift) - tk.src.block0, last_page)];
         };
@@ -857,7 +925,7 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
         const bool all = tk.full(tile) && (tile + 1) * kTile <= min_lim;  // the same for all waves
         if (!all) {
           const int pages = tile_at(tk.src, tile * kTile).page;
-          w.mask(a, it, row0, s, tile * kTile, pages);
+          w.mask(a, cur, row0, s, tile * kTile, pages);
           if (clean_values<DP>(vt, pages)) sh.odd = 1;
         }
         const bool raise = w.peaks(s, c, mx);
@@ -866,6 +934,7 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
         w.values(vt, at_lane.fresh(), p, [] {});
       }
     }
+    }
 #pragma unroll
     for (int r = 0; r < RT; r++) {
       float l = w.l[r];
@@ -873,6 +942,16 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
       l += __shfl_xor(l, 32);
       const int row = row0 + r * 16 + n;
       if (row >= it.rows) continue;
+      if (a.direct) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* to = out_at(a, it, row);
+#pragma unroll
+        for (int b = 0; b < W::NB; b++)
+          if (b * 16 + g * 4 < a.d) store_out(to + b * 16 + g * 4, w.o[r][b] * inv);
+        if (g == 0 && a.lse)
+          a.lse[(int64_t)(it.q0 + row / a.G) * a.H + it.head * a.G + row % a.G] = lse_of(w.m[r], l);
+        continue;
+      }
       const int64_t at = part_at(a, it, row);
       if (g == 0) {
         a.ml[2 * at] = w.m[r];
@@ -883,7 +962,7 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
         if (b * 16 + g * 4 < a.d) *(f4*)(a.part + at * a.d + b * 16 + g * 4) = w.o[r][b];
     }
     __syncthreads();
-    if (sh.odd) add_odd_values<kThreads>(a, it, tk, tk.first, end, rt * tile_rows, min(it.rows, (rt + 1) * tile_rows));
+    if (sh.odd) tk.template add_odd<kThreads>(a, it, sh, ranges, rt * tile_rows, (rt + 1) * tile_rows);
     __syncthreads();
   }
 }
@@ -891,7 +970,8 @@ __device__ __forceinline__ void run_ring(const Attn& a, const Item& it, Shared<D
 // The w-th item of the launch: first (group, split, row tile, kv head), kv heads
 // fastest, for the shared prefixes, then the same per sequence for what lies behind
 // them.  False: nothing to do.
-__device__ __forceinline__ bool item_of(const Attn& a, int w, Item& it) {
+template <class A>
+__device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
   it.head = w % a.kv;
   w /= a.kv;
   const int pre_items = a.pre_groups * a.pre_splits * a.pre_tiles;
@@ -939,7 +1019,24 @@ __device__ __forceinline__ bool item_of(const Attn& a, int w, Item& it) {
   it.least = kRestTiles;
   it.slot0 = a.pre_splits;
   it.row_tiles = a.rest_tiles;
-  return q.ok && q.m > 0;
+  if (a.direct && q.first >= 0) {
+    it.lender = row_of(a, q.first);
+    it.ok = q.ok && lends(a, it.lender, q.pre);
+  }
+  return it.ok && q.m > 0;
+}
+
+// Direct: outputs of a refused sequence's queries, of the item's kv head.
+__device__ __forceinline__ void refuse(const Attn& a, const Item& it) {
+  if (it.row_tile != 0) return;
+  const int n = a.G * a.d;
+  for (int q = max(it.q0, 0); q < min(it.q_end, a.n_q); q++) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+      a.out[q * a.out_stride + (int64_t)it.head * n + i] = 0;
+    for (int i = threadIdx.x; a.lse && i < a.G; i += blockDim.x)
+      a.lse[(int64_t)q * a.H + it.head * a.G + i] = -__builtin_inff();
+  }
+  if (it.says && threadIdx.x == 0 && it.q0 < it.q_end) atomicOr(a.status, kRefused);
 }
 
 // For the join: where the sums of a sequence's queries are.
@@ -960,16 +1057,16 @@ constexpr int kBlock = 256, kTiles = 4;
 // workgroups on a compute unit, as LDS and registers allow
 __host__ __device__ constexpr int resident(int dp) { return dp == 256 ? 1 : 2; }
 
-template <int DP, int MODE>
-__device__ __forceinline__ void run_item(const Attn& a, const Item& it, Shared<DP, 4, kTiles>& sh) {
+template <int DP, int MODE, class A>
+__device__ __forceinline__ void run_item(const A& a, const Item& it, Shared<DP, 4, kTiles>& sh) {
   if constexpr (MODE <= kRows32) run_split<DP, 1 + MODE, 4>(a, it, sh);
   else run_ring<DP, MODE == kRows128 ? 2 : 1, 4, kTiles>(a, it, sh);
 }
 
 // Items of the shared prefixes and of the rest in one launch: the former keep the
 // matrix cores busy, the latter HBM.
-template <int DP, int PRE, int REST>
-__global__ __launch_bounds__(kBlock, resident(DP)) void k_attention(Attn a, int first, int end) {
+template <int DP, int PRE, int REST, bool kDirect>
+__global__ __launch_bounds__(kBlock, resident(DP)) void k_attention(Call<kDirect> a, int first, int end) {
   __shared__ Shared<DP, 4, kTiles> sh;
   for (int w = first + blockIdx.x; w < end; w += gridDim.x) {
     Item it;
@@ -978,7 +1075,11 @@ __global__ __launch_bounds__(kBlock, resident(DP)) void k_attention(Attn a, int 
       if (PRE == REST || it.slot0 == 0) run_item<DP, PRE>(a, it, sh);
       else run_item<DP, REST>(a, it, sh);
     }
-    if (it.says) say_used(a, it);
+    if (a.direct) {
+      if (!it.ok) refuse(a, it);
+    } else if (it.says) {
+      say_used(a, it);
+    }
   }
 }
 
@@ -1030,43 +1131,41 @@ __global__ __launch_bounds__(kThreads) void k_join(Attn a) {
     return;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  ushort4 r;
-  r.x = float_to_half_bits(o[0] * inv);
-  r.y = float_to_half_bits(o[1] * inv);
-  r.z = float_to_half_bits(o[2] * inv);
-  r.w = float_to_half_bits(o[3] * inv);
-  *(ushort4*)(a.out + qi * a.out_stride + (int64_t)h * a.d + quad * 4) = r;
-  if (quad == 0 && a.lse)
-    a.lse[(int64_t)qi * a.H + h] = l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945309f;
+  store_out(a.out + qi * a.out_stride + (int64_t)h * a.d + quad * 4, o * inv);
+  if (quad == 0 && a.lse) a.lse[(int64_t)qi * a.H + h] = lse_of(m, l);
 }
 
 // How many splits and row tiles the launch has, from the call's numbers alone.
 struct Plan {
   int dp, pre_splits, rest_splits, pre_tiles, rest_tiles, pre_mode, rest_mode, pre_groups;
+  bool direct;
   size_t words;
 };
 
 // Items first .. end - 1 of the launch's list, if there is a kernel for both kinds.
 template <int DP>
-bool launch(int pre, int rest, const Attn& a, int64_t first, int64_t end, hipStream_t st) {
+bool launch(bool direct, int pre, int rest, const Attn& a, int64_t first, int64_t end, hipStream_t st) {
   if (end <= first) return true;
   const int grid = (int)std::min<int64_t>(end - first, 1 << 22);
-#define GO(PRE, REST)                                                                    \
-  if (pre == PRE && rest == REST) {                                                      \
-    k_attention<DP, PRE, REST><<<grid, kBlock, 0, st>>>(a, (int)first, (int)end);        \
+#define GO(PRE, REST, DIRECT)                                                            \
+  if (direct == DIRECT && pre == PRE && rest == REST) {                                  \
+    k_attention<DP, PRE, REST, DIRECT><<<grid, kBlock, 0, st>>>({a}, (int)first, (int)end); \
     return true;                                                                         \
   }
-  GO(kRows16, kRows16) GO(kRows64, kRows64) GO(kRows64, kRows16)
+  GO(kRows16, kRows16, false) GO(kRows64, kRows64, false) GO(kRows64, kRows16, false)
+  GO(kRows16, kRows16, true) GO(kRows64, kRows64, true)
   if constexpr (DP <= 128) {
-    GO(kRows32, kRows32) GO(kRows128, kRows128) GO(kRows32, kRows16) GO(kRows128, kRows16)
-    GO(kRows64, kRows32) GO(kRows128, kRows32)
+    GO(kRows32, kRows32, false) GO(kRows128, kRows128, false) GO(kRows32, kRows16, false)
+    GO(kRows128, kRows16, false) GO(kRows64, kRows32, false) GO(kRows128, kRows32, false)
+    GO(kRows32, kRows32, true) GO(kRows128, kRows128, true)
   }
 #undef GO
   return false;
 }
-bool launch(int dp, int pre, int rest, const Attn& a, int64_t first, int64_t end, hipStream_t st) {
-  return dp == 64 ? launch<64>(pre, rest, a, first, end, st)
-         : dp == 128 ? launch<128>(pre, rest, a, first, end, st) : launch<256>(pre, rest, a, first, end, st);
+bool launch(int dp, bool direct, int pre, int rest, const Attn& a, int64_t first, int64_t end, hipStream_t st) {
+  return dp == 64    ? launch<64>(direct, pre, rest, a, first, end, st)
+         : dp == 128 ? launch<128>(direct, pre, rest, a, first, end, st)
+                     : launch<256>(direct, pre, rest, a, first, end, st);
 }
 
 // The smallest that holds `rows`.  Waves of 32 rows of 256 channels would not fit
@@ -1113,6 +1212,18 @@ Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
   }
   p.rest_splits = splits((int64_t)std::max(1, x.n_seqs) * kv * p.rest_tiles,
                          std::max(0, x.max_len - (shared ? x.max_prefix : 0)), slots, kRestTiles);
+  // Sharing saves (sequences - 1) times the prefix and costs a second kernel and its
+  // start, about 5 us: not for little.
+  const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
+  p.direct = saved <= (int64_t)16 << 20 && x.max_prefix <= 512 &&
+             splits((int64_t)std::max(1, x.n_seqs) * kv * p.rest_tiles, x.max_len, slots, kRestTiles) == 1;
+  if (p.direct) {
+    p.pre_groups = 0;
+    p.pre_splits = 0;
+    p.rest_splits = 1;
+    p.words = 4;
+    return p;
+  }
   p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + x.n_q + 4;
   return p;
 }
@@ -1200,9 +1311,13 @@ int cg_attention_prefix_async(const cg_paged_cache* c, const cg_attention* a, vo
   const int64_t rest = (int64_t)a->n_seqs * p.rest_splits * p.rest_tiles * v.kv;
   hipStream_t st = (hipStream_t)stream;
   const int only = pre ? p.pre_mode : p.rest_mode;
-  if (!launch(p.dp, only, p.rest_mode, v, 0, pre + rest, st)) {  // unusual pairs: one after the other
-    launch(p.dp, p.pre_mode, p.pre_mode, v, 0, pre, st);
-    launch(p.dp, p.rest_mode, p.rest_mode, v, pre, pre + rest, st);
+  if (!launch(p.dp, p.direct, only, p.rest_mode, v, 0, pre + rest, st)) {  // unusual pairs: one after the other
+    launch(p.dp, false, p.pre_mode, p.pre_mode, v, 0, pre, st);
+    launch(p.dp, false, p.rest_mode, p.rest_mode, v, pre, pre + rest, st);
+  }
+  if (p.direct) {
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? CG_OK : hip_fail(e, "attention");
   }
   const int total = p.pre_splits + p.rest_splits;
   v.join = std::min(total <= 2 ? 1 : total <= 8 ? 2 : 8, kThreads / (v.d / 4));

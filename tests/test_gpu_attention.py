@@ -104,6 +104,11 @@ def check(x, layer, q, scale, rows, q_starts, group_starts=None, prefix_lens=Non
     got = gpu_attention(x, layer, q, scale, rows, q_starts, group_starts, prefix_lens, **kw)
     want = pc.attention(x.o, layer, q, scale, rows, q_starts, group_starts, prefix_lens)
     compare(got, want, q)
+    if not kw:  # and as a long context is computed: prefixes shared, tokens split, sums joined
+        most = max(1, int(np.max(np.diff(q_starts), initial=0)))
+        for hints in ((most, 1 << 20, 1 << 21), (most, 0, 1 << 21)):
+            compare(gpu_attention(x, layer, q, scale, rows, q_starts, group_starts, prefix_lens, hints=hints),
+                    want, q)
     return got
 
 
@@ -195,6 +200,71 @@ def test_group_of_many():
     counts = rng.integers(0, 4, 70)
     q = queries(rng, int(counts.sum()), 8, 64)
     check(x, 0, q, 0.125, rows, starts_of(counts), [0, 70], [333])
+
+
+@pytest.mark.parametrize("kv,G,d,P,prefix,seqs", [
+    (2, 4, 128, 16, 1500, 40), (1, 8, 128, 8, 1111, 20), (1, 3, 64, 64, 2047, 25), (1, 5, 64, 8, 1300, 50),
+    (2, 2, 256, 16, 1200, 40), (1, 6, 80, 16, 1055, 30), (1, 4, 128, 1, 1100, 33), (1, 5, 96, 4, 700, 30),
+    (1, 4, 128, 4, 900, 12), (1, 2, 256, 128, 1900, 9), (4, 8, 64, 32, 3200, 16)])
+def test_long_shared_prefix(kv, G, d, P, prefix, seqs):
+    """The rounds of a ring of tiles over several splits, for each width of head and
+    number of rows, pages that they take and that they do not."""
+    rng = np.random.default_rng(prefix + d)
+    tails = [[int(n) for n in rng.integers(2, 60, seqs)]]
+    c, rows = build(rng, 1, kv * d, P, [prefix], tails)
+    x = Pair(c)
+    counts = rng.integers(0, 3, seqs)
+    q = queries(rng, int(counts.sum()), kv * G, d)
+    check(x, 0, q, d ** -0.5, rows, starts_of(counts), [0, seqs], [prefix])
+    # a page of the prefix outside the pool, in the middle of a round
+    c.tables[rows[0], (prefix // 2) // P] = -1
+    check(Pair(c), 0, q, d ** -0.5, rows, starts_of(counts), [0, seqs], [prefix])
+
+
+@pytest.mark.parametrize("d,G,P", [(128, 4, 16), (64, 9, 8), (256, 2, 32), (72, 3, 16)])
+def test_long_prompts(d, G, P):
+    """Sequences whose queries are a prompt of hundreds of tokens, behind a context."""
+    rng = np.random.default_rng(d)
+    tails = [[300, 140], [33]]
+    c, rows = build(rng, 1, d, P, [420, 64], tails)
+    counts = [260, 131, 33]
+    q = queries(rng, sum(counts), G, d)
+    check(Pair(c), 0, q, d ** -0.5, rows, starts_of(counts), [0, 2, 3], [420, 64])
+    check(Pair(c), 0, q, d ** -0.5, rows, starts_of(counts))
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_masked_places_in_many_rows(bad):
+    """Values that are no finite number in a prompt's own tokens: the queries before
+    them are not touched, those behind them get what the formula says."""
+    rng = np.random.default_rng(21)
+    c, rows = build(rng, 1, 128, 16, [300], [[200, 90]])
+    want = c.copy()
+    counts = [150, 70]
+    hit = {0: [100, 120], 1: [40]}  # queries of a sequence whose own token is bad
+    for s, js in hit.items():
+        for j in js:
+            t = int(c.lens[rows[s]]) - counts[s] + j
+            c.v[0, c.tables[rows[s], t // 16], t % 16, ::5] = bad
+    x = Pair(c)
+    q = queries(rng, sum(counts), 4, 64)
+    base = [0, counts[0]]
+    _, recs = pc.attention(want, 0, q, 0.125, rows, starts_of(counts), [0, 2], [300])
+    spoilt = np.zeros(128, bool)
+    spoilt[::5] = True
+    for hints in (None, (150, 1 << 20, 1 << 21), (150, 0, 1 << 21)):
+        st, out, lse = gpu_attention(x, 0, q, 0.125, rows, starts_of(counts), [0, 2], [300], hints=hints)
+        assert st == 0
+        for s in (0, 1):
+            first = base[s] + min(hit[s])
+            for j in range(base[s], base[s] + counts[s]):
+                for h in range(4):
+                    ch = spoilt[64 * (h // 2):64 * (h // 2) + 64]
+                    if j >= first:  # those channels, and no other
+                        assert not np.isfinite(out[j, h][ch]).any()
+                        out[j, h][ch] = recs[j][h]["out"][ch]
+                    assert np.isfinite(out[j, h]).all()
+        compare((st, out, lse), (0, recs), q)
 
 
 def test_rows_default_and_empty_rows():
