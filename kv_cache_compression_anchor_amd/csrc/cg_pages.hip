@@ -5,7 +5,7 @@
 // sums over the requests and over refs; each call does it in one workgroup of
 // 1,024 threads, so that one launch suffices and page numbers do not depend on
 // scheduling.  Moving K and V is a plain copy bound by HBM; it is cut into
-// pieces of kPieceUnits units spread over the chip.
+// pieces spread over the chip.
 #include <algorithm>
 
 #include "cg_hostapi.h"
@@ -15,11 +15,15 @@
 namespace cg {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kThreads = 1024;            // of a bookkeeping workgroup
 constexpr int kWaves = kThreads / 64;
 constexpr int kScanPages = 16 * kThreads; // pages of refs looked at per scan step
 constexpr int kCopyThreads = 256;
-constexpr int kPieceUnits = 2048;         // units a copying workgroup moves per piece
+// Units a copying workgroup moves per piece: four loads in flight a thread where there
+// is enough to do, one where workgroups are scarce.
+constexpr int kPieceMost = 4 * kCopyThreads, kPieceLeast = kCopyThreads;
 constexpr uint32_t kBadPage = 2u, kRefused = 4u, kNoPages = 8u;  // status bits
 
 struct Cache {  // the device side's view of cg_paged_cache
@@ -63,39 +67,58 @@ __device__ int64_t block_scan(int64_t x, ScanLds& s, int64_t* total) {
   return base + inc - x;
 }
 
-// Calls f(page, rank) for every page in [from, to) that is free (kFree) or in use
-// (!kFree), rank in ascending order, until `limit` were found; returns how many
-// there are up to where it stopped.  A wave looks at 1,024 consecutive pages per
-// step: 16 coalesced loads in flight, one ballot each.
+// A wave's share of a scan step: 1,024 consecutive pages, 16 coalesced loads in flight.
+struct Counts {
+  int32_t r[16];
+  __device__ __forceinline__ static int page(int base, int i) {
+    return base + (threadIdx.x >> 6) * 1024 + lane_id() + 64 * i;
+  }
+  __device__ __forceinline__ void load(const int32_t* refs, int base, int to) {
+#pragma unroll
+    for (int i = 0; i < 16; i++) r[i] = page(base, i) < to ? refs[page(base, i)] : -1;
+  }
+};
+
+// Calls f(page, rank) for those of a step's pages in [from, to) that are free (kFree) or
+// in use (!kFree), rank in ascending order from `found` on; returns how many.
 template <bool kFree, class F>
-__device__ int scan_pages(const int32_t* refs, int from, int to, int limit, ScanLds& s, F f) {
+__device__ __forceinline__ int scan_step(const Counts& c, int base, int from, int to, int found, ScanLds& s, F f) {
+  uint64_t hit[16];
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    const int p = Counts::page(base, i);
+    hit[i] = __ballot(p >= from && p < to && (kFree ? c.r[i] == 0 : c.r[i] > 0));
+    n += __popcll(hit[i]);
+  }
+  int64_t all;
+  const int at = (int)block_scan(lane_id() == 0 ? n : 0, s, &all);
+  int rank = found + __shfl(at, 0);
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    if ((hit[i] >> lane_id()) & 1) f(Counts::page(base, i), rank + below(hit[i]));
+    rank += __popcll(hit[i]);
+  }
+  return (int)all;
+}
+
+// The same for all steps of [from, to), until `limit` were found; returns how many
+// there are up to where it stopped.  first: the first step's counts, loaded before.
+template <bool kFree, class F>
+__device__ int scan_pages(const int32_t* refs, const Counts& first, int from, int to, int limit, ScanLds& s, F f) {
   int found = 0;
+  Counts c = first;
   for (int base = from; base < to && found < limit; base += kScanPages) {
-    const int p0 = base + (threadIdx.x >> 6) * 1024 + lane_id();
-    uint64_t hit[16];
-    int n = 0;
-    int32_t r[16];
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const int p = p0 + 64 * i;
-      r[i] = p < to ? refs[p] : (kFree ? 1 : 0);
-    }
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-      hit[i] = __ballot(kFree ? r[i] == 0 : r[i] > 0);
-      n += __popcll(hit[i]);
-    }
-    int64_t all;
-    const int at = (int)block_scan(lane_id() == 0 ? n : 0, s, &all);
-    int rank = found + __shfl(at, 0);
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-      if ((hit[i] >> lane_id()) & 1) f(p0 + 64 * i, rank + below(hit[i]));
-      rank += __popcll(hit[i]);
-    }
-    found += (int)all;
+    if (base != from) c.load(refs, base, to);
+    found += scan_step<kFree>(c, base, from, to, found, s, f);
   }
   return found;
+}
+template <bool kFree, class F>
+__device__ int scan_pages(const int32_t* refs, int from, int to, int limit, ScanLds& s, F f) {
+  Counts c;
+  c.load(refs, from, to);
+  return scan_pages<kFree>(refs, c, from, to, limit, s, f);
 }
 
 // One bit per row of the cache (n_rows <= 65536).
@@ -130,6 +153,11 @@ __device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {
   return lo;
 }
 
+// a / b of numbers that mostly fit 32 bits
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // ---------------------------------------------------------------------------
 // Moving rows of pages
 // ---------------------------------------------------------------------------
@@ -138,35 +166,39 @@ __device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {
 // (kv, layer)s are numbered through.  Four loads are in flight per thread.
 template <class U>
 __device__ __forceinline__ void copy_piece(const Cache& c, int src, int dst, uint32_t units,
-                                           int64_t piece) {
+                                           int64_t piece, int piece_units) {
   const int64_t all = (int64_t)2 * c.L * units;
-  const int64_t first = piece * kPieceUnits;
+  const int64_t first = piece * piece_units;
   const int64_t page_bytes = (int64_t)c.P * c.C * 2;
-  const uint32_t n = (uint32_t)(all - first < kPieceUnits ? all - first : kPieceUnits);
-  const uint32_t sl0 = (uint32_t)(first / units), u0 = (uint32_t)(first % units);
-  for (uint32_t i = threadIdx.x; i < n; i += 4 * kCopyThreads) {
-    U x[4];
-    int64_t off[4];
-    char* base[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const uint32_t e = i + j * kCopyThreads;
-      if (e < n) {
-        const uint32_t sl = sl0 + (u0 + e) / units, u = (u0 + e) % units;
-        base[j] = sl < (uint32_t)c.L ? c.k : c.v;
-        const int64_t l = sl < (uint32_t)c.L ? sl : sl - c.L;
-        off[j] = l * c.N * page_bytes + (int64_t)u * sizeof(U);
-        x[j] = *(const U*)(base[j] + off[j] + src * page_bytes);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-      if (i + j * kCopyThreads < n) *(U*)(base[j] + off[j] + dst * page_bytes) = x[j];
+  const uint32_t n = (uint32_t)(all - first < piece_units ? all - first : piece_units);
+  // a 64-bit division is a microsecond of latency
+  const uint32_t sl0 = all >> 32 ? (uint32_t)(first / units) : (uint32_t)first / units;
+  const uint32_t u0 = (uint32_t)(first - (int64_t)sl0 * units);
+  const int64_t from = src * page_bytes, to = dst * page_bytes;
+  auto place = [&](uint32_t e) {  // of unit u0 + e in page 0
+    const uint32_t more = e / units, u = e - more * units, sl = sl0 + more;
+    const bool v = sl >= (uint32_t)c.L;
+    return (v ? c.v : c.k) + (int64_t)(v ? sl - c.L : sl) * c.N * page_bytes + (int64_t)u * sizeof(U);
+  };
+  uint32_t i = threadIdx.x;
+  for (; i + 3 * kCopyThreads < n; i += 4 * kCopyThreads) {
+    char *a0 = place(u0 + i), *a1 = place(u0 + i + kCopyThreads), *a2 = place(u0 + i + 2 * kCopyThreads),
+         *a3 = place(u0 + i + 3 * kCopyThreads);
+    const U x0 = *(const U*)(a0 + from), x1 = *(const U*)(a1 + from), x2 = *(const U*)(a2 + from),
+            x3 = *(const U*)(a3 + from);
+    *(U*)(a0 + to) = x0;
+    *(U*)(a1 + to) = x1;
+    *(U*)(a2 + to) = x2;
+    *(U*)(a3 + to) = x3;
+  }
+  for (; i < n; i += kCopyThreads) {
+    char* a0 = place(u0 + i);
+    *(U*)(a0 + to) = *(const U*)(a0 + from);
   }
 }
 
-__host__ __device__ __forceinline__ int64_t pieces_of(int L, int64_t units) {
-  return (2 * (int64_t)L * units + kPieceUnits - 1) / kPieceUnits;
+__host__ __device__ __forceinline__ int64_t pieces_of(int L, int64_t units, int piece) {
+  return (2 * (int64_t)L * units + piece - 1) / piece;
 }
 
 // Pair i is copied unless its dst is named twice or its src is a dst: every
@@ -174,9 +206,10 @@ __host__ __device__ __forceinline__ int64_t pieces_of(int L, int64_t units) {
 // which needs no workspace and no second launch.
 template <class U>
 __global__ __launch_bounds__(kCopyThreads) void k_pages_copy(Cache c, int n, const int32_t* src,
-                                                             const int32_t* dst, int64_t pieces) {
+                                                             const int32_t* dst, int64_t pieces,
+                                                             int piece_units) {
   for (int64_t w = blockIdx.x; w < n * pieces; w += gridDim.x) {
-    const int i = (int)(w / pieces);
+    const int i = (int)quotient(w, pieces);
     const int s = src[i], d = dst[i];
     bool clash = false;
     for (int j = threadIdx.x; j < n; j += kCopyThreads) {
@@ -189,10 +222,15 @@ __global__ __launch_bounds__(kCopyThreads) void k_pages_copy(Cache c, int n, con
     } else if (clash) {
       if (threadIdx.x == 0) atomicOr(c.status, kRefused);
     } else {
-      copy_piece<U>(c, s, d, (uint32_t)((int64_t)c.P * c.C * 2 / sizeof(U)), w % pieces);
+      copy_piece<U>(c, s, d, (uint32_t)((int64_t)c.P * c.C * 2 / sizeof(U)), w - i * pieces, piece_units);
     }
   }
 }
+
+// Up to kFew requests, one a thread, and their dealt pages are kept in registers and
+// LDS: a bookkeeping kernel's time is its chain of dependent global loads, and searches
+// and lists in global memory made most of it.
+constexpr int kFew = kThreads, kFewPages = 4096;
 
 // ---------------------------------------------------------------------------
 // Reserve
@@ -285,6 +323,79 @@ __global__ __launch_bounds__(kThreads) void k_reserve(Cache c, int n, const int3
   if (!slots) return;
   __syncthreads();
   fill_slots(c, n, rows, starts, ok, slots, threadIdx.x, n_tokens, kThreads);
+}
+
+__global__ __launch_bounds__(kThreads) void k_reserve_few(Cache c, int n, const int32_t* rows,
+                                                          const int32_t* starts, int n_tokens,
+                                                          int64_t* slots, int32_t* list) {
+  __shared__ ScanLds s;
+  __shared__ uint32_t seen[kRowWords], twice[kRowWords];
+  __shared__ int32_t cum[kFew + 1], start[kFew + 1], old_len[kFew], old_page[kFew], dealt[kFewPages];
+  const int i = threadIdx.x;
+  const int row = i < n ? rows[i] : -1, a = i < n ? starts[i] : 0, b = i < n ? starts[i + 1] : 0;
+  Counts counts;
+  counts.load(c.refs, 0, c.N);
+  clear_bits(seen, c.R);
+  clear_bits(twice, c.R);
+  const bool known = row_ok(c, row);
+  const int len = known ? c.lens[row] : -1;
+  __syncthreads();
+  if (known && set_bit(seen, row)) set_bit(twice, row);
+  const bool fits = known && a >= 0 && a <= b && b <= n_tokens && len_ok(c, len) &&
+                    len_ok(c, (int64_t)len + (b - a));
+  const int last = fits && (len & (c.P - 1)) ? entry(c, row, blocks_of(c, len) - 1) : -1;
+  __syncthreads();
+  const bool good = fits && !test_bit(twice, row);
+  if (i < n && !good) atomicOr(c.status, kRefused);
+  const int need = good ? blocks_of(c, (int64_t)len + (b - a)) - blocks_of(c, len) : 0;
+  constexpr int64_t kMany = 1 << 30;  // sums are cut there: no pool has so many pages
+  int64_t sum;
+  const int64_t at = block_scan(need, s, &sum);
+  const int total = (int)(sum < kMany ? sum : kMany);
+  if (i < n) {
+    cum[i] = (int)(at < kMany ? at : kMany);
+    start[i] = a;
+    old_page[i] = last;
+    if (i == n - 1) {
+      cum[n] = total;
+      start[n] = b;
+    }
+  }
+  int32_t* pages = total <= kFewPages ? dealt : list;
+  const int found = total ? scan_pages<true>(c.refs, counts, 0, c.N, total, s,
+                                             [&](int page, int rank) {
+                                               if (rank < total) pages[rank] = page;
+                                             })
+                          : 0;
+  const int have = min(found, total);
+  if (i < n) {
+    const bool granted = good && (need == 0 || at + need <= have);
+    old_len[i] = granted ? len : -1;
+    if (granted) c.lens[row] = len + (b - a);
+    else if (good) atomicOr(c.status, kNoPages);
+  }
+  __syncthreads();
+  for (int r = i; r < have; r += kThreads) {
+    const int j = last_at_most(cum, n, r);  // the last of equal ones: the request that needs pages
+    if (old_len[j] < 0) continue;
+    const int page = pages[r];
+    entry(c, rows[j], blocks_of(c, old_len[j]) + (r - cum[j])) = page;
+    c.refs[page] = 1;
+  }
+  for (int t = i; slots && t < n_tokens; t += kThreads) {
+    int64_t slot = -1;
+    const int j = last_at_most(start, n, t);
+    if (j >= 0 && t < start[j + 1] && old_len[j] >= 0) {
+      const int64_t pos = (int64_t)old_len[j] + (t - start[j]);
+      const int blk = (int)(pos >> c.shift), old = blocks_of(c, old_len[j]);
+      const int page = blk < old ? old_page[j] : pages[cum[j] + blk - old];
+      if (page_ok(c, page))
+        slot = ((int64_t)page << c.shift) + (pos & (c.P - 1));
+      else
+        atomicOr(c.status, kBadPage);
+    }
+    slots[t] = slot;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -391,11 +502,63 @@ __global__ __launch_bounds__(kThreads) void k_fork_plan(Cache c, int n, const in
   }
 }
 
+__global__ __launch_bounds__(kThreads) void k_fork_plan_few(Cache c, int n, const int32_t* parents,
+                                                            const int32_t* children, int32_t* ok,
+                                                            int32_t* aux) {
+  __shared__ ScanLds s;
+  __shared__ uint32_t kids[kRowWords], twice[kRowWords], olds[kRowWords];
+  __shared__ int32_t dealt[kFew];
+  const int i = threadIdx.x;
+  const int par = i < n ? parents[i] : -1, kid = i < n ? children[i] : -1;
+  Counts counts;
+  counts.load(c.refs, 0, c.N);
+  clear_bits(kids, c.R);
+  clear_bits(twice, c.R);
+  clear_bits(olds, c.R);
+  const bool known = row_ok(c, par) && row_ok(c, kid);
+  const int len = known ? c.lens[par] : -1, kid_len = known ? c.lens[kid] : -1;
+  __syncthreads();
+  if (row_ok(c, kid) && set_bit(kids, kid)) set_bit(twice, kid);
+  if (row_ok(c, par)) set_bit(olds, par);
+  const bool fits = known && kid_len == 0 && len_ok(c, len);
+  const int part = fits ? len & (c.P - 1) : 0;
+  const int last = part ? entry(c, par, blocks_of(c, len) - 1) : -1;
+  __syncthreads();
+  bool good = fits && !test_bit(twice, kid) && !test_bit(olds, kid);
+  if (i < n && !good) atomicOr(c.status, kRefused);
+  if (good && part && !page_ok(c, last)) {
+    good = false;
+    atomicOr(c.status, kBadPage);
+  }
+  const int need = good && part;
+  int64_t total;
+  const int at = (int)block_scan(need, s, &total);
+  const int found = total ? scan_pages<true>(c.refs, counts, 0, c.N, (int)total, s,
+                                             [&](int page, int rank) {
+                                               if (rank < (int)total) dealt[rank] = page;
+                                             })
+                          : 0;
+  __syncthreads();
+  if (i >= n) return;
+  if (need && at >= found) {
+    good = false;
+    atomicOr(c.status, kNoPages);
+  }
+  ok[i] = good;
+  if (!good) return;
+  aux[3 * i] = last;
+  aux[3 * i + 1] = need ? dealt[at] : -1;
+  aux[3 * i + 2] = part;
+  if (need) c.refs[dealt[at]] = 1;
+  c.lens[kid] = len;
+}
+
 // blockIdx.y 0: the child's table row and the counts; others: pieces of the copy
 template <class U>
 __global__ __launch_bounds__(kCopyThreads) void k_fork_copy(Cache c, const int32_t* parents,
                                                             const int32_t* children,
-                                                            const int32_t* ok, const int32_t* aux) {
+                                                            const int32_t* ok, const int32_t* aux,
+                                                            int piece_units) {
   const int i = blockIdx.x;
   if (!(ok[i] & 1)) return;
   const int part = aux[3 * i + 2], to = aux[3 * i + 1];
@@ -416,9 +579,9 @@ __global__ __launch_bounds__(kCopyThreads) void k_fork_copy(Cache c, const int32
   }
   if (!part) return;
   const uint32_t units = (uint32_t)((int64_t)part * c.C * 2 / sizeof(U));
-  const int64_t pieces = pieces_of(c.L, units);
+  const int64_t pieces = pieces_of(c.L, units, piece_units);
   for (int64_t w = blockIdx.y - 1; w < pieces; w += gridDim.y - 1)
-    copy_piece<U>(c, aux[3 * i], to, units, w);
+    copy_piece<U>(c, aux[3 * i], to, units, w, piece_units);
 }
 
 // ---------------------------------------------------------------------------
@@ -474,6 +637,39 @@ __global__ __launch_bounds__(kThreads) void k_compact_plan(Cache c, int32_t* liv
   }
 }
 
+// Up to one scan step of pages: refs are read once and the lists pass through LDS.
+__global__ __launch_bounds__(kThreads) void k_compact_plan_few(Cache c, int32_t* live_out, int32_t* ws,
+                                                               int32_t* to, int32_t* from) {
+  __shared__ ScanLds s;
+  __shared__ uint16_t below_live[kScanPages / 2], above_live[kScanPages / 2];
+  static_assert(kScanPages <= 65536, "page numbers in 16 bits");
+  Counts counts;
+  counts.load(c.refs, 0, c.N);
+  const int live = scan_step<false>(counts, 0, 0, c.N, 0, s, [](int, int) {});
+  // no more than half of the pages can be free below the live count, or in use above it,
+  // unless counts are negative: those further on are left where they are
+  const int frees = scan_step<true>(counts, 0, 0, live, 0, s, [&](int page, int rank) {
+    if (rank < kScanPages / 2) below_live[rank] = (uint16_t)page;
+  });
+  const int above = scan_step<false>(counts, 0, live, c.N, 0, s, [&](int page, int rank) {
+    if (rank < kScanPages / 2) above_live[rank] = (uint16_t)page;
+  });
+  const int moves = min(min(frees, above), kScanPages / 2);
+  if (frees != above && threadIdx.x == 0) atomicOr(c.status, kRefused);
+  __syncthreads();
+  for (int j = threadIdx.x; j < moves; j += kThreads) {
+    const int a = above_live[j], b = below_live[j];
+    to[j] = b;
+    from[j] = a;
+    c.refs[b] = c.refs[a];
+    c.refs[a] = 0;
+  }
+  if (threadIdx.x == 0) {
+    ws[0] = moves;
+    if (live_out) *live_out = live;
+  }
+}
+
 // Tables follow (an entry's move by binary search in the ascending `from`), then
 // the pages are copied; both spread over a fixed grid, as the host does not know
 // how many there are.
@@ -481,7 +677,7 @@ template <class U>
 __global__ __launch_bounds__(kCopyThreads) void k_compact_move(Cache c, const int32_t* ws,
                                                                const int32_t* to,
                                                                const int32_t* from,
-                                                               int64_t pieces) {
+                                                               int64_t pieces, int piece_units) {
   const int moves = ws[0];
   if (moves == 0) return;
   const int first = from[0];
@@ -498,8 +694,8 @@ __global__ __launch_bounds__(kCopyThreads) void k_compact_move(Cache c, const in
   }
   const uint32_t units = (uint32_t)((int64_t)c.P * c.C * 2 / sizeof(U));
   for (int64_t w = blockIdx.x; w < moves * pieces; w += gridDim.x) {
-    const int j = (int)(w / pieces);
-    copy_piece<U>(c, from[j], to[j], units, w % pieces);
+    const int j = (int)quotient(w, pieces);
+    copy_piece<U>(c, from[j], to[j], units, w - j * pieces, piece_units);
   }
 }
 
@@ -519,10 +715,14 @@ uint64_t pool_bits(const cg_paged_cache& c) { return (uintptr_t)c.k_pool_dev | (
 
 #define BY_UNIT(unit, call)                        \
   do {                                             \
-    if ((unit) == 16) { using U = uint4; call; }   \
+    if ((unit) == 16) { using U = u32x4; call; }   \
     else if ((unit) == 4) { using U = uint32_t; call; } \
     else { using U = uint16_t; call; }             \
   } while (0)
+
+int piece_for(int64_t copies, int L, int64_t units) {
+  return copies * 2 * L * units >= (int64_t)2048 * kPieceMost ? kPieceMost : kPieceLeast;
+}
 
 int launched(const char* what) {
   const hipError_t e = hipGetLastError();
@@ -561,10 +761,11 @@ int cg_pages_copy_async(const cg_paged_cache* c, int32_t n, const int32_t* src_d
   if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
   const int64_t page = (int64_t)c->page_tokens * c->channels * 2;
   const int unit = unit_of((uint64_t)page | pool_bits(*c));
-  const int64_t pieces = pieces_of(c->layers, page / unit);
+  const int piece = piece_for(n, c->layers, page / unit);
+  const int64_t pieces = pieces_of(c->layers, page / unit, piece);
   const int grid = (int)std::min(n * pieces, kMaxGrid);
   BY_UNIT(unit, (k_pages_copy<U><<<grid, kCopyThreads, 0, (hipStream_t)stream>>>(
-                    view(*c), n, src_dev, dst_dev, pieces)));
+                    view(*c), n, src_dev, dst_dev, pieces, piece)));
   return launched("page copy");
 }
 
@@ -581,8 +782,12 @@ int cg_pages_reserve_async(const cg_paged_cache* c, int32_t n, const int32_t* ro
   if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
   const PagesWs w = pages_ws(*c);
   int32_t* ws = (int32_t*)workspace_dev;
-  k_reserve<<<1, kThreads, 0, (hipStream_t)stream>>>(view(*c), n, rows_dev, starts_dev, n_tokens,
-                                                     slots_dev, ws + w.cum, ws + w.ok, ws + w.list);
+  if (n <= kFew)
+    k_reserve_few<<<1, kThreads, 0, (hipStream_t)stream>>>(view(*c), n, rows_dev, starts_dev,
+                                                           n_tokens, slots_dev, ws + w.list);
+  else
+    k_reserve<<<1, kThreads, 0, (hipStream_t)stream>>>(view(*c), n, rows_dev, starts_dev, n_tokens,
+                                                       slots_dev, ws + w.cum, ws + w.ok, ws + w.list);
   return launched("reserve");
 }
 
@@ -607,7 +812,8 @@ int cg_pages_write_async(const cg_paged_cache* c, int32_t layer0, int32_t n_laye
                            (uintptr_t)v_new_dev | (uint64_t)(2 * token_stride) |
                            (uint64_t)(n_layers > 1 ? 2 * layer_stride : 0));
   const uint32_t units = (uint32_t)(row / unit);
-  const int tile = (int)std::max<int64_t>(1, kPieceUnits / units);
+  const int piece = piece_for(n_tokens, n_layers, units);
+  const int tile = (int)std::max<int64_t>(1, piece / units);
   const dim3 grid((unsigned)((n_tokens + tile - 1) / tile), 2 * n_layers);
   BY_UNIT(unit, (k_write<U><<<grid, kCopyThreads, 0, (hipStream_t)stream>>>(
                     view(*c), layer0, n_layers, n_tokens, slots_dev, (const char*)k_new_dev,
@@ -628,17 +834,22 @@ int cg_pages_fork_async(const cg_paged_cache* c, int32_t n, const int32_t* paren
   const PagesWs w = pages_ws(*c);
   int32_t* ws = (int32_t*)workspace_dev;
   hipStream_t st = (hipStream_t)stream;
-  k_fork_plan<<<1, kThreads, 0, st>>>(view(*c), n, parents_dev, children_dev, ws + w.ok,
-                                      ws + w.cum, ws + w.aux, ws + w.list);
+  if (n <= kFew)
+    k_fork_plan_few<<<1, kThreads, 0, st>>>(view(*c), n, parents_dev, children_dev, ws + w.ok,
+                                            ws + w.aux);
+  else
+    k_fork_plan<<<1, kThreads, 0, st>>>(view(*c), n, parents_dev, children_dev, ws + w.ok,
+                                        ws + w.cum, ws + w.aux, ws + w.list);
   if (int rc = launched("fork")) return rc;
   // the copy's rows are known on the device only: pieces for a full page, the
   // surplus workgroups return at once
   const int64_t row = (int64_t)c->channels * 2;
   const int unit = unit_of((uint64_t)row | pool_bits(*c));
-  const int64_t pieces = pieces_of(c->layers, (c->page_tokens - 1) * row / unit);
+  const int piece = piece_for(n, c->layers, (c->page_tokens - 1) * row / unit);
+  const int64_t pieces = pieces_of(c->layers, (c->page_tokens - 1) * row / unit, piece);
   const dim3 grid(n, (unsigned)(1 + std::min<int64_t>(pieces, std::max<int64_t>(1, 32768 / n))));
   BY_UNIT(unit, (k_fork_copy<U><<<grid, kCopyThreads, 0, st>>>(view(*c), parents_dev, children_dev,
-                                                               ws + w.ok, ws + w.aux)));
+                                                               ws + w.ok, ws + w.aux, piece)));
   return launched("fork");
 }
 
@@ -663,14 +874,18 @@ int cg_pages_compact_async(const cg_paged_cache* c, int32_t* n_live_dev, void* w
   const PagesWs w = pages_ws(*c);
   int32_t* ws = (int32_t*)workspace_dev;
   hipStream_t st = (hipStream_t)stream;
-  k_compact_plan<<<1, kThreads, 0, st>>>(view(*c), n_live_dev, ws, ws + w.list, ws + w.list2);
+  if (c->num_pages <= kScanPages)
+    k_compact_plan_few<<<1, kThreads, 0, st>>>(view(*c), n_live_dev, ws, ws + w.list, ws + w.list2);
+  else
+    k_compact_plan<<<1, kThreads, 0, st>>>(view(*c), n_live_dev, ws, ws + w.list, ws + w.list2);
   if (int rc = launched("compact")) return rc;
   const int64_t page = (int64_t)c->page_tokens * c->channels * 2;
   const int unit = unit_of((uint64_t)page | pool_bits(*c));
-  const int64_t pieces = pieces_of(c->layers, page / unit);
+  const int piece = piece_for(c->num_pages / 4, c->layers, page / unit);
+  const int64_t pieces = pieces_of(c->layers, page / unit, piece);
   const int grid = (int)std::min<int64_t>(2048, std::max<int64_t>(c->n_rows, c->num_pages / 2 * pieces));
   BY_UNIT(unit, (k_compact_move<U><<<grid, kCopyThreads, 0, st>>>(view(*c), ws, ws + w.list,
-                                                                  ws + w.list2, pieces)));
+                                                                  ws + w.list2, pieces, piece)));
   return launched("compact");
 }
 
