@@ -393,16 +393,19 @@ def cg_decode_streamed(t: Tables, host_blobs, infos, k_out, v_out, staging, stat
                                     _stream(copy_stream), _stream(compute_stream)))
 
 
-def _rows3(t, dtype, device, last, what):
-    """(stride of axis 0, stride of axis 1) of a 3-d device tensor whose last axis
-    is contiguous, as the library counts them: an axis of one element, whose stride
-    a view leaves at anything, gets the one it would have if contiguous."""
-    if (t.dim() != 3 or t.dtype != dtype or t.device != device or t.shape[2] != last
-            or (t.stride(2) != 1 and last > 1 and t.numel())):
+def _rows3(t, dtype, index, last, what):
+    """(stride of axis 0, stride of axis 1) of a 3-d tensor on device `index` whose
+    last axis is contiguous, as the library counts them: an axis of one element,
+    whose stride a view leaves at anything, gets the one it would have if contiguous."""
+    n0, n1, n2 = t.shape
+    s0, s1, s2 = t.stride()
+    if (t.dtype != dtype or t.get_device() != index or n2 != last
+            or (s2 != 1 and last > 1 and n0 * n1 > 0)):
         raise ValueError(f"{what} must be {dtype} [.., .., {last}] on the cache's device, its last "
                          "axis contiguous")
-    s1 = t.stride(1) if t.shape[1] > 1 else last
-    return (t.stride(0) if t.shape[0] > 1 else s1 * t.shape[1]), s1
+    if n1 <= 1:
+        s1 = last
+    return (s0 if n0 > 1 else s1 * n1), s1
 
 
 class PagedCache:
@@ -430,17 +433,23 @@ class PagedCache:
             if t.device != self.device:
                 raise ValueError("the tensors of a cache must be on one device")
             setattr(s, name + "_dev", _dev_ptr(t, dtype, name))
-        s.device = self.device.index
+        s.device = self.index = self.device.index
         s.layers, s.num_pages, s.page_tokens, s.channels = k_pool.shape
         s.n_rows, s.max_blocks = tables.shape
         self.struct = s
         self.ref = C.byref(s)
+        self.channels = s.channels
+        # what every call needs, looked up once: the calls of a decoding step are short
+        self.lib = lib()
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.i32, self.i64, self.u8 = torch.int32, torch.int64, torch.uint8
+        self.f16, self.f32 = torch.float16, torch.float32
 
     def _ptr(self, t, dtype, what, numel=None):
         """Device address of a tensor of a call on this cache (None: NULL)."""
         if t is None:
             return None
-        if (t.dtype != dtype or t.device != self.device or not t.is_contiguous()
+        if (t.dtype != dtype or t.get_device() != self.index or not t.is_contiguous()
                 or (numel is not None and t.numel() != numel)):
             raise ValueError(f"{what} must be contiguous {dtype} on the cache's device"
                              + (f" with {numel} elements" if numel is not None else ""))
@@ -448,95 +457,86 @@ class PagedCache:
 
     def _stream(self, stream):
         if stream is None:
+            if self._raw_stream is not None:
+                return self._raw_stream(self.index)
             import torch
             return torch.cuda.current_stream(self.device).cuda_stream
         return _stream(stream)
 
-    def _ws(self, ws):
-        import torch
-        return self._ptr(ws, torch.uint8, "workspace"), ws.numel()
-
 
 def cg_pages_workspace(cache: PagedCache) -> int:
     n = C.c_size_t(0)
-    _check(lib().cg_pages_workspace(cache.ref, C.byref(n)))
+    _check(cache.lib.cg_pages_workspace(cache.ref, C.byref(n)))
     return n.value
 
 
 def cg_pages_copy_async(cache: PagedCache, src, dst, stream=None):
     """Copies page src[i] to page dst[i] in every layer (int32 device tensors)."""
-    import torch
     n = src.numel()
-    _check(lib().cg_pages_copy_async(cache.ref, n, cache._ptr(src, torch.int32, "src"),
-                                     cache._ptr(dst, torch.int32, "dst", n),
-                                     cache._stream(stream)))
+    _check(cache.lib.cg_pages_copy_async(cache.ref, n, cache._ptr(src, cache.i32, "src"),
+                                         cache._ptr(dst, cache.i32, "dst", n),
+                                         cache._stream(stream)))
 
 
 def cg_pages_reserve_async(cache: PagedCache, rows, starts, slots, workspace, n_tokens=None,
                            stream=None):
     """Room for tokens starts[i] .. starts[i+1]-1 in row rows[i]; slots (int64, one
     per token) receives where they go.  slots None: n_tokens says how many there are."""
-    import torch
     n = rows.numel()
     if n_tokens is None:
         n_tokens = slots.numel()
-    ws, nws = cache._ws(workspace)
-    _check(lib().cg_pages_reserve_async(cache.ref, n, cache._ptr(rows, torch.int32, "rows"),
-                                        cache._ptr(starts, torch.int32, "starts", n + 1), n_tokens,
-                                        cache._ptr(slots, torch.int64, "slots", n_tokens),
-                                        ws, nws, cache._stream(stream)))
+    _check(cache.lib.cg_pages_reserve_async(
+        cache.ref, n, cache._ptr(rows, cache.i32, "rows"),
+        cache._ptr(starts, cache.i32, "starts", n + 1), n_tokens,
+        cache._ptr(slots, cache.i64, "slots", n_tokens),
+        cache._ptr(workspace, cache.u8, "workspace"), workspace.numel(), cache._stream(stream)))
 
 
 def cg_pages_write_async(cache: PagedCache, layer0, slots, k_new, v_new, stream=None):
     """Writes k_new / v_new (fp16 [layers, tokens, channels], channels contiguous,
     both with the same strides) to `slots` in layers layer0 .."""
-    import torch
-    ch = cache.struct.channels
-    ls, ts = _rows3(k_new, torch.float16, cache.device, ch, "k_new")
-    if k_new.shape != v_new.shape or (ls, ts) != _rows3(v_new, torch.float16, cache.device, ch,
-                                                        "v_new"):
+    strides = _rows3(k_new, cache.f16, cache.index, cache.channels, "k_new")
+    if (k_new.shape != v_new.shape
+            or strides != _rows3(v_new, cache.f16, cache.index, cache.channels, "v_new")):
         raise ValueError("k_new and v_new must have the same shape and strides")
     layers, n, _ = k_new.shape
-    _check(lib().cg_pages_write_async(cache.ref, layer0, layers, n,
-                                      cache._ptr(slots, torch.int64, "slots", n), k_new.data_ptr(),
-                                      v_new.data_ptr(), ts, ls, cache._stream(stream)))
+    _check(cache.lib.cg_pages_write_async(cache.ref, layer0, layers, n,
+                                          cache._ptr(slots, cache.i64, "slots", n),
+                                          k_new.data_ptr(), v_new.data_ptr(), strides[1],
+                                          strides[0], cache._stream(stream)))
 
 
 def cg_pages_fork_async(cache: PagedCache, parents, children, workspace, stream=None):
     """Row children[i] continues row parents[i]: full pages shared, the rows in
     use of a last page that is not full copied."""
-    import torch
     n = parents.numel()
-    ws, nws = cache._ws(workspace)
-    _check(lib().cg_pages_fork_async(cache.ref, n, cache._ptr(parents, torch.int32, "parents"),
-                                     cache._ptr(children, torch.int32, "children", n), ws, nws,
-                                     cache._stream(stream)))
+    _check(cache.lib.cg_pages_fork_async(
+        cache.ref, n, cache._ptr(parents, cache.i32, "parents"),
+        cache._ptr(children, cache.i32, "children", n),
+        cache._ptr(workspace, cache.u8, "workspace"), workspace.numel(), cache._stream(stream)))
 
 
 def cg_pages_free_async(cache: PagedCache, rows, stream=None):
     """Empties rows; pages that no other row names become free."""
-    import torch
-    _check(lib().cg_pages_free_async(cache.ref, rows.numel(), cache._ptr(rows, torch.int32, "rows"),
-                                     cache._stream(stream)))
+    _check(cache.lib.cg_pages_free_async(cache.ref, rows.numel(),
+                                         cache._ptr(rows, cache.i32, "rows"),
+                                         cache._stream(stream)))
 
 
 def cg_pages_compact_async(cache: PagedCache, workspace, n_live=None, stream=None):
     """Packs the pages in use into the lowest numbers; n_live (int32 [1]) receives
     how many there are."""
-    import torch
-    ws, nws = cache._ws(workspace)
-    _check(lib().cg_pages_compact_async(cache.ref, cache._ptr(n_live, torch.int32, "n_live", 1),
-                                        ws, nws, cache._stream(stream)))
+    _check(cache.lib.cg_pages_compact_async(cache.ref, cache._ptr(n_live, cache.i32, "n_live", 1),
+                                            cache._ptr(workspace, cache.u8, "workspace"),
+                                            workspace.numel(), cache._stream(stream)))
 
 
 def cg_attention_workspace(cache: PagedCache, n_q, n_heads, head_dim, n_seqs, n_groups, max_q,
                            max_prefix, max_len) -> int:
     """Bytes of workspace of a cg_attention_prefix_async call of these numbers."""
-    a = cg_attention()
-    a.n_q, a.n_heads, a.head_dim, a.n_seqs, a.n_groups = n_q, n_heads, head_dim, n_seqs, n_groups
-    a.max_q, a.max_prefix, a.max_len = max_q, max_prefix, max_len
+    a = cg_attention(0, n_heads, head_dim, 1.0, n_seqs, n_q, n_groups, max_q, max_prefix, max_len)
     n = C.c_size_t(0)
-    _check(lib().cg_attention_workspace(cache.ref, C.byref(a), C.byref(n)))
+    _check(cache.lib.cg_attention_workspace(cache.ref, C.byref(a), C.byref(n)))
     return n.value
 
 
@@ -547,28 +547,22 @@ def cg_attention_prefix_async(cache: PagedCache, layer, q, out, scale, rows, q_s
     cache into out (the same shape) and lse (fp32 [tokens, heads], may be None).
     rows None: sequence s is row s.  group_starts / prefix_lens None: no shared
     prefixes.  q and out may have a longer stride between tokens."""
-    import torch
     n_q, heads, dim = q.shape
-    q_stride, s1 = _rows3(q, torch.float16, cache.device, dim, "q")
-    out_stride, s2 = _rows3(out, torch.float16, cache.device, dim, "out")
+    q_stride, s1 = _rows3(q, cache.f16, cache.index, dim, "q")
+    out_stride, s2 = _rows3(out, cache.f16, cache.index, dim, "out")
     if out.shape != q.shape or (n_q and (s1 != dim or s2 != dim)):
         raise ValueError("out must have the shape of q, the heads of both contiguous")
     n = q_starts.numel() - 1
     groups = 0 if group_starts is None else group_starts.numel() - 1
-    a = cg_attention()
-    a.layer, a.n_heads, a.head_dim, a.scale = layer, heads, dim, scale
-    a.n_seqs, a.n_q, a.n_groups = n, n_q, groups
-    a.max_q, a.max_prefix, a.max_len = max_q, max_prefix, max_len
-    i32 = torch.int32
-    a.rows_dev = cache._ptr(rows, i32, "rows", n)
-    a.q_starts_dev = cache._ptr(q_starts, i32, "q_starts")
-    a.group_starts_dev = cache._ptr(group_starts, i32, "group_starts")
-    a.prefix_lens_dev = cache._ptr(prefix_lens, i32, "prefix_lens", groups)
-    a.q_dev, a.out_dev = q.data_ptr(), out.data_ptr()
-    a.lse_dev = cache._ptr(lse, torch.float32, "lse", n_q * heads)
-    a.q_stride, a.out_stride = q_stride, out_stride
-    ws, nws = cache._ws(workspace)
-    _check(lib().cg_attention_prefix_async(cache.ref, C.byref(a), ws, nws, cache._stream(stream)))
+    i32, ptr = cache.i32, cache._ptr
+    a = cg_attention(layer, heads, dim, scale, n, n_q, groups, max_q, max_prefix, max_len,
+                     ptr(rows, i32, "rows", n), ptr(q_starts, i32, "q_starts"),
+                     ptr(group_starts, i32, "group_starts"),
+                     ptr(prefix_lens, i32, "prefix_lens", groups), q.data_ptr(), out.data_ptr(),
+                     ptr(lse, cache.f32, "lse", n_q * heads), q_stride, out_stride)
+    _check(cache.lib.cg_attention_prefix_async(cache.ref, C.byref(a),
+                                               ptr(workspace, cache.u8, "workspace"),
+                                               workspace.numel(), cache._stream(stream)))
 
 
 def cg_release_cached():
