@@ -46,6 +46,7 @@ struct Attn {
   // the launch: splits of a prefix and of a sequence's rest, row tiles that have
   // workgroups of their own (there may be more)
   int pre_splits, rest_splits, pre_tiles, rest_tiles, pre_groups, join;
+  int rest_heads;  // kv heads of a workgroup that deals out the rest's tokens: 1, 2 or 4
   float* part;  // [pre_splits + rest_splits][n_q][H][d] sums, not divided
   float* ml;    // the same with [2]: reference exponent m, sum of weights l
   // [n_q]: splits of the prefix and (in the upper half) of the rest that the query's
@@ -280,7 +281,7 @@ __device__ __forceinline__ bool clean_values(char* tile, int pages) {
 }
 
 struct Item {
-  int head;                 // kv head
+  int head, heads;          // first kv head, and how many
   int q0, rows;             // first query; rows = queries x heads of the kv head
   int lo, hi;               // tokens
   int lim0;                 // tokens that the first query sees (each later one 1 more)
@@ -295,8 +296,8 @@ struct Item {
   int lender;               // direct: table row that the first `pre` tokens are read through
 };
 
-__device__ __forceinline__ int64_t part_at(const Attn& a, const Item& it, int row) {
-  return ((int64_t)(it.slot0 + it.split) * a.n_q + it.q0 + row / a.G) * a.H + it.head * a.G + row % a.G;
+__device__ __forceinline__ int64_t part_at(const Attn& a, const Item& it, int head, int row) {
+  return ((int64_t)(it.slot0 + it.split) * a.n_q + it.q0 + row / a.G) * a.H + head * a.G + row % a.G;
 }
 
 // The two stretches of tokens of a direct item, or an item's only one.
@@ -311,8 +312,11 @@ __device__ __forceinline__ Item range_of(const Item& it, int ranges, int i) {
   }
   return r;
 }
-__device__ __forceinline__ uint16_t* out_at(const Attn& a, const Item& it, int row) {
-  return a.out + (it.q0 + row / a.G) * a.out_stride + (int64_t)(it.head * a.G + row % a.G) * a.d;
+__device__ __forceinline__ uint16_t* out_at(const Attn& a, const Item& it, int head, int row) {
+  return a.out + (it.q0 + row / a.G) * a.out_stride + (int64_t)(head * a.G + row % a.G) * a.d;
+}
+__device__ __forceinline__ float* lse_at(const Attn& a, const Item& it, int head, int row) {
+  return a.lse + (int64_t)(it.q0 + row / a.G) * a.H + head * a.G + row % a.G;
 }
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945309f;
@@ -385,13 +389,13 @@ struct Wave {
 
   // Queries of rows row0 .. row0 + 16 RT - 1 (row = query x heads of the kv head +
   // head); rows past the item's are zeros that see everything.
-  __device__ __forceinline__ void load_queries(const Attn& a, const Item& it, int row0) {
+  __device__ __forceinline__ void load_queries(const Attn& a, const Item& it, int head, int row0) {
     const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int r = 0; r < RT; r++) {
       const int row = row0 + r * 16 + n;
       const bool in = row < it.rows;
-      const int qi = in ? row / a.G : 0, h = it.head * a.G + (in ? row % a.G : 0);
+      const int qi = in ? row / a.G : 0, h = head * a.G + (in ? row % a.G : 0);
       const uint16_t* from = a.q + (it.q0 + qi) * a.q_stride + (int64_t)h * a.d;
 #pragma unroll
       for (int ks = 0; ks < KS; ks++) {
@@ -543,6 +547,7 @@ struct Shared {
   int32_t list[kList];
   float m[NW][32], l[NW][32], scale[NW][32];
   uint32_t odd;  // clean_values() found something
+  uint32_t bad;  // a page met so far is outside the pool
 };
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
@@ -554,10 +559,9 @@ template <int DP, class Sh>
 struct Tokens {
   static constexpr int kThreads = sizeof(Sh::m) / 128 * 64;
   Source src;
-  const char *kp, *vp;
   int first, last;  // tiles
   int list_tiles;   // tiles whose pages the list holds, wherever in a page they begin
-  bool bad;         // a page of the present stretch is outside the pool
+  bool bad;         // a page of this or an earlier stretch is outside the pool
 
   __device__ __forceinline__ bool start(const Attn& a, const Item& it, Sh& sh) {
     const Split sp = split_of(it.lo, it.hi, it.splits, it.least);
@@ -566,8 +570,6 @@ struct Tokens {
     last = min(first + sp.per, sp.tile0 + sp.tiles);
     const uint32_t row_bytes = (uint32_t)a.C * 2;
     src = Source{sh.list, 0, it.lo, it.hi, a.shift, a.P - 1, a.d / 8, row_bytes * (uint32_t)a.P, row_bytes};
-    kp = a.k + it.head * a.d * 2;
-    vp = a.v + it.head * a.d * 2;
     list_tiles = (int)((int64_t)(Sh::kList - 1) * a.P / kTile) - 1;
     return true;
   }
@@ -584,14 +586,14 @@ struct Tokens {
     const int b0 = max(base * kTile, it.lo) >> a.shift;
     const int b1 = (min(stop * kTile, it.hi) - 1) >> a.shift;
     __syncthreads();  // the list and the tiles are free
-    bad = false;
     for (int i = threadIdx.x; i <= b1 - b0; i += kThreads) {
       const int page = a.tables[(int64_t)it.trow * a.B + b0 + i];
       const bool ok = page >= 0 && page < a.N;
       sh.list[i] = ok ? page : -1;
-      bad |= !ok;
+      if (!ok) sh.bad = 1;
     }
-    bad = __syncthreads_or(bad);
+    __syncthreads();
+    bad = __builtin_amdgcn_readfirstlane(sh.bad) != 0;
     if (bad && threadIdx.x == 0) atomicOr(a.status, kBadPage);
     src.block0 = b0;
   }
@@ -618,20 +620,21 @@ struct Tokens {
       for (int t = max(first * kTile, cur.lo); t < end; t++) {
         const int page = a.tables[(int64_t)cur.trow * a.B + (t >> a.shift)];
         if (page < 0 || page >= a.N) continue;
-        const char* v = vp + (uint64_t)(uint32_t)page * src.page_bytes +
-                        (uint64_t)(uint32_t)(t & src.pmask) * src.row_bytes;
+        const char* v = a.v + (uint64_t)(uint32_t)page * src.page_bytes +
+                        (uint64_t)(uint32_t)(t & src.pmask) * src.row_bytes + it.head * a.d * 2;
 #pragma unroll 1
-        for (int ch = tid; ch < a.d; ch += kThreads) {
-          const float x = half_bits_to_float(((const uint16_t*)v)[ch]);
+        for (int i = tid; i < it.heads * a.d; i += kThreads) {
+          const float x = half_bits_to_float(((const uint16_t*)v)[i]);
           if (x - x == 0.0f) continue;
+          const int head = it.head + i / a.d, ch = i % a.d;
 #pragma unroll 1
           for (int row = row0; row < row1; row++) {
             if (t >= row_lim(a, cur, row)) continue;
             if (a.direct) {
-              uint16_t* to = out_at(a, it, row) + ch;
+              uint16_t* to = out_at(a, it, head, row) + ch;
               *to = float_to_half_bits(half_bits_to_float(*to) + x);
             } else {
-              a.part[part_at(a, it, row) * a.d + ch] += x;
+              a.part[part_at(a, it, head, row) * a.d + ch] += x;
             }
           }
         }
@@ -646,10 +649,11 @@ __device__ __forceinline__ float log2_scale(const Attn& a) {
   return a.scale == 0 ? 1.0f : fminf(fabsf(a.scale) * 1.44269504088896341f, 3.4e38f);
 }
 
-// Few rows: every wave holds all 16 RT of a row tile and takes the split's token
-// tiles in turn; the waves share nothing until the end.  Each has room for one tile
-// of K and one of V: the next K is on its way while the weights and the values are
-// computed, the next V while the scores are.
+// Few rows: every wave holds all 16 RT of a row tile of its kv head.  The waves of a
+// head (all, or half of them, or one, as the item has one, two or four heads) take the
+// split's token tiles in turn; the waves share nothing until the end.  Each has room
+// for one tile of K and one of V: the next K is on its way while the weights and the
+// values are computed, the next V while the scores are.
 template <int DP, int RT, int kWaves, class A>
 __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP, kWaves, kWaves>& sh) {
   constexpr int kThreads = 64 * kWaves;
@@ -661,6 +665,9 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
   if (!a.direct && !tk.start(a, it, sh)) return;
   const int ranges = ranges_of(a, it);
   const Places<DP> at_lane;
+  const int turn = kWaves / it.heads;  // waves of a head
+  const int head = it.head + wave / turn;
+  const char *kp = a.k + head * a.d * 2, *vp = a.v + head * a.d * 2;
   char *kt = sh.tile[wave][0], *vt = sh.tile[wave][1];
   const uint32_t klds = lds_address(kt), vlds = klds + Ge::BYTES;
   const float c = log2_scale(a);
@@ -669,9 +676,9 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
   for (int rt = it.row_tile; rt < row_tiles; rt += it.row_tiles) {
     W w;
     w.clear();
-    w.load_queries(a, it, rt * 16 * RT);
+    w.load_queries(a, it, head, rt * 16 * RT);
     tk.clear_tiles(a, sh);
-    if (threadIdx.x == 0) sh.odd = 0;
+    if (threadIdx.x == 0) sh.odd = sh.bad = 0;
 #pragma unroll 1
     for (int range = 0; range < ranges; range++) {
     const Item cur = range_of(it, ranges, range);
@@ -683,7 +690,7 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
       tk.stretch(a, cur, sh, base, stop);
       // the tile in hand, where its tokens are, whether its queries see all of it; the
       // next one
-      int tile = base + wave, next;
+      int tile = base + wave % turn, next;
       TileAt at{-1, 0, 0}, next_at{-1, 0, 0};
       bool all = false, more = false, full = false;
       auto look = [&](int nt) {
@@ -692,8 +699,8 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
         full = more && tk.full(nt);
         if (more) next_at = tile_at(tk.src, nt * kTile);
       };
-      auto load_k = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, tk.kp, klds, next_at, full); };
-      auto load_v = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, tk.vp, vlds, next_at, full); };
+      auto load_k = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, kp, klds, next_at, full); };
+      auto load_v = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, vp, vlds, next_at, full); };
       auto step = [&] {
         tile = next;
         at = next_at;
@@ -706,7 +713,7 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
       while (tile < stop) {
         f4 s[RT][2];
         h8 p[RT];
-        look(tile + kWaves);
+        look(tile + turn);
         wait_loads<Ge::NI>();
         w.scores(kt, at_lane.fresh(), s, [] {});
         wait_lds();
@@ -737,57 +744,47 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
       }
     }
     __syncthreads();  // all waves are done with their tiles
-    if (tid < 16 * RT) {
+    if (tid < 16 * RT * it.heads) {
+      const int x = tid % (16 * RT), hh = tid / (16 * RT), w0 = hh * turn;
       float m = -__builtin_inff(), l = 0.0f;
-#pragma unroll
-      for (int x = 0; x < kWaves; x++) m = fmaxf(m, sh.m[x][tid]);
-#pragma unroll
-      for (int x = 0; x < kWaves; x++) {
+      for (int y = w0; y < w0 + turn; y++) m = fmaxf(m, sh.m[y][x]);
+      for (int y = w0; y < w0 + turn; y++) {
         // a wave without a reference has weighed nothing, or only what is no number
-        const float mx = sh.m[x][tid];
-        const float f = mx == m ? 1.0f : mx == -__builtin_inff() && sh.l[x][tid] != 0.0f
-                            ? 1.0f : __builtin_amdgcn_exp2f(mx - m);
-        sh.scale[x][tid] = f;
-        l += f * sh.l[x][tid];
+        const float my = sh.m[y][x];
+        const float f = my == m ? 1.0f : my == -__builtin_inff() && sh.l[y][x] != 0.0f
+                            ? 1.0f : __builtin_amdgcn_exp2f(my - m);
+        sh.scale[y][x] = f;
+        l += f * sh.l[y][x];
       }
-      const int row = rt * 16 * RT + tid;
+      const int row = rt * 16 * RT + x;
       if (a.direct) {
-        sh.l[0][tid] = l == 0.0f ? 0.0f : 1.0f / l;
-        if (row < it.rows && a.lse)
-          a.lse[(int64_t)(it.q0 + row / a.G) * a.H + it.head * a.G + row % a.G] = lse_of(m, l);
+        sh.l[w0][x] = l == 0.0f ? 0.0f : 1.0f / l;
+        if (row < it.rows && a.lse) *lse_at(a, it, it.head + hh, row) = lse_of(m, l);
       } else if (row < it.rows) {
-        const int64_t at = part_at(a, it, row);
+        const int64_t at = part_at(a, it, it.head + hh, row);
         a.ml[2 * at] = m;
         a.ml[2 * at + 1] = l;
       }
     }
-    constexpr int kRounds = RT > 2 ? RT / 2 : 1;      // as the tiles' room allows
-    constexpr int kBlocks = W::NB / kRounds;          // 16-channel blocks a round
-    constexpr int kQuads = kBlocks * 4;               // 4-channel groups of a row and round
+    constexpr int kQuads = W::NB * 4;  // 4-channel groups of a row
     static_assert(sizeof(sh.tile) >= (size_t)kWaves * 16 * RT * kQuads * 16, "room for the sums");
-    f4* sums = (f4*)sh.tile;                          // [wave][row][quad], quads rotated by row
+    f4* sums = (f4*)sh.tile;           // [wave][row][quad], quads rotated by row
 #pragma unroll
-    for (int round = 0; round < kRounds; round++) {
-      __syncthreads();  // scale is written; the last round is read
+    for (int r = 0; r < RT; r++)
 #pragma unroll
-      for (int r = 0; r < RT; r++)
-#pragma unroll
-        for (int b = 0; b < kBlocks; b++)
-          sums[(wave * 16 * RT + r * 16 + n) * kQuads + ((b * 4 + g + r * 16 + n) & (kQuads - 1))] =
-              w.o[r][round * kBlocks + b];
-      __syncthreads();
+      for (int b = 0; b < W::NB; b++)
+        sums[(wave * 16 * RT + r * 16 + n) * kQuads + ((b * 4 + g + r * 16 + n) & (kQuads - 1))] = w.o[r][b];
+    __syncthreads();
 #pragma unroll 1
-      for (int i = tid; i < 16 * RT * kQuads; i += kThreads) {
-        const int row = i / kQuads, quad = i % kQuads;
-        const int ch = round * kBlocks * 16 + quad * 4, gr = rt * 16 * RT + row;
-        if (gr >= it.rows || ch >= a.d) continue;
-        f4 x{0, 0, 0, 0};
-#pragma unroll
-        for (int y = 0; y < kWaves; y++)
-          x += sh.scale[y][row] * sums[(y * 16 * RT + row) * kQuads + ((quad + row) & (kQuads - 1))];
-        if (a.direct) store_out(out_at(a, it, gr) + ch, x * sh.l[0][row]);
-        else *(f4*)(a.part + part_at(a, it, gr) * a.d + ch) = x;
-      }
+    for (int i = tid; i < it.heads * 16 * RT * kQuads; i += kThreads) {
+      const int quad = i % kQuads, row = i / kQuads % (16 * RT), hh = i / (16 * RT * kQuads), w0 = hh * turn;
+      const int ch = quad * 4, gr = rt * 16 * RT + row;
+      if (gr >= it.rows || ch >= a.d) continue;
+      f4 x{0, 0, 0, 0};
+      for (int y = w0; y < w0 + turn; y++)
+        x += sh.scale[y][row] * sums[(y * 16 * RT + row) * kQuads + ((quad + row) & (kQuads - 1))];
+      if (a.direct) store_out(out_at(a, it, it.head + hh, gr) + ch, x * sh.l[w0][row]);
+      else *(f4*)(a.part + part_at(a, it, it.head + hh, gr) * a.d + ch) = x;
     }
     __syncthreads();  // m, l and scale are free
     if (sh.odd) tk.template add_odd<kThreads>(a, it, sh, ranges, rt * 16 * RT, (rt + 1) * 16 * RT);
@@ -811,6 +808,7 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
   if (!a.direct && !tk.start(a, it, sh)) return;
   const int ranges = ranges_of(a, it);
   const Places<DP> at_lane;
+  const char *kp = a.k + it.head * a.d * 2, *vp = a.v + it.head * a.d * 2;
   const uint32_t lds = lds_address(sh.tile);
   const float c = log2_scale(a);
   const int tile_rows = 16 * RT * kWaves, row_tiles = (it.rows + tile_rows - 1) / tile_rows;
@@ -819,9 +817,9 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
     const int row0 = rt * tile_rows + wave * 16 * RT;
     W w;
     w.clear();
-    w.load_queries(a, it, row0);
+    w.load_queries(a, it, it.head, row0);
     tk.clear_tiles(a, sh);
-    if (threadIdx.x == 0) sh.odd = 0;
+    if (threadIdx.x == 0) sh.odd = sh.bad = 0;
 #pragma unroll 1
     for (int range = 0; range < ranges; range++) {
     const Item cur = range_of(it, ranges, range);
@@ -837,8 +835,8 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
         if (tile >= stop) return;
         const TileAt at = tile_at(tk.src, tile * kTile);
         const uint32_t to = lds + slot_of(tile) * (2 * Ge::BYTES);
-        load_tile<DP, kMine>(tk.src, tk.kp, to, at, tk.full(tile), wave * kMine);
-        load_tile<DP, kMine>(tk.src, tk.vp, to + Ge::BYTES, at, tk.full(tile), wave * kMine);
+        load_tile<DP, kMine>(tk.src, kp, to, at, tk.full(tile), wave * kMine);
+        load_tile<DP, kMine>(tk.src, vp, to + Ge::BYTES, at, tk.full(tile), wave * kMine);
       };
       // Behind the barrier the tile is there for all waves, and none reads the slot of
       // the one before it any more, which takes the tile kStages - 1 ahead.
@@ -885,8 +883,8 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
           // A wave's loads are spread over the step: issued at once by all waves they
           // queue for hundreds of cycles, and the waves with them.
           auto load = [&](int i) {
-            if (i < kMine) load_lds(to + i * 1024, tk.kp + off, at_row[i < kMine ? i : 0]);
-            else load_lds(to + Ge::BYTES + (i - kMine) * 1024, tk.vp + off, at_row[i < kMine ? 0 : i - kMine]);
+            if (i < kMine) load_lds(to + i * 1024, kp + off, at_row[i < kMine ? i : 0]);
+            else load_lds(to + Ge::BYTES + (i - kMine) * 1024, vp + off, at_row[i < kMine ? 0 : i - kMine]);
           };
           constexpr int kQuarter = kMine >= 2 ? kMine / 2 : 1;
           auto some = [&](int from) {
@@ -944,15 +942,14 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
       if (row >= it.rows) continue;
       if (a.direct) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t* to = out_at(a, it, row);
+        uint16_t* to = out_at(a, it, it.head, row);
 #pragma unroll
         for (int b = 0; b < W::NB; b++)
           if (b * 16 + g * 4 < a.d) store_out(to + b * 16 + g * 4, w.o[r][b] * inv);
-        if (g == 0 && a.lse)
-          a.lse[(int64_t)(it.q0 + row / a.G) * a.H + it.head * a.G + row % a.G] = lse_of(w.m[r], l);
+        if (g == 0 && a.lse) *lse_at(a, it, it.head, row) = lse_of(w.m[r], l);
         continue;
       }
-      const int64_t at = part_at(a, it, row);
+      const int64_t at = part_at(a, it, it.head, row);
       if (g == 0) {
         a.ml[2 * at] = w.m[r];
         a.ml[2 * at + 1] = l;
@@ -972,10 +969,11 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
 // them.  False: nothing to do.
 template <class A>
 __device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
-  it.head = w % a.kv;
-  w /= a.kv;
-  const int pre_items = a.pre_groups * a.pre_splits * a.pre_tiles;
+  const int pre_items = a.pre_groups * a.pre_splits * a.pre_tiles * a.kv;
   if (w < pre_items) {
+    it.head = w % a.kv;
+    it.heads = 1;
+    w /= a.kv;
     it.row_tile = w % a.pre_tiles;
     w /= a.pre_tiles;
     it.split = w % a.pre_splits;
@@ -1000,6 +998,9 @@ __device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
     return true;
   }
   w -= pre_items;
+  it.head = w % (a.kv / a.rest_heads) * a.rest_heads;
+  it.heads = a.rest_heads;
+  w /= a.kv / a.rest_heads;
   it.row_tile = w % a.rest_tiles;
   w /= a.rest_tiles;
   it.split = w % a.rest_splits;
@@ -1026,15 +1027,14 @@ __device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
   return it.ok && q.m > 0;
 }
 
-// Direct: outputs of a refused sequence's queries, of the item's kv head.
+// Direct: outputs of a refused sequence's queries, of the item's kv heads.
 __device__ __forceinline__ void refuse(const Attn& a, const Item& it) {
   if (it.row_tile != 0) return;
-  const int n = a.G * a.d;
+  const int h0 = it.head * a.G, n = it.heads * a.G;
   for (int q = max(it.q0, 0); q < min(it.q_end, a.n_q); q++) {
-    for (int i = threadIdx.x; i < n; i += blockDim.x)
-      a.out[q * a.out_stride + (int64_t)it.head * n + i] = 0;
-    for (int i = threadIdx.x; a.lse && i < a.G; i += blockDim.x)
-      a.lse[(int64_t)q * a.H + it.head * a.G + i] = -__builtin_inff();
+    for (int i = threadIdx.x; i < n * a.d; i += blockDim.x) a.out[q * a.out_stride + h0 * a.d + i] = 0;
+    for (int i = threadIdx.x; a.lse && i < n; i += blockDim.x)
+      a.lse[(int64_t)q * a.H + h0 + i] = -__builtin_inff();
   }
   if (it.says && threadIdx.x == 0 && it.q0 < it.q_end) atomicOr(a.status, kRefused);
 }
@@ -1137,7 +1137,7 @@ __global__ __launch_bounds__(kThreads) void k_join(Attn a) {
 
 // How many splits and row tiles the launch has, from the call's numbers alone.
 struct Plan {
-  int dp, pre_splits, rest_splits, pre_tiles, rest_tiles, pre_mode, rest_mode, pre_groups;
+  int dp, pre_splits, rest_splits, pre_tiles, rest_tiles, pre_mode, rest_mode, pre_groups, rest_heads;
   bool direct;
   size_t words;
 };
@@ -1212,6 +1212,16 @@ Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
   }
   p.rest_splits = splits((int64_t)std::max(1, x.n_seqs) * kv * p.rest_tiles,
                          std::max(0, x.max_len - (shared ? x.max_prefix : 0)), slots, kRestTiles);
+  // Several heads a workgroup share its start (about 5 us of latencies) and leave fewer
+  // waves to wait for the one with most tiles, as long as there are workgroups enough
+  // (64 sequences of 300 tokens and 8 heads: 15 us for each of 512 workgroups of one).
+  auto heads = [&](int splits) {
+    int n = 1;
+    while (n < 4 && p.rest_mode <= kRows32 && kv % (2 * n) == 0 &&
+           (int64_t)x.n_seqs * kv / (2 * n) * p.rest_tiles * splits >= 256)
+      n *= 2;
+    return n;
+  };
   // Sharing saves (sequences - 1) times the prefix and costs a second kernel and its
   // start, about 5 us: not for little.
   const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
@@ -1221,9 +1231,11 @@ Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
     p.pre_groups = 0;
     p.pre_splits = 0;
     p.rest_splits = 1;
+    p.rest_heads = heads(1);
     p.words = 4;
     return p;
   }
+  p.rest_heads = heads(p.rest_splits);
   p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + x.n_q + 4;
   return p;
 }
@@ -1303,12 +1315,13 @@ int cg_attention_prefix_async(const cg_paged_cache* c, const cg_attention* a, vo
   v.rest_splits = p.rest_splits;
   v.pre_tiles = p.pre_tiles;
   v.rest_tiles = p.rest_tiles;
+  v.rest_heads = p.rest_heads;
   v.pre_groups = p.pre_groups;
   v.part = (float*)workspace_dev;
   v.ml = v.part + (size_t)(p.pre_splits + p.rest_splits) * a->n_q * a->n_heads * a->head_dim;
   v.used = (int32_t*)(v.ml + (size_t)2 * (p.pre_splits + p.rest_splits) * a->n_q * a->n_heads);
   const int64_t pre = (int64_t)p.pre_groups * p.pre_splits * p.pre_tiles * v.kv;
-  const int64_t rest = (int64_t)a->n_seqs * p.rest_splits * p.rest_tiles * v.kv;
+  const int64_t rest = (int64_t)a->n_seqs * p.rest_splits * p.rest_tiles * (v.kv / p.rest_heads);
   hipStream_t st = (hipStream_t)stream;
   const int only = pre ? p.pre_mode : p.rest_mode;
   if (!launch(p.dp, p.direct, only, p.rest_mode, v, 0, pre + rest, st)) {  // unusual pairs: one after the other

@@ -191,6 +191,42 @@ def test_many_sequences():
     check(x, 0, q, 0.125, rows, np.arange(n + 1), gs[10:41], prefixes[10:40])
 
 
+@pytest.mark.parametrize("seqs,kv,G,d", [(130, 4, 2, 40), (129, 6, 3, 128), (256, 4, 1, 64), (70, 8, 4, 32)])
+def test_many_sequences_of_several_heads(seqs, kv, G, d):
+    """A batch whose workgroups take two or four kv heads each, with what is no finite
+    number behind the rows' ends and, for the last head, in a token of the first row."""
+    rng = np.random.default_rng(seqs + d)
+    tails = [[int(n) for n in rng.integers(2, 20, seqs // 2)], [int(n) for n in rng.integers(2, 150, seqs - seqs // 2)]]
+    c, rows = build(rng, 1, kv * d, 8, [21, 9], tails)
+    gone = rows[seqs // 3]
+    c.tables[gone, 3] = -1
+    counts = rng.integers(0, 3, seqs)
+    n = int(counts.sum())
+    x = Pair(c)
+    q = queries(rng, n, kv * G, d)
+    starts = starts_of(counts)
+    check(x, 0, q, d ** -0.5, rows, starts, group_starts_of(tails), [21, 9])
+    check(x, 0, q, d ** -0.5, rows, starts)
+    counts[0], counts[1:] = 2, 1
+    n = int(counts.sum())
+    q, starts = queries(rng, n, kv * G, d), starts_of(counts)
+    _, recs = pc.attention(c, 0, q, d ** -0.5, rows, starts)
+    last = int(c.lens[rows[0]]) - 1  # only the second query of the first sequence sees it
+    c.v[0, c.tables[rows[0], last // 8], last % 8, (kv - 1) * d + 3] = np.inf
+    for row in range(len(c.tables)):
+        for t in range(int(c.lens[row]), 8 * c.tables.shape[1]):
+            page = c.tables[row, t // 8]
+            if page >= 0 and c.refs[page] == 1:
+                c.k[0, page, t % 8] = c.v[0, page, t % 8] = np.nan
+    for hints in (None, (2, 0, 1 << 21)):
+        st, out, lse = gpu_attention(Pair(c), 0, q, d ** -0.5, rows, starts, None, None, hints=hints)
+        hit = out[1, (kv - 1) * G:, 3]
+        assert (hit == np.inf).all()
+        for h in range((kv - 1) * G, kv * G):
+            out[1, h, 3] = recs[1][h]["out"][3]
+        compare((st, out, lse), (pc.BAD_PAGE, recs), q)
+
+
 def test_group_of_many():
     """More rows than one tile of the shared part: 70 sequences of 4 heads, ragged queries."""
     rng = np.random.default_rng(14)
