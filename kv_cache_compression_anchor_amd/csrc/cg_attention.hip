@@ -1088,7 +1088,7 @@ __global__ __launch_bounds__(kBlock, resident(DP)) void k_attention(Call<kDirect
 // loads under way that counts.
 __global__ __launch_bounds__(kThreads) void k_join(Attn a) {
   __shared__ f4 sums[kThreads];
-  __shared__ float ls[kThreads];
+  __shared__ float ms[kThreads], ls[kThreads];
   const int qi = blockIdx.x, tid = threadIdx.x;
   const int from = a.q_starts[0], to = a.q_starts[a.n_seqs], said = a.used[qi];
   if (qi < from || qi >= to) return;  // no sequence's query
@@ -1100,33 +1100,58 @@ __global__ __launch_bounds__(kThreads) void k_join(Attn a) {
   const bool in = hl < heads && h < a.H;
   const int64_t slot_step = (int64_t)a.n_q * a.H, at0 = (int64_t)qi * a.H + h;
   auto at = [&](int x) { return at0 + slot_step * (x < pre ? x : a.pre_splits + x - pre); };
-  // splits that weighed nothing have l = 0 and no reference exponent
+  // A sum against reference `from` is worth this much against `to`; without a reference
+  // it holds nothing, or only what is no number and stays so.
+  auto worth = [](float from, float to) {
+    return from == to || from == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(from - to);
+  };
   float m = -__builtin_inff(), l = 0.0f;
   f4 o{0, 0, 0, 0};
   if (in) {
-#pragma unroll 8
-    for (int x = 0; x < used; x++) m = fmaxf(m, a.ml[2 * at(x)]);
-#pragma unroll 4
-    for (int x = part; x < used; x += a.join) {
-      const float mx = a.ml[2 * at(x)], lx = a.ml[2 * at(x) + 1];
-      const f4 ox = *(const f4*)(a.part + at(x) * a.d + quad * 4);
-      const float f = mx == m ? 1.0f : __builtin_amdgcn_exp2f(mx - m);
-      // nothing weighed: what the split left in o is not looked at; no number stays one
-      if (lx != 0.0f) {
-        o += ox * (mx == -__builtin_inff() ? 1.0f : f);
-        l += lx * (mx == -__builtin_inff() ? 1.0f : f);
+    constexpr int kBatch = 4;  // splits whose loads are issued together
+    for (int x0 = part; x0 < used; x0 += kBatch * a.join) {
+      float mx[kBatch], lx[kBatch];
+      f4 ox[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; i++) {
+        const int64_t slot = at(min(x0 + i * a.join, used - 1));
+        const float2 ml = *(const float2*)(a.ml + 2 * slot);
+        mx[i] = ml.x;
+        lx[i] = x0 + i * a.join < used ? ml.y : 0.0f;
+        ox[i] = *(const f4*)(a.part + slot * a.d + quad * 4);
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kBatch; i++) top = fmaxf(top, lx[i] != 0.0f ? mx[i] : top);
+      const float keep = worth(m, top);
+      o *= keep;
+      l *= keep;
+      m = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; i++) {
+        if (lx[i] == 0.0f) continue;  // nothing weighed: what the split left in o is not looked at
+        const float f = worth(mx[i], m);
+        o += ox[i] * f;
+        l += lx[i] * f;
       }
     }
   }
   if (a.join > 1) {
     sums[tid] = o;
+    ms[tid] = m;
     ls[tid] = l;
     __syncthreads();
     if (!in || part) return;
+    float top = m;
+    for (int x = 1; x < a.join; x++) top = fmaxf(top, ms[tid + x * quads]);
+    o *= worth(m, top);
+    l *= worth(m, top);
     for (int x = 1; x < a.join; x++) {
-      o += sums[tid + x * quads];
-      l += ls[tid + x * quads];
+      const float f = worth(ms[tid + x * quads], top);
+      o += sums[tid + x * quads] * f;
+      l += ls[tid + x * quads] * f;
     }
+    m = top;
   } else if (!in) {
     return;
   }
