@@ -42,32 +42,48 @@ __device__ __forceinline__ int below(uint64_t mask) {  // set bits below this la
 }
 
 struct ScanLds {
-  int64_t wave[kWaves];
+  uint32_t wave[kWaves];
 };
 
-// exclusive sum of one value per thread; *total receives the sum
-__device__ int64_t block_scan(int64_t x, ScanLds& s, int64_t* total) {
-  int64_t inc = x;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t y = __shfl_up(inc, d);
-    if (lane_id() >= d) inc += y;
-  }
+// Sums stay at 2^32 - 1 once they are there: no pool has so many pages.
+__device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
+
+// exclusive sum of one value per wave
+__device__ __forceinline__ uint32_t wave_sums(uint32_t of_wave, ScanLds& s, uint32_t* total) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   __syncthreads();  // s is free again
-  if (lane_id() == 63) s.wave[threadIdx.x >> 6] = inc;
+  if (lane_id() == 0) s.wave[wave] = of_wave;
   __syncthreads();
-  int64_t base = 0, all = 0;
+  uint32_t base = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; w++) {
-    const int64_t t = s.wave[w];
-    if (w < (int)(threadIdx.x >> 6)) base += t;
-    all += t;
+    const uint32_t x = s.wave[w];
+    if (w < wave) base = add(base, x);
+    all = add(all, x);
   }
   *total = all;
-  return base + inc - x;
+  return base;
 }
 
-// A wave's share of a scan step: 1,024 consecutive pages, 16 coalesced loads in flight.
+// Exclusive sum of one value per thread; *total receives the sum.  Within a wave by
+// moves between lanes of the vector unit, a tenth of the latency of moves through LDS.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, ScanLds& s, uint32_t* total) {
+  uint32_t inc = x;
+#define FROM(ctrl, rows) add(inc, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)inc, ctrl, rows, 0xF, false))
+  inc = FROM(0x111, 0xF);  // from 1, 2, 4 and 8 lanes below in a row of 16
+  inc = FROM(0x112, 0xF);
+  inc = FROM(0x114, 0xF);
+  inc = FROM(0x118, 0xF);
+  inc = FROM(0x142, 0xA);  // from the last lane of the row below to rows 1 and 3
+  inc = FROM(0x143, 0xC);  // from lane 31 to rows 2 and 3
+#undef FROM
+  uint32_t before = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)inc, 0x138, 0xF, 0xF, false);  // of the lane below
+  return add(wave_sums((uint32_t)__builtin_amdgcn_readlane((int)inc, 63), s, total), before);
+}
+
+// A wave's share of a scan step: 1,024 consecutive pages, 16 coalesced loads in flight
+// (loads that are each under a condition wait for one another, 5 us in all: those past
+// the end read the last count, which nobody looks at).
 struct Counts {
   int32_t r[16];
   __device__ __forceinline__ static int page(int base, int i) {
@@ -75,7 +91,7 @@ struct Counts {
   }
   __device__ __forceinline__ void load(const int32_t* refs, int base, int to) {
 #pragma unroll
-    for (int i = 0; i < 16; i++) r[i] = page(base, i) < to ? refs[page(base, i)] : -1;
+    for (int i = 0; i < 16; i++) r[i] = refs[min(page(base, i), to - 1)];
   }
 };
 
@@ -91,9 +107,8 @@ __device__ __forceinline__ int scan_step(const Counts& c, int base, int from, in
     hit[i] = __ballot(p >= from && p < to && (kFree ? c.r[i] == 0 : c.r[i] > 0));
     n += __popcll(hit[i]);
   }
-  int64_t all;
-  const int at = (int)block_scan(lane_id() == 0 ? n : 0, s, &all);
-  int rank = found + __shfl(at, 0);
+  uint32_t all;
+  int rank = found + (int)wave_sums(n, s, &all);
 #pragma unroll
   for (int i = 0; i < 16; i++) {
     if ((hit[i] >> lane_id()) & 1) f(Counts::page(base, i), rank + below(hit[i]));
@@ -117,7 +132,7 @@ __device__ int scan_pages(const int32_t* refs, const Counts& first, int from, in
 template <bool kFree, class F>
 __device__ int scan_pages(const int32_t* refs, int from, int to, int limit, ScanLds& s, F f) {
   Counts c;
-  c.load(refs, from, to);
+  if (from < to) c.load(refs, from, to);
   return scan_pages<kFree>(refs, c, from, to, limit, s, f);
 }
 
@@ -284,7 +299,7 @@ __global__ __launch_bounds__(kThreads) void k_reserve(Cache c, int n, const int3
       }
       if (!good) atomicOr(c.status, kRefused);
     }
-    int64_t all;
+    uint32_t all;
     const int64_t at = sum + block_scan(need, s, &all);
     if (i < n) {
       cum[i] = (int)(at < kMany ? at : kMany);
@@ -330,31 +345,34 @@ __global__ __launch_bounds__(kThreads) void k_reserve_few(Cache c, int n, const 
                                                           int64_t* slots, int32_t* list) {
   __shared__ ScanLds s;
   __shared__ uint32_t seen[kRowWords], twice[kRowWords];
-  __shared__ int32_t cum[kFew + 1], start[kFew + 1], old_len[kFew], old_page[kFew], dealt[kFewPages];
+  __shared__ int32_t cum[kFew + 1], start[kFew + 1], old_len[kFew], old_page[kFew], of_row[kFew], dealt[kFewPages];
   const int i = threadIdx.x;
-  const int row = i < n ? rows[i] : -1, a = i < n ? starts[i] : 0, b = i < n ? starts[i + 1] : 0;
+  // all loads are made without conditions, which would have them wait for one another
+  const int ic = min(i, n - 1), some_row = rows[ic], a = starts[ic], b = starts[ic + 1];
   Counts counts;
   counts.load(c.refs, 0, c.N);
   clear_bits(seen, c.R);
   clear_bits(twice, c.R);
+  const int row = i < n ? some_row : -1;
   const bool known = row_ok(c, row);
-  const int len = known ? c.lens[row] : -1;
+  const int some_len = c.lens[known ? row : 0], len = known ? some_len : -1;
   __syncthreads();
   if (known && set_bit(seen, row)) set_bit(twice, row);
   const bool fits = known && a >= 0 && a <= b && b <= n_tokens && len_ok(c, len) &&
                     len_ok(c, (int64_t)len + (b - a));
-  const int last = fits && (len & (c.P - 1)) ? entry(c, row, blocks_of(c, len) - 1) : -1;
+  const int last = entry(c, fits ? row : 0, fits && len ? blocks_of(c, len) - 1 : 0);
   __syncthreads();
   const bool good = fits && !test_bit(twice, row);
   if (i < n && !good) atomicOr(c.status, kRefused);
   const int need = good ? blocks_of(c, (int64_t)len + (b - a)) - blocks_of(c, len) : 0;
-  constexpr int64_t kMany = 1 << 30;  // sums are cut there: no pool has so many pages
-  int64_t sum;
-  const int64_t at = block_scan(need, s, &sum);
+  constexpr uint32_t kMany = 1 << 30;  // sums are cut there: no pool has so many pages
+  uint32_t sum;
+  const uint32_t at = block_scan(need, s, &sum);
   const int total = (int)(sum < kMany ? sum : kMany);
   if (i < n) {
     cum[i] = (int)(at < kMany ? at : kMany);
     start[i] = a;
+    of_row[i] = row;
     old_page[i] = last;
     if (i == n - 1) {
       cum[n] = total;
@@ -369,7 +387,7 @@ __global__ __launch_bounds__(kThreads) void k_reserve_few(Cache c, int n, const 
                           : 0;
   const int have = min(found, total);
   if (i < n) {
-    const bool granted = good && (need == 0 || at + need <= have);
+    const bool granted = good && (need == 0 || (int64_t)at + need <= have);
     old_len[i] = granted ? len : -1;
     if (granted) c.lens[row] = len + (b - a);
     else if (good) atomicOr(c.status, kNoPages);
@@ -379,7 +397,7 @@ __global__ __launch_bounds__(kThreads) void k_reserve_few(Cache c, int n, const 
     const int j = last_at_most(cum, n, r);  // the last of equal ones: the request that needs pages
     if (old_len[j] < 0) continue;
     const int page = pages[r];
-    entry(c, rows[j], blocks_of(c, old_len[j]) + (r - cum[j])) = page;
+    entry(c, of_row[j], blocks_of(c, old_len[j]) + (r - cum[j])) = page;
     c.refs[page] = 1;
   }
   for (int t = i; slots && t < n_tokens; t += kThreads) {
@@ -472,7 +490,7 @@ __global__ __launch_bounds__(kThreads) void k_fork_plan(Cache c, int n, const in
       aux[3 * i] = last;
       aux[3 * i + 2] = part;
     }
-    int64_t all;
+    uint32_t all;
     const int64_t at = block_scan(need, s, &all);
     if (i < n) {
       cum[i] = total + (int)at;
@@ -509,20 +527,21 @@ __global__ __launch_bounds__(kThreads) void k_fork_plan_few(Cache c, int n, cons
   __shared__ uint32_t kids[kRowWords], twice[kRowWords], olds[kRowWords];
   __shared__ int32_t dealt[kFew];
   const int i = threadIdx.x;
-  const int par = i < n ? parents[i] : -1, kid = i < n ? children[i] : -1;
+  const int ic = min(i, n - 1), some_par = parents[ic], some_kid = children[ic];
   Counts counts;
   counts.load(c.refs, 0, c.N);
   clear_bits(kids, c.R);
   clear_bits(twice, c.R);
   clear_bits(olds, c.R);
+  const int par = i < n ? some_par : -1, kid = i < n ? some_kid : -1;
   const bool known = row_ok(c, par) && row_ok(c, kid);
-  const int len = known ? c.lens[par] : -1, kid_len = known ? c.lens[kid] : -1;
+  const int some_len = c.lens[known ? par : 0], kid_len = c.lens[known ? kid : 0], len = known ? some_len : -1;
   __syncthreads();
   if (row_ok(c, kid) && set_bit(kids, kid)) set_bit(twice, kid);
   if (row_ok(c, par)) set_bit(olds, par);
   const bool fits = known && kid_len == 0 && len_ok(c, len);
   const int part = fits ? len & (c.P - 1) : 0;
-  const int last = part ? entry(c, par, blocks_of(c, len) - 1) : -1;
+  const int last = entry(c, part ? par : 0, part ? blocks_of(c, len) - 1 : 0);
   __syncthreads();
   bool good = fits && !test_bit(twice, kid) && !test_bit(olds, kid);
   if (i < n && !good) atomicOr(c.status, kRefused);
@@ -531,7 +550,7 @@ __global__ __launch_bounds__(kThreads) void k_fork_plan_few(Cache c, int n, cons
     atomicOr(c.status, kBadPage);
   }
   const int need = good && part;
-  int64_t total;
+  uint32_t total;
   const int at = (int)block_scan(need, s, &total);
   const int found = total ? scan_pages<true>(c.refs, counts, 0, c.N, (int)total, s,
                                              [&](int page, int rank) {
@@ -782,7 +801,7 @@ int cg_pages_reserve_async(const cg_paged_cache* c, int32_t n, const int32_t* ro
   if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
   const PagesWs w = pages_ws(*c);
   int32_t* ws = (int32_t*)workspace_dev;
-  if (n <= kFew)
+  if (n > 0 && n <= kFew)  // without a request there is no list to read the first one from
     k_reserve_few<<<1, kThreads, 0, (hipStream_t)stream>>>(view(*c), n, rows_dev, starts_dev,
                                                            n_tokens, slots_dev, ws + w.list);
   else
