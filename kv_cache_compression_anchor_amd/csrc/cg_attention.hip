@@ -252,7 +252,7 @@ __device__ __forceinline__ void load_tile(const Source& s, const char* pool, uin
 // not see some token: a value there that is no finite number must not meet the
 // zero weight of such a query.  Rows of tokens that do not exist (which hold
 // anything) become zeros, and so does every value that is no finite number; returns
-// whether there was one: add_odd_values() gives it to the queries that see it.
+// whether there was one: add_odd() gives it to the queries that see it.
 template <int DP>
 __device__ __forceinline__ bool clean_values(char* tile, int pages) {
   using Ge = Geo<DP>;
@@ -329,7 +329,6 @@ __device__ __forceinline__ void store_out(uint16_t* to, f4 x) {  // 4 channels
   r.w = float_to_half_bits(x[3]);
   *(ushort4*)to = r;
 }
-
 
 // tokens that the query of a row sees
 __device__ __forceinline__ int row_lim(const Attn& a, const Item& it, int row) {
@@ -681,56 +680,56 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
     if (threadIdx.x == 0) sh.odd = sh.bad = 0;
 #pragma unroll 1
     for (int range = 0; range < ranges; range++) {
-    const Item cur = range_of(it, ranges, range);
-    if (a.direct && !tk.start(a, cur, sh)) continue;
-    const int min_lim = row_lim(a, cur, rt * 16 * RT);
-    const int end = tk.seen_end(a, cur, (rt + 1) * 16 * RT - 1);
-    for (int base = tk.first; base < end; base += tk.list_tiles) {
-      const int stop = min(base + tk.list_tiles, end);
-      tk.stretch(a, cur, sh, base, stop);
-      // the tile in hand, where its tokens are, whether its queries see all of it; the
-      // next one
-      int tile = base + wave % turn, next;
-      TileAt at{-1, 0, 0}, next_at{-1, 0, 0};
-      bool all = false, more = false, full = false;
-      auto look = [&](int nt) {
-        next = nt;
-        more = nt < stop;
-        full = more && tk.full(nt);
-        if (more) next_at = tile_at(tk.src, nt * kTile);
-      };
-      auto load_k = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, kp, klds, next_at, full); };
-      auto load_v = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, vp, vlds, next_at, full); };
-      auto step = [&] {
-        tile = next;
-        at = next_at;
-        all = full && (next + 1) * kTile <= min_lim;
-      };
-      look(tile);
-      load_k();
-      load_v();
-      step();
-      while (tile < stop) {
-        f4 s[RT][2];
-        h8 p[RT];
-        look(tile + turn);
-        wait_loads<Ge::NI>();
-        w.scores(kt, at_lane.fresh(), s, [] {});
-        wait_lds();
+      const Item cur = range_of(it, ranges, range);
+      if (a.direct && !tk.start(a, cur, sh)) continue;
+      const int min_lim = row_lim(a, cur, rt * 16 * RT);
+      const int end = tk.seen_end(a, cur, (rt + 1) * 16 * RT - 1);
+      for (int base = tk.first; base < end; base += tk.list_tiles) {
+        const int stop = min(base + tk.list_tiles, end);
+        tk.stretch(a, cur, sh, base, stop);
+        // the tile in hand, where its tokens are, whether its queries see all of it; the
+        // next one
+        int tile = base + wave % turn, next;
+        TileAt at{-1, 0, 0}, next_at{-1, 0, 0};
+        bool all = false, more = false, full = false;
+        auto look = [&](int nt) {
+          next = nt;
+          more = nt < stop;
+          full = more && tk.full(nt);
+          if (more) next_at = tile_at(tk.src, nt * kTile);
+        };
+        auto load_k = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, kp, klds, next_at, full); };
+        auto load_v = [&] { if (more) load_tile<DP, Ge::NI>(tk.src, vp, vlds, next_at, full); };
+        auto step = [&] {
+          tile = next;
+          at = next_at;
+          all = full && (next + 1) * kTile <= min_lim;
+        };
+        look(tile);
         load_k();
-        if (!all) w.mask(a, cur, rt * 16 * RT, s, tile * kTile, at.page);
-        float mx[RT];
-        const bool raise = w.peaks(s, c, mx);
-        w.reference(raise, mx, c);
-        w.weights(s, c, p);
-        if (more) wait_loads<Ge::NI>(); else wait_loads<0>();
-        if (!all && clean_values<DP>(vt, at.page)) sh.odd = 1;
-        w.values(vt, at_lane.fresh(), p, [] {});
-        wait_lds();
         load_v();
         step();
+        while (tile < stop) {
+          f4 s[RT][2];
+          h8 p[RT];
+          look(tile + turn);
+          wait_loads<Ge::NI>();
+          w.scores(kt, at_lane.fresh(), s, [] {});
+          wait_lds();
+          load_k();
+          if (!all) w.mask(a, cur, rt * 16 * RT, s, tile * kTile, at.page);
+          float mx[RT];
+          const bool raise = w.peaks(s, c, mx);
+          w.reference(raise, mx, c);
+          w.weights(s, c, p);
+          if (more) wait_loads<Ge::NI>(); else wait_loads<0>();
+          if (!all && clean_values<DP>(vt, at.page)) sh.odd = 1;
+          w.values(vt, at_lane.fresh(), p, [] {});
+          wait_lds();
+          load_v();
+          step();
+        }
       }
-    }
     }
     // the waves' sums together, against the largest reference exponent
 #pragma unroll
@@ -822,116 +821,116 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
     if (threadIdx.x == 0) sh.odd = sh.bad = 0;
 #pragma unroll 1
     for (int range = 0; range < ranges; range++) {
-    const Item cur = range_of(it, ranges, range);
-    if (a.direct && !tk.start(a, cur, sh)) continue;
-    const int min_lim = row_lim(a, cur, rt * tile_rows);
-    const int end = tk.seen_end(a, cur, (rt + 1) * tile_rows - 1);
-    for (int base = tk.first; base < end; base += tk.list_tiles) {
-      const int stop = min(base + tk.list_tiles, end);
-      tk.stretch(a, cur, sh, base, stop);
-      char* ring = sh.tile[0][0];
-      auto slot_of = [&](int tile) { return (tile - base) & (kStages - 1); };
-      auto load = [&](int tile) {
-        if (tile >= stop) return;
-        const TileAt at = tile_at(tk.src, tile * kTile);
-        const uint32_t to = lds + slot_of(tile) * (2 * Ge::BYTES);
-        load_tile<DP, kMine>(tk.src, kp, to, at, tk.full(tile), wave * kMine);
-        load_tile<DP, kMine>(tk.src, vp, to + Ge::BYTES, at, tk.full(tile), wave * kMine);
-      };
-      // Behind the barrier the tile is there for all waves, and none reads the slot of
-      // the one before it any more, which takes the tile kStages - 1 ahead.
-      auto publish = [&] {
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-      };
-      for (int i = 0; i < kStages - 1; i++) load(base + i);
-
-      // Tiles of which every query sees all, and the tiles loaded meanwhile too, in
-      // rounds of the ring's slots: no branch but one, LDS offsets are immediates, and
-      // a wave's 8 rows of a tile lie in one page, whose number is read a tile ahead.
-      // (A wave that finds its way through the conditions below instead spends a third
-      // of its time on them and on addresses: 165 us against 128 for 32 requests on 81920
-      // tokens.)
-      int tile = base;
-      const int seen = tk.bad || base * kTile < cur.lo ? base : min(stop, min_lim / kTile);
-      if (tk.src.pmask >= 7 && tk.src.nc == Ge::NC && tile + 2 * kStages - 1 <= seen) {
-        const int last_page = ((min(stop * kTile, cur.hi) - 1) >> tk.src.shift) - tk.src.block0;
-        auto page_of = [&](int tl) {
-          return sh.list[min(((tl * kTile + wave * 8) >> tk.src.shift) - tk.src.block0, last_page)];
+      const Item cur = range_of(it, ranges, range);
+      if (a.direct && !tk.start(a, cur, sh)) continue;
+      const int min_lim = row_lim(a, cur, rt * tile_rows);
+      const int end = tk.seen_end(a, cur, (rt + 1) * tile_rows - 1);
+      for (int base = tk.first; base < end; base += tk.list_tiles) {
+        const int stop = min(base + tk.list_tiles, end);
+        tk.stretch(a, cur, sh, base, stop);
+        char* ring = sh.tile[0][0];
+        auto slot_of = [&](int tile) { return (tile - base) & (kStages - 1); };
+        auto load = [&](int tile) {
+          if (tile >= stop) return;
+          const TileAt at = tile_at(tk.src, tile * kTile);
+          const uint32_t to = lds + slot_of(tile) * (2 * Ge::BYTES);
+          load_tile<DP, kMine>(tk.src, kp, to, at, tk.full(tile), wave * kMine);
+          load_tile<DP, kMine>(tk.src, vp, to + Ge::BYTES, at, tk.full(tile), wave * kMine);
         };
-        const int lrow = lane / Ge::NC, lc = lane % Ge::NC;
-        uint32_t at_row[kMine];
-#pragma unroll
-        for (int j = 0; j < kMine; j++)
-          at_row[j] = (j * Ge::RPI + lrow) * tk.src.row_bytes +
-                      (lc ^ swizzle<DP>((wave * kMine + j) * Ge::RPI + lrow)) * 16;
-        int page = page_of(tile + kStages - 1);
-        auto step = [&](auto slot_c) {
-          constexpr int kSlot = decltype(slot_c)::value;
-          char* kt = ring + kSlot * 2 * Ge::BYTES;
-          const uint32_t to = lds + ((kSlot + kStages - 1) & (kStages - 1)) * 2 * Ge::BYTES + wave * kMine * 1024;
+        // Behind the barrier the tile is there for all waves, and none reads the slot of
+        // the one before it any more, which takes the tile kStages - 1 ahead.
+        auto publish = [&] {
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        };
+        for (int i = 0; i < kStages - 1; i++) load(base + i);
+
+        // Tiles of which every query sees all, and the tiles loaded meanwhile too, in
+        // rounds of the ring's slots: no branch but one, LDS offsets are immediates, and
+        // a wave's 8 rows of a tile lie in one page, whose number is read a tile ahead.
+        // (A wave that finds its way through the conditions below instead spends a third
+        // of its time on them and on addresses: 165 us against 128 for 32 requests on 81920
+        // tokens.)
+        int tile = base;
+        const int seen = tk.bad || base * kTile < cur.lo ? base : min(stop, min_lim / kTile);
+        if (tk.src.pmask >= 7 && tk.src.nc == Ge::NC && tile + 2 * kStages - 1 <= seen) {
+          const int last_page = ((min(stop * kTile, cur.hi) - 1) >> tk.src.shift) - tk.src.block0;
+          auto page_of = [&](int tl) {
+            return sh.list[min(((tl * kTile + wave * 8) >> tk.src.shift) - tk.src.block0, last_page)];
+          };
+          const int lrow = lane / Ge::NC, lc = lane % Ge::NC;
+          uint32_t at_row[kMine];
+  #pragma unroll
+          for (int j = 0; j < kMine; j++)
+            at_row[j] = (j * Ge::RPI + lrow) * tk.src.row_bytes +
+                        (lc ^ swizzle<DP>((wave * kMine + j) * Ge::RPI + lrow)) * 16;
+          int page = page_of(tile + kStages - 1);
+          auto step = [&](auto slot_c) {
+            constexpr int kSlot = decltype(slot_c)::value;
+            char* kt = ring + kSlot * 2 * Ge::BYTES;
+            const uint32_t to = lds + ((kSlot + kStages - 1) & (kStages - 1)) * 2 * Ge::BYTES + wave * kMine * 1024;
+            f4 s[RT][2];
+            h8 p[RT];
+            float mx[RT];
+            wait_lds();
+            wait_loads<(kStages - 2) * 2 * kMine>();
+            publish();
+            const int next = tile + kStages - 1;
+            const uint64_t off =
+                (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(page) * tk.src.page_bytes +
+                (uint64_t)((uint32_t)((next * kTile + wave * 8) & tk.src.pmask) * tk.src.row_bytes);
+            // A wave's loads are spread over the step: issued at once by all waves they
+            // queue for hundreds of cycles, and the waves with them.
+            auto load = [&](int i) {
+              if (i < kMine) load_lds(to + i * 1024, kp + off, at_row[i < kMine ? i : 0]);
+              else load_lds(to + Ge::BYTES + (i - kMine) * 1024, vp + off, at_row[i < kMine ? 0 : i - kMine]);
+            };
+            constexpr int kQuarter = kMine >= 2 ? kMine / 2 : 1;
+            auto some = [&](int from) {
+  #pragma unroll
+              for (int i = from * kQuarter; i < (from + 1) * kQuarter && i < 2 * kMine; i++) load(i);
+            };
+            w.scores(kt, at_lane.fresh(), s, [&] { some(0); });
+            some(1);
+            page = page_of(next + 1);
+            const bool raise = w.peaks(s, c, mx);
+            w.reference(raise, mx, c);
+            w.weights(s, c, p);
+            some(2);
+            w.values(kt + Ge::BYTES, at_lane.fresh(), p, [&] { some(3); });
+            tile++;
+          };
+          do {
+            step(std::integral_constant<int, 0>());
+            step(std::integral_constant<int, 1>());
+            step(std::integral_constant<int, 2>());
+            step(std::integral_constant<int, 3>());
+          } while (tile + 2 * kStages - 1 <= seen);
+        }
+        for (; tile < stop; tile++) {
+          char* kt = ring + slot_of(tile) * (2 * Ge::BYTES);
+          char* vt = kt + Ge::BYTES;
           f4 s[RT][2];
           h8 p[RT];
           float mx[RT];
           wait_lds();
-          wait_loads<(kStages - 2) * 2 * kMine>();
+          if (tile + kStages - 1 <= stop) wait_loads<(kStages - 2) * 2 * kMine>();
+          else wait_loads<0>();
           publish();
-          const int next = tile + kStages - 1;
-          const uint64_t off =
-              (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(page) * tk.src.page_bytes +
-              (uint64_t)((uint32_t)((next * kTile + wave * 8) & tk.src.pmask) * tk.src.row_bytes);
-          // A wave's loads are spread over the step: issued at once by all waves they
-          // queue for hundreds of cycles, and the waves with them.
-          auto load = [&](int i) {
-            if (i < kMine) load_lds(to + i * 1024, kp + off, at_row[i < kMine ? i : 0]);
-            else load_lds(to + Ge::BYTES + (i - kMine) * 1024, vp + off, at_row[i < kMine ? 0 : i - kMine]);
-          };
-          constexpr int kQuarter = kMine >= 2 ? kMine / 2 : 1;
-          auto some = [&](int from) {
-#pragma unroll
-            for (int i = from * kQuarter; i < (from + 1) * kQuarter && i < 2 * kMine; i++) load(i);
-          };
-          w.scores(kt, at_lane.fresh(), s, [&] { some(0); });
-          some(1);
-          page = page_of(next + 1);
+          load(tile + kStages - 1);
+          w.scores(kt, at_lane.fresh(), s, [] {});
+          const bool all = tk.full(tile) && (tile + 1) * kTile <= min_lim;  // the same for all waves
+          if (!all) {
+            const int pages = tile_at(tk.src, tile * kTile).page;
+            w.mask(a, cur, row0, s, tile * kTile, pages);
+            if (clean_values<DP>(vt, pages)) sh.odd = 1;
+          }
           const bool raise = w.peaks(s, c, mx);
           w.reference(raise, mx, c);
           w.weights(s, c, p);
-          some(2);
-          w.values(kt + Ge::BYTES, at_lane.fresh(), p, [&] { some(3); });
-          tile++;
-        };
-        do {
-          step(std::integral_constant<int, 0>());
-          step(std::integral_constant<int, 1>());
-          step(std::integral_constant<int, 2>());
-          step(std::integral_constant<int, 3>());
-        } while (tile + 2 * kStages - 1 <= seen);
-      }
-      for (; tile < stop; tile++) {
-        char* kt = ring + slot_of(tile) * (2 * Ge::BYTES);
-        char* vt = kt + Ge::BYTES;
-        f4 s[RT][2];
-        h8 p[RT];
-        float mx[RT];
-        wait_lds();
-        if (tile + kStages - 1 <= stop) wait_loads<(kStages - 2) * 2 * kMine>();
-        else wait_loads<0>();
-        publish();
-        load(tile + kStages - 1);
-        w.scores(kt, at_lane.fresh(), s, [] {});
-        const bool all = tk.full(tile) && (tile + 1) * kTile <= min_lim;  // the same for all waves
-        if (!all) {
-          const int pages = tile_at(tk.src, tile * kTile).page;
-          w.mask(a, cur, row0, s, tile * kTile, pages);
-          if (clean_values<DP>(vt, pages)) sh.odd = 1;
+          w.values(vt, at_lane.fresh(), p, [] {});
         }
-        const bool raise = w.peaks(s, c, mx);
-        w.reference(raise, mx, c);
-        w.weights(s, c, p);
-        w.values(vt, at_lane.fresh(), p, [] {});
       }
-    }
     }
 #pragma unroll
     for (int r = 0; r < RT; r++) {

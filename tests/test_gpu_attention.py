@@ -191,7 +191,8 @@ def test_many_sequences():
     check(x, 0, q, 0.125, rows, np.arange(n + 1), gs[10:41], prefixes[10:40])
 
 
-@pytest.mark.parametrize("seqs,kv,G,d", [(130, 4, 2, 40), (129, 6, 3, 128), (256, 4, 1, 64), (70, 8, 4, 32)])
+@pytest.mark.parametrize("seqs,kv,G,d", [(130, 4, 2, 40), (129, 6, 3, 128), (256, 4, 1, 64), (70, 8, 4, 32),
+                                         (131, 4, 2, 200)])
 def test_many_sequences_of_several_heads(seqs, kv, G, d):
     """A batch whose workgroups take two or four kv heads each, with what is no finite
     number behind the rows' ends and, for the last head, in a token of the first row."""
@@ -210,7 +211,7 @@ def test_many_sequences_of_several_heads(seqs, kv, G, d):
     counts[0], counts[1:] = 2, 1
     n = int(counts.sum())
     q, starts = queries(rng, n, kv * G, d), starts_of(counts)
-    _, recs = pc.attention(c, 0, q, d ** -0.5, rows, starts)
+    ost, recs = pc.attention(c, 0, q, d ** -0.5, rows, starts)
     last = int(c.lens[rows[0]]) - 1  # only the second query of the first sequence sees it
     c.v[0, c.tables[rows[0], last // 8], last % 8, (kv - 1) * d + 3] = np.inf
     for row in range(len(c.tables)):
@@ -224,7 +225,7 @@ def test_many_sequences_of_several_heads(seqs, kv, G, d):
         assert (hit == np.inf).all()
         for h in range((kv - 1) * G, kv * G):
             out[1, h, 3] = recs[1][h]["out"][3]
-        compare((st, out, lse), (pc.BAD_PAGE, recs), q)
+        compare((st, out, lse), (ost, recs), q)
 
 
 def test_group_of_many():
@@ -468,6 +469,81 @@ def test_streams_and_repeats():
     for s in (None, side, None, side):
         st, o, l = gpu_attention(x, *args, stream=s)
         assert st == 0 and gu.same_bits(o, out) and np.array_equal(l, lse)
+
+
+def test_two_calls_at_once():
+    """On two streams, each with its workspace, over one cache."""
+    rng = np.random.default_rng(17)
+    tails = [[30, 1, 500], [2, 64]]
+    c, rows = build(rng, 2, 256, 16, [900, 65], tails)
+    x = Pair(c)
+    t, cg = x.t, x.cg
+    numbers = (5, 8, 64, 5, 2, 1, 900, 1400)
+    calls = []
+    for layer in (0, 1):
+        q = queries(rng, 5, 8, 64)
+        calls.append(dict(layer=layer, q=q, qd=gu.to_dev(q), out=gu.to_dev(np.zeros_like(q)),
+                          lse=t.zeros((5, 8), dtype=t.float32, device="cuda"), stream=t.cuda.Stream(),
+                          ws=t.empty(cg.cg_attention_workspace(x.cache, *numbers), dtype=t.uint8, device="cuda")))
+    lists = [x.i32(y) for y in (rows, np.arange(6), group_starts_of(tails), [900, 65])]
+    t.cuda.synchronize()
+    for _ in range(5):
+        for y in calls:
+            cg.cg_attention_prefix_async(x.cache, y["layer"], y["qd"], y["out"], 0.125, *lists, *numbers[5:], y["ws"],
+                                         lse=y["lse"], stream=y["stream"])
+    t.cuda.synchronize()
+    for y in calls:
+        want = pc.attention(c, y["layer"], y["q"], 0.125, rows, np.arange(6), group_starts_of(tails), [900, 65])
+        compare((int(x.status.item()), y["out"].cpu().numpy(), y["lse"].cpu().numpy()), want, y["q"])
+
+
+def test_most_heads():
+    """1,024 query heads of one kv head: more row tiles than one workgroup's."""
+    rng = np.random.default_rng(18)
+    c, rows = build(rng, 1, 16, 16, [70], [[5, 33]])
+    q = queries(rng, 3, 1024, 16)
+    check(Pair(c), 0, q, 0.25, rows, [0, 1, 3], [0, 2], [70])
+
+
+@pytest.mark.parametrize("heads", [1, 64])
+def test_longest_row(heads):
+    """Rows of 2^30 tokens, all of whose table entries name one page.  Keys are 0, so
+    all weights are one power of two and their sums, 2^30 of them in halves of
+    halves, are exact; values repeat every 65,536 tokens, small integers whose sums
+    are exact too.  A row is full then: a token more is refused."""
+    import kv_cache_compression_anchor_amd as cg
+    t = gu.torch()
+    P, B, d = 65536, 16384, 64
+    n = P * B
+    k = t.zeros((1, 2, P, d), dtype=t.float16, device="cuda")
+    v = t.ones((1, 2, P, d), dtype=t.float16, device="cuda")
+    v[0, :, ::4, 1::2] = -3.0  # one token in four: the mean is 0
+    tables = t.zeros((2, B), dtype=t.int32, device="cuda")
+    lens = t.tensor([n, n], dtype=t.int32, device="cuda")
+    refs = t.tensor([B, 0], dtype=t.int32, device="cuda")
+    status = t.zeros(1, dtype=t.int32, device="cuda")
+    c = cg.PagedCache(k, v, tables, lens, refs, status)
+    i32 = lambda y: t.tensor(y, dtype=t.int32, device="cuda")  # noqa: E731
+    q = t.randn((2, heads, d), device="cuda").half()
+    for groups, prefix in ((None, None), ([0, 2], [n - P])):
+        hint = 0 if prefix is None else prefix[0]
+        numbers = (2, heads, d, 2, 0 if prefix is None else 1, 1, hint, n)
+        ws = t.full((cg.cg_attention_workspace(c, *numbers),), 0xFF, dtype=t.uint8, device="cuda")
+        out = t.full((2, heads, d), 9.0, dtype=t.float16, device="cuda")
+        lse = t.zeros((2, heads), dtype=t.float32, device="cuda")
+        opt = lambda y: None if y is None else i32(y)  # noqa: E731
+        cg.cg_attention_prefix_async(c, 0, q, out, 0.125, None, i32([0, 1, 2]), opt(groups), opt(prefix), 1, hint, n,
+                                     ws, lse=lse)
+        t.cuda.synchronize()
+        assert int(status.item()) == 0
+        assert (out[..., ::2] == 1).all() and (out[..., 1::2] == 0).all()
+        # log 2^30 with log2f's and one product's roundings
+        assert ((lse - 30 * np.log(2)).abs() <= 4 * E * 30).all()
+    pages = t.empty(cg.cg_pages_workspace(c), dtype=t.uint8, device="cuda")
+    slots = t.empty(2, dtype=t.int64, device="cuda")
+    lens[1] = n - 1
+    cg.cg_pages_reserve_async(c, i32([0, 1]), i32([0, 1, 2]), slots, pages)
+    assert slots.tolist() == [-1, P - 1] and lens.tolist() == [n, n] and int(status.item()) == pc.REFUSED
 
 
 def test_captured_decode_loop():

@@ -216,6 +216,14 @@ def test_write_layers_and_strides():
         x.write(2, slots[5:6], want[5:6], one[:, :1], -one[:, :1])
 
 
+def test_reserve_without_slots():
+    rng = np.random.default_rng(12)
+    x = Pair(randomised(pc.empty(1, 30, 4, 64, 5, 6), rng))
+    for rows, starts in (([3, 1], [0, 9, 14]), ([0], [2, 5]), ([3, 4], [0, 15, 16])):
+        x.cg.cg_pages_reserve_async(x.cache, x.i32(rows), x.i32(starts), None, x.ws, n_tokens=16)
+        x.check(pc.reserve(x.o, rows, starts, 16)[0], rows)
+
+
 def test_another_stream():
     rng = np.random.default_rng(10)
     x = Pair(randomised(pc.empty(2, 64, 4, 64, 6, 12), rng))
