@@ -22,9 +22,14 @@ typedef __attribute__((address_space(3))) s4 lds_s4;
 
 constexpr int kTile = 32;        // tokens of a tile: the depth of one 16x16x32 product
 constexpr int kThreads = 256;    // of a joining workgroup
-// Tiles of a split, at least: of the shared prefixes, whose partial sums are many rows
-// each (64 requests on a 9K context: 54 us with 16 splits, 65 with 32), and of the rest.
-constexpr int kPreTiles = 16, kRestTiles = 8;
+// Tiles of a split, at least: one for each wave.  With more, short contexts leave most
+// of the chip idle (8 requests of 20 heads on 992 shared and 630 own tokens: 20 us with
+// 4, 24 with 8, 45 with 16 of the shared part's and 8 of the rest).
+constexpr int kLeast = 4;
+// Tiles of a split of shared prefixes that take all of the chip's slots and leave the rest
+// to wait for them: with fewer, half of the slots are the faster choice (14 requests of
+// 64 heads on 2,005 shared tokens: 31 us with half, 35 with all).
+constexpr int kLong = 32;
 // Weights are 2^(score - m) with m at most kSlack above what the running maximum
 // was when it was last raised, and kLift below it: up to 2^14, and binary16's
 // normal range reaches down to 2^-20 of the largest.
@@ -135,15 +140,15 @@ __device__ __forceinline__ bool lends(const Attn& a, int row, int pre) {
 }
 
 // Tokens [lo, hi) in tiles that start at multiples of kTile, dealt to `splits`
-// workgroups in turn, at least `least` each.
+// workgroups in turn, at least kLeast each.
 struct Split {
   int tile0, tiles, per, used;
 };
-__device__ __forceinline__ Split split_of(int lo, int hi, int splits, int least) {
+__device__ __forceinline__ Split split_of(int lo, int hi, int splits) {
   Split s;
   s.tile0 = lo / kTile;
   s.tiles = hi > lo ? (hi + kTile - 1) / kTile - s.tile0 : 0;
-  s.per = max(least, (s.tiles + splits - 1) / splits);
+  s.per = max(kLeast, (s.tiles + splits - 1) / splits);
   s.used = (s.tiles + s.per - 1) / s.per;
   return s;
 }
@@ -286,7 +291,7 @@ struct Item {
   int lo, hi;               // tokens
   int lim0;                 // tokens that the first query sees (each later one 1 more)
   int trow;                 // table row
-  int splits, split, least; // of the tokens; tiles of one at least
+  int splits, split;        // of the tokens
   int slot0;                // first partial of this kind
   int row_tile, row_tiles;  // this workgroup's first row tile and its stride
   // of a sequence's rest: whether this item says where its queries' sums are, and what
@@ -563,7 +568,7 @@ struct Tokens {
   bool bad;         // a page of this or an earlier stretch is outside the pool
 
   __device__ __forceinline__ bool start(const Attn& a, const Item& it, Sh& sh) {
-    const Split sp = split_of(it.lo, it.hi, it.splits, it.least);
+    const Split sp = split_of(it.lo, it.hi, it.splits);
     if (it.split >= sp.used) return false;
     first = sp.tile0 + it.split * sp.per;
     last = min(first + sp.per, sp.tile0 + sp.tiles);
@@ -848,9 +853,9 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
         // Tiles of which every query sees all, and the tiles loaded meanwhile too, in
         // rounds of the ring's slots: no branch but one, LDS offsets are immediates, and
         // a wave's 8 rows of a tile lie in one page, whose number is read a tile ahead.
-        // (A wave that finds its way through the conditions below instead spends a third
-        // of its time on them and on addresses: 165 us against 128 for 32 requests on 81920
-        // tokens.)
+        // (A wave that finds its way through the conditions below instead spends a quarter
+        // of its time on them and on addresses: 178 us against 139 for 32 requests of 64
+        // heads on 81,920 tokens.)
         int tile = base;
         const int seen = tk.bad || base * kTile < cur.lo ? base : min(stop, min_lim / kTile);
         if (tk.src.pmask >= 7 && tk.src.nc == Ge::NC && tile + 2 * kStages - 1 <= seen) {
@@ -991,7 +996,6 @@ __device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
     it.rows = (q1 - it.q0) * a.G;
     it.lim0 = it.hi;
     it.splits = a.pre_splits;
-    it.least = kPreTiles;
     it.slot0 = 0;
     it.row_tiles = a.pre_tiles;
     return true;
@@ -1016,7 +1020,6 @@ __device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
   it.rows = q.m * a.G;
   it.lim0 = q.len - q.m + 1;
   it.splits = a.rest_splits;
-  it.least = kRestTiles;
   it.slot0 = a.pre_splits;
   it.row_tiles = a.rest_tiles;
   if (a.direct && q.first >= 0) {
@@ -1041,8 +1044,8 @@ __device__ __forceinline__ void refuse(const Attn& a, const Item& it) {
 // For the join: where the sums of a sequence's queries are.
 __device__ __forceinline__ void say_used(const Attn& a, const Item& it) {
   const bool ok = it.ok && (it.first < 0 || lends(a, row_of(a, it.first), it.pre));
-  const int used = ok ? split_of(0, it.pre, a.pre_splits, kPreTiles).used |
-                            split_of(it.pre, it.hi, a.rest_splits, kRestTiles).used << 16
+  const int used = ok ? split_of(0, it.pre, a.pre_splits).used |
+                            split_of(it.pre, it.hi, a.rest_splits).used << 16
                       : -1;
   for (int i = max(it.q0, 0) + (int)threadIdx.x; i < min(it.q_end, a.n_q); i += blockDim.x) a.used[i] = used;
   if (!ok && threadIdx.x == 0 && it.q0 < it.q_end) atomicOr(a.status, kRefused);
@@ -1229,16 +1232,17 @@ Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
     // the prefixes of a batch take half of the slots, and leave the others to the rest,
     // unless they are long
     const int64_t items = (int64_t)x.n_groups * kv * p.pre_tiles, tokens = shared ? x.max_prefix : 0;
-    p.pre_splits = splits(items, tokens, slots, 2 * kPreTiles);
-    if (items * p.pre_splits < slots * 3 / 4) p.pre_splits = splits(items, tokens, slots / 2, kPreTiles);
+    p.pre_splits = splits(items, tokens, slots, kLong);
+    if (items * p.pre_splits < slots * 3 / 4) p.pre_splits = splits(items, tokens, slots / 2, kLeast);
   } else {
     p.pre_splits = 0;
   }
   p.rest_splits = splits((int64_t)std::max(1, x.n_seqs) * kv * p.rest_tiles,
-                         std::max(0, x.max_len - (shared ? x.max_prefix : 0)), slots, kRestTiles);
+                         std::max(0, x.max_len - (shared ? x.max_prefix : 0)), slots, kLeast);
   // Several heads a workgroup share its start (about 5 us of latencies) and leave fewer
   // waves to wait for the one with most tiles, as long as there are workgroups enough
-  // (64 sequences of 300 tokens and 8 heads: 15 us for each of 512 workgroups of one).
+  // (64 sequences of 8 kv heads and up to 600 tokens behind 9,216 shared ones: the call
+  // takes 51 us with one head, 44 with two, and 53 with four, which leaves 128 workgroups).
   auto heads = [&](int splits) {
     int n = 1;
     while (n < 4 && p.rest_mode <= kRows32 && kv % (2 * n) == 0 &&
@@ -1250,7 +1254,7 @@ Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
   // start, about 5 us: not for little.
   const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
   p.direct = saved <= (int64_t)16 << 20 && x.max_prefix <= 512 &&
-             splits((int64_t)std::max(1, x.n_seqs) * kv * p.rest_tiles, x.max_len, slots, kRestTiles) == 1;
+             splits((int64_t)std::max(1, x.n_seqs) * kv * p.rest_tiles, x.max_len, slots, kLeast) == 1;
   if (p.direct) {
     p.pre_groups = 0;
     p.pre_splits = 0;
