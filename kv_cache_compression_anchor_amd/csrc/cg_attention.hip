@@ -38,6 +38,7 @@ typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s4 lds_s4;
 
@@ -279,28 +280,35 @@ __device__ __forceinline__ void load_tile(const Source& s, const char* pool, uin
 // zero weight of such a query.  Rows of tokens that do not exist (which hold
 // anything) become zeros, and so does every value that is no finite number; returns
 // whether there was one: add_odd() gives it to the queries that see it.
-template <int DP>
+// kBatch: chunks that are read together, as registers allow.
+template <int DP, int kBatch>
 __device__ __forceinline__ bool clean_values(char* tile, int pages) {
   using Ge = Geo<DP>;
   const int lane = rare_lane();
   bool odd = false;
+  static_assert(Ge::NI % kBatch == 0, "");
 #pragma unroll 1
-  for (int i = 0; i < Ge::NI; i++) {
-    uint4* at = (uint4*)(tile + i * 1024 + lane * 16);
-    uint4 x = *at;
-    if (__shfl(pages, i * Ge::RPI + lane / Ge::NC) < 0) {
-      x = uint4{0, 0, 0, 0};
-    } else {
-      uint32_t* y = &x.x;
+  for (int i0 = 0; i0 < Ge::NI; i0 += kBatch) {
+    u4* at = (u4*)(tile + i0 * 1024 + lane * 16);
+    u4 x[kBatch];
+    int page[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; i++) {
+      x[i] = at[i * 64];
+      page[i] = __shfl(pages, (i0 + i) * Ge::RPI + lane / Ge::NC);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; i++) {
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        const uint32_t keep = ((y[j] & 0x7C00u) == 0x7C00u ? 0 : 0xFFFFu) |
-                              ((y[j] & 0x7C000000u) == 0x7C000000u ? 0 : 0xFFFF0000u);
-        odd |= keep != 0xFFFFFFFFu;
-        y[j] &= keep;
+        const uint32_t y = x[i][j];
+        const uint32_t keep = ((y & 0x7C00u) == 0x7C00u ? 0 : 0xFFFFu) |
+                              ((y & 0x7C000000u) == 0x7C000000u ? 0 : 0xFFFF0000u);
+        odd |= page[i] >= 0 && keep != 0xFFFFFFFFu;
+        x[i][j] = page[i] >= 0 ? y & keep : 0;
       }
+      at[i * 64] = x[i];
     }
-    *at = x;
   }
   wait_lds();
   return __any(odd);
@@ -749,7 +757,7 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
           w.reference(raise, mx, c);
           w.weights(s, c, p);
           if (more) wait_loads<Ge::NI>(); else wait_loads<0>();
-          if (!all && clean_values<DP>(vt, at.page)) sh.odd = 1;
+          if (!all && clean_values<DP, RT == 1 ? 4 : 1>(vt, at.page)) sh.odd = 1;
           w.values(vt, at_lane.fresh(), p, [] {});
           wait_lds();
           load_v();
@@ -769,17 +777,35 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
       }
     }
     __syncthreads();  // all waves are done with their tiles
+    constexpr int kQuads = W::NB * 4;  // 4-channel groups of a row
+    static_assert(sizeof(sh.tile) >= (size_t)kWaves * 16 * RT * kQuads * 16, "room for the sums");
+    f4* sums = (f4*)sh.tile;           // [wave][row][quad], quads rotated by row
+#pragma unroll
+    for (int r = 0; r < RT; r++)
+#pragma unroll
+      for (int b = 0; b < W::NB; b++)
+        sums[(wave * 16 * RT + r * 16 + n) * kQuads + ((b * 4 + g + r * 16 + n) & (kQuads - 1))] = w.o[r][b];
     if (tid < 16 * RT * it.heads) {
       const int x = tid % (16 * RT), hh = tid / (16 * RT), w0 = hh * turn;
+      // All waves' are read, other heads' for nothing: without conditions, together
+      // (where two row tiles take the registers, one after the other).
+      constexpr int kTogether = RT == 1 ? kWaves : 1;
       float m = -__builtin_inff(), l = 0.0f;
-      for (int y = w0; y < w0 + turn; y++) m = fmaxf(m, sh.m[y][x]);
-      for (int y = w0; y < w0 + turn; y++) {
+#pragma unroll kTogether
+      for (int y = 0; y < kWaves; y++) {
+        const float my = sh.m[(w0 + y) % kWaves][x];
+        m = y < turn ? fmaxf(m, my) : m;
+      }
+#pragma unroll kTogether
+      for (int y = 0; y < kWaves; y++) {
         // a wave without a reference has weighed nothing, or only what is no number
-        const float my = sh.m[y][x];
-        const float f = my == m ? 1.0f : my == -__builtin_inff() && sh.l[y][x] != 0.0f
+        const float my = sh.m[(w0 + y) % kWaves][x], ly = sh.l[(w0 + y) % kWaves][x];
+        const float f = my == m ? 1.0f : my == -__builtin_inff() && ly != 0.0f
                             ? 1.0f : __builtin_amdgcn_exp2f(my - m);
-        sh.scale[y][x] = f;
-        l += f * sh.l[y][x];
+        if (y < turn) {
+          sh.scale[w0 + y][x] = f;
+          l += f * ly;
+        }
       }
       const int row = rt * 16 * RT + x;
       if (a.direct) {
@@ -791,23 +817,23 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
         a.ml[2 * at + 1] = l;
       }
     }
-    constexpr int kQuads = W::NB * 4;  // 4-channel groups of a row
-    static_assert(sizeof(sh.tile) >= (size_t)kWaves * 16 * RT * kQuads * 16, "room for the sums");
-    f4* sums = (f4*)sh.tile;           // [wave][row][quad], quads rotated by row
-#pragma unroll
-    for (int r = 0; r < RT; r++)
-#pragma unroll
-      for (int b = 0; b < W::NB; b++)
-        sums[(wave * 16 * RT + r * 16 + n) * kQuads + ((b * 4 + g + r * 16 + n) & (kQuads - 1))] = w.o[r][b];
     __syncthreads();
 #pragma unroll 1
     for (int i = tid; i < it.heads * 16 * RT * kQuads; i += kThreads) {
       const int quad = i % kQuads, row = i / kQuads % (16 * RT), hh = i / (16 * RT * kQuads), w0 = hh * turn;
       const int ch = quad * 4, gr = rt * 16 * RT + row;
       if (gr >= it.rows || ch >= a.d) continue;
-      f4 x{0, 0, 0, 0};
-      for (int y = w0; y < w0 + turn; y++)
-        x += sh.scale[y][row] * sums[(y * 16 * RT + row) * kQuads + ((quad + row) & (kQuads - 1))];
+      float f[kWaves];
+      f4 part[kWaves], x{0, 0, 0, 0};
+#pragma unroll
+      for (int y = 0; y < kWaves; y++) {
+        const int of = (w0 + y) % kWaves;
+        f[y] = sh.scale[of][row];
+        part[y] = sums[(of * 16 * RT + row) * kQuads + ((quad + row) & (kQuads - 1))];
+      }
+#pragma unroll
+      for (int y = 0; y < kWaves; y++)
+        if (y < turn) x += f[y] * part[y];
       if (a.direct) store_out(out_at(a, it, it.head + hh, gr) + ch, x * sh.l[w0][row]);
       else *(f4*)(a.part + part_at(a, it, it.head + hh, gr) * a.d + ch) = x;
     }
@@ -949,7 +975,7 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
           if (!all) {
             const int pages = tile_at(tk.src, tile * kTile).page;
             w.mask(a, cur, row0, s, tile * kTile, pages);
-            if (clean_values<DP>(vt, pages)) sh.odd = 1;
+            if (clean_values<DP, RT == 1 ? 4 : 1>(vt, pages)) sh.odd = 1;
           }
           const bool raise = w.peaks(s, c, mx);
           w.reference(raise, mx, c);
