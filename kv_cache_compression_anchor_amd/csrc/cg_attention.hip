@@ -14,13 +14,13 @@
 // Bounds: reading every token of K and V once, or the products.  Measured, k_attention
 // and k_join, the call repeated (and with other data in the caches in between): 64
 // requests of 32 heads (8 of K and V, 128 channels) on 9,216 shared and up to 600 own
-// tokens, 122 MB and 10 GFLOP, in 35 + 7 us (51): the tail of the sequences' own tokens
+// tokens, 122 MB and 10 GFLOP, in 34 + 7 us (50): the tail of the sequences' own tokens
 // and the join's reading back of the sums are what is left above the 26 us of a copy of
 // these bytes.  21 requests of 32 heads, each with its K and V, 121 MB, in 28 + 5 us
-// (37).  32 requests of 64 heads on 81,920 shared tokens, 366 MB and 86 GFLOP, in 112 + 10
-// us (127): 0.77 PFLOP/s against 1.3 of a large library product; the matrix units are
-// busy for 38% of the time and share the issue slots with the exponentials (about as
-// many vector cycles as products), LDS reads and barriers.
+// (38).  32 requests of 64 heads on 81,920 shared tokens, 366 MB and 86 GFLOP, in 112 + 10
+// us (126; 142 when repeated without a pause, as power then allows): 0.77 PFLOP/s against
+// 1.3 of a large library product; the matrix units are busy for 38% of the time and share
+// the issue slots with the exponentials (about as many vector cycles as products).
 #include <algorithm>
 #include <type_traits>
 
