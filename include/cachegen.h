@@ -413,8 +413,9 @@ int cg_pages_compact_async(const cg_paged_cache* cache, int32_t* n_live_dev,
  * through the row of the group's first sequence, which must be as long (whether or
  * not it has queries); if it is not, the group is refused.  Every sequence of the
  * group that has queries must be at least prefix_lens[g] + m long; one that is not
- * is refused.  A refused sequence gets zeros, lse = -infinity and bit 2.  Sequences in no group, and n_groups = 0
- * (pointers may be NULL), are computed by themselves.
+ * is refused.  A refused sequence gets zeros, lse = -infinity and bit 2.
+ * Sequences in no group, and n_groups = 0 (pointers may be NULL), are computed by
+ * themselves.
  *
  * Rows of out and lse that no sequence has queries for are left as they were.
  * Tokens of pages outside the pool are left out (bit 1). */

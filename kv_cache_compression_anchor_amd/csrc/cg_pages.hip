@@ -4,8 +4,8 @@
 // Two kinds of work.  Bookkeeping (who gets which page) is a handful of prefix
 // sums over the requests and over refs; each call does it in one workgroup of
 // 1,024 threads, so that one launch suffices and page numbers do not depend on
-// scheduling.  Its time is its chain of dependent loads and barriers: 5 to 7 us
-// for up to 1,024 requests and 16,384 pages.  Moving K and V is a plain copy bound
+// scheduling.  Its time is its chain of dependent loads and barriers: 5 to 10 us
+// for up to 1,024 requests and 16,384 pages, 35 us for a compaction over 131,072.  Moving K and V is a plain copy bound
 // by HBM; it is cut into pieces spread over the chip.  Measured, counting bytes
 // read and written: 96 pages of 32 layers x 16 tokens x 4,096 channels (1.6 GB)
 // copied in 315 us, 5.1 TB/s; 5,850 tokens of 32 layers x 1,024 channels (1.5 GB)
