@@ -195,18 +195,23 @@ __device__ __forceinline__ int swizzle(int row) {
 
 // LDS <- global, 16 bytes a lane: lane i's bytes land at lds + 16 i.  No register
 // receives them, and the compiler does not count them: wait_loads<n>() waits
-// until at most n of the wave's newest are on their way.
+// until at most n of the wave's newest are on their way.  Nor does it keep the
+// instructions' distances here: a load takes m0 one wait state after its write, and
+// a scalar address five after a write by the vector unit (a lane read back, say).
+// The copy of the address is that state, and leaves a scalar write, which needs none.
+// (The compiler warns that it keeps m0 for itself; it is to know that m0 changes.)
 __device__ __forceinline__ void load_lds(uint32_t lds, const char* base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :
+  const char* copy;
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+               : "=&s"(copy)
                : "s"(lds), "v"(off), "s"(base)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds(uint32_t lds, const char* addr) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(lds), "v"(addr)
-               : "memory");
+               : "memory", "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
