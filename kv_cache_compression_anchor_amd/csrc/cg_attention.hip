@@ -402,11 +402,9 @@ struct Places {
   }
 };
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
-}
+// One instruction, of the compiler's making: it keeps the distance to the products
+// whose results these are, which it would not to a statement of assembly.
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 template <int DP, int RT>
 struct Wave {

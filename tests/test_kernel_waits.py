@@ -89,3 +89,16 @@ def test_addresses_wait_for_vector_writes(code):
                 for r in registers(ops[0]):
                     since.pop(r, None)
     assert not short, (len(short), short[:3])
+
+
+def test_attention_computes_nothing_in_assembly():
+    """A product's result is there up to 18 wait states after its instruction, which the
+    compiler keeps for its own vector instructions and not for those of a statement."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "kv_cache_compression_anchor_amd", "csrc", "cg_attention.hip")) as f:
+        text = f.read()
+    statements = re.findall(r"\basm(?:\s+volatile)?\s*\(\s*((?:\"[^\"]*\"\s*)*)", text)
+    assert len(statements) >= 4
+    words = [line.split()[0] for s in statements for line in "".join(re.findall(r'"([^"]*)"', s)).split("\\n\\t") if line]
+    assert "global_load_lds_dwordx4" in words
+    assert not [w for w in words if w.startswith("v_")]
