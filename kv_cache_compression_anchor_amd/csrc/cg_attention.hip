@@ -145,7 +145,8 @@ __device__ __forceinline__ Seq sequence(const Attn& a, int s) {
   const bool in = q.row >= 0 && q.row < a.R;
   q.len = a.lens[in ? q.row : 0];
   q.ok = in && len_ok(a, q.len) && q.q0 >= 0 && end <= a.n_q;
-  q.m = end - q.q0;
+  // none where the starts descend or leave the batch: a difference of any two could wrap around
+  q.m = q.q0 >= 0 && end > q.q0 && end <= a.n_q ? end - q.q0 : 0;
   q.pre = 0;
   q.first = -1;
   if (g >= 0 && s < next && pre != 0) {
@@ -1067,8 +1068,6 @@ __device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
   it.hi = q.len;
   it.trow = q.row;
   it.q0 = q.q0;
-  it.rows = q.m * a.G;
-  it.lim0 = q.len - q.m + 1;
   it.splits = a.rest_splits;
   it.slot0 = a.pre_splits;
   it.row_tiles = a.rest_tiles;
@@ -1076,14 +1075,22 @@ __device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
     it.lender = row_of(a, q.first);
     it.ok = q.ok && lends(a, it.lender, q.pre);
   }
-  return it.ok && q.m > 0;
+  if (!it.ok || q.m == 0) return false;
+  it.rows = q.m * a.G;
+  it.lim0 = q.len - q.m + 1;
+  return true;
 }
+
+// The queries that a sequence names, as far as the batch has them, from begin_of to
+// end_of (its starts may be any numbers).
+__device__ __forceinline__ int begin_of(const Attn& a, const Item& it) { return min(max(it.q0, 0), a.n_q); }
+__device__ __forceinline__ int end_of(const Attn& a, const Item& it) { return min(it.q_end, a.n_q); }
 
 // Direct: outputs of a refused sequence's queries, of the item's kv heads.
 __device__ __forceinline__ void refuse(const Attn& a, const Item& it) {
   if (it.row_tile != 0) return;
   const int h0 = it.head * a.G, n = it.heads * a.G;
-  for (int q = max(it.q0, 0); q < min(it.q_end, a.n_q); q++) {
+  for (int q = begin_of(a, it); q < end_of(a, it); q++) {
     for (int i = threadIdx.x; i < n * a.d; i += blockDim.x) a.out[q * a.out_stride + h0 * a.d + i] = 0;
     for (int i = threadIdx.x; a.lse && i < n; i += blockDim.x)
       a.lse[(int64_t)q * a.H + h0 + i] = -__builtin_inff();
@@ -1097,7 +1104,7 @@ __device__ __forceinline__ void say_used(const Attn& a, const Item& it) {
   const int used = ok ? split_of(0, it.pre, a.pre_splits).used |
                             split_of(it.pre, it.hi, a.rest_splits).used << 16
                       : -1;
-  for (int i = max(it.q0, 0) + (int)threadIdx.x; i < min(it.q_end, a.n_q); i += blockDim.x) a.used[i] = used;
+  for (int i = begin_of(a, it) + (int)threadIdx.x; i < end_of(a, it); i += blockDim.x) a.used[i] = used;
   if (!ok && threadIdx.x == 0 && it.q0 < it.q_end) atomicOr(a.status, kRefused);
 }
 

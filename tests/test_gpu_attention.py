@@ -346,6 +346,35 @@ def test_malformed_lists_stay_in_bounds():
             assert (big[0] == 55.0).all() and (big[7] == 55.0).all()
 
 
+@pytest.mark.parametrize("G,hints", [(2, (2, 30, 40)), (2, (2, 0, 1 << 21)), (2, (2, 1 << 20, 1 << 21)),
+                                     (20, (40, 30, 40)), (20, (40, 1 << 20, 1 << 21))])
+def test_extreme_numbers_in_lists_stay_in_bounds(G, hints):
+    """Starts whose differences pass 32 bits, lengths, rows and prefixes at both ends of
+    the type: nothing outside the outputs is touched, and a sequence whose numbers are
+    right is computed."""
+    rng = np.random.default_rng(22)
+    c, rows = build(rng, 1, 64, 8, [30], [[4, 6, 9]])
+    x = Pair(c)
+    q = queries(rng, 6, G, 64)
+    t, lo, hi = x.t, -(1 << 31), (1 << 31) - 1
+    for qs in ([1, lo, 0, 2], [0, 2, lo, hi], [hi, lo, lo, 3], [2, lo + 1, hi, 6], [lo, hi, 1, lo], [3, 5, hi, lo + 3]):
+        for gs, pl in (([0, 3], [25]), ([0, 3], [hi]), ([lo, hi], [lo]), ([1, lo], [hi]), (None, None)):
+            big = t.full((8, G, 64), 55.0, dtype=t.float16, device="cuda")
+            gpu_attention(x, 0, q, 0.125, rows, qs, gs, pl, hints=hints, out=big[1:7])
+            assert (big[0] == 55.0).all() and (big[7] == 55.0).all(), (qs, gs, pl)
+            for rr in ([lo, rows[1], hi], None):
+                gpu_attention(x, 0, q, 0.125, rr, [0, 2, 4, 6], gs, pl, hints=hints, out=big[1:7])
+                assert (big[0] == 55.0).all() and (big[7] == 55.0).all(), (qs, gs, pl)
+    # descending starts: the second sequence has no queries, the third's are its own
+    _, out, lse = gpu_attention(x, 0, q, 0.125, rows, [1, lo, 2, 5], None, None, hints=hints)
+    ost, recs = pc.attention(c, 0, q, 0.125, [rows[2]], [2, 5])
+    out[[0, 1, 5]], lse[[0, 1, 5]] = 123.0, 321.0
+    compare((ost, out, lse), (ost, recs), q)
+    x.lens.copy_(t.tensor([lo, hi] + [hi] * (len(x.o.lens) - 2), dtype=t.int32))
+    st, out, lse = gpu_attention(x, 0, q, 0.125, rows, [0, 2, 4, 6], None, None, hints=hints)
+    assert st == pc.REFUSED and (out == 0).all() and (lse == -np.inf).all()
+
+
 def test_pages_outside_the_pool():
     rng = np.random.default_rng(8)
     tails = [[4, 40, 9]]
