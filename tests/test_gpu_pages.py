@@ -224,6 +224,63 @@ def test_reserve_without_slots():
         x.check(pc.reserve(x.o, rows, starts, 16)[0], rows)
 
 
+# channels 64 and 8: 16-byte units; 138: 4; 65: 2.  4,096 pairs are the most of the simpler kernel
+@pytest.mark.parametrize("n,N,P,C,L", [(4096, 9000, 4, 64, 2), (4097, 9000, 4, 64, 2), (5000, 12000, 1, 65, 3),
+                                       (12295, 30000, 8, 138, 1), (6000, 12100, 16, 1024, 3),
+                                       (1 << 20, 1 << 21, 1, 8, 1), (1 << 23, 1 << 24, 1, 8, 1)])
+def test_copies_of_many_pairs(n, N, P, C, L):
+    """Among them pairs with one dst, with the dst of another as src, onto themselves and
+    out of range; in a time that does not grow with the square of their number."""
+    import kv_cache_compression_anchor_amd as cg
+    t = gu.torch()
+    g = t.Generator(device="cuda").manual_seed(n + C)
+    pools = [t.randint(-(1 << 15), 1 << 15, (L, N, P, C), generator=g, device="cuda", dtype=t.int16).view(t.float16)
+             for _ in range(2)]
+    before = [p.clone() for p in pools]
+    status = t.zeros(1, dtype=t.int32, device="cuda")
+    meta = t.full((1, 1), -1, dtype=t.int32, device="cuda")
+    cache = cg.PagedCache(*pools, meta, t.zeros(1, dtype=t.int32, device="cuda"),
+                          t.ones(N, dtype=t.int32, device="cuda"), status)
+    order = t.randperm(N, generator=g, device="cuda").int()
+    some = lambda share: t.nonzero(t.rand(n, generator=g, device="cuda") < share).flatten()  # noqa: E731
+    for kinds in ((), ("dst twice",), ("a dst as src",), ("itself",), ("out of range",),
+                  ("dst twice", "a dst as src", "itself", "out of range")):
+        src, dst = order[:n].clone(), order[N - n:].clone()  # they overlap where N < 2 n
+        for kind in kinds:
+            at = some(0.02)
+            other = t.randint(0, n, at.shape, generator=g, device="cuda")
+            if kind == "dst twice":
+                dst[at] = dst[other]
+            elif kind == "a dst as src":
+                src[at] = dst[other]
+            elif kind == "itself":
+                src[at] = dst[at]
+            else:
+                bad = t.tensor([-1, N, 1 << 30, -(1 << 31), (1 << 31) - 1], dtype=t.int32, device="cuda")
+                src[at[::2]] = bad[other[::2] % 5]
+                dst[at[1::3]] = bad[other[1::3] % 5]
+        inside = (src >= 0) & (src < N) & (dst >= 0) & (dst < N)
+        named = t.bincount(dst[(dst >= 0) & (dst < N)].long(), minlength=N)
+        clash = (named[src.clamp(0, N - 1).long()] > 0) | (named[dst.clamp(0, N - 1).long()] > 1)
+        want = (pc.BAD_PAGE if not bool(inside.all()) else 0) | (pc.REFUSED if bool((inside & clash).any()) else 0)
+        for p, q in zip(pools, before):
+            p.copy_(q)
+        ev = [t.cuda.Event(enable_timing=True) for _ in range(2)]
+        ev[0].record()
+        cg.cg_pages_copy_async(cache, src, dst)
+        ev[1].record()
+        t.cuda.synchronize()
+        assert ev[0].elapsed_time(ev[1]) < 1000, (n, kinds)
+        assert int(status.item()) == want, kinds
+        status.zero_()
+        go = inside & ~clash
+        assert kinds or bool(go.any())
+        for p, q in zip(pools, before):
+            q = q.view(t.int16).clone()
+            q[:, dst[go].long()] = q[:, src[go].long()]
+            assert t.equal(p.view(t.int16), q), kinds
+
+
 def test_another_stream():
     rng = np.random.default_rng(10)
     x = Pair(randomised(pc.empty(2, 64, 4, 64, 6, 12), rng))
