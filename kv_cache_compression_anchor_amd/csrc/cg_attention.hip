@@ -361,6 +361,9 @@ __device__ __forceinline__ float* lse_at(const Attn& a, const Item& it, int head
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945309f;
 }
+// A sum over its weights' sum, given as 1 / l, or 0 where nothing weighed anything: what
+// the sum holds then (zero times what is no number, say) does not count.
+__device__ __forceinline__ f4 quotient_of(f4 x, float inv) { return inv == 0.0f ? f4{0, 0, 0, 0} : x * inv; }
 __device__ __forceinline__ void store_out(uint16_t* to, f4 x) {  // 4 channels
   ushort4 r;
   r.x = float_to_half_bits(x[0]);
@@ -644,8 +647,9 @@ struct Tokens {
   // After the sums of rows [row0, row1) are stored: what clean_values() took out, for the
   // rows that see it (a sum with such a value is an infinity or no number whatever
   // the weight, and stays so where the value was counted already).  Rare, and slow.
-  template <int kThreads, class A>
-  __device__ __forceinline__ void add_odd(const A& a, const Item& it, Sh& sh, int ranges, int row0, int row1) {
+  // empty(head, row): of a direct item, whether nothing weighed anything for a row.
+  template <int kThreads, class A, class F>
+  __device__ __forceinline__ void add_odd(const A& a, const Item& it, Sh& sh, int ranges, int row0, int row1, F empty) {
     const int tid = kThreads - 1 - threadIdx.x;  // nothing here is worth sharing with the loops above
     row1 = min(row1, it.rows);
 #pragma unroll 1
@@ -666,7 +670,7 @@ struct Tokens {
           const int head = it.head + i / a.d, ch = i % a.d;
 #pragma unroll 1
           for (int row = row0; row < row1; row++) {
-            if (t >= row_lim(a, cur, row)) continue;
+            if (t >= row_lim(a, cur, row) || (a.direct && empty(head, row))) continue;
             if (a.direct) {
               uint16_t* to = out_at(a, it, head, row) + ch;
               *to = float_to_half_bits(half_bits_to_float(*to) + x);
@@ -838,11 +842,14 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
 #pragma unroll
       for (int y = 0; y < kWaves; y++)
         if (y < turn) x += f[y] * part[y];
-      if (a.direct) store_out(out_at(a, it, it.head + hh, gr) + ch, x * sh.l[w0][row]);
+      if (a.direct) store_out(out_at(a, it, it.head + hh, gr) + ch, quotient_of(x, sh.l[w0][row]));
       else *(f4*)(a.part + part_at(a, it, it.head + hh, gr) * a.d + ch) = x;
     }
     __syncthreads();  // m, l and scale are free
-    if (sh.odd) tk.template add_odd<kThreads>(a, it, sh, ranges, rt * 16 * RT, (rt + 1) * 16 * RT);
+    if (sh.odd)
+      tk.template add_odd<kThreads>(a, it, sh, ranges, rt * 16 * RT, (rt + 1) * 16 * RT, [&](int h, int row) {
+        return sh.l[(h - it.head) * turn][row - rt * 16 * RT] == 0.0f;
+      });
     __syncthreads();
   }
 }
@@ -1000,7 +1007,8 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
         uint16_t* to = out_at(a, it, it.head, row);
 #pragma unroll
         for (int b = 0; b < W::NB; b++)
-          if (b * 16 + g * 4 < a.d) store_out(to + b * 16 + g * 4, w.o[r][b] * inv);
+          if (b * 16 + g * 4 < a.d) store_out(to + b * 16 + g * 4, quotient_of(w.o[r][b], inv));
+        if (g == 0) sh.l[wave][r * 16 + n] = inv;
         if (g == 0 && a.lse) *lse_at(a, it, it.head, row) = lse_of(w.m[r], l);
         continue;
       }
@@ -1014,7 +1022,10 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
         if (b * 16 + g * 4 < a.d) *(f4*)(a.part + at * a.d + b * 16 + g * 4) = w.o[r][b];
     }
     __syncthreads();
-    if (sh.odd) tk.template add_odd<kThreads>(a, it, sh, ranges, rt * tile_rows, (rt + 1) * tile_rows);
+    if (sh.odd)
+      tk.template add_odd<kThreads>(a, it, sh, ranges, rt * tile_rows, (rt + 1) * tile_rows, [&](int, int row) {
+        return sh.l[(row - rt * tile_rows) / (16 * RT)][row % (16 * RT)] == 0.0f;
+      });
     __syncthreads();
   }
 }

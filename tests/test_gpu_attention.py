@@ -447,6 +447,28 @@ def test_infinite_scores():
     assert np.isfinite(out[[0, 2]]).all()
 
 
+ALL_HINTS = (None, (5, 1 << 20, 1 << 21), (5, 0, 1 << 21))  # one kernel; prefixes shared and sums joined; joined
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("kv,G,d", [(2, 1, 64), (1, 4, 128), (4, 2, 40), (1, 9, 128), (1, 20, 128), (1, 40, 64),
+                                    (2, 1, 256), (1, 7, 256)])
+def test_nothing_but_infinite_scores(kv, G, d, bad):
+    """Queries that see only scores of -infinity get zeros whatever the values hold, in
+    tiles that all queries see and in those that some do."""
+    rng = np.random.default_rng(kv * 100 + G + d)
+    c, rows = build(rng, 1, kv * d, 16, [100], [[5, 40]])
+    c.k[..., ::d] = -np.inf  # the first channel of each head
+    c.v[:, :, ::3, 1::7] = bad
+    counts = [3, 5]
+    q = queries(rng, sum(counts), kv * G, d)
+    q[..., 0] = np.abs(q[..., 0]) + 0.5
+    for groups in (([0, 2], [100]), (None, None)):
+        for hints in ALL_HINTS:
+            st, out, lse = gpu_attention(Pair(c), 0, q, d ** -0.5, rows, starts_of(counts), *groups, hints=hints)
+            assert st == 0 and (out == 0).all() and (lse == -np.inf).all(), (groups, hints)
+
+
 def test_large_scores_and_spread():
     """Peaked weights (one token takes all) and scores whose exponentials overflow
     without the maximum."""
