@@ -406,7 +406,8 @@ int cg_pages_compact_async(const cg_paged_cache* cache, int32_t* n_live_dev,
  * with scores, sums and lse in binary32 and the weights p rounded to binary16
  * for the product with v.  What a masked or missing token holds (also NaN
  * or infinity) has no influence.  A query that sees nothing, or only scores of
- * -infinity, gets zeros and lse = -infinity.
+ * -infinity, gets zeros and lse = -infinity; one that sees other scores too gets no finite
+ * number in a channel where it sees one that is not, however little it weighs.
  *
  * Group g: sequences group_starts[g] .. group_starts[g+1] - 1, whose first
  * prefix_lens[g] tokens are the same, as forks of one row have them; they are read

@@ -1199,7 +1199,9 @@ __global__ __launch_bounds__(kThreads) void k_join(Attn a) {
       m = top;
 #pragma unroll
       for (int i = 0; i < kBatch; i++) {
-        if (lx[i] == 0.0f) continue;  // nothing weighed: what the split left in o is not looked at
+        // a split in which nothing weighed anything left zeros, or what is no number: it
+        // counts, unless nothing weighs anything in the others either
+        if (x0 + i * a.join >= used) continue;
         const float f = worth(mx[i], m);
         o += ox[i] * f;
         l += lx[i] * f;
@@ -1226,7 +1228,7 @@ __global__ __launch_bounds__(kThreads) void k_join(Attn a) {
     return;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  store_out(a.out + qi * a.out_stride + (int64_t)h * a.d + quad * 4, o * inv);
+  store_out(a.out + qi * a.out_stride + (int64_t)h * a.d + quad * 4, quotient_of(o, inv));
   if (quad == 0 && a.lse) a.lse[(int64_t)qi * a.H + h] = lse_of(m, l);
 }
 

@@ -469,6 +469,43 @@ def test_nothing_but_infinite_scores(kv, G, d, bad):
             assert st == 0 and (out == 0).all() and (lse == -np.inf).all(), (groups, hints)
 
 
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("kv,G,d", [(2, 1, 64), (1, 4, 128), (1, 20, 128), (1, 40, 64), (1, 3, 256)])
+def test_weights_of_zero_and_odd_values(kv, G, d, bad):
+    """Zero times what is no finite number is none either: values of tokens whose scores
+    are -infinity, which are whole splits of the tokens when they are joined, and those
+    channels alone."""
+    rng = np.random.default_rng(kv * 100 + G + d)
+    c, rows = build(rng, 1, kv * d, 16, [400], [[5, 40]])
+    want = c.copy()
+    tt = np.arange(200)
+    pages, at = c.tables[rows[0], tt // 16], tt % 16
+    for x in (c, want):
+        x.k[0, pages, at, ::d] = -np.inf
+    odd = np.zeros(kv * d, bool)
+    odd[2::7] = True
+    c.v[0, pages[70], at[70], odd] = bad
+    counts = [3, 5]
+    q = queries(rng, sum(counts), kv * G, d)
+    q[..., 0] = np.abs(q[..., 0]) + 0.5
+    _, recs = pc.attention(want, 0, q, d ** -0.5, rows, starts_of(counts))
+    finite = want.copy()  # for the size of the scores that are
+    finite.k[0, pages, at, ::d] = 0
+    _, sizes = pc.attention(finite, 0, q, d ** -0.5, rows, starts_of(counts))
+    for j in recs:
+        for r, x in zip(recs[j], sizes[j]):
+            r["size"] = x["size"]
+    for groups in (([0, 2], [400]), (None, None)):
+        for hints in ALL_HINTS:
+            st, out, lse = gpu_attention(Pair(c), 0, q, d ** -0.5, rows, starts_of(counts), *groups, hints=hints)
+            for h in range(kv * G):
+                ch = odd[h // G * d:h // G * d + d]
+                assert not np.isfinite(out[:, h, ch]).any(), (groups, hints, h)
+                for j in recs:
+                    out[j, h, ch] = recs[j][h]["out"][ch]
+            compare((st, out, lse), (0, recs), q)
+
+
 def test_large_scores_and_spread():
     """Peaked weights (one token takes all) and scores whose exponentials overflow
     without the maximum."""
