@@ -27,6 +27,7 @@
 #include "cg_hostapi.h"
 #include "cg_internal.h"
 #include "cg_paged.h"
+#include "cg_ranges.h"
 
 namespace cg {
 namespace {
@@ -42,12 +43,7 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s4 lds_s4;
 
-constexpr int kTile = 32;        // tokens of a tile: the depth of one 16x16x32 product
 constexpr int kThreads = 256;    // of a joining workgroup
-// Tiles of a split, at least: one for each wave.  With more, short contexts leave most
-// of the chip idle (8 requests of 20 heads on 992 shared and 630 own tokens: 20 us with
-// 4, 24 with 8, 45 with 16 of the shared part's and 8 of the rest).
-constexpr int kLeast = 4;
 // Tiles of a split of shared prefixes that take all of the chip's slots and leave the rest
 // to wait for them: with fewer, half of the slots are the faster choice (14 requests of
 // 64 heads on 2,005 shared tokens: 31 us with half, 35 with all).
@@ -145,8 +141,7 @@ __device__ __forceinline__ Seq sequence(const Attn& a, int s) {
   const bool in = q.row >= 0 && q.row < a.R;
   q.len = a.lens[in ? q.row : 0];
   q.ok = in && len_ok(a, q.len) && q.q0 >= 0 && end <= a.n_q;
-  // none where the starts descend or leave the batch: a difference of any two could wrap around
-  q.m = q.q0 >= 0 && end > q.q0 && end <= a.n_q ? end - q.q0 : 0;
+  q.m = queries_of(q.q0, end, a.n_q);
   q.pre = 0;
   q.first = -1;
   if (g >= 0 && s < next && pre != 0) {
@@ -160,20 +155,6 @@ __device__ __forceinline__ Seq sequence(const Attn& a, int s) {
 // Whether row `row` can lend its first `pre` tokens.
 __device__ __forceinline__ bool lends(const Attn& a, int row, int pre) {
   return row >= 0 && row < a.R && a.lens[row] >= pre && len_ok(a, a.lens[row]);
-}
-
-// Tokens [lo, hi) in tiles that start at multiples of kTile, dealt to `splits`
-// workgroups in turn, at least kLeast each.
-struct Split {
-  int tile0, tiles, per, used;
-};
-__device__ __forceinline__ Split split_of(int lo, int hi, int splits) {
-  Split s;
-  s.tile0 = lo / kTile;
-  s.tiles = hi > lo ? (hi + kTile - 1) / kTile - s.tile0 : 0;
-  s.per = max(kLeast, (s.tiles + splits - 1) / splits);
-  s.used = (s.tiles + s.per - 1) / s.per;
-  return s;
 }
 
 // ---------------------------------------------------------------------------
@@ -1053,9 +1034,9 @@ __device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
     if (it.trow < 0 || it.trow >= a.R || !len_ok(a, a.lens[it.trow]) || a.lens[it.trow] < it.hi)
       return false;
     it.q0 = a.q_starts[s0];
-    const int q1 = a.q_starts[s1];
-    if (it.q0 < 0 || q1 <= it.q0 || q1 > a.n_q) return false;
-    it.rows = (q1 - it.q0) * a.G;
+    const int m = queries_of(it.q0, a.q_starts[s1], a.n_q);
+    if (m == 0) return false;
+    it.rows = m * a.G;
     it.lim0 = it.hi;
     it.splits = a.pre_splits;
     it.slot0 = 0;
@@ -1092,16 +1073,11 @@ __device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
   return true;
 }
 
-// The queries that a sequence names, as far as the batch has them, from begin_of to
-// end_of (its starts may be any numbers).
-__device__ __forceinline__ int begin_of(const Attn& a, const Item& it) { return min(max(it.q0, 0), a.n_q); }
-__device__ __forceinline__ int end_of(const Attn& a, const Item& it) { return min(it.q_end, a.n_q); }
-
 // Direct: outputs of a refused sequence's queries, of the item's kv heads.
 __device__ __forceinline__ void refuse(const Attn& a, const Item& it) {
   if (it.row_tile != 0) return;
   const int h0 = it.head * a.G, n = it.heads * a.G;
-  for (int q = begin_of(a, it); q < end_of(a, it); q++) {
+  for (int q = begin_of(it.q0, a.n_q); q < end_of(it.q_end, a.n_q); q++) {
     for (int i = threadIdx.x; i < n * a.d; i += blockDim.x) a.out[q * a.out_stride + h0 * a.d + i] = 0;
     for (int i = threadIdx.x; a.lse && i < n; i += blockDim.x)
       a.lse[(int64_t)q * a.H + h0 + i] = -__builtin_inff();
@@ -1115,7 +1091,7 @@ __device__ __forceinline__ void say_used(const Attn& a, const Item& it) {
   const int used = ok ? split_of(0, it.pre, a.pre_splits).used |
                             split_of(it.pre, it.hi, a.rest_splits).used << 16
                       : -1;
-  for (int i = begin_of(a, it) + (int)threadIdx.x; i < end_of(a, it); i += blockDim.x) a.used[i] = used;
+  for (int i = begin_of(it.q0, a.n_q) + (int)threadIdx.x; i < end_of(it.q_end, a.n_q); i += blockDim.x) a.used[i] = used;
   if (!ok && threadIdx.x == 0 && it.q0 < it.q_end) atomicOr(a.status, kRefused);
 }
 
