@@ -407,7 +407,9 @@ int cg_pages_compact_async(const cg_paged_cache* cache, int32_t* n_live_dev,
  * for the product with v.  What a masked or missing token holds (also NaN
  * or infinity) has no influence.  A query that sees nothing, or only scores of
  * -infinity, gets zeros and lse = -infinity; one that sees other scores too gets no finite
- * number in a channel where it sees one that is not, however little it weighs.
+ * number in a channel where it sees one that is not, however little it weighs.  A score
+ * past binary32's range (2^127 may be) is an infinity, and a query with one of +infinity
+ * gets NaN.
  *
  * Group g: sequences group_starts[g] .. group_starts[g+1] - 1, whose first
  * prefix_lens[g] tokens are the same, as forks of one row have them; they are read
@@ -424,7 +426,7 @@ typedef struct {
   int32_t layer;                /* 0 .. layers - 1 */
   int32_t n_heads, head_dim;    /* head_dim a multiple of 8 up to 256 that divides channels;
                                    n_heads a multiple of kv_heads, at most 1024 */
-  float scale;                  /* finite */
+  float scale;                  /* at most 2^127 in size */
   int32_t n_seqs, n_q, n_groups; /* 0 .. n_rows, 0 .. 2^20 (rows of q), 0 .. n_seqs */
   int32_t max_q, max_prefix, max_len; /* what to size the launch for, >= 0: queries of a
                                    sequence, longest shared prefix, longest row.  Other

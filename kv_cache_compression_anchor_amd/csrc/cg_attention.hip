@@ -515,6 +515,14 @@ struct Wave {
       }
     }
   }
+  // A row's sum of weights, over the lanes.  Against a reference of infinity, which a
+  // score past binary32's range gives, they came out as 0: exp(inf - inf) is no number.
+  __device__ __forceinline__ float sum(int r) const {
+    float x = l[r];
+    x += __shfl_xor(x, 16);
+    x += __shfl_xor(x, 32);
+    return m[r] == __builtin_inff() ? __builtin_nanf("") : x;
+  }
   // Scores to weights, which are summed before they are rounded.
   __device__ __forceinline__ void weights(const f4 (&s)[RT][2], float c, h8 (&p)[RT]) {
 #pragma unroll
@@ -668,7 +676,7 @@ struct Tokens {
 
 // The exponent's scale: scores are c (q . k) in units of log 2.
 __device__ __forceinline__ float log2_scale(const Attn& a) {
-  return a.scale == 0 ? 1.0f : fminf(fabsf(a.scale) * 1.44269504088896341f, 3.4e38f);
+  return a.scale == 0 ? 1.0f : fabsf(a.scale) * 1.44269504088896341f;
 }
 
 // Few rows: every wave holds all 16 RT of a row tile of its kv head.  The waves of a
@@ -757,9 +765,7 @@ __device__ __forceinline__ void run_split(const A& a, const Item& it, Shared<DP,
     // the waves' sums together, against the largest reference exponent
 #pragma unroll
     for (int r = 0; r < RT; r++) {
-      float l = w.l[r];
-      l += __shfl_xor(l, 16);
-      l += __shfl_xor(l, 32);
+      const float l = w.sum(r);
       if (g == 0) {
         sh.m[wave][r * 16 + n] = w.m[r];
         sh.l[wave][r * 16 + n] = l;
@@ -978,9 +984,7 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
     }
 #pragma unroll
     for (int r = 0; r < RT; r++) {
-      float l = w.l[r];
-      l += __shfl_xor(l, 16);
-      l += __shfl_xor(l, 32);
+      const float l = w.sum(r);
       const int row = row0 + r * 16 + n;
       if (row >= it.rows) continue;
       if (a.direct) {

@@ -35,7 +35,8 @@ int check_attention(const cg_paged_cache* c, const cg_attention* a) {
   const int kv = c->channels / a->head_dim;
   if (a->n_heads < 1 || a->n_heads > 1024 || a->n_heads % kv)
     return fail(CG_E_INVAL, "n_heads must be a multiple of channels / head_dim, at most 1024");
-  if (!isfinite(a->scale)) return fail(CG_E_INVAL, "scale must be finite");
+  // scores are computed in units of log 2: the scale has to stay finite in them
+  if (!(fabsf(a->scale) <= 0x1p127f)) return fail(CG_E_INVAL, "scale must be a number of at most 2^127 in size");
   if (a->n_seqs < 0 || a->n_seqs > c->n_rows || a->n_q < 0 || a->n_q > 1 << 20 ||
       a->n_groups < 0 || a->n_groups > a->n_seqs)
     return fail(CG_E_INVAL, "n_seqs, n_q or n_groups out of range");

@@ -447,7 +447,8 @@ def test_infinite_scores():
     assert np.isfinite(out[[0, 2]]).all()
 
 
-ALL_HINTS = (None, (5, 1 << 20, 1 << 21), (5, 0, 1 << 21))  # one kernel; prefixes shared and sums joined; joined
+# the lengths'; one kernel; prefixes shared and sums joined; joined
+ALL_HINTS = (None, (5, 0, 0), (5, 1 << 20, 1 << 21), (5, 0, 1 << 21))
 
 
 @pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
@@ -504,6 +505,34 @@ def test_weights_of_zero_and_odd_values(kv, G, d, bad):
                 for j in recs:
                     out[j, h, ch] = recs[j][h]["out"][ch]
             compare((st, out, lse), (0, recs), q)
+
+
+@pytest.mark.parametrize("kv,G,d", [(2, 1, 64), (1, 4, 128), (1, 20, 128), (1, 40, 64), (1, 3, 256)])
+@pytest.mark.parametrize("scale", [2.0 ** 126, -2.0 ** 126, 2.0 ** 127])
+def test_scores_past_the_range(kv, G, d, scale):
+    """A score past binary32's range is an infinity: exp(inf - inf) is no number, and a
+    query of scores of -infinity alone gets zeros.  Products are +-d, so that every score
+    passes the range by far; one query's products with the shared tokens have the other
+    sign, and one's are all 0, whose scores are finite."""
+    rng = np.random.default_rng(kv * 100 + G + d)
+    c, rows = build(rng, 1, kv * d, 16, [300], [[5, 40]])
+    c.k[:] = 1
+    q = np.ones((6, kv * G, d), np.float16)
+    q[1], q[4], q[5] = -1, -1, 0
+    counts = [3, 3]
+    for groups in (([0, 2], [300]), (None, None)):
+        for hints in ALL_HINTS:
+            st, out, lse = gpu_attention(Pair(c), 0, q, scale, rows, starts_of(counts), *groups, hints=hints)
+            up = [0, 2, 3] if scale > 0 else [1, 4]
+            down = [1, 4] if scale > 0 else [0, 2, 3]
+            assert st == 0 and np.isnan(out[up]).all() and np.isnan(lse[up]).all(), (groups, hints)
+            assert (out[down] == 0).all() and (lse[down] == -np.inf).all(), (groups, hints)
+            mean = np.stack([c.v[0, c.tables[rows[1], t // 16], t % 16] for t in range(340)]).astype(np.float64)
+            want = mean.mean(0).reshape(kv, 1, d)
+            # equal weights of a power of two: the values' sum in binary32, n e A, and one rounding
+            tol = U * np.abs(want) + 340 * E * np.abs(mean).mean(0).reshape(kv, 1, d) + 2.0 ** -25
+            assert (np.abs(out[5].reshape(kv, G, d) - want) <= tol).all()
+            assert np.abs(lse[5] - np.log(340)).max() <= 8 * E * np.log(340)
 
 
 def test_large_scores_and_spread():

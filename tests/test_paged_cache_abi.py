@@ -124,6 +124,14 @@ def test_attention_checks_its_arguments(cg, bad):
     assert rc == cg.CG_E_INVAL and cg.cg_last_error()
 
 
+@pytest.mark.parametrize("scale,ok", [(2.0 ** 127, True), (-2.0 ** 127, True), (1.5 * 2.0 ** 127, False),
+                                      (-1.0001 * 2.0 ** 127, False), (3.4e38, False)])
+def test_attention_takes_scales_up_to_2_127(cg, scale, ok):
+    n = C.c_size_t()
+    rc = cg.lib().cg_attention_workspace(C.byref(cache(cg)), C.byref(call(cg, scale=scale)), C.byref(n))
+    assert rc == (cg.CG_OK if ok else cg.CG_E_INVAL)
+
+
 def test_attention_checks_memory(cg):
     L, c, n = cg.lib(), cache(cg), C.c_size_t()
     a = call(cg)
