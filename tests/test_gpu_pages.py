@@ -195,6 +195,64 @@ def test_many_rows_and_pages():
     x.compact()
 
 
+def test_more_bad_requests_than_threads():
+    """Repeated, invalid and refused requests, and a pool that ends, among 1,500."""
+    rng = np.random.default_rng(13)
+    R, n = 3000, 1500
+    x = Pair(randomised(pc.empty(1, 3700, 2, 8, R, 6), rng))
+    odd = [-1, R, 1 << 30, -(1 << 31), (1 << 31) - 1]
+
+    def rows_of(count, least=0):
+        rows = least + rng.permutation(R - least)[:count].astype(np.int64)
+        rows[rng.random(count) < 0.02] = rng.choice(odd)
+        again = rng.random(count) < 0.02
+        rows[again] = rows[rng.integers(0, count, int(again.sum()))]
+        return rows
+
+    for step in range(3):
+        counts = rng.integers(0, 5, n)
+        starts = np.concatenate([[0], np.cumsum(counts)])
+        x.reserve(rows_of(n), starts, int(starts[-1]) + step, ("reserve", step))
+        x.fork(rng.choice(np.concatenate([np.arange(R // 2), odd]), n), rows_of(n, R // 2), ("fork", step))
+        full = (x.o.refs > 0).all()
+        x.free(rows_of(400), ("free", step))
+        x.compact(("compact", step))
+    assert full
+
+
+@pytest.mark.parametrize("n", [7, 1100])
+def test_extreme_numbers_stay_in_bounds(n):
+    """Rows, lengths, entries, counts and starts at both ends of the type: flagged, and
+    pools whose pages no valid number names keep their contents."""
+    rng = np.random.default_rng(n)
+    lo, hi = -(1 << 31), (1 << 31) - 1
+    ends = np.array([lo, lo + 1, -1, hi, hi - 1, 1 << 30, -(1 << 30)])
+    x = Pair(randomised(pc.empty(1, 40, 4, 64, 1200, 5), rng))
+    cg, c, t = x.cg, x.cache, x.t
+    slots = t.zeros(50, dtype=t.int64, device="cuda")
+    mixed = lambda size, top: np.where(rng.random(size) < 0.7, rng.choice(ends, size),  # noqa: E731
+                                       rng.integers(0, top, size))
+    for _ in range(20):
+        x.tables.copy_(x.i32(mixed(x.tables.shape, 44)))
+        x.lens.copy_(x.i32(mixed(1200, 22)))
+        x.refs.copy_(x.i32(mixed(40, 3)))
+        cg.cg_pages_reserve_async(c, x.i32(mixed(n, 1200)), x.i32(mixed(n + 1, 52)), slots, x.ws)
+        cg.cg_pages_fork_async(c, x.i32(mixed(n, 1200)), x.i32(mixed(n, 1200)), x.ws)
+        cg.cg_pages_free_async(c, x.i32(mixed(n, 1200)))
+        cg.cg_pages_compact_async(c, x.ws)
+        m = min(n, 40)
+        cg.cg_pages_copy_async(c, x.i32(mixed(m, 44)), x.i32(mixed(m, 44)))
+        t.cuda.synchronize()
+        assert int(x.status.item()) & ~14 == 0 and int(x.status.item())
+    far = t.tensor([lo, hi, -(1 << 63), (1 << 63) - 1, 160, -2], dtype=t.int64, device="cuda")
+    k, v = x.k.clone(), x.v.clone()
+    new = t.ones((1, 6, 64), dtype=t.float16, device="cuda")
+    x.status.zero_()
+    cg.cg_pages_write_async(c, 0, far, new, new)
+    assert int(x.status.item()) == pc.BAD_PAGE
+    assert t.equal(k.view(t.int16), x.k.view(t.int16)) and t.equal(v.view(t.int16), x.v.view(t.int16))
+
+
 def test_write_layers_and_strides():
     """Layer ranges, K and V as slices of a wider projection, slots outside the pool."""
     rng = np.random.default_rng(9)
