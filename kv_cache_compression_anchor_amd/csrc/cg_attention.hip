@@ -9,18 +9,18 @@
 // once; a sequence's own tokens are computed for its rows alone; long stretches are
 // dealt to several workgroups.  k_join adds up and divides.  l, o and m are
 // binary32; the weights 2^(s_t - m) are rounded to binary16 (a relative 2^-11 each) for
-// the product with v, after they went into l.
+// the product with v, after they went into l, which lse takes unrounded.
 //
 // Bounds: reading every token of K and V once, or the products.  Measured, k_attention
 // and k_join, the call repeated (and with other data in the caches in between): 64
 // requests of 32 heads (8 of K and V, 128 channels) on 9,216 shared and up to 600 own
-// tokens, 122 MB and 10 GFLOP, in 34 + 7 us (50): the tail of the sequences' own tokens
+// tokens, 122 MB and 10 GFLOP, in 35 + 7 us (50): the tail of the sequences' own tokens
 // and the join's reading back of the sums are what is left above the 26 us of a copy of
-// these bytes.  21 requests of 32 heads, each with its K and V, 121 MB, in 28 + 5 us
-// (38).  32 requests of 64 heads on 81,920 shared tokens, 366 MB and 86 GFLOP, in 112 + 10
-// us (126; 142 when repeated without a pause, as power then allows): 0.77 PFLOP/s against
-// 1.3 of a large library product; the matrix units are busy for 38% of the time and share
-// the issue slots with the exponentials (about as many vector cycles as products).
+// these bytes.  21 requests of 32 heads, each with its K and V, 121 MB, in 29 + 5 us
+// (37).  32 requests of 64 heads on 81,920 shared tokens, 366 MB and 86 GFLOP, in 115 + 10
+// us at least (128; 137 when repeated without a pause, as power then allows): 0.75 PFLOP/s
+// against 1.3 of a large library product; the matrix units are busy for 39% of the time and
+// share the issue slots with the exponentials (about as many vector cycles as products).
 #include <algorithm>
 #include <type_traits>
 
@@ -46,7 +46,7 @@ typedef __attribute__((address_space(3))) s4 lds_s4;
 constexpr int kThreads = 256;    // of a joining workgroup
 // Tiles of a split of shared prefixes that take all of the chip's slots and leave the rest
 // to wait for them: with fewer, half of the slots are the faster choice (14 requests of
-// 64 heads on 2,005 shared tokens: 31 us with half, 35 with all).
+// 64 heads, 32 of K and V, on 2,005 shared tokens: 30 us with half, 34 with all).
 constexpr int kLong = 32;
 // Weights are 2^(score - m) with m at most kSlack above what the running maximum
 // was when it was last raised, and kLift below it: up to 2^14, and binary16's
@@ -899,8 +899,8 @@ __device__ __forceinline__ void run_ring(const A& a, const Item& it, Shared<DP, 
         // rounds of the ring's slots: no branch but one, LDS offsets are immediates, and
         // a wave's 8 rows of a tile lie in one page, whose number is read a tile ahead.
         // (A wave that finds its way through the conditions below instead spends a quarter
-        // of its time on them and on addresses: 178 us against 139 for 32 requests of 64
-        // heads on 81,920 tokens.)
+        // of its time on them and on addresses: 191 us against 137 for 32 requests of 64
+        // heads on 81,920 tokens, the call repeated.)
         int tile = base;
         const int seen = tk.bad || base * kTile < cur.lo ? base : min(stop, min_lim / kTile);
         if (tk.src.pmask >= 7 && tk.src.nc == Ge::NC && tile + 2 * kStages - 1 <= seen) {
@@ -1291,8 +1291,9 @@ Plan plan_of(const cg_paged_cache& c, const cg_attention& x) {
                          std::max(0, x.max_len - (shared ? x.max_prefix : 0)), slots, kLeast);
   // Several heads a workgroup share its start (about 5 us of latencies) and leave fewer
   // waves to wait for the one with most tiles, as long as there are workgroups enough
-  // (64 sequences of 8 kv heads and up to 600 tokens behind 9,216 shared ones: the call
-  // takes 51 us with one head, 44 with two, and 53 with four, which leaves 128 workgroups).
+  // (64 sequences of 8 kv heads and up to 600 tokens behind 9,216 shared ones: the call,
+  // repeated, takes 50 us with one head, 43 with two, and 52 with four, which leaves 128
+  // workgroups).
   auto heads = [&](int splits) {
     int n = 1;
     while (n < 4 && p.rest_mode <= kRows32 && kv % (2 * n) == 0 &&

@@ -4,13 +4,15 @@
 // Two kinds of work.  Bookkeeping (who gets which page) is a handful of prefix
 // sums over the requests and over refs; each call does it in one workgroup of
 // 1,024 threads, so that one launch suffices and page numbers do not depend on
-// scheduling.  Its time is its chain of dependent loads and barriers: 5 to 10 us
-// for up to 1,024 requests and 16,384 pages, 35 us for a compaction over 131,072.  Moving K and V is a plain copy bound
+// scheduling.  Its time is its chain of dependent loads and barriers: 5 to 11 us
+// for up to 1,024 requests, 6,000 tokens and 16,384 pages; 88 us where the slots of
+// 100,000 tokens are asked for and 1.9 ms for 2^21, which one workgroup finds one by
+// one; 45 us for a compaction over 131,072 pages.  Moving K and V is a plain copy bound
 // by HBM; it is cut into pieces spread over the chip.  Measured, counting bytes
 // read and written: 96 pages of 32 layers x 16 tokens x 4,096 channels (1.6 GB)
-// copied in 315 us, 5.1 TB/s; 5,850 tokens of 32 layers x 1,024 channels (1.5 GB)
-// written in 296 us, 5.2 TB/s; 48 of 96 rows freed and 271 pages of the rest
-// moved (1.1 GB) in 231 us, 4.9 TB/s; 64 forks of one row (a copy of 11 tokens
+// copied in 318 us, 5.1 TB/s; 5,850 tokens of 32 layers x 1,024 channels (1.5 GB)
+// written in 297 us, 5.2 TB/s; 48 of 96 rows freed and 271 pages of the rest
+// moved (1.1 GB) in 233 us, 4.9 TB/s; 64 forks of one row (a copy of 11 tokens
 // each, 185 MB) in 25 us, 7.4 TB/s as their sources are read from the caches.  A
 // large device-to-device copy reaches 4.7 TB/s here.
 #include <algorithm>

@@ -6,8 +6,8 @@ namespace cg {
 
 constexpr int kTile = 32;  // tokens of a tile: the depth of one 16x16x32 product
 // Tiles of a split, at least: one for each wave.  With more, short contexts leave most
-// of the chip idle (8 requests of 20 heads on 992 shared and 630 own tokens: 20 us with
-// 4, 24 with 8, 45 with 16 of the shared part's and 8 of the rest).
+// of the chip idle (8 requests of 20 heads, 5 of K and V, on 992 shared and 630 own tokens:
+// 17 us with 4, 18 with 8, 24 with 16).
 constexpr int kLeast = 4;
 
 // Queries start .. end - 1 of a batch of n_q: how many, none where the starts descend
