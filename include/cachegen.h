@@ -449,6 +449,77 @@ int cg_attention_workspace(const cg_paged_cache* cache, const cg_attention* call
 int cg_attention_prefix_async(const cg_paged_cache* cache, const cg_attention* call,
                               void* workspace_dev, size_t workspace_bytes, void* stream);
 
+/* Where tokens of rows are: request i asks for tokens firsts[i] + 0, 1, .. of row
+ * rows[i] (device int32 arrays of n; firsts_dev NULL: from token 0), starts[i+1] -
+ * starts[i] of them, which are tokens starts[i] .. of the n_tokens (starts ascending within
+ * 0 .. n_tokens <= 2^21, n + 1 entries; n <= n_rows, a row may be named often).  slots_dev
+ * (int64 [n_tokens]) receives page x page_tokens + row of the page, as reserve gives them.
+ * A request that asks past its row's length, or for a bad row, is refused (bit 2): its
+ * slots are -1, as are those of tokens of no request and of pages outside the pool (bit 1). */
+int cg_pages_slots_async(const cg_paged_cache* cache, int32_t n, const int32_t* rows_dev,
+                         const int32_t* firsts_dev, const int32_t* starts_dev, int32_t n_tokens,
+                         int64_t* slots_dev, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Caches held in 4 bits: 0.5625 bytes a number instead of 2 (heads of whole groups), for
+ * contexts that stay on the device.  Such a cache is a cg_paged_cache whose `channels`
+ * count the 16-bit units of a row, as cg_quant_row gives them: reserve, fork, free, compact,
+ * copy and slots work on it as they are.  K and V are written, read back and attended to
+ * through the calls below.
+ *
+ * A row holds one token's K (or V) of one layer: `channels` numbers, heads of head_dim
+ * channels, each head in groups of 32 channels (the last may be shorter).  With a the
+ * largest magnitude of a group, the group's scale is
+ *   s = the smallest binary16 number of at most 8 significant bits with 7 s >= a,
+ *       at most 9344,
+ * a number x is held as n = floor(x / s + 1/2), in -7 .. 7, and stands for s n.  That is a
+ * binary16 number (8 + 3 bits), so reading back rounds nothing, and is off from x by s / 2
+ * at most.  A group of zeros has s = 0; a group with a number that is not finite has s = NaN
+ * and stands for NaNs.
+ *   row: codes of all heads, 16 ceil(head_dim / 32) bytes each: 8 channels a little-endian
+ *        32-bit word, n + 8 of channel e of them at bit 16 (e mod 2) + 4 (e / 2), channels
+ *        behind the head 8; then the scales, binary16, group by group; then up to 14 bytes
+ *        that no call touches, to a multiple of 16.
+ * Pools are 16-byte aligned. */
+typedef struct {
+  int32_t channels;  /* of a token: 1 .. 65536 */
+  int32_t head_dim;  /* a multiple of 8 up to 256 that divides channels */
+  int32_t bits;      /* 4 */
+  int32_t reserved;  /* 0 */
+} cg_quant_form;
+
+/* The `channels` of a cg_paged_cache that holds rows of this form (row bytes / 2, a multiple
+ * of 8); CG_E_INVAL also where that is more than 65536.  Host only. */
+int cg_quant_row(const cg_quant_form* form, int32_t* cache_channels);
+
+/* cg_pages_write_async into a cache of this form: the same arguments, with token_stride >=
+ * form->channels.  k_held_dev and v_held_dev, both or neither NULL, receive the numbers
+ * that the cache holds, of every token, whatever its slot, with the strides held_token_stride and
+ * held_layer_stride; they may be k_new_dev and v_new_dev themselves with the same strides,
+ * but not overlap them otherwise. */
+int cg_quant_write_async(const cg_paged_cache* cache, const cg_quant_form* form, int32_t layer0,
+                         int32_t n_layers, int32_t n_tokens, const int64_t* slots_dev,
+                         const void* k_new_dev, const void* v_new_dev, int64_t token_stride,
+                         int64_t layer_stride, void* k_held_dev, void* v_held_dev,
+                         int64_t held_token_stride, int64_t held_layer_stride, void* stream);
+
+/* The numbers held at slots (as cg_pages_slots_async gives them, in any order and also
+ * repeated) in layers layer0 .. layer0 + n_layers - 1, to fp16 k_out_dev, v_out_dev: token t of
+ * layer layer0 + l at element l x layer_stride + t x token_stride, channels contiguous.  A
+ * slot of -1 leaves its token of the outputs as it was, any other outside the pool too (bit 1). */
+int cg_quant_read_async(const cg_paged_cache* cache, const cg_quant_form* form, int32_t layer0,
+                        int32_t n_layers, int32_t n_tokens, const int64_t* slots_dev,
+                        void* k_out_dev, void* v_out_dev, int64_t token_stride,
+                        int64_t layer_stride, void* stream);
+
+/* cg_attention_prefix_async over a cache of this form: the same call (head_dim is the
+ * form's), results and refusals as if the cache held what cg_quant_read_async gives. */
+int cg_quant_attention_workspace(const cg_paged_cache* cache, const cg_quant_form* form,
+                                 const cg_attention* call, size_t* bytes);
+int cg_quant_attention_async(const cg_paged_cache* cache, const cg_quant_form* form,
+                             const cg_attention* call, void* workspace_dev,
+                             size_t workspace_bytes, void* stream);
+
 /* For long-running processes: frees the device memory the library keeps
  * between calls, on every device it has used — the table-build and encode
  * workspaces (and their pinned host words), and the blocks its per-device

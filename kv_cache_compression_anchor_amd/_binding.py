@@ -27,7 +27,8 @@ EXPORTS = ["cg_build_tables", "cg_build_tables_grouped", "cg_tables_free", "cg_t
            "cg_decode_streamed", "cg_pages_workspace", "cg_pages_copy_async",
            "cg_pages_reserve_async", "cg_pages_write_async", "cg_pages_fork_async",
            "cg_pages_free_async", "cg_pages_compact_async", "cg_attention_workspace",
-           "cg_attention_prefix_async",
+           "cg_attention_prefix_async", "cg_pages_slots_async", "cg_quant_row", "cg_quant_write_async",
+           "cg_quant_read_async", "cg_quant_attention_workspace", "cg_quant_attention_async",
            "cg_plan_chunk", "cg_release_cached", "cg_last_error"]
 
 
@@ -77,6 +78,11 @@ class cg_attention(C.Structure):
                 ("q_stride", C.c_int64), ("out_stride", C.c_int64)]
 
 
+class cg_quant_form(C.Structure):
+    _fields_ = [("channels", C.c_int32), ("head_dim", C.c_int32), ("bits", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
 _lib = None
 
 
@@ -120,6 +126,13 @@ def lib():
             "cg_pages_compact_async": (I, [P, P, P, SZ, P]),
             "cg_attention_workspace": (I, [P, P, C.POINTER(SZ)]),
             "cg_attention_prefix_async": (I, [P, P, P, SZ, P]),
+            "cg_pages_slots_async": (I, [P, I32, P, P, P, I32, P, P]),
+            "cg_quant_row": (I, [P, C.POINTER(I32)]),
+            "cg_quant_write_async": (I, [P, P, I32, I32, I32, P, P, P, C.c_int64, C.c_int64, P, P,
+                                         C.c_int64, C.c_int64, P]),
+            "cg_quant_read_async": (I, [P, P, I32, I32, I32, P, P, P, C.c_int64, C.c_int64, P]),
+            "cg_quant_attention_workspace": (I, [P, P, P, C.POINTER(SZ)]),
+            "cg_quant_attention_async": (I, [P, P, P, P, SZ, P]),
             "cg_plan_chunk": (I, [C.POINTER(cg_chunk_plan_in), C.POINTER(I32),
                                   C.POINTER(C.c_double)]),
             "cg_release_cached": (I, []),
@@ -540,13 +553,9 @@ def cg_attention_workspace(cache: PagedCache, n_q, n_heads, head_dim, n_seqs, n_
     return n.value
 
 
-def cg_attention_prefix_async(cache: PagedCache, layer, q, out, scale, rows, q_starts, group_starts,
-                              prefix_lens, max_q, max_prefix, max_len, workspace, lse=None,
-                              stream=None):
-    """Attention of q (fp16 [tokens, heads, head_dim]) over layer `layer` of the
-    cache into out (the same shape) and lse (fp32 [tokens, heads], may be None).
-    rows None: sequence s is row s.  group_starts / prefix_lens None: no shared
-    prefixes.  q and out may have a longer stride between tokens."""
+def _attention_call(cache, layer, q, out, scale, rows, q_starts, group_starts, prefix_lens, max_q,
+                    max_prefix, max_len, lse):
+    """The cg_attention of a call's tensors."""
     n_q, heads, dim = q.shape
     q_stride, s1 = _rows3(q, cache.f16, cache.index, dim, "q")
     out_stride, s2 = _rows3(out, cache.f16, cache.index, dim, "out")
@@ -555,14 +564,124 @@ def cg_attention_prefix_async(cache: PagedCache, layer, q, out, scale, rows, q_s
     n = q_starts.numel() - 1
     groups = 0 if group_starts is None else group_starts.numel() - 1
     i32, ptr = cache.i32, cache._ptr
-    a = cg_attention(layer, heads, dim, scale, n, n_q, groups, max_q, max_prefix, max_len,
-                     ptr(rows, i32, "rows", n), ptr(q_starts, i32, "q_starts"),
-                     ptr(group_starts, i32, "group_starts"),
-                     ptr(prefix_lens, i32, "prefix_lens", groups), q.data_ptr(), out.data_ptr(),
-                     ptr(lse, cache.f32, "lse", n_q * heads), q_stride, out_stride)
+    return cg_attention(layer, heads, dim, scale, n, n_q, groups, max_q, max_prefix, max_len,
+                        ptr(rows, i32, "rows", n), ptr(q_starts, i32, "q_starts"),
+                        ptr(group_starts, i32, "group_starts"),
+                        ptr(prefix_lens, i32, "prefix_lens", groups), q.data_ptr(), out.data_ptr(),
+                        ptr(lse, cache.f32, "lse", n_q * heads), q_stride, out_stride)
+
+
+def cg_attention_prefix_async(cache: PagedCache, layer, q, out, scale, rows, q_starts, group_starts,
+                              prefix_lens, max_q, max_prefix, max_len, workspace, lse=None,
+                              stream=None):
+    """Attention of q (fp16 [tokens, heads, head_dim]) over layer `layer` of the
+    cache into out (the same shape) and lse (fp32 [tokens, heads], may be None).
+    rows None: sequence s is row s.  group_starts / prefix_lens None: no shared
+    prefixes.  q and out may have a longer stride between tokens."""
+    a = _attention_call(cache, layer, q, out, scale, rows, q_starts, group_starts, prefix_lens, max_q,
+                        max_prefix, max_len, lse)
     _check(cache.lib.cg_attention_prefix_async(cache.ref, C.byref(a),
-                                               ptr(workspace, cache.u8, "workspace"),
+                                               cache._ptr(workspace, cache.u8, "workspace"),
                                                workspace.numel(), cache._stream(stream)))
+
+
+def cg_pages_slots_async(cache: PagedCache, rows, firsts, starts, slots, stream=None):
+    """Where tokens firsts[i] .. of row rows[i] are (firsts None: from token 0): those of
+    request i are slots[starts[i]:starts[i + 1]] (int64, page x page_tokens + row)."""
+    n = rows.numel()
+    _check(cache.lib.cg_pages_slots_async(
+        cache.ref, n, cache._ptr(rows, cache.i32, "rows"), cache._ptr(firsts, cache.i32, "firsts", n),
+        cache._ptr(starts, cache.i32, "starts", n + 1), slots.numel(),
+        cache._ptr(slots, cache.i64, "slots"), cache._stream(stream)))
+
+
+def cg_quant_row(channels: int, head_dim: int) -> int:
+    """16-bit units of a row of `channels` channels held in 4 bits: a pool of such a cache is
+    uint8 [layers, num_pages, page_tokens, 2 x that]."""
+    f = cg_quant_form(channels, head_dim, 4, 0)
+    n = C.c_int32(0)
+    _check(lib().cg_quant_row(C.byref(f), C.byref(n)))
+    return n.value
+
+
+class QuantCache(PagedCache):
+    """A paged cache held in 4 bits: pools uint8 [layers, num_pages, page_tokens,
+    2 x cg_quant_row(channels, head_dim)], the rest as PagedCache has it.  The cg_pages_* calls
+    take it, and the cg_quant_* calls for what its rows stand for."""
+
+    def __init__(self, k_pool, v_pool, tables, lens, refs, status, channels, head_dim):
+        import torch
+        row = 2 * cg_quant_row(channels, head_dim)
+        for t in (k_pool, v_pool):
+            if t.dtype != torch.uint8 or t.dim() != 4 or t.shape[3] != row or not t.is_contiguous():
+                raise ValueError("pools must be contiguous uint8 [layers, num_pages, page_tokens, "
+                                 f"{row}]")
+            if t.data_ptr() % 16:
+                raise ValueError("pools must be 16-byte aligned")
+        super().__init__(k_pool.view(torch.float16), v_pool.view(torch.float16), tables, lens, refs,
+                         status)
+        self.form = cg_quant_form(channels, head_dim, 4, 0)
+        self.form_ref = C.byref(self.form)
+        self.numbers = channels  # channels of a token
+
+
+def _quant_rows(cache, a, b, names):
+    """Strides (token, layer) of a pair of fp16 tensors [layers, tokens, channels]."""
+    strides = _rows3(a, cache.f16, cache.index, cache.numbers, names[0])
+    if a.shape != b.shape or strides != _rows3(b, cache.f16, cache.index, cache.numbers, names[1]):
+        raise ValueError(f"{names[0]} and {names[1]} must have the same shape and strides")
+    return strides[1], strides[0]
+
+
+def cg_quant_write_async(cache: QuantCache, layer0, slots, k_new, v_new, k_held=None, v_held=None,
+                         stream=None):
+    """Writes k_new / v_new (fp16 [layers, tokens, channels], channels contiguous, both with
+    the same strides) in 4 bits to `slots` in layers layer0 ..; k_held / v_held (the same
+    shape) receive what the cache holds, and may be k_new / v_new."""
+    new = _quant_rows(cache, k_new, v_new, ("k_new", "v_new"))
+    kh = vh = None
+    held = (cache.numbers, 0)
+    if k_held is not None and v_held is not None:
+        held = _quant_rows(cache, k_held, v_held, ("k_held", "v_held"))
+        kh, vh = k_held.data_ptr(), v_held.data_ptr()
+        if k_held.shape != k_new.shape:
+            raise ValueError("k_held and v_held must have the shape of k_new")
+    elif k_held is not None or v_held is not None:
+        raise ValueError("k_held and v_held must both be given or neither")
+    layers, n, _ = k_new.shape
+    _check(cache.lib.cg_quant_write_async(cache.ref, cache.form_ref, layer0, layers, n,
+                                          cache._ptr(slots, cache.i64, "slots", n), k_new.data_ptr(),
+                                          v_new.data_ptr(), *new, kh, vh, *held,
+                                          cache._stream(stream)))
+
+
+def cg_quant_read_async(cache: QuantCache, layer0, slots, k_out, v_out, stream=None):
+    """What the cache holds at `slots` in layers layer0 .. into k_out / v_out (fp16 [layers,
+    tokens, channels], channels contiguous, both with the same strides)."""
+    strides = _quant_rows(cache, k_out, v_out, ("k_out", "v_out"))
+    layers, n, _ = k_out.shape
+    _check(cache.lib.cg_quant_read_async(cache.ref, cache.form_ref, layer0, layers, n,
+                                         cache._ptr(slots, cache.i64, "slots", n), k_out.data_ptr(),
+                                         v_out.data_ptr(), *strides, cache._stream(stream)))
+
+
+def cg_quant_attention_workspace(cache: QuantCache, n_q, n_heads, n_seqs, n_groups, max_q, max_prefix,
+                                 max_len) -> int:
+    """Bytes of workspace of a cg_quant_attention_async call of these numbers."""
+    a = cg_attention(0, n_heads, cache.form.head_dim, 1.0, n_seqs, n_q, n_groups, max_q, max_prefix, max_len)
+    n = C.c_size_t(0)
+    _check(cache.lib.cg_quant_attention_workspace(cache.ref, cache.form_ref, C.byref(a), C.byref(n)))
+    return n.value
+
+
+def cg_quant_attention_async(cache: QuantCache, layer, q, out, scale, rows, q_starts, group_starts,
+                             prefix_lens, max_q, max_prefix, max_len, workspace, lse=None, stream=None):
+    """cg_attention_prefix_async over a cache held in 4 bits."""
+    a = _attention_call(cache, layer, q, out, scale, rows, q_starts, group_starts, prefix_lens, max_q,
+                        max_prefix, max_len, lse)
+    _check(cache.lib.cg_quant_attention_async(cache.ref, cache.form_ref, C.byref(a),
+                                              cache._ptr(workspace, cache.u8, "workspace"),
+                                              workspace.numel(), cache._stream(stream)))
 
 
 def cg_release_cached():

@@ -17,7 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libcachegen.so")
 SOURCES = ["cg_tables.hip", "cg_encode.hip", "cg_decode.hip", "cg_api.hip",
-           "cg_pages.hip", "cg_attention.hip"]
+           "cg_pages.hip", "cg_attention.hip", "cg_quant.hip", "cg_quant_attention.hip"]
 HOST_SOURCES = ["cg_host.cpp", "cg_paged_host.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX", "g++")

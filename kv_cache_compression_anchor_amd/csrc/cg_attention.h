@@ -265,7 +265,10 @@ struct Wave {
   }
 
   // Queries of rows row0 .. row0 + 16 RT - 1 (row = query x heads of the kv head +
-  // head); rows past the item's are zeros that see everything.
+  // head); rows past the item's are zeros that see everything.  A product's depth takes the
+  // channels in any order that K has too: product ks takes chunk 4 ks + lane / 16 from a
+  // lane, or (kSpans) a lane's chunks are neighbours.
+  template <bool kSpans = false>
   __device__ __forceinline__ void load_queries(const Attn& a, const Item& it, int head, int row0) {
     const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
 #pragma unroll
@@ -276,7 +279,7 @@ struct Wave {
       const uint16_t* from = a.q + (it.q0 + qi) * a.q_stride + (int64_t)h * a.d;
 #pragma unroll
       for (int ks = 0; ks < KS; ks++) {
-        const int ch = ks * 4 + g;
+        const int ch = kSpans ? g * KS + ks : ks * 4 + g;
         q[r][ks] = __builtin_bit_cast(h8, in && ch < a.d / 8 ? *(const uint4*)(from + ch * 8) : uint4{0, 0, 0, 0});
       }
     }

@@ -750,20 +750,9 @@ int cg_attention_prefix_async(const cg_paged_cache* c, const cg_attention* a, vo
   if (int rc = check_attention(c, a)) return rc;
   size_t need = 0;
   if (int rc = cg_attention_workspace(c, a, &need)) return rc;
-  if (a->q_stride < (int64_t)a->n_heads * a->head_dim || a->q_stride > (int64_t)1 << 40 ||
-      a->out_stride < (int64_t)a->n_heads * a->head_dim || a->out_stride > (int64_t)1 << 40 ||
-      (a->q_stride | a->out_stride) % 8)
-    return fail(CG_E_INVAL, "q_stride and out_stride must be multiples of 8 and at least n_heads x head_dim");
+  if (int rc = check_attention_strides(a)) return rc;
   if (a->n_seqs == 0 || a->n_q == 0) return CG_OK;
-  if (!a->q_starts_dev || !a->q_dev || !a->out_dev ||
-      (a->n_groups > 0 && (!a->group_starts_dev || !a->prefix_lens_dev)))
-    return fail(CG_E_INVAL, "NULL pointer in the call");
-  if (((uintptr_t)a->q_dev | (uintptr_t)a->out_dev | (uintptr_t)c->k_pool_dev |
-       (uintptr_t)c->v_pool_dev) % 16)
-    return fail(CG_E_INVAL, "pools, q and out must be 16-byte aligned");
-  if (!workspace_dev || (uintptr_t)workspace_dev % 16)
-    return fail(CG_E_INVAL, "workspace NULL or not 16-byte aligned");
-  if (workspace_bytes < need) return fail(CG_E_CAPACITY, "workspace too small");
+  if (int rc = check_attention_memory(c, a, workspace_dev, workspace_bytes, need)) return rc;
   DeviceGuard dg(c->device);
   if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
   const Plan p = plan_of(*c, *a);

@@ -26,13 +26,13 @@ int check_paged_cache(const cg_paged_cache* c) {
   return CG_OK;
 }
 
-int check_attention(const cg_paged_cache* c, const cg_attention* a) {
-  if (int rc = check_paged_cache(c)) return rc;
+// The call's numbers on a cache of `channels` channels a token.
+static int check_call(const cg_paged_cache* c, const cg_attention* a, int channels) {
   if (!a) return fail(CG_E_INVAL, "call is NULL");
   if (a->layer < 0 || a->layer >= c->layers) return fail(CG_E_INVAL, "layer out of range");
-  if (a->head_dim < 8 || a->head_dim > 256 || a->head_dim % 8 || c->channels % a->head_dim)
+  if (a->head_dim < 8 || a->head_dim > 256 || a->head_dim % 8 || channels % a->head_dim)
     return fail(CG_E_INVAL, "head_dim must be a multiple of 8 up to 256 that divides channels");
-  const int kv = c->channels / a->head_dim;
+  const int kv = channels / a->head_dim;
   if (a->n_heads < 1 || a->n_heads > 1024 || a->n_heads % kv)
     return fail(CG_E_INVAL, "n_heads must be a multiple of channels / head_dim, at most 1024");
   // scores are computed in units of log 2: the scale has to stay finite in them
@@ -45,4 +45,65 @@ int check_attention(const cg_paged_cache* c, const cg_attention* a) {
   return CG_OK;
 }
 
+int check_attention(const cg_paged_cache* c, const cg_attention* a) {
+  if (int rc = check_paged_cache(c)) return rc;
+  return check_call(c, a, c->channels);
+}
+
+int check_attention_strides(const cg_attention* a) {
+  if (a->q_stride < (int64_t)a->n_heads * a->head_dim || a->q_stride > (int64_t)1 << 40 ||
+      a->out_stride < (int64_t)a->n_heads * a->head_dim || a->out_stride > (int64_t)1 << 40 ||
+      (a->q_stride | a->out_stride) % 8)
+    return fail(CG_E_INVAL, "q_stride and out_stride must be multiples of 8 and at least n_heads x head_dim");
+  return CG_OK;
+}
+
+int check_attention_memory(const cg_paged_cache* c, const cg_attention* a, const void* workspace,
+                           size_t bytes, size_t need) {
+  if (!a->q_starts_dev || !a->q_dev || !a->out_dev ||
+      (a->n_groups > 0 && (!a->group_starts_dev || !a->prefix_lens_dev)))
+    return fail(CG_E_INVAL, "NULL pointer in the call");
+  if (((uintptr_t)a->q_dev | (uintptr_t)a->out_dev | (uintptr_t)c->k_pool_dev |
+       (uintptr_t)c->v_pool_dev) % 16)
+    return fail(CG_E_INVAL, "pools, q and out must be 16-byte aligned");
+  if (!workspace || (uintptr_t)workspace % 16)
+    return fail(CG_E_INVAL, "workspace NULL or not 16-byte aligned");
+  if (bytes < need) return fail(CG_E_CAPACITY, "workspace too small");
+  return CG_OK;
+}
+
+static int check_form(const cg_quant_form* f) {
+  if (!f) return fail(CG_E_INVAL, "form is NULL");
+  if (f->bits != 4 || f->reserved != 0) return fail(CG_E_INVAL, "bits must be 4 and reserved 0");
+  if (f->channels < 1 || f->channels > 65536) return fail(CG_E_INVAL, "channels must be in 1..65536");
+  if (f->head_dim < 8 || f->head_dim > 256 || f->head_dim % 8 || f->channels % f->head_dim)
+    return fail(CG_E_INVAL, "head_dim must be a multiple of 8 up to 256 that divides channels");
+  if (quant_row(*f).row > 2 * 65536) return fail(CG_E_INVAL, "a row would take more than 131,072 bytes");
+  return CG_OK;
+}
+
+int check_quant(const cg_paged_cache* c, const cg_quant_form* f) {
+  if (int rc = check_paged_cache(c)) return rc;
+  if (int rc = check_form(f)) return rc;
+  if (2 * c->channels != quant_row(*f).row)
+    return fail(CG_E_INVAL, "the cache's channels are not those that cg_quant_row gives");
+  if (((uintptr_t)c->k_pool_dev | (uintptr_t)c->v_pool_dev) % 16)
+    return fail(CG_E_INVAL, "pools must be 16-byte aligned");
+  return CG_OK;
+}
+
+int check_quant_attention(const cg_paged_cache* c, const cg_quant_form* f, const cg_attention* a) {
+  if (int rc = check_quant(c, f)) return rc;
+  if (int rc = check_call(c, a, f->channels)) return rc;
+  if (a->head_dim != f->head_dim) return fail(CG_E_INVAL, "head_dim must be the form's");
+  return CG_OK;
+}
+
 }  // namespace cg
+
+extern "C" int cg_quant_row(const cg_quant_form* form, int32_t* cache_channels) {
+  if (int rc = cg::check_form(form)) return rc;
+  if (!cache_channels) return cg::fail(CG_E_INVAL, "cache_channels is NULL");
+  *cache_channels = cg::quant_row(*form).row / 2;
+  return CG_OK;
+}

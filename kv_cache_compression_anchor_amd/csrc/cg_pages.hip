@@ -519,6 +519,46 @@ __global__ __launch_bounds__(kThreads) void k_reserve_few(Cache c, int n, const 
 }
 
 // ---------------------------------------------------------------------------
+// Slots
+// ---------------------------------------------------------------------------
+// A token a thread; the first n threads also check a request each.  A chain of dependent
+// loads (request, row, length, table), the search of up to 1,024 starts in LDS.
+__global__ __launch_bounds__(kCopyThreads) void k_slots(Cache c, int n, const int32_t* rows, const int32_t* firsts,
+                                                        const int32_t* starts, int n_tokens, int64_t* slots) {
+  __shared__ int32_t few[kFew + 1];
+  const int t = blockIdx.x * kCopyThreads + threadIdx.x;
+  const bool staged = n <= kFew;
+  if (staged) {
+    for (int i = threadIdx.x; i <= n && n > 0; i += kCopyThreads) few[i] = starts[i];
+    __syncthreads();
+  }
+  const int32_t* from = staged ? few : starts;
+  // where request i's tokens begin in its row, or -1 if it is refused
+  auto first_of = [&](int i, int* row) {
+    const int a = from[i], b = from[i + 1], f = firsts ? firsts[i] : 0;
+    *row = rows[i];
+    const bool known = row_ok(c, *row);
+    const int len = c.lens[known ? *row : 0];
+    return known && len_ok(c, len) && a >= 0 && a <= b && b <= n_tokens && f >= 0 && (int64_t)f + (b - a) <= len ? f
+                                                                                                               : -1;
+  };
+  int row;
+  if (t < n && first_of(t, &row) < 0) atomicOr(c.status, kRefused);
+  if (t >= n_tokens) return;
+  int64_t slot = -1;
+  const int j = last_at_most(from, n, t);
+  if (j >= 0 && t < from[j + 1]) {
+    const int f = first_of(j, &row);
+    if (f >= 0) {
+      const int pos = f + (t - from[j]), page = entry(c, row, pos >> c.shift);
+      if (page_ok(c, page)) slot = ((int64_t)page << c.shift) + (pos & (c.P - 1));
+      else atomicOr(c.status, kBadPage);
+    }
+  }
+  slots[t] = slot;
+}
+
+// ---------------------------------------------------------------------------
 // Write
 // ---------------------------------------------------------------------------
 // A workgroup writes `tile` tokens of one (kv, layer): a token's row is `units`
@@ -916,6 +956,23 @@ int cg_pages_reserve_async(const cg_paged_cache* c, int32_t n, const int32_t* ro
     k_reserve<<<1, kThreads, 0, (hipStream_t)stream>>>(view(*c), n, rows_dev, starts_dev, n_tokens,
                                                        slots_dev, ws + w.cum, ws + w.ok, ws + w.list);
   return launched("reserve");
+}
+
+int cg_pages_slots_async(const cg_paged_cache* c, int32_t n, const int32_t* rows_dev,
+                         const int32_t* firsts_dev, const int32_t* starts_dev, int32_t n_tokens,
+                         int64_t* slots_dev, void* stream) {
+  if (int rc = check_paged_cache(c)) return rc;
+  if (n < 0 || n > c->n_rows || n_tokens < 0 || n_tokens > kMaxTokens)
+    return fail(CG_E_INVAL, "n must be in 0..n_rows and n_tokens in 0..2^21");
+  if (n == 0 && n_tokens == 0) return CG_OK;
+  if ((n > 0 && (!rows_dev || !starts_dev)) || (n_tokens > 0 && !slots_dev))
+    return fail(CG_E_INVAL, "NULL list");
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(CG_E_HIP, "cannot select the cache's device");
+  const int threads = std::max(n, n_tokens);
+  k_slots<<<(threads + kCopyThreads - 1) / kCopyThreads, kCopyThreads, 0, (hipStream_t)stream>>>(
+      view(*c), n, rows_dev, firsts_dev, starts_dev, n_tokens, slots_dev);
+  return launched("slots");
 }
 
 int cg_pages_write_async(const cg_paged_cache* c, int32_t layer0, int32_t n_layers,
