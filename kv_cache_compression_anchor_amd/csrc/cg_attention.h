@@ -503,11 +503,15 @@ __device__ __forceinline__ void refuse(const Attn& a, const Item& it) {
   if (it.says && threadIdx.x == 0 && it.q0 < it.q_end) atomicOr(a.status, kRefused);
 }
 
+// How a prefix's and a sequence's own tokens are split.
+__device__ __forceinline__ Split prefix_split(const Attn& a, int hi) { return split_of(0, hi, a.pre_splits); }
+__device__ __forceinline__ Split rest_split(const Attn& a, int lo, int hi) { return split_of(lo, hi, a.rest_splits); }
+
 // For the join: where the sums of a sequence's queries are.
-__device__ __forceinline__ void say_used(const Attn& a, const Item& it) {
+template <class A>
+__device__ __forceinline__ void say_used(const A& a, const Item& it) {
   const bool ok = it.ok && (it.first < 0 || lends(a, row_of(a, it.first), it.pre));
-  const int used = ok ? split_of(0, it.pre, a.pre_splits).used |
-                            split_of(it.pre, it.hi, a.rest_splits).used << 16
+  const int used = ok ? prefix_split(a, it.pre).used | rest_split(a, it.pre, it.hi).used << 16
                       : -1;
   for (int i = begin_of(it.q0, a.n_q) + (int)threadIdx.x; i < end_of(it.q_end, a.n_q); i += blockDim.x) a.used[i] = used;
   if (!ok && threadIdx.x == 0 && it.q0 < it.q_end) atomicOr(a.status, kRefused);

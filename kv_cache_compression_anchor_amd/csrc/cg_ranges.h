@@ -20,15 +20,15 @@ constexpr int begin_of(int start, int n_q) { return start < 0 ? 0 : start < n_q 
 constexpr int end_of(int end, int n_q) { return end < n_q ? end : n_q; }
 
 // Tokens [lo, hi) in tiles that start at multiples of kTile, dealt to `splits`
-// workgroups in turn, at least kLeast each.  Without tokens there may be no splits.
+// workgroups in turn, at least `least` each.  Without tokens there may be no splits.
 struct Split {
   int tile0, tiles, per, used;
 };
-constexpr Split split_of(int lo, int hi, int splits) {
+constexpr Split split_of(int lo, int hi, int splits, int least = kLeast) {
   Split s{lo / kTile, hi > lo ? (hi + kTile - 1) / kTile - lo / kTile : 0, 0, 0};
   if (splits < 1) splits = 1;
   s.per = (s.tiles + splits - 1) / splits;
-  if (s.per < kLeast) s.per = kLeast;
+  if (s.per < least) s.per = least;
   s.used = (s.tiles + s.per - 1) / s.per;
   return s;
 }
