@@ -702,7 +702,7 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   p.pre_splits = 0;
   p.pre_least = kLeast;
   if (x.n_groups)
-    cut((int64_t)x.n_groups * kv * p.pre_tiles, shared ? x.max_prefix : 0, PkRounds * slots, p.pre_splits, p.pre_least);
+    cut((int64_t)x.n_groups * kv * p.pre_tiles, shared ? x.max_prefix : 0, slots, p.pre_splits, p.pre_least);
   // Sharing saves (sequences - 1) times the prefix and costs a second kernel and its
   // start, about 5 us: not for little.
   const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
