@@ -269,8 +269,8 @@ struct Wave {
   // channels in any order that K has too: product ks takes chunk 4 ks + lane / 16 from a
   // lane, or (kSpans) a lane's chunks are neighbours.
   template <bool kSpans = false>
-  __device__ __forceinline__ void load_queries(const Attn& a, const Item& it, int head, int row0) {
-    const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  __device__ __forceinline__ void load_queries(const Attn& a, const Item& it, int head, int row0, int lane = threadIdx.x & 63) {
+    const int n = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int r = 0; r < RT; r++) {
       const int row = row0 + r * 16 + n;
@@ -429,16 +429,46 @@ __device__ __forceinline__ float log2_scale(const Attn& a) {
   return a.scale == 0 ? 1.0f : fabsf(a.scale) * 1.44269504088896341f;
 }
 
+// kv heads of an item of a shared prefix.
+__device__ __forceinline__ constexpr int prefix_heads(const Attn&) { return 1; }
+
+// Sequence s's own tokens (direct: all of them) for the item's row tile, kv heads and split.
+template <class A>
+__device__ __forceinline__ bool rest_item(const A& a, int s, Item& it) {
+  const Seq q = sequence(a, s);
+  it.says = it.head == 0 && it.split == 0 && it.row_tile == 0;
+  it.ok = q.ok;
+  it.pre = q.pre;
+  it.first = q.first;
+  it.q_end = a.q_starts[s + 1];
+  it.lo = q.pre;
+  it.hi = q.len;
+  it.trow = q.row;
+  it.q0 = q.q0;
+  it.splits = a.rest_splits;
+  it.slot0 = a.pre_splits;
+  it.row_tiles = a.rest_tiles;
+  if (a.direct && q.first >= 0) {
+    it.lender = row_of(a, q.first);
+    it.ok = q.ok && lends(a, it.lender, q.pre);
+  }
+  if (!it.ok || q.m == 0) return false;
+  it.rows = q.m * a.G;
+  it.lim0 = q.len - q.m + 1;
+  return true;
+}
+
 // The w-th item of the launch: first (group, split, row tile, kv head), kv heads
 // fastest, for the shared prefixes, then the same per sequence for what lies behind
 // them.  False: nothing to do.
 template <class A>
 __device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
-  const int pre_items = a.pre_groups * a.pre_splits * a.pre_tiles * a.kv;
+  const int pre_items = a.pre_groups * a.pre_splits * a.pre_tiles * (a.kv / prefix_heads(a));
   if (w < pre_items) {
-    it.head = w % a.kv;
-    it.heads = 1;
-    w /= a.kv;
+    const int heads = prefix_heads(a), columns = a.kv / heads;
+    it.head = w % columns * heads;
+    it.heads = heads;
+    w /= columns;
     it.row_tile = w % a.pre_tiles;
     w /= a.pre_tiles;
     it.split = w % a.pre_splits;
@@ -468,27 +498,7 @@ __device__ __forceinline__ bool item_of(const A& a, int w, Item& it) {
   it.row_tile = w % a.rest_tiles;
   w /= a.rest_tiles;
   it.split = w % a.rest_splits;
-  const Seq q = sequence(a, w / a.rest_splits);
-  it.says = it.head == 0 && it.split == 0 && it.row_tile == 0;
-  it.ok = q.ok;
-  it.pre = q.pre;
-  it.first = q.first;
-  it.q_end = a.q_starts[w / a.rest_splits + 1];
-  it.lo = q.pre;
-  it.hi = q.len;
-  it.trow = q.row;
-  it.q0 = q.q0;
-  it.splits = a.rest_splits;
-  it.slot0 = a.pre_splits;
-  it.row_tiles = a.rest_tiles;
-  if (a.direct && q.first >= 0) {
-    it.lender = row_of(a, q.first);
-    it.ok = q.ok && lends(a, it.lender, q.pre);
-  }
-  if (!it.ok || q.m == 0) return false;
-  it.rows = q.m * a.G;
-  it.lim0 = q.len - q.m + 1;
-  return true;
+  return rest_item(a, w / a.rest_splits, it);
 }
 
 // Direct: outputs of a refused sequence's queries, of the item's kv heads.
@@ -503,16 +513,11 @@ __device__ __forceinline__ void refuse(const Attn& a, const Item& it) {
   if (it.says && threadIdx.x == 0 && it.q0 < it.q_end) atomicOr(a.status, kRefused);
 }
 
-// How a prefix's and a sequence's own tokens are split.
-__device__ __forceinline__ Split prefix_split(const Attn& a, int hi) { return split_of(0, hi, a.pre_splits); }
-__device__ __forceinline__ Split rest_split(const Attn& a, int lo, int hi) { return split_of(lo, hi, a.rest_splits); }
-
-// For the join: where the sums of a sequence's queries are.
-template <class A>
-__device__ __forceinline__ void say_used(const A& a, const Item& it) {
+// For the join: where the sums of a sequence's queries are, in `pre` splits of its prefix and
+// `rest` of its own tokens.
+__device__ __forceinline__ void say_used(const Attn& a, const Item& it, int pre, int rest) {
   const bool ok = it.ok && (it.first < 0 || lends(a, row_of(a, it.first), it.pre));
-  const int used = ok ? prefix_split(a, it.pre).used | rest_split(a, it.pre, it.hi).used << 16
-                      : -1;
+  const int used = ok ? pre | rest << 16 : -1;
   for (int i = begin_of(it.q0, a.n_q) + (int)threadIdx.x; i < end_of(it.q_end, a.n_q); i += blockDim.x) a.used[i] = used;
   if (!ok && threadIdx.x == 0 && it.q0 < it.q_end) atomicOr(a.status, kRefused);
 }

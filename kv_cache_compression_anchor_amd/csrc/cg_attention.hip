@@ -619,7 +619,7 @@ __global__ __launch_bounds__(kBlock, resident(DP)) void k_attention(Call<kDirect
     if (a.direct) {
       if (!it.ok) refuse(a, it);
     } else if (it.says) {
-      say_used(a, it);
+      say_used(a, it, split_of(0, it.pre, a.pre_splits).used, split_of(it.pre, it.hi, a.rest_splits).used);
     }
   }
 }

@@ -18,21 +18,22 @@ struct QuantAttn : Attn {
   int head_bytes, groups, scales;  // of a head: codes, scales; where the scales begin
   uint32_t row_bytes, page_bytes;
   int pre_least, rest_least;  // tiles of a split, at least
+  int turn;                   // tiles of a super tile
+  bool direct;                // one item has all of its queries' tokens and writes the outputs
+  // not 0: the tiles of all sequences' own tokens, one sequence's behind the other's, are cut
+  // into so many equal parts for each (row tile, kv heads), a workgroup each
+  int parts;
 };
-__device__ __forceinline__ Split prefix_split(const QuantAttn& a, int hi) {
-  return split_of(0, hi, a.pre_splits, a.pre_least);
-}
-__device__ __forceinline__ Split rest_split(const QuantAttn& a, int lo, int hi) {
-  return split_of(lo, hi, a.rest_splits, a.rest_least);
-}
-template <bool kDirect>
-struct QuantCall : QuantAttn {
-  static constexpr bool direct = kDirect;
+__device__ __forceinline__ int prefix_heads(const QuantAttn& a) { return a.rest_heads; }
+
+// Tiles [from, to) of a stretch of tokens.
+struct Span {
+  int from, to;
 };
-// The tiles of an item's tokens (of one of a direct item's stretches), and its part of them.
-template <class A>
-__device__ __forceinline__ Split split_of(const A& a, const Item& it) {
-  return !a.direct && it.slot0 == 0 && a.pre_splits > 0 ? prefix_split(a, it.hi) : rest_split(a, it.lo, it.hi);
+__device__ __forceinline__ Span span_of(int lo, int hi, int split, int splits, int least) {
+  const Split s = split_of(lo, hi, splits, least);
+  const int from = s.tile0 + split * s.per;
+  return split < s.used ? Span{from, min(from + s.per, s.tile0 + s.tiles)} : Span{0, 0};
 }
 
 // ---------------------------------------------------------------------------
@@ -63,47 +64,30 @@ __device__ __forceinline__ h2 both(uint16_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// Tiles of codes and scales in LDS
+// Super tiles of codes and scales in LDS
 // ---------------------------------------------------------------------------
-// A wave's tile is 32 tokens' rows of K and of V of one head, as they are in memory, brought
-// by loads that no register receives.  n = lane & 15, g = lane >> 4.
-//   K: row r of DP / 2 bytes in 16-byte chunks, chunk c at position c ^ twist(r): a lane reads
-//      channels g DP / 4 .. of tokens n and 16 + n, 16 rows of one chunk each fall into 16
-//      different positions of the 256 bytes of all banks.
-//   V: row r = 4 g + i of a half tile at 4 i + g: a lane reads its channels of tokens
-//      4 g + i, for one i four neighbouring rows.
-//   scales: of each half tile, 16 tokens of K and 16 of V, a window of 8 (DP = 256: 16) bytes
-//      that holds the head's, from the second half on where they begin in the middle of a
-//      word; for DP = 64 one word twice.
-// A lane's channels of V follow from how scales are read: a transposing read gives lane n
-// those of 4 tokens at place n % 4 (DP = 64: n % 2, DP = 256: n % 8) of the window.
+// A workgroup takes `heads` neighbouring kv heads of its tokens: of each token's row of K and
+// of V one stretch of codes and one of scales.  A super tile is `turn` tiles of 32 tokens,
+// brought to LDS as whole stretches by all waves; each wave then computes one head of one of its tiles.
+// (Waves that bring their own heads' parts, 64 and 8 bytes of a row at a time, reach 4.0 TB/s
+// with nothing else to do, 5.3 without the scales: half of what moves between the caches is
+// not asked for.)
+//   In LDS a row is `cpr` 16-byte chunks: the codes, then the scales' stretch from a multiple of
+//   16 bytes on.  A head's chunk c (of DP / 32) of row r of a half tile lies at c ^ twist(r), which
+//   spreads 16 rows of one chunk over the banks.
 template <int DP>
-struct Stage {
-  static constexpr int ROW = DP / 2, CH = ROW / 16;    // bytes and chunks of a row
-  static constexpr int RPL = 64 / CH;                  // rows of a load
-  static constexpr int WIN = DP == 256 ? 16 : 8;       // bytes of a window
-  static constexpr int CODES = 32 * ROW, SCALES = 16 * WIN;
-  static constexpr int BYTES = 2 * CODES + 4 * SCALES;
-  static constexpr int LOADS = 2 * (32 / RPL) + (DP == 256 ? 4 : 2);
+struct Geo4 {
+  static constexpr int kWaves = DP == 256 ? 4 : 8, kThreads = 64 * kWaves;
+  static constexpr int CH = DP / 32;                  // chunks of a head of DP channels
+  static constexpr int kStage = 37 * 1024;            // bytes of a super tile, two of which are in LDS
+  static constexpr int kBlocks = (kStage / 2048 + kWaves - 1) / kWaves;  // loads of a wave of K, at most, and of V
   __device__ __forceinline__ static int twist(int r) { return CH == 2 ? (r >> 3) & 1 : CH == 4 ? (r >> 2) & 3 : (r >> 1) & 7; }
 };
 
-// LDS <- global, 16 or 4 bytes a lane, lane i's at lds + 16 i or 4 i.  The compiler does not
-// count these loads (wait_loads does) and keeps no distances here: a load takes m0 one wait
-// state after its write, and a scalar address five after a write by the vector unit; the copy
-// of the address is that state, and leaves a scalar write, which needs none.
-__device__ __forceinline__ void load_lds16(uint32_t lds, const char* base, uint32_t off) {
-  const char* copy;
-  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
-               : "=&s"(copy)
-               : "s"(lds), "v"(off), "s"(base)
-               : "memory", "m0");
-}
-__device__ __forceinline__ void load_lds16(uint32_t lds, const char* addr) {
+// LDS <- global, 16 bytes a lane, lane i's at lds + 16 i.  The compiler does not count these
+// loads (wait_loads does), and a load takes m0 one wait state after its write.
+__device__ __forceinline__ void load_lds(uint32_t lds, const char* addr) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(addr) : "memory", "m0");
-}
-__device__ __forceinline__ void load_lds4(uint32_t lds, const char* addr) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(addr) : "memory", "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -125,155 +109,163 @@ struct Pages {
   int block0, lo, hi, shift, pmask;
 };
 
-// Where tile t0's tokens are.  Lane i (mod 32) knows token t0 + i: its page (of the nearest
-// token there is, if it does not exist); alive: bits of the tokens that exist.
-struct At {
-  int page;
-  uint32_t alive;
-};
-__device__ __forceinline__ At find(const Pages& p, int t0) {
-  const int t = t0 + (threadIdx.x & 31), c = min(max(t, p.lo), p.hi - 1);
-  const int page = p.list[(c >> p.shift) - p.block0];
-  return {max(page, 0), (uint32_t)__ballot(t == c && page >= 0)};
+// Bits of the tokens of tile t0 that exist.
+__device__ __forceinline__ uint32_t find(const Pages& p, int t0) {
+  const int t = t0 + (rare_lane() & 31), c = min(max(t, p.lo), p.hi - 1);
+  return (uint32_t)__ballot(t == c && p.list[(c >> p.shift) - p.block0] >= 0);
 }
 
-// A lane's part in bringing tiles of one head, and in reading them.
-template <int DP>
-struct Head {
-  using St = Stage<DP>;
-  static constexpr int KPH = 16 / St::RPL ? 16 / St::RPL : 1;  // loads of a half tile
-  const char *k, *v;         // the layer's pools
-  uint32_t koff[KPH], voff;  // of the lane's chunk in a half tile whose rows follow one another
-  const char* sbase;         // pool of the lane's scales, at their place in a row
-  uint32_t soff;             // (for V: DP = 256)
-  int kread, kscale, kstep, vread, vscale;
-  uint32_t bytes;            // DP = 64: where the lane's channels of V are in their word
-  int channel;               // the lane's first channel of V, DP / 16 of them; d or more: none
+// What a workgroup's super tiles are like.
+struct Columns {
+  int heads, first;      // kv heads, the first of them
+  int cpr, codes;        // chunks of a row in LDS, those of codes
+  int window, skew;      // where the scales' stretch begins in a row of the cache, and the first head's in it
+  int turn, vat;         // tiles; where V begins in a stage
+  template <class A>
+  __device__ __forceinline__ Columns(const A& a, int head, int n) : heads(n), first(head) {
+    codes = n * a.head_bytes / 16;
+    const int at = a.scales + 2 * head * a.groups;
+    window = at & ~15;
+    skew = at & 15;
+    cpr = codes + (skew + 2 * n * a.groups + 15) / 16;
+    turn = a.turn;
+    vat = (turn * 512 * cpr + 1023) & ~1023;
+  }
+};
 
-  __device__ __forceinline__ Head(const QuantAttn& a, int head) : k(a.k), v(a.v) {
-    const int lane = rare_lane(), n = lane & 15, g = lane >> 4;
-    const int codes = head * a.head_bytes, last = a.head_bytes / 16 - 1;
-    const int row = lane / St::CH, c = lane % St::CH;
+// A wave's part in bringing super tiles: blocks of 64 chunks, wave, wave + kWaves, .. of K's
+// and the same of V's.  A lane remembers of each its token's number in the super tile (from bit
+// 24) and the chunk's place in the token's half tile, rows of the cache following one another.
+template <int DP>
+struct Loader {
+  using Ge = Geo4<DP>;
+  uint32_t at[Ge::kBlocks];
+  template <class A>
+  __device__ __forceinline__ Loader(const A& a, const Columns& co, int wave) {
+    const int lane = rare_lane();
+    const uint32_t inv = (65535u + co.cpr) / (uint32_t)co.cpr;  // of numbers below 65,536 / cpr, which these are
 #pragma unroll
-    for (int j = 0; j < KPH; j++) {
-      const int r = j * St::RPL + row;
-      koff[j] = (DP == 64 ? row & 15 : r) * a.row_bytes + codes + min(c ^ St::twist(r & 15), last) * 16;
+    for (int j = 0; j < Ge::kBlocks; j++) {
+      const int q = min((wave + j * Ge::kWaves) * 64 + lane, 32 * co.turn * co.cpr - 1);
+      const int row = (int)(q * inv >> 16), c = q - row * co.cpr, r = row & 15;
+      // a head's chunks change places where there are as many as the products take
+      const int chunk = a.head_bytes == Ge::CH * 16 ? c ^ Ge::twist(r) : c;
+      const int col = c < co.codes ? co.first * a.head_bytes + chunk * 16 : co.window + (c - co.codes) * 16;
+      at[j] = (uint32_t)row << 24 | (uint32_t)(r * a.row_bytes + col);
     }
-    const int half = row & 15;
-    voff = (4 * (half & 3) + (half >> 2)) * a.row_bytes + codes + min(c, last) * 16;
-    // scales
-    const int odd = (head * a.groups) & 1, window = a.scales + 2 * (head * a.groups - odd);
-    const int token = DP == 256 ? lane >> 2 : (lane & 31) >> 1, word = DP == 256 ? lane & 3 : DP == 64 ? 0 : lane & 1;
-    soff = min(window + 4 * word, (int)a.row_bytes - 4) + token * a.row_bytes;
-    sbase = DP == 256 || lane < 32 ? a.k : a.v;
-    kread = DP == 64 ? n * 32 + ((g >> 1) ^ St::twist(n)) * 16 + (g & 1) * 8
-                     : n * St::ROW + ((DP == 256 ? 2 * g : g) ^ St::twist(n)) * 16;
-    const int kg = DP == 64 ? g >> 1 : DP == 128 ? g : 2 * g;
-    kscale = n * St::WIN + 2 * (odd + min(kg, a.groups - 1));
-    kstep = kg + 1 < a.groups ? 2 : 0;
-    const int place = DP == 64 ? n & 1 : DP == 128 ? n & 3 : (n >> 2 & 1) * 4 + (n & 3);
-    const int j = DP == 64 ? n >> 1 : DP == 128 ? n >> 2 : n >> 3;  // of the lanes of a group
-    const int group = place - odd;
-    const bool in = group >= 0 && group < a.groups;
-    const int first = (in ? group * 32 : 0) + j * (DP / 16);
-    channel = in ? first : 256;
-    vread = g * St::ROW + first / 8 * 4;
-    bytes = 0x0C040C00u + (first & 4 ? 0x00010001u : 0);
-    vscale = (4 * g + (n >> 2)) * St::WIN + (DP == 256 ? (n & 1) * 8 : 0);
   }
 
-  // Issues the loads of tile t0 to the stage at LDS address `lds`; always St::LOADS of them.
-  __device__ __forceinline__ void load(const QuantAttn& a, const Pages& p, const At& at, int t0, uint32_t lds) const {
-    const uint32_t klds = lds, vlds = lds + St::CODES, slds = lds + 2 * St::CODES;
-    if (p.pmask >= 15) {  // the 16 tokens of a half tile lie in one page
-      uint64_t off[2];
+  // Issues the loads of the super tile at token t0 to the stage at LDS address `lds`.
+  // kNarrow: pages of less than 16 tokens.
+  template <bool kNarrow, class A>
+  __device__ __forceinline__ void load(const A& a, const Columns& co, const Pages& p, int wave, int t0, uint32_t lds) const {
+    auto row_at = [&](int t) {  // where a token's row is in a pool
+      const int page = max(p.list[(min(max(t, p.lo), p.hi - 1) >> p.shift) - p.block0], 0);
+      return (uint64_t)(uint32_t)page * a.page_bytes + (uint64_t)(uint32_t)(t & p.pmask) * a.row_bytes;
+    };
+    // lane i knows half tile i, whose 16 tokens lie in one page
+    const uint64_t base = kNarrow ? 0 : row_at(t0 + 16 * min((int)(threadIdx.x & 63), 2 * co.turn - 1));
+    const int lo = (int)(uint32_t)base, hi = (int)(base >> 32);
+    uint32_t to = lds + wave * 1024;
+    asm volatile("" : "+s"(to));  // computed anew for each block: all of them are more than fits scalar registers
 #pragma unroll
-      for (int h = 0; h < 2; h++)
-        off[h] = (uint64_t)(uint32_t)__builtin_amdgcn_readlane(at.page, 16 * h) * a.page_bytes +
-                 (uint64_t)(uint32_t)((t0 + 16 * h) & p.pmask) * a.row_bytes;
-      if constexpr (DP == 64) {  // a load brings both halves
-        const uint64_t my = (threadIdx.x & 32) ? off[1] : off[0];
-        load_lds16(klds, k + my + koff[0]);
-        load_lds16(vlds, v + my + voff);
+    for (int j = 0; j < Ge::kBlocks; j++) {
+      if (wave + j * Ge::kWaves >= co.vat / 1024) break;
+      uint32_t mine = at[j];
+      asm volatile("" : "+v"(mine));  // nor are parts of it kept
+      uint64_t off = mine & 0xFFFFFFu;
+      if constexpr (kNarrow) {
+        const int tok = mine >> 24;
+        off += row_at(t0 + tok) - (uint64_t)((tok & 15) * a.row_bytes);
       } else {
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int j = 0; j < KPH; j++) {
-            load_lds16(klds + (h * KPH + j) * 1024, k + off[h], koff[j]);
-            load_lds16(vlds + (h * KPH + j) * 1024, v + off[h] + 2 * j * a.row_bytes, voff);
-          }
+        const int half = mine >> 28;
+        off += (uint64_t)(uint32_t)__shfl(hi, half) << 32 | (uint32_t)__shfl(lo, half);
       }
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        load_lds4(slds + h * 2 * St::SCALES, sbase + off[h] + soff);
-        if constexpr (DP == 256) load_lds4(slds + h * 2 * St::SCALES + St::SCALES, v + off[h] + soff);
-      }
-    } else {
-      const int lane = rare_lane();
-      auto row = [&](int tok) {  // where the token's row is, less that of its place in a half tile
-        return (uint64_t)(uint32_t)__shfl(at.page, tok) * a.page_bytes +
-               (uint64_t)(uint32_t)((t0 + tok) & p.pmask) * a.row_bytes - (uint64_t)((tok & 15) * a.row_bytes);
-      };
-      const int r = lane / St::CH;
-#pragma unroll 1
-      for (int i = 0; i < 32 / St::RPL; i++) {
-        const int kt = i * St::RPL + r, half = kt & 15, vt = (kt & 16) + 4 * (half & 3) + (half >> 2);
-        load_lds16(klds + i * 1024, k + row(kt) + (KPH == 2 && (i & 1) ? koff[KPH - 1] : koff[0]));
-        load_lds16(vlds + i * 1024, v + row(vt) + voff + (DP == 256 ? (i & 1) * 2 * a.row_bytes : 0));
-      }
-      const int st = DP == 256 ? lane >> 2 : (lane & 31) >> 1;
-#pragma unroll 1
-      for (int h = 0; h < 2; h++) {
-        const uint64_t off = row(16 * h + st);
-        load_lds4(slds + h * 2 * St::SCALES, sbase + off + soff);
-        if constexpr (DP == 256) load_lds4(slds + h * 2 * St::SCALES + St::SCALES, v + off + soff);
-      }
+      load_lds(to + j * Ge::kWaves * 1024, a.k + off);
+      load_lds(to + j * Ge::kWaves * 1024 + co.vat, a.v + off);
     }
+  }
+};
+
+// Where a lane finds its part of a tile of one head, in bytes from the tile's first row.
+// n = lane & 15, g = lane >> 4.
+//   K: channels g DP / 4 .. of tokens n and 16 + n.
+//   V: of tokens 4 g + i and 16 + 4 g + i the channels of column n of V^T's blocks, DP / 16 neighbours.
+//      Where a head has the groups that the products take, a transposing read gives lane n
+//      the scales of 4 tokens of group n % 4 (DP = 256: n % 8), and its channels are of that
+//      group; elsewhere they are n DP / 16 .., and their scales are read one by one.
+template <int DP>
+struct Head {
+  using Ge = Geo4<DP>;
+  int kread, kscale, kstep, kmore, vread, vflip, vscale;
+  int row;        // bytes of a row
+  uint32_t bytes; // DP = 64: where the lane's channels of V are in their word
+  int channel;    // the lane's first channel of V
+  bool transposed;
+
+  template <class A>
+  __device__ __forceinline__ Head(const A& a, const Columns& co, int head) {
+    const int lane = rare_lane(), n = lane & 15, g = lane >> 4;
+    row = co.cpr * 16;
+    const int codes = head * a.head_bytes, scales = co.codes * 16 + co.skew + 2 * head * a.groups;
+    const bool full = a.head_bytes == Ge::CH * 16;
+    const int last = a.head_bytes / 16 - 1;
+    const int c = DP == 64 ? g >> 1 : DP == 128 ? g : 2 * g;
+    // DP = 256: chunk c + 1 is at c's position ^ 1, or where the head has fewer the last again
+    kread = n * row + codes + (full ? c ^ Ge::twist(n) : min(c, last)) * 16 + (DP == 64 ? (g & 1) * 8 : 0);
+    kstep = DP == 256 ? (full ? (n * row + codes + ((c + 1) ^ Ge::twist(n)) * 16) : n * row + codes + min(c + 1, last) * 16) - kread : 0;
+    kscale = n * row + scales + 2 * min(c, a.groups - 1);  // DP = 64: group g / 2 is chunk g / 2's
+    kmore = c + 1 < a.groups ? 2 : 0;
+    transposed = DP != 64 && full;
+    const int group = DP == 128 ? n & 3 : (n >> 2 & 1) * 4 + (n & 3), j = DP == 128 ? n >> 2 : n >> 3;
+    channel = transposed ? group * 32 + j * (DP / 16) : n * (DP / 16);
+    const int word = min(channel / 8, a.head_bytes / 4 - (DP == 256 ? 2 : 1));  // what lies behind the head is nobody's
+    // rows 4 g + i, i < 4, have one twist, for DP = 256 two
+    const int first = full ? Ge::twist(4 * g) * 16 : 0, second = full ? Ge::twist(4 * g + 2) * 16 : 0;
+    vread = 4 * g * row + codes + ((word * 4) ^ first);
+    vflip = ((word * 4) ^ second) - ((word * 4) ^ first);
+    bytes = 0x0C040C00u + (channel & 4 ? 0x00010001u : 0);
+    vscale = transposed ? (4 * g + (n >> 2)) * row + scales + (DP == 256 ? (n & 1) * 8 : 0)
+                        : 4 * g * row + scales + 2 * min(channel / 32, a.groups - 1);
   }
 };
 
 // Scores of a tile: S^T = K Q^T.
 template <int DP, int RT>
-__device__ __forceinline__ void scores(const Wave<DP, RT>& w, const Head<DP>& hd, const Nibbles& nb, const char* stage,
+__device__ __forceinline__ void scores(const Wave<DP, RT>& w, const Head<DP>& hd, const Nibbles& nb, const char* kt,
                                        f4 (&s)[RT][2]) {
-  using St = Stage<DP>;
   constexpr int KS = DP / 32;
 #pragma unroll
   for (int r = 0; r < RT; r++) s[r][0] = s[r][1] = f4{0, 0, 0, 0};
-  uint32_t k[2][KS];
-  uint16_t ks[2][DP == 256 ? 2 : 1];
 #pragma unroll
   for (int sub = 0; sub < 2; sub++) {
-    const char* at = stage + sub * 16 * St::ROW + hd.kread;
+    uint32_t k[KS];
+    uint16_t ks[DP == 256 ? 2 : 1];
+    const char* at = kt + sub * 16 * hd.row + hd.kread;
     if constexpr (DP == 64) {
       const uint2 x = *(const uint2*)at;
-      k[sub][0] = x.x;
-      k[sub][1] = x.y;
+      k[0] = x.x;
+      k[1] = x.y;
     } else {
 #pragma unroll
       for (int j = 0; j < KS / 4; j++) {
-        // chunk 2 g + 1 of 8 is at chunk 2 g's position ^ 1
-        const u4 x = *(const u4*)(stage + sub * 16 * St::ROW + (hd.kread ^ (j * 16)));
+        const u4 x = *(const u4*)(at + (j ? hd.kstep : 0));
 #pragma unroll
-        for (int e = 0; e < 4; e++) k[sub][4 * j + e] = x[e];
+        for (int e = 0; e < 4; e++) k[4 * j + e] = x[e];
       }
     }
-    const char* sc = stage + 2 * St::CODES + sub * 2 * St::SCALES + hd.kscale;
-    ks[sub][0] = *(const uint16_t*)sc;
-    if constexpr (DP == 256) ks[sub][1] = *(const uint16_t*)(sc + hd.kstep);
-  }
-  // a fence for the scheduler behind each step, which else makes all numbers first and runs out of registers
-  __builtin_amdgcn_sched_barrier(0);
+    const char* sc = kt + sub * 16 * hd.row + hd.kscale;
+    ks[0] = *(const uint16_t*)sc;
+    if constexpr (DP == 256) ks[1] = *(const uint16_t*)(sc + hd.kmore);
+    // fences for the scheduler, which else makes all numbers first and runs out of registers
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < KS; i++) {
-#pragma unroll
-    for (int sub = 0; sub < 2; sub++) {
-      const h8 x = nb.numbers(k[sub][i], both(ks[sub][DP == 256 ? i / 4 : 0]));
+    for (int i = 0; i < KS; i++) {
+      const h8 x = nb.numbers(k[i], both(ks[DP == 256 ? i / 4 : 0]));
 #pragma unroll
       for (int r = 0; r < RT; r++) s[r][sub] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w.q[r][i], s[r][sub], 0, 0, 0);
+      if (i % 2) __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -282,12 +274,12 @@ __device__ __forceinline__ void scores(const Wave<DP, RT>& w, const Head<DP>& hd
 // query.  In the stage, scales of tokens that do not exist become 0, and so do those that are
 // no finite number, and codes whose number is none; returns whether there was such a number:
 // add_odd() gives it to the queries that see it.
-template <int DP>
-__device__ __forceinline__ bool clean_values(const QuantAttn& a, int head, char* stage, uint32_t alive) {
-  using St = Stage<DP>;
-  const int lane = rare_lane(), tok = lane & 31, r = tok & 15, odd = (head * a.groups) & 1;
-  uint16_t* scale = (uint16_t*)(stage + 2 * St::CODES + ((tok >> 4) * 2 + 1) * St::SCALES + r * St::WIN) + odd;
-  uint32_t* codes = (uint32_t*)(stage + St::CODES + ((tok >> 4) * 16 + 4 * (r & 3) + (r >> 2)) * St::ROW);
+template <int DP, class A>
+__device__ __forceinline__ bool clean_values(const A& a, const Columns& co, int head, char* vt, uint32_t alive) {
+  const int lane = rare_lane(), tok = lane & 31;
+  char* row = vt + tok * co.cpr * 16;
+  uint16_t* scale = (uint16_t*)(row + co.codes * 16 + co.skew + 2 * head * a.groups);
+  const int twist = a.head_bytes == Geo4<DP>::CH * 16 ? Geo4<DP>::twist(tok & 15) : 0;
   const bool there = (alive >> tok) & 1;
   bool found = false;
 #pragma unroll 1
@@ -296,17 +288,17 @@ __device__ __forceinline__ bool clean_values(const QuantAttn& a, int head, char*
     if (there && size <= 0x6FFE) continue;  // 8 s is finite
     if (!there || size >= 0x7C00) {
       scale[j] = 0;
-      if (DP == 64) scale[j ^ 2] = 0;  // the window is one word twice
       found |= there;
       continue;
     }
     const float s = half_bits_to_float(bits);
+    uint32_t* codes = (uint32_t*)(row + head * a.head_bytes + (j ^ twist) * 16);
 #pragma unroll 1
     for (int i = 0; i < 32; i++) {
-      const uint32_t w = codes[j * 4 + i / 8];
+      const uint32_t w = codes[i / 8];
       const float x = (float)(_Float16)((float)((int)(w >> 4 * (i % 8) & 15) - 8) * s);
       if (x - x == 0.0f) continue;
-      codes[j * 4 + i / 8] = (w & ~(15u << 4 * (i % 8))) | 8u << 4 * (i % 8);
+      codes[i / 8] = (w & ~(15u << 4 * (i % 8))) | 8u << 4 * (i % 8);
       found = true;
     }
   }
@@ -317,17 +309,16 @@ __device__ __forceinline__ bool clean_values(const QuantAttn& a, int head, char*
 // o += V^T P^T.  Row n of block b of V^T is channel b of the lane's, so that a lane's
 // channels are neighbours in its word; its tokens come together two at a time.
 template <int DP, int RT>
-__device__ __forceinline__ void values(Wave<DP, RT>& w, const Head<DP>& hd, const Nibbles& nb, const char* stage,
+__device__ __forceinline__ void values(Wave<DP, RT>& w, const Head<DP>& hd, const Nibbles& nb, const char* vt,
                                        const h8 (&p)[RT]) {
-  using St = Stage<DP>;
   constexpr int VW = DP == 256 ? 2 : 1, HALVES = DP == 64 ? 1 : 2;  // words of a lane, halves of a word
   uint32_t x[8][VW];
-  union { s4 t[2]; h2 s[4]; } sc;  // scales of tokens 4 g .. + 3, 16 + 4 g .. + 3
+  union { s4 t[2]; h2 s[4]; uint16_t u[8]; } sc;  // scales of tokens 4 g .. + 3, 16 + 4 g .. + 3
 #pragma unroll
   for (int sub = 0; sub < 2; sub++) {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      const char* at = stage + St::CODES + sub * 16 * St::ROW + i * 4 * St::ROW + hd.vread;
+      const char* at = vt + (16 * sub + i) * hd.row + hd.vread + (DP == 256 && i >= 2 ? hd.vflip : 0);
       if constexpr (VW == 2) {
         const uint2 y = *(const uint2*)at;
         x[4 * sub + i][0] = y.x;
@@ -336,28 +327,37 @@ __device__ __forceinline__ void values(Wave<DP, RT>& w, const Head<DP>& hd, cons
         x[4 * sub + i][0] = *(const uint32_t*)at;
       }
     }
-    sc.t[sub] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_s4*)(stage + 2 * St::CODES + (2 * sub + 1) * St::SCALES + hd.vscale));
+  }
+  int transposed = __builtin_amdgcn_readfirstlane(DP != 64 && hd.transposed);
+  asm volatile("" : "+s"(transposed));  // one loop, not one for each case
+  if (transposed) {
+#pragma unroll
+    for (int sub = 0; sub < 2; sub++)
+      sc.t[sub] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(vt + 16 * sub * hd.row + hd.vscale));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      sc.u[i] = *(const uint16_t*)(vt + (16 * (i >> 2) + (i & 3)) * hd.row + hd.vscale);
   }
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int y = 0; y < VW * HALVES; y++) {  // 4 channels: bytes y % 2 and 2 + y % 2 of words y / 2
-    union { uint32_t u[4]; h8 h; } v[4];
+  for (int y = 0; y < 2 * VW * HALVES; y++) {  // 2 channels, of byte y / 2 % 2 or (odd y) 2 + that of words y / 4
+    union { uint32_t u[4]; h8 h; } v[2];
 #pragma unroll
     for (int j = 0; j < 4; j++) {  // tokens 4 g + 2 j, + 1 (j < 2), 16 + 4 g + 2 (j - 2), + 1
-      const uint32_t w0 = x[2 * j][y / HALVES], w1 = x[2 * j + 1][y / HALVES];
-      const uint32_t sel = DP == 64 ? hd.bytes : 0x0C040C00u + (y & 1) * 0x00010001u;
-      const uint32_t even = __builtin_amdgcn_perm(w1, w0, sel), odd = __builtin_amdgcn_perm(w1, w0, sel + 0x00020002u);
-      v[0].u[j] = __builtin_bit_cast(uint32_t, nb.get<false>(even) * sc.s[j]);
-      v[1].u[j] = __builtin_bit_cast(uint32_t, nb.get<false>(odd) * sc.s[j]);
-      v[2].u[j] = __builtin_bit_cast(uint32_t, nb.get<true>(even) * sc.s[j]);
-      v[3].u[j] = __builtin_bit_cast(uint32_t, nb.get<true>(odd) * sc.s[j]);
+      const uint32_t w0 = x[2 * j][y / 2 / HALVES], w1 = x[2 * j + 1][y / 2 / HALVES];
+      const uint32_t sel = (DP == 64 ? hd.bytes : 0x0C040C00u + (y / 2 & 1) * 0x00010001u) + (y & 1) * 0x00020002u;
+      const uint32_t both = __builtin_amdgcn_perm(w1, w0, sel);
+      v[0].u[j] = __builtin_bit_cast(uint32_t, nb.get<false>(both) * sc.s[j]);
+      v[1].u[j] = __builtin_bit_cast(uint32_t, nb.get<true>(both) * sc.s[j]);
     }
 #pragma unroll
-    for (int b = 0; b < 4; b++)
+    for (int b = 0; b < 2; b++) {
+      const int block = y / 2 * 4 + 2 * b + (y & 1);
 #pragma unroll
       for (int r = 0; r < RT; r++)
-        w.o[r][y * 4 + b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[b].h, p[r], w.o[r][y * 4 + b], 0, 0, 0);
+        w.o[r][block] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[b].h, p[r], w.o[r][block], 0, 0, 0);
+    }
     __builtin_amdgcn_sched_barrier(0);
   }
 }
@@ -384,17 +384,17 @@ __device__ __forceinline__ void mask_scores(const QuantAttn& a, const Item& it, 
 // One workgroup: a tile of rows against a split of the tokens
 // ---------------------------------------------------------------------------
 constexpr int kList = 512;  // table entries staged at a time
-constexpr int kStages = 2;
 template <int DP>
 struct QuantShared {
-  static constexpr int kWaves = kBlock / 64;
-  __attribute__((aligned(1024))) char stage[kWaves][kStages][Stage<DP>::BYTES];  // then the sums of the waves
+  static constexpr int kWaves = Geo4<DP>::kWaves;
+  __attribute__((aligned(1024))) char stage[2][Geo4<DP>::kStage];  // then the sums of the waves
   int32_t list[kList];
   float m[kWaves][32], l[kWaves][32], scale[kWaves][32];
-  uint32_t odd;  // values() found something
+  uint32_t odd;  // clean_values() found something
   uint32_t bad;  // a page met so far is outside the pool
+  int sums[kWaves], most[kWaves];
 };
-static_assert(sizeof(QuantShared<128>) <= 160 * 1024 / 4, "four workgroups a compute unit");
+static_assert(sizeof(QuantShared<128>) <= 160 * 1024 / 2, "two workgroups a compute unit");
 
 // Half of channel ch of kv head `head` in the row at p.
 __device__ __forceinline__ float number_at(const QuantAttn& a, const char* p, int head, int ch) {
@@ -408,24 +408,23 @@ __device__ __forceinline__ float number_at(const QuantAttn& a, const char* p, in
 // see it (a sum with such a number is an infinity or none whatever the weight, and stays
 // so where the number was counted already).  Rare, and slow.  empty(head, row): of a
 // direct item, whether nothing weighed anything for a row.
-template <class A, class F>
-__device__ __forceinline__ void add_odd(const A& a, const Item& it, int ranges, int row0, int row1, F empty) {
+template <int kThreads, class A, class F>
+__device__ __forceinline__ void add_odd(const A& a, const Item& it, const Span& span, int ranges, int row0, int row1,
+                                        F empty) {
   const int tid = rare_thread();
   row1 = min(row1, it.rows);
 #pragma unroll 1
   for (int range = 0; range < ranges; range++) {
     const Item cur = range_of(it, ranges, range);
-    const Split sp = split_of(a, cur);
-    if (cur.split >= sp.used) continue;
-    const int first = sp.tile0 + cur.split * sp.per, last = min(first + sp.per, sp.tile0 + sp.tiles);
-    const int end = min(min(last * kTile, cur.hi), row_lim(a, cur, row1 - 1));
+    const Span sp = a.direct ? span_of(cur.lo, cur.hi, 0, 1, 1) : span;
+    const int end = min(min(sp.to * kTile, cur.hi), row_lim(a, cur, row1 - 1));
 #pragma unroll 1
-    for (int t = max(first * kTile, cur.lo); t < end; t++) {
+    for (int t = max(sp.from * kTile, cur.lo); t < end; t++) {
       const int page = a.tables[(int64_t)cur.trow * a.B + (t >> a.shift)];
       if (page < 0 || page >= a.N) continue;
       const char* v = a.v + (uint64_t)(uint32_t)page * a.page_bytes + (uint64_t)(uint32_t)(t & (a.P - 1)) * a.row_bytes;
 #pragma unroll 1
-      for (int i = tid; i < it.heads * a.d; i += kBlock) {
+      for (int i = tid; i < it.heads * a.d; i += kThreads) {
         const int head = it.head + i / a.d, ch = i % a.d;
         const float x = number_at(a, v, head, ch);
         if (x - x == 0.0f) continue;
@@ -445,48 +444,46 @@ __device__ __forceinline__ void add_odd(const A& a, const Item& it, int ranges, 
   }
 }
 
-// Every wave holds all 16 RT of a row tile of its kv head.  The waves of a head (all, or
-// half of them, or one, as the item has one, two or four heads) take the split's token
-// tiles in turn and share nothing until the end; a wave's next tile is on its way to
-// registers while it computes one.
-template <int DP, int RT, class A>
-__device__ __forceinline__ void run_few(const A& a, const Item& it, QuantShared<DP>& sh) {
-  constexpr int kWaves = kBlock / 64;
+// A wave holds all 16 RT rows of a row tile of its kv head and takes every turn-th tile of
+// them; the waves share nothing but the super tiles until the end.  The next super tile is on its
+// way while one is computed.
+template <int DP, int RT, bool kNarrow>
+__device__ __forceinline__ void run_few(const QuantAttn& a, const Item& it, const Span& span, QuantShared<DP>& sh) {
   using W = Wave<DP, RT>;
+  constexpr int kWaves = Geo4<DP>::kWaves, kThreads = Geo4<DP>::kThreads;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ranges = ranges_of(a, it);
-  const int turn = kWaves / it.heads;  // waves of a head
-  const int head = it.head + wave / turn;
+  const Columns co(a, it.head, it.heads);
+  const int mine = wave / it.heads, hh = wave % it.heads;  // the wave's tile of a super tile, and its head
+  const bool busy = mine < co.turn;
   const float c = log2_scale(a);
   const int row_tiles = (it.rows + 16 * RT - 1) / (16 * RT);
   const int list_tiles = (int)((int64_t)(kList - 1) * a.P / kTile) - 1;
-  {
-    const Split sp = split_of(a, it);
-    if (!a.direct && it.split >= sp.used) return;
-  }
-  const uint32_t lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char*)sh.stage[wave][0]);
+  if (!a.direct && span.from >= span.to) return;
+  const uint32_t lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char*)sh.stage[0]);
 
+#pragma unroll 1
   for (int rt = it.row_tile; rt < row_tiles; rt += it.row_tiles) {
-    const Head<DP> hd(a, head);
+    const Loader<DP> ld(a, co, wave);
+    const Head<DP> hd(a, co, hh);
     const Nibbles nb;
     W w;
     w.clear();
-    w.template load_queries<true>(a, it, head, rt * 16 * RT);
+    w.template load_queries<true>(a, it, it.head + hh, rt * 16 * RT, rare_lane());
     if (threadIdx.x == 0) sh.odd = sh.bad = 0;
 #pragma unroll 1
     for (int range = 0; range < ranges; range++) {
       const Item cur = range_of(it, ranges, range);
-      const Split sp = split_of(a, cur);
-      if (cur.split >= sp.used) continue;
-      const int first = sp.tile0 + cur.split * sp.per, last = min(first + sp.per, sp.tile0 + sp.tiles);
+      const Span sp = a.direct ? span_of(cur.lo, cur.hi, 0, 1, 1) : span;
       const int min_lim = row_lim(a, cur, rt * 16 * RT);
       // tiles behind this one nobody of these rows sees
-      const int end = min(last, (row_lim(a, cur, (rt + 1) * 16 * RT - 1) + kTile - 1) / kTile);
-      for (int base = first; base < end; base += list_tiles) {
+      const int end = min(sp.to, (row_lim(a, cur, (rt + 1) * 16 * RT - 1) + kTile - 1) / kTile);
+#pragma unroll 1
+      for (int base = sp.from; base < end; base += list_tiles) {
         const int stop = min(base + list_tiles, end);
         const int b0 = max(base * kTile, cur.lo) >> a.shift, b1 = (min(stop * kTile, cur.hi) - 1) >> a.shift;
-        __syncthreads();  // the list is free
-        for (int i = rare_thread(); i <= b1 - b0; i += kBlock) {
+        __syncthreads();  // the list and the stages are free
+        for (int i = rare_thread(); i <= b1 - b0; i += kThreads) {
           const int page = a.tables[(int64_t)cur.trow * a.B + b0 + i];
           const bool ok = page >= 0 && page < a.N;
           sh.list[i] = ok ? page : -1;
@@ -494,140 +491,287 @@ __device__ __forceinline__ void run_few(const A& a, const Item& it, QuantShared<
         }
         __syncthreads();
         // tokens that exist for this stretch lie in its blocks
+        const bool bad = __builtin_amdgcn_readfirstlane(sh.bad) != 0;
         const Pages pages{sh.list, b0, max(base * kTile, cur.lo), min(stop * kTile, cur.hi), a.shift, a.P - 1};
-        At at{0, 0}, next_at{0, 0};
-        int tile = base + wave % turn, slot = 0;
-        if (tile < stop) {
-          at = find(pages, tile * kTile);
-          hd.load(a, pages, at, tile * kTile, lds);
-        }
-        for (; tile < stop; tile += turn, slot ^= 1, at = next_at) {
-          const int next = tile + turn;
-          if (next < stop) {
-            next_at = find(pages, next * kTile);
-            wait_lds();  // the stage that is filled now has been read
-            hd.load(a, pages, next_at, next * kTile, lds + (slot ^ 1) * Stage<DP>::BYTES);
-            wait_loads<Stage<DP>::LOADS>();
-          } else {
-            wait_loads<0>();
+        const int limit = busy ? stop : 0, whole_lo = bad ? 0x7FFFFFFF : pages.lo;
+        int slot = 0;
+        ld.template load<kNarrow>(a, co, pages, wave, base * kTile, lds);
+        // The queries are here before the loop: the compiler would wait for them in each step, and
+        // with them for all loads under way.
+#pragma unroll
+        for (int r = 0; r < RT; r++)
+#pragma unroll
+          for (int ks = 0; ks < W::KS; ks++) asm volatile("" : "+v"(w.q[r][ks]));
+#pragma unroll 1
+        for (int at = base; at < stop; at += co.turn, slot ^= 1) {
+          wait_loads<0>();
+          wait_lds();
+          __builtin_amdgcn_s_barrier();  // the super tile is there, and the other stage has been read
+          asm volatile("" ::: "memory");
+          if (at + co.turn < stop)
+            ld.template load<kNarrow>(a, co, pages, wave, (at + co.turn) * kTile, lds + (slot ^ 1) * Geo4<DP>::kStage);
+          const int tile = at + mine;
+          if (tile < limit) {
+            const char* kt = sh.stage[slot] + mine * 512 * co.cpr;
+            char* vt = sh.stage[slot] + co.vat + mine * 512 * co.cpr;
+            const bool whole = tile * kTile >= whole_lo && (tile + 1) * kTile <= pages.hi;
+            const uint32_t alive = whole ? 0xFFFFFFFFu : find(pages, tile * kTile);
+            f4 s[RT][2];
+            h8 p[RT];
+            float mx[RT];
+            scores(w, hd, nb, kt, s);
+            const bool all = alive == 0xFFFFFFFFu && (tile + 1) * kTile <= min_lim;
+            if (!all) mask_scores<DP, RT>(a, cur, rt * 16 * RT, s, tile * kTile, alive);
+            const bool raise = w.peaks(s, c, mx);
+            w.reference(raise, mx, c);
+            w.weights(s, c, p);
+            if (!all && clean_values<DP>(a, co, hh, vt, alive)) sh.odd = 1;
+            values(w, hd, nb, vt, p);
           }
-          char* stage = sh.stage[wave][slot];
-          f4 s[RT][2];
-          h8 p[RT];
-          float mx[RT];
-          scores(w, hd, nb, stage, s);
-          const bool all = at.alive == 0xFFFFFFFFu && (tile + 1) * kTile <= min_lim;
-          if (!all) mask_scores<DP, RT>(a, cur, rt * 16 * RT, s, tile * kTile, at.alive);
-          const bool raise = w.peaks(s, c, mx);
-          w.reference(raise, mx, c);
-          w.weights(s, c, p);
-          if (!all && clean_values<DP>(a, head, stage, at.alive)) sh.odd = 1;
-          values(w, hd, nb, stage, p);
+          asm volatile("" ::: "memory");  // one end of the loop's body, not two loops
+        }
+      }
+    }
+    const int tid = rare_thread(), n = tid & 15, g = (tid & 63) >> 4;
+    __syncthreads();  // the stages are free, and bad is known
+    if (sh.bad && tid == 0) atomicOr(a.status, kBadPage);
+    const int row0 = rt * 16 * RT, rows = min(it.rows - row0, 16 * RT);
+    // A lane has row n of 16, and of each row 4 g + i of a block of results the channel of lane 4 g + i.
+    auto quad_of = [&](int r, int b, int i) {
+      return r == 0 ? f4{w.o[0][b][i], w.o[0][b + 1][i], w.o[0][b + 2][i], w.o[0][b + 3][i]}
+                    : f4{w.o[RT - 1][b][i], w.o[RT - 1][b + 1][i], w.o[RT - 1][b + 2][i], w.o[RT - 1][b + 3][i]};
+    };
+    auto store = [&](int h, int row, int ch, f4 x) {
+      if (a.direct) store_out(out_at(a, it, it.head + h, row0 + row) + ch, quotient_of(x, sh.m[h][row]));
+      else *(f4*)(a.part + part_at(a, it, it.head + h, row0 + row) * a.d + ch) = x;
+    };
+    auto store_sums = [&](int h, int row, float m, float l) {
+      if (a.direct) {
+        sh.m[h][row] = l == 0.0f ? 0.0f : 1.0f / l;
+        if (row < rows && a.lse) *lse_at(a, it, it.head + h, row0 + row) = lse_of(m, l);
+      } else if (row < rows) {
+        const int64_t at = part_at(a, it, it.head + h, row0 + row);
+        *(float2*)(a.ml + 2 * at) = float2{m, l};
+      }
+    };
+    if (co.turn == 1) {  // a wave has all of its head's sums
+      if (busy) {
+#pragma unroll
+        for (int r = 0; r < RT; r++) {
+          const float l = w.sum(r);
+          if (g == 0) store_sums(hh, r * 16 + n, w.m[r], l);
         }
         wait_lds();
-      }
-    }
-    // the waves' sums together, against the largest reference exponent
-    const int tid = rare_thread(), n = tid & 15, g = (tid & 63) >> 4;
+#pragma unroll 1
+        for (int r = 0; r < RT; r++)
 #pragma unroll
-    for (int r = 0; r < RT; r++) {
-      const float l = w.sum(r);
-      if (g == 0) {
-        sh.m[wave][r * 16 + n] = w.m[r];
-        sh.l[wave][r * 16 + n] = l;
-      }
-    }
-    __syncthreads();
-    if (sh.bad && tid == 0) atomicOr(a.status, kBadPage);
-    if (tid < 16 * RT * it.heads) {
-      const int x = tid % (16 * RT), hh = tid / (16 * RT), w0 = hh * turn;
-      float m = -__builtin_inff(), l = 0.0f;
+          for (int i = 0; i < 4; i++) {
+            const int ch = __shfl(hd.channel, 4 * g + i);
 #pragma unroll
-      for (int y = 0; y < kWaves; y++) {
-        const float my = sh.m[(w0 + y) % kWaves][x];
-        m = y < turn ? fmaxf(m, my) : m;
+            for (int b = 0; b < W::NB; b += 4)
+              if (r * 16 + n < rows && ch + b < a.d) store(hh, r * 16 + n, ch + b, quad_of(r, b, i));
+          }
       }
+    } else {
+      // the waves' sums together, against the largest reference exponent
 #pragma unroll
-      for (int y = 0; y < kWaves; y++) {
-        // a wave without a reference has weighed nothing, or only what is no number
-        const float my = sh.m[(w0 + y) % kWaves][x], ly = sh.l[(w0 + y) % kWaves][x];
-        const float f = my == m ? 1.0f : my == -__builtin_inff() && ly != 0.0f
-                            ? 1.0f : __builtin_amdgcn_exp2f(my - m);
-        if (y < turn) {
-          sh.scale[w0 + y][x] = f;
+      for (int r = 0; r < RT; r++) {
+        const float l = w.sum(r);
+        if (g == 0) {
+          sh.m[wave][r * 16 + n] = w.m[r];
+          sh.l[wave][r * 16 + n] = l;
+        }
+      }
+      __syncthreads();
+      const int waves = it.heads * co.turn;  // wave h + heads y has tile y of head h
+      if (tid < 16 * RT * it.heads) {
+        const int x = tid % (16 * RT), h = tid / (16 * RT);
+        float m = -__builtin_inff(), l = 0.0f;
+        for (int y = h; y < waves; y += it.heads) m = fmaxf(m, sh.m[y][x]);
+        for (int y = h; y < waves; y += it.heads) {
+          // a wave without a reference has weighed nothing, or only what is no number
+          const float my = sh.m[y][x], ly = sh.l[y][x];
+          const float f = my == m ? 1.0f : my == -__builtin_inff() && ly != 0.0f
+                              ? 1.0f : __builtin_amdgcn_exp2f(my - m);
+          sh.scale[y][x] = f;
           l += f * ly;
         }
+        store_sums(h, x, m, l);
       }
-      const int row = rt * 16 * RT + x;
-      if (a.direct) {
-        sh.m[w0][x] = l == 0.0f ? 0.0f : 1.0f / l;
-        if (row < it.rows && a.lse) *lse_at(a, it, it.head + hh, row) = lse_of(m, l);
-      } else if (row < it.rows) {
-        const int64_t at = part_at(a, it, it.head + hh, row);
-        a.ml[2 * at] = m;
-        a.ml[2 * at + 1] = l;
-      }
-    }
-    // 4-channel quads of a row, rotated by row; the lane's channels are neighbours, of each row 4 g + i of
-    // the products' results one, whose lane says which
-    constexpr int kQuads = DP / 4;
-    static_assert(sizeof(sh.stage) >= (size_t)kWaves * 16 * kQuads * 16, "room for the sums");
-    f4* sums = (f4*)sh.stage;
+      constexpr int kQuads = DP / 4;  // of a row, rotated by row
+      static_assert(sizeof(sh.stage) >= (size_t)kWaves * 16 * kQuads * 16, "room for the sums");
+      f4* sums = (f4*)sh.stage;
 #pragma unroll 1
-    for (int r = 0; r < RT; r++) {
-      __syncthreads();
+      for (int r = 0; r * 16 < rows; r++) {
+        __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int ch = __shfl(hd.channel, 4 * g + i);
+        for (int i = 0; i < 4; i++) {
+          const int ch = __shfl(hd.channel, 4 * g + i);
 #pragma unroll
-        for (int b = 0; b < W::NB; b += 4) {
-          f4 x = r == 0 ? f4{w.o[0][b][i], w.o[0][b + 1][i], w.o[0][b + 2][i], w.o[0][b + 3][i]}
-                        : f4{w.o[RT - 1][b][i], w.o[RT - 1][b + 1][i], w.o[RT - 1][b + 2][i], w.o[RT - 1][b + 3][i]};
-          if (ch < a.d) sums[(wave * 16 + n) * kQuads + (((ch + b) / 4 + n) & (kQuads - 1))] = x;
+          for (int b = 0; b < W::NB; b += 4)
+            if (r * 16 + n < rows) sums[(wave * 16 + n) * kQuads + (((ch + b) / 4 + n) & (kQuads - 1))] = quad_of(r, b, i);
         }
-      }
-      __syncthreads();
+        __syncthreads();
+        const int here = min(rows - r * 16, 16);
 #pragma unroll 1
-      for (int i = tid; i < it.heads * 16 * kQuads; i += kBlock) {
-        const int quad = i % kQuads, x = i / kQuads % 16, hh = i / (16 * kQuads), w0 = hh * turn;
-        const int ch = quad * 4, row = r * 16 + x, gr = rt * 16 * RT + row;
-        if (gr >= it.rows || ch >= a.d) continue;
-        f4 sum{0, 0, 0, 0};
-#pragma unroll
-        for (int y = 0; y < kWaves; y++) {
-          const int of = (w0 + y) % kWaves;
-          const float f = sh.scale[of][row];
-          const f4 part = sums[(of * 16 + x) * kQuads + ((quad + x) & (kQuads - 1))];
-          if (y < turn) sum += f * part;
+        for (int i = tid; i < it.heads * here * kQuads; i += kThreads) {
+          const int quad = i % kQuads, x = i / kQuads % here, h = i / (here * kQuads), row = r * 16 + x;
+          if (quad * 4 >= a.d) continue;
+          f4 sum{0, 0, 0, 0};
+          for (int y = h; y < waves; y += it.heads)
+            sum += sh.scale[y][row] * sums[(y * 16 + x) * kQuads + ((quad + x) & (kQuads - 1))];
+          store(h, row, quad * 4, sum);
         }
-        if (a.direct) store_out(out_at(a, it, it.head + hh, gr) + ch, quotient_of(sum, sh.m[w0][row]));
-        else *(f4*)(a.part + part_at(a, it, it.head + hh, gr) * a.d + ch) = sum;
       }
     }
     __syncthreads();
     if (sh.odd)
-      add_odd(a, it, ranges, rt * 16 * RT, (rt + 1) * 16 * RT,
-              [&](int h, int row) { return sh.m[(h - it.head) * turn][row - rt * 16 * RT] == 0.0f; });
+      add_odd<kThreads>(a, it, span, ranges, row0, row0 + 16 * RT,
+                        [&](int h, int row) { return sh.m[h - it.head][row - row0] == 0.0f; });
     __syncthreads();  // m, l, scale and the sums are free
   }
 }
 
 // Workgroups on a compute unit, as LDS and registers allow.
-__host__ __device__ constexpr int resident4(int dp, int rt) { return dp == 256 || (dp == 128 && rt == 2) ? 2 : rt == 2 ? 3 : 4; }
+__host__ __device__ constexpr int resident4(int dp, int rt) { return dp == 128 && rt == 2 ? 1 : 2; }
 
-template <int DP, int RT, bool kDirect>
-__global__ __launch_bounds__(kBlock, resident4(DP, RT)) void k_quant_attention(QuantCall<kDirect> a, int first, int end) {
+// Tiles of sequence s's own tokens, 0 without queries.
+__device__ __forceinline__ int tiles_of(const QuantAttn& a, int s) {
+  const int row = row_of(a, s);
+  const bool in = row >= 0 && row < a.R;
+  const int len = a.lens[in ? row : 0], m = queries_of(a.q_starts[s], a.q_starts[s + 1], a.n_q);
+  int pre = 0;
+  if (a.n_groups) {  // the last group that begins at or before s
+    int lo = -1, hi = a.n_groups;
+    while (hi - lo > 1) {
+      const int at = (lo + hi) >> 1;
+      if (a.group_starts[at] <= s) lo = at; else hi = at;
+    }
+    if (lo >= 0 && s < a.group_starts[lo + 1]) pre = max(a.prefix_lens[lo], 0);
+  }
+  return in && m > 0 && len_ok(a, len) && len > pre ? (len + kTile - 1) / kTile - pre / kTile : 0;
+}
+
+// The tiles of each sequence's own tokens, added up: at[s] before sequence s, at[n_seqs] in all.  Returns
+// how many are a part: as equal as they come, no sequence in more than rest_splits of them.
+// (Cut into splits of one length the last of them run when most are done, and the chip's
+// dispatcher does not fill all slots evenly: 64 sequences of 1,000 to 9,216 tokens
+// took 123 to 136 us.)
+constexpr int kMostListed = 4096;  // sequences
+__device__ __forceinline__ int add_up(const QuantAttn& a, int* at, int* sums, int* most) {
+  const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x / 64;
+  const int mine = (a.n_seqs + blockDim.x - 1) / blockDim.x, s0 = min(tid * mine, a.n_seqs), s1 = min(s0 + mine, a.n_seqs);
+  int sum = 0, top = 0;
+#pragma unroll 1
+  for (int s = s0; s < s1; s++) {
+    const int n = tiles_of(a, s);
+    at[s] = sum;
+    sum += n;
+    top = max(top, n);
+  }
+  int before = sum;
+#pragma unroll
+  for (int i = 1; i < 64; i <<= 1) {
+    const int x = __shfl_up(before, i);
+    top = max(top, __shfl_xor(top, i));
+    if (lane >= i) before += x;
+  }
+  if (lane == 63) {
+    sums[tid >> 6] = before;
+    most[tid >> 6] = top;
+  }
+  __syncthreads();
+  before -= sum;
+  int all = 0;
+  top = 0;
+#pragma unroll 1
+  for (int w = 0; w < waves; w++) {
+    if (w < tid >> 6) before += sums[w];
+    all += sums[w];
+    top = max(top, most[w]);
+  }
+#pragma unroll 1
+  for (int s = s0; s < s1; s++) at[s] += before;
+  if (tid == 0) at[a.n_seqs] = all;
+  __syncthreads();
+  all = __builtin_amdgcn_readfirstlane(all);
+  top = __builtin_amdgcn_readfirstlane(top);
+  return max(max((int)(((uint32_t)all + a.parts - 1) / (uint32_t)a.parts),
+                 (int)(((uint32_t)top + a.rest_splits - 2) / (uint32_t)(a.rest_splits - 1))), a.rest_least);
+}
+
+// What a workgroup computes next: items of the launch, or its part of the sequences' own tokens,
+// for one row tile of theirs and its kv heads.
+struct Work {
+  int part, per, base, pos, end;  // tiles, of the sequences' behind one another: base where sequence s begins
+  int s, w;                       // the next sequence, or item
+  bool parts;
+};
+
+template <int DP, int RT, bool kNarrow>
+__global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(DP, RT) * Geo4<DP>::kWaves / 4) void k_quant_attention(
+    QuantAttn a, int first, int end) {
   __shared__ QuantShared<DP> sh;
-  // Neighbouring items, the kv heads of the same tokens, run on one of the 8 XCDs, to which
-  // workgroups are dealt in turn: they share cache lines.
-  const int b = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
-  for (int w = first + b; w < end; w += gridDim.x) {
-    Item it;
-    if (item_of(a, w, it)) run_few<DP, RT>(a, it, sh);
+  const int columns = a.kv / a.rest_heads, pre_items = a.pre_groups * a.pre_splits * a.pre_tiles * columns;
+  Item it;
+  Work wk{0, 1, 0, 0, 0, 0, first + (int)blockIdx.x, a.parts && first + (int)blockIdx.x >= pre_items};
+  if (wk.parts) {
+    static_assert(sizeof(sh.stage) >= (kMostListed + 1) * 4, "room for the sums of tiles");
+    int* at = (int*)sh.stage;
+    wk.per = add_up(a, at, sh.sums, sh.most);
+    uint32_t w = wk.w - pre_items;
+    it.heads = a.rest_heads;
+    it.head = w % columns * a.rest_heads;
+    w /= columns;
+    it.row_tile = w % a.rest_tiles;
+    wk.part = w / a.rest_tiles;
+    const int all = __builtin_amdgcn_readfirstlane(at[a.n_seqs]);
+    wk.pos = (int)min((int64_t)wk.part * wk.per, (int64_t)all);
+    wk.end = min(wk.pos + wk.per, all);
+    if (it.head == 0 && it.row_tile == 0)  // sequences without tiles of their own have no other workgroup
+#pragma unroll 1
+      for (int s = wk.part; s < a.n_seqs; s += a.parts) {
+        if (__builtin_amdgcn_readfirstlane(at[s + 1] - at[s]) != 0) continue;
+        it.split = 0;
+        rest_item(a, s, it);
+        say_used(a, it, split_of(0, it.pre, a.pre_splits, a.pre_least).used, 0);
+      }
+    int s = -1;  // the last sequence that begins at or before the part
+    for (int hi = a.n_seqs; hi - s > 1;) {
+      const int m = (s + hi) >> 1;
+      if (__builtin_amdgcn_readfirstlane(at[m]) <= wk.pos) s = m; else hi = m;
+    }
+    wk.s = s;
+    wk.base = __builtin_amdgcn_readfirstlane(at[s]);  // the stages take the place of the sums from here
+  }
+#pragma unroll 1
+  while (wk.parts ? wk.pos < wk.end : wk.w < end) {
+    Span span{0, 0};
+    bool go;
+    int own = -1;  // splits of the sequence's own tokens
+    if (wk.parts) {
+      const int s = wk.s++, tiles = tiles_of(a, s);
+      if (tiles == 0) continue;
+      const int at = (uint32_t)wk.base / (uint32_t)wk.per;
+      const int from = wk.pos - wk.base, n = min(tiles - from, wk.end - wk.pos);
+      it.split = wk.part - at;
+      go = rest_item(a, s, it);
+      own = (int)((uint32_t)(wk.base + tiles - 1) / (uint32_t)wk.per) - at + 1;
+      if (go) span = Span{it.lo / kTile + from, it.lo / kTile + from + n};
+      wk.pos += n;
+      wk.base += tiles;
+    } else {
+      go = item_of(a, wk.w, it);
+      if (go) span = wk.w < pre_items ? span_of(0, it.hi, it.split, a.pre_splits, a.pre_least)
+                                      : span_of(it.lo, it.hi, it.split, a.rest_splits, a.rest_least);
+      wk.w += gridDim.x;
+    }
+    if (go) run_few<DP, RT, kNarrow>(a, it, span, sh);
     if (a.direct) {
       if (!it.ok) refuse(a, it);
     } else if (it.says) {
-      say_used(a, it);
+      say_used(a, it, split_of(0, it.pre, a.pre_splits, a.pre_least).used,
+               own < 0 ? split_of(it.pre, it.hi, a.rest_splits, a.rest_least).used : own);
     }
   }
 }
@@ -638,26 +782,26 @@ __global__ __launch_bounds__(kBlock, resident4(DP, RT)) void k_quant_attention(Q
 // How many splits and row tiles the launch has, from the call's numbers alone.
 struct Plan {
   int dp, pre_splits, rest_splits, pre_least, rest_least, pre_tiles, rest_tiles, pre_mode, rest_mode, pre_groups,
-      rest_heads;
+      rest_heads, turn, parts;
   bool direct;
   size_t words;
 };
 
 template <int DP>
-void launch(bool direct, int mode, const QuantAttn& a, int64_t first, int64_t end, hipStream_t st) {
+void launch(int mode, const QuantAttn& a, int64_t first, int64_t end, hipStream_t st) {
   if (end <= first) return;
-  const int grid = (int)std::min<int64_t>((end - first + 7) / 8 * 8, 1 << 22);  // a multiple of 8
-#define GO(MODE, DIRECT)                                                                             \
-  if (direct == DIRECT && mode == MODE)                                                              \
-    k_quant_attention<DP, 1 + MODE, DIRECT><<<grid, kBlock, 0, st>>>({a}, (int)first, (int)end);
+  const int grid = (int)std::min<int64_t>(end - first, 1 << 22);
+#define GO(MODE, NARROW)                                                                             \
+  if (mode == MODE && (a.P < 16) == NARROW)                                                          \
+    k_quant_attention<DP, 1 + MODE, NARROW><<<grid, Geo4<DP>::kThreads, 0, st>>>(a, (int)first, (int)end);
   GO(kRows16, false) GO(kRows16, true)
   if constexpr (DP <= 128) { GO(kRows32, false) GO(kRows32, true) }
 #undef GO
 }
-void launch(int dp, bool direct, int mode, const QuantAttn& a, int64_t first, int64_t end, hipStream_t st) {
-  if (dp == 64) launch<64>(direct, mode, a, first, end, st);
-  else if (dp == 128) launch<128>(direct, mode, a, first, end, st);
-  else launch<256>(direct, mode, a, first, end, st);
+void launch(int dp, int mode, const QuantAttn& a, int64_t first, int64_t end, hipStream_t st) {
+  if (dp == 64) launch<64>(mode, a, first, end, st);
+  else if (dp == 128) launch<128>(mode, a, first, end, st);
+  else launch<256>(mode, a, first, end, st);
 }
 
 int mode_of(int64_t rows, int dp) { return rows <= 16 || dp == 256 ? kRows16 : kRows32; }
@@ -680,40 +824,61 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   p.pre_mode = mode_of(pre_rows, p.dp);
   const int pre_tile = rows_of(p.pre_mode);
   p.pre_tiles = (int)std::min(most((int64_t)x.n_groups * kv), (pre_rows + pre_tile - 1) / pre_tile);
-  // Tiles of a split: so many that the launch, were all rows of the greatest length, is `slots`
-  // workgroups, and at most kMostSplits splits, whose sums the join reads.
-  constexpr int kMostSplits = 64, kRounds = 2;
-  auto cut = [&](int64_t items, int64_t tokens, int64_t slots, int& splits, int& least) {
-    const int64_t tiles = (tokens + kTile - 1) / kTile;
-    int64_t per = (items * tiles + slots - 1) / slots;
-    per = std::max<int64_t>({per, (tiles + kMostSplits - 1) / kMostSplits, kLeast});
-    splits = (int)std::max<int64_t>(1, (tiles + per - 1) / per);
-    least = (int)std::min<int64_t>(per, 1 << 26);
-  };
-  auto heads = [&]() {
-    int n = 1;
-    while (n < 4 && kv % (2 * n) == 0) n *= 2;
-    return n;
-  };
-  p.rest_heads = heads();
-  const int64_t slots = 256 * resident4(p.dp, p.rest_mode + 1);
+  // kv heads of a workgroup: as many neighbours as it has waves, so that it reads whole
+  // stretches of rows; and tiles of a super tile: as many as waves are left for, and as LDS holds.
+  const int waves = p.dp == 256 ? 4 : 8;
   const int64_t own = std::max(0, x.max_len - (shared ? x.max_prefix : 0));
-  cut((int64_t)std::max(1, x.n_seqs) * kv / p.rest_heads * p.rest_tiles, own, kRounds * slots, p.rest_splits, p.rest_least);
+  const int64_t slots = 256 * resident4(p.dp, p.rest_mode + 1);
+  // Where there are not two rounds of super tiles one head a workgroup, whose waves share the
+  // tokens: fewer splits to join.
+  p.rest_heads = (int64_t)x.n_seqs * p.rest_tiles * kv * ((own + kTile - 1) / kTile) < 2 * waves * slots ? 1 : waves;
+  while (kv % p.rest_heads) p.rest_heads--;
+  const QuantRow row = quant_row(f);
+  int cpr = 0;  // as the kernel has it, at most
+  for (int head = 0; head < kv && head < 8 * p.rest_heads; head += p.rest_heads)
+    cpr = std::max(cpr, p.rest_heads * row.head / 16 +
+                            ((row.scales + 2 * head * row.groups) % 16 + 2 * p.rest_heads * row.groups + 15) / 16);
+  p.turn = waves / p.rest_heads;
+  while ((p.turn * 512 * cpr + 1023) / 1024 * 1024 > 37 * 1024 / 2) p.turn--;
+  // Tiles of a split, at least `least`: so many that the items, were all of the greatest length,
+  // are `slots` workgroups, and at most kMostSplits splits, whose sums the join reads.
+  constexpr int kMostSplits = 64;
+  const int least = std::max(p.turn, kLeast);
+  auto cut = [&](int64_t items, int64_t tokens, int64_t slots, int& splits, int& per) {
+    const int64_t tiles = (tokens + kTile - 1) / kTile;
+    const int64_t n = std::max<int64_t>({(items * tiles + slots - 1) / slots, (tiles + kMostSplits - 1) / kMostSplits, least});
+    splits = (int)std::max<int64_t>(1, (tiles + n - 1) / n);
+    per = (int)std::min<int64_t>(n, 1 << 25);
+  };
+  const int64_t columns = (int64_t)p.rest_tiles * (kv / p.rest_heads), items = std::max(1, x.n_seqs) * columns;
+  cut(items, own, slots, p.rest_splits, p.rest_least);
+  p.parts = 0;
   p.pre_splits = 0;
   p.pre_least = kLeast;
   if (x.n_groups)
-    cut((int64_t)x.n_groups * kv * p.pre_tiles, shared ? x.max_prefix : 0, slots, p.pre_splits, p.pre_least);
+    cut((int64_t)x.n_groups * kv / p.rest_heads * p.pre_tiles, shared ? x.max_prefix : 0,
+        256 * resident4(p.dp, p.pre_mode + 1), p.pre_splits, p.pre_least);
+  // the sums of tiles fit 31 bits
+  const bool listed = x.n_seqs <= kMostListed && (int64_t)x.n_seqs * c.max_blocks * c.page_tokens < (int64_t)1 << 35;
+  if (p.rest_splits > 1 && x.n_seqs > 1 && listed) {
+    // lengths that differ: equal parts of all of them, on the slots that the prefixes leave
+    const int64_t pre = (int64_t)p.pre_splits * x.n_groups * kv / p.rest_heads * p.pre_tiles;
+    p.parts = (int)std::max<int64_t>(1, std::max(slots - pre, slots / 2) / columns);
+    p.rest_least = p.turn;
+    p.rest_splits = (int)std::max<int64_t>(2, std::min<int64_t>(130, 2 + 4 * ((p.parts + x.n_seqs - 1) / x.n_seqs)));
+  }
   // Sharing saves (sequences - 1) times the prefix and costs a second kernel and its
   // start, about 5 us: not for little.
   const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
   int all = 1, some = 1;
-  cut((int64_t)std::max(1, x.n_seqs) * kv / p.rest_heads * p.rest_tiles, x.max_len, kRounds * slots, all, some);
+  cut(items, x.max_len, slots, all, some);
   p.direct = saved <= (int64_t)16 << 20 && x.max_prefix <= 512 && all == 1;
   if (p.direct) {
     p.pre_groups = 0;
     p.pre_splits = 0;
     p.rest_splits = 1;
     p.rest_least = 1;
+    p.parts = 0;
     p.words = 4;
     return p;
   }
@@ -747,7 +912,7 @@ int cg_quant_attention_async(const cg_paged_cache* c, const cg_quant_form* f, co
   const Plan p = plan_of(*c, *f, *a);
   const QuantRow r = quant_row(*f);
   QuantAttn v{view(*c, *a, f->channels), r.head, r.groups, r.scales, (uint32_t)r.row,
-              (uint32_t)r.row * (uint32_t)c->page_tokens, p.pre_least, p.rest_least};
+              (uint32_t)r.row * (uint32_t)c->page_tokens, p.pre_least, p.rest_least, p.turn, p.direct, p.parts};
   const int64_t layer = (int64_t)a->layer * c->num_pages * v.page_bytes;
   v.k = (const char*)c->k_pool_dev + layer;
   v.v = (const char*)c->v_pool_dev + layer;
@@ -760,14 +925,14 @@ int cg_quant_attention_async(const cg_paged_cache* c, const cg_quant_form* f, co
   v.part = (float*)workspace_dev;
   v.ml = v.part + (size_t)(p.pre_splits + p.rest_splits) * a->n_q * a->n_heads * a->head_dim;
   v.used = (int32_t*)(v.ml + (size_t)2 * (p.pre_splits + p.rest_splits) * a->n_q * a->n_heads);
-  const int64_t pre = (int64_t)p.pre_groups * p.pre_splits * p.pre_tiles * v.kv;
-  const int64_t rest = (int64_t)a->n_seqs * p.rest_splits * p.rest_tiles * (v.kv / p.rest_heads);
+  const int64_t pre = (int64_t)p.pre_groups * p.pre_splits * p.pre_tiles * (v.kv / p.rest_heads);
+  const int64_t rest = (int64_t)(p.parts ? p.parts : a->n_seqs * (int64_t)p.rest_splits) * p.rest_tiles * (v.kv / p.rest_heads);
   hipStream_t st = (hipStream_t)stream;
   if (p.pre_mode == p.rest_mode || !pre) {
-    launch(p.dp, p.direct, p.rest_mode, v, 0, pre + rest, st);
+    launch(p.dp, p.rest_mode, v, 0, pre + rest, st);
   } else {
-    launch(p.dp, false, p.pre_mode, v, 0, pre, st);
-    launch(p.dp, false, p.rest_mode, v, pre, pre + rest, st);
+    launch(p.dp, p.pre_mode, v, 0, pre, st);
+    launch(p.dp, p.rest_mode, v, pre, pre + rest, st);
   }
   if (!p.direct) {
     const int total = p.pre_splits + p.rest_splits;
