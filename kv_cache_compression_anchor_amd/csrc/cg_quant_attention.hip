@@ -460,10 +460,19 @@ __device__ __forceinline__ void run_few(const QuantAttn& a, const Item& it, cons
   const int row_tiles = (it.rows + 16 * RT - 1) / (16 * RT);
   const int list_tiles = (int)((int64_t)(kList - 1) * a.P / kTile) - 1;
   if (!a.direct && span.from >= span.to) return;
+  const Span whole_span = a.direct ? span_of(it.lo, it.hi, 0, 1, 1) : span;
+  const int span_from = whole_span.from, span_end = whole_span.to;
   const uint32_t lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char*)sh.stage[0]);
 
 #pragma unroll 1
   for (int rt = it.row_tile; rt < row_tiles; rt += it.row_tiles) {
+    // the first stretch's pages are on their way while what needs none of them is worked out
+    int early = 0, early_base = -1;
+    if (ranges == 1 && span_end > span_from) {
+      early_base = span_from;
+      const int b0 = max(span_from * kTile, it.lo) >> a.shift, b1 = (min(span_end * kTile, it.hi) - 1) >> a.shift;
+      early = a.tables[(int64_t)it.trow * a.B + min(b0 + (int)threadIdx.x, b1)];
+    }
     const Loader<DP> ld(a, co, wave);
     const Head<DP> hd(a, co, hh);
     const Nibbles nb;
@@ -484,7 +493,7 @@ __device__ __forceinline__ void run_few(const QuantAttn& a, const Item& it, cons
         const int b0 = max(base * kTile, cur.lo) >> a.shift, b1 = (min(stop * kTile, cur.hi) - 1) >> a.shift;
         __syncthreads();  // the list and the stages are free
         for (int i = rare_thread(); i <= b1 - b0; i += kThreads) {
-          const int page = a.tables[(int64_t)cur.trow * a.B + b0 + i];
+          const int page = early_base == base && i < kThreads ? early : a.tables[(int64_t)cur.trow * a.B + b0 + i];
           const bool ok = page >= 0 && page < a.N;
           sh.list[i] = ok ? page : -1;
           if (!ok) sh.bad = 1;
@@ -781,7 +790,7 @@ __global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(DP, RT) * Geo4<DP>::k
 // ---------------------------------------------------------------------------
 // How many splits and row tiles the launch has, from the call's numbers alone.
 struct Plan {
-  int dp, pre_splits, rest_splits, pre_least, rest_least, pre_tiles, rest_tiles, pre_mode, rest_mode, pre_groups,
+  int dp, pre_splits, rest_splits, pre_least, rest_least, pre_tiles, rest_tiles, pre_mode, rest_mode, mode, pre_groups,
       rest_heads, turn, parts;
   bool direct;
   size_t words;
@@ -815,72 +824,79 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   auto most = [&](int64_t items) { return std::max<int64_t>(1, (1 << 22) / std::max<int64_t>(1, items)); };
   const int64_t rows = (int64_t)std::max(1, std::min(x.max_q, x.n_q)) * G;
   p.rest_mode = mode_of(rows, p.dp);
-  const int rest_rows = rows_of(p.rest_mode);
-  p.rest_tiles = (int)std::min(most((int64_t)x.n_seqs * kv), (rows + rest_rows - 1) / rest_rows);
   const bool shared = x.n_groups > 0 && x.max_prefix > 0;
   p.pre_groups = x.n_groups;
   // rows of an average group
   const int64_t pre_rows = std::max<int64_t>(1, x.n_groups ? (x.n_q + x.n_groups - 1) / x.n_groups : 1) * G;
   p.pre_mode = mode_of(pre_rows, p.dp);
-  const int pre_tile = rows_of(p.pre_mode);
-  p.pre_tiles = (int)std::min(most((int64_t)x.n_groups * kv), (pre_rows + pre_tile - 1) / pre_tile);
-  // kv heads of a workgroup: as many neighbours as it has waves, so that it reads whole
-  // stretches of rows; and tiles of a super tile: as many as waves are left for, and as LDS holds.
-  const int waves = p.dp == 256 ? 4 : 8;
+  // Prefixes and the rest are one launch, of the larger number of rows: two, one after the other,
+  // leave the chip half empty (64 requests on 9,216 shared and up to 600 own tokens: 40 + 38 us).
+  p.mode = shared ? std::max(p.pre_mode, p.rest_mode) : p.rest_mode;
+  p.rest_tiles = (int)std::min(most((int64_t)x.n_seqs * kv), (rows + rows_of(p.mode) - 1) / rows_of(p.mode));
+  p.pre_tiles = (int)std::min(most((int64_t)x.n_groups * kv), (pre_rows + rows_of(p.mode) - 1) / rows_of(p.mode));
+  const int64_t slots = 256 * resident4(p.dp, p.mode + 1);
   const int64_t own = std::max(0, x.max_len - (shared ? x.max_prefix : 0));
-  const int64_t slots = 256 * resident4(p.dp, p.rest_mode + 1);
-  // Where there are not two rounds of super tiles one head a workgroup, whose waves share the
-  // tokens: fewer splits to join.
-  p.rest_heads = (int64_t)x.n_seqs * p.rest_tiles * kv * ((own + kTile - 1) / kTile) < 2 * waves * slots ? 1 : waves;
-  while (kv % p.rest_heads) p.rest_heads--;
+  auto tiles_in = [](int64_t tokens) { return (tokens + kTile - 1) / kTile; };
+  // kv heads of a workgroup, and tiles of a super tile: as many as waves are left for, and as LDS holds.
+  const int waves = p.dp == 256 ? 4 : 8;
   const QuantRow row = quant_row(f);
-  int cpr = 0;  // as the kernel has it, at most
-  for (int head = 0; head < kv && head < 8 * p.rest_heads; head += p.rest_heads)
-    cpr = std::max(cpr, p.rest_heads * row.head / 16 +
-                            ((row.scales + 2 * head * row.groups) % 16 + 2 * p.rest_heads * row.groups + 15) / 16);
-  p.turn = waves / p.rest_heads;
-  while ((p.turn * 512 * cpr + 1023) / 1024 * 1024 > 37 * 1024 / 2) p.turn--;
-  // Tiles of a split, at least `least`: so many that the items, were all of the greatest length,
-  // are `slots` workgroups, and at most kMostSplits splits, whose sums the join reads.
-  constexpr int kMostSplits = 64;
-  const int least = std::max(p.turn, kLeast);
-  auto cut = [&](int64_t items, int64_t tokens, int64_t slots, int& splits, int& per) {
-    const int64_t tiles = (tokens + kTile - 1) / kTile;
-    const int64_t n = std::max<int64_t>({(items * tiles + slots - 1) / slots, (tiles + kMostSplits - 1) / kMostSplits, least});
-    splits = (int)std::max<int64_t>(1, (tiles + n - 1) / n);
-    per = (int)std::min<int64_t>(n, 1 << 25);
+  auto heads = [&](int n) {
+    while (kv % n) n--;
+    int cpr = 0;  // as the kernel has it, at most
+    for (int head = 0; head < kv && head < 8 * n; head += n)
+      cpr = std::max(cpr, n * row.head / 16 + ((row.scales + 2 * head * row.groups) % 16 + 2 * n * row.groups + 15) / 16);
+    p.rest_heads = n;
+    p.turn = waves / n;
+    while ((p.turn * 512 * cpr + 1023) / 1024 * 1024 > 37 * 1024 / 2) p.turn--;
   };
-  const int64_t columns = (int64_t)p.rest_tiles * (kv / p.rest_heads), items = std::max(1, x.n_seqs) * columns;
-  cut(items, own, slots, p.rest_splits, p.rest_least);
-  p.parts = 0;
-  p.pre_splits = 0;
-  p.pre_least = kLeast;
-  if (x.n_groups)
-    cut((int64_t)x.n_groups * kv / p.rest_heads * p.pre_tiles, shared ? x.max_prefix : 0,
-        256 * resident4(p.dp, p.pre_mode + 1), p.pre_splits, p.pre_least);
-  // the sums of tiles fit 31 bits
-  const bool listed = x.n_seqs <= kMostListed && (int64_t)x.n_seqs * c.max_blocks * c.page_tokens < (int64_t)1 << 35;
-  if (p.rest_splits > 1 && x.n_seqs > 1 && listed) {
-    // lengths that differ: equal parts of all of them, on the slots that the prefixes leave
-    const int64_t pre = (int64_t)p.pre_splits * x.n_groups * kv / p.rest_heads * p.pre_tiles;
-    p.parts = (int)std::max<int64_t>(1, std::max(slots - pre, slots / 2) / columns);
-    p.rest_least = p.turn;
-    p.rest_splits = (int)std::max<int64_t>(2, std::min<int64_t>(130, 2 + 4 * ((p.parts + x.n_seqs - 1) / x.n_seqs)));
-  }
-  // Sharing saves (sequences - 1) times the prefix and costs a second kernel and its
-  // start, about 5 us: not for little.
+  // Few tokens: one head a workgroup, whose waves share the tokens, in one kernel that writes the
+  // outputs itself, without a join (5 us and the start of a kernel).  Sharing prefixes saves
+  // (sequences - 1) times their reading: not for little.
+  constexpr int kSteps = 6;  // super tiles that a workgroup takes rather than have sums joined
   const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
-  int all = 1, some = 1;
-  cut(items, x.max_len, slots, all, some);
-  p.direct = saved <= (int64_t)16 << 20 && x.max_prefix <= 512 && all == 1;
+  heads(1);
+  p.direct = saved <= (int64_t)16 << 20 && tiles_in(x.max_len) <= kSteps * p.turn &&
+             (int64_t)x.n_seqs * p.rest_tiles * kv * tiles_in(x.max_len) <= 4 * waves * slots;
   if (p.direct) {
+    p.mode = p.rest_mode;
+    p.rest_tiles = (int)std::min(most((int64_t)x.n_seqs * kv), (rows + rows_of(p.mode) - 1) / rows_of(p.mode));
     p.pre_groups = 0;
     p.pre_splits = 0;
+    p.pre_least = p.rest_least = 1;
     p.rest_splits = 1;
-    p.rest_least = 1;
     p.parts = 0;
     p.words = 4;
     return p;
+  }
+  // Otherwise as many neighbours as there are waves, so that whole stretches of rows are read.
+  heads(waves);
+  // Tiles of a split, at least `least`: so many that the items, were all of the greatest length,
+  // are `slots` workgroups, and at most kMostSplits splits, whose sums the join reads.  A
+  // workgroup's start and end take as long as kWorth super tiles.
+  constexpr int kMostSplits = 64, kWorth = 8;
+  auto cut = [&](int64_t items, int64_t tiles, int64_t slots, int least, int& splits, int& per) {
+    const int64_t n = std::max<int64_t>({(items * tiles + slots - 1) / std::max<int64_t>(1, slots),
+                                         (tiles + kMostSplits - 1) / kMostSplits, least});
+    splits = (int)std::max<int64_t>(1, (tiles + n - 1) / n);
+    per = (int)std::min<int64_t>(n, 1 << 25);
+  };
+  const int64_t columns = kv / p.rest_heads, items = std::max(1, x.n_seqs) * p.rest_tiles * columns;
+  const int64_t pre_items = (int64_t)x.n_groups * columns * p.pre_tiles;
+  // prefixes and the rest get slots by their work; lengths are mostly below the greatest
+  const int64_t pre_work = shared ? pre_items * tiles_in(x.max_prefix) : 0, work = items * tiles_in(own) / 2;
+  const int64_t pre_slots = pre_work ? std::min(std::max(slots * pre_work / (pre_work + work), slots / 8), slots * 7 / 8) : 0;
+  p.pre_splits = 0;
+  p.pre_least = kLeast;
+  if (x.n_groups) cut(pre_items, shared ? tiles_in(x.max_prefix) : 0, pre_slots, kLeast, p.pre_splits, p.pre_least);
+  cut(items, tiles_in(own), slots - pre_slots, kWorth * p.turn, p.rest_splits, p.rest_least);
+  p.parts = 0;
+  // the sums of tiles fit 31 bits
+  const bool listed = x.n_seqs <= kMostListed && (int64_t)x.n_seqs * c.max_blocks * c.page_tokens < (int64_t)1 << 35;
+  if (x.n_seqs > 1 && listed && work >= kWorth * p.turn * (slots - pre_slots)) {
+    // lengths that differ: equal parts of all of them
+    p.parts = (int)std::max<int64_t>(1, (slots - pre_slots) / (columns * p.rest_tiles));
+    p.rest_least = p.turn;
+    p.rest_splits = (int)std::max<int64_t>(2, std::min<int64_t>(130, 2 + 4 * ((p.parts + x.n_seqs - 1) / x.n_seqs)));
   }
   p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + x.n_q + 4;
   return p;
@@ -928,12 +944,7 @@ int cg_quant_attention_async(const cg_paged_cache* c, const cg_quant_form* f, co
   const int64_t pre = (int64_t)p.pre_groups * p.pre_splits * p.pre_tiles * (v.kv / p.rest_heads);
   const int64_t rest = (int64_t)(p.parts ? p.parts : a->n_seqs * (int64_t)p.rest_splits) * p.rest_tiles * (v.kv / p.rest_heads);
   hipStream_t st = (hipStream_t)stream;
-  if (p.pre_mode == p.rest_mode || !pre) {
-    launch(p.dp, p.rest_mode, v, 0, pre + rest, st);
-  } else {
-    launch(p.dp, p.pre_mode, v, 0, pre, st);
-    launch(p.dp, p.rest_mode, v, pre, pre + rest, st);
-  }
+  launch(p.dp, p.mode, v, 0, pre + rest, st);
   if (!p.direct) {
     const int total = p.pre_splits + p.rest_splits;
     v.join = std::min(total <= 2 ? 1 : total <= 8 ? 2 : 8, kThreads / (v.d / 4));
