@@ -107,6 +107,11 @@ __device__ __forceinline__ int rare_thread() {
 struct Pages {
   const int32_t* list;  // pages of blocks block0 .., -1 outside the pool
   int block0, lo, hi, shift, pmask;
+  // Where token t's row is in a pool; of a token that does not exist some row.
+  __device__ __forceinline__ uint64_t row_at(int t, uint32_t page_bytes, uint32_t row_bytes) const {
+    const int page = max(list[(min(max(t, lo), hi - 1) >> shift) - block0], 0);
+    return (uint64_t)(uint32_t)page * page_bytes + (uint64_t)(uint32_t)(t & pmask) * row_bytes;
+  }
 };
 
 // Bits of the tokens of tile t0 that exist.
@@ -135,7 +140,7 @@ struct Columns {
 
 // A wave's part in bringing super tiles: blocks of 64 chunks, wave, wave + kWaves, .. of K's
 // and the same of V's.  A lane remembers of each its token's number in the super tile (from bit
-// 24) and the chunk's place in the token's half tile, rows of the cache following one another.
+// 24) and the chunk's place in the token's row.
 template <int DP>
 struct Loader {
   using Ge = Geo4<DP>;
@@ -151,21 +156,13 @@ struct Loader {
       // a head's chunks change places where there are as many as the products take
       const int chunk = a.head_bytes == Ge::CH * 16 ? c ^ Ge::twist(r) : c;
       const int col = c < co.codes ? co.first * a.head_bytes + chunk * 16 : co.window + (c - co.codes) * 16;
-      at[j] = (uint32_t)row << 24 | (uint32_t)(r * a.row_bytes + col);
+      at[j] = (uint32_t)row << 24 | (uint32_t)col;
     }
   }
 
   // Issues the loads of the super tile at token t0 to the stage at LDS address `lds`.
-  // kNarrow: pages of less than 16 tokens.
-  template <bool kNarrow, class A>
+  template <class A>
   __device__ __forceinline__ void load(const A& a, const Columns& co, const Pages& p, int wave, int t0, uint32_t lds) const {
-    auto row_at = [&](int t) {  // where a token's row is in a pool
-      const int page = max(p.list[(min(max(t, p.lo), p.hi - 1) >> p.shift) - p.block0], 0);
-      return (uint64_t)(uint32_t)page * a.page_bytes + (uint64_t)(uint32_t)(t & p.pmask) * a.row_bytes;
-    };
-    // lane i knows half tile i, whose 16 tokens lie in one page
-    const uint64_t base = kNarrow ? 0 : row_at(t0 + 16 * min((int)(threadIdx.x & 63), 2 * co.turn - 1));
-    const int lo = (int)(uint32_t)base, hi = (int)(base >> 32);
     uint32_t to = lds + wave * 1024;
     asm volatile("" : "+s"(to));  // computed anew for each block: all of them are more than fits scalar registers
 #pragma unroll
@@ -173,14 +170,7 @@ struct Loader {
       if (wave + j * Ge::kWaves >= co.vat / 1024) break;
       uint32_t mine = at[j];
       asm volatile("" : "+v"(mine));  // nor are parts of it kept
-      uint64_t off = mine & 0xFFFFFFu;
-      if constexpr (kNarrow) {
-        const int tok = mine >> 24;
-        off += row_at(t0 + tok) - (uint64_t)((tok & 15) * a.row_bytes);
-      } else {
-        const int half = mine >> 28;
-        off += (uint64_t)(uint32_t)__shfl(hi, half) << 32 | (uint32_t)__shfl(lo, half);
-      }
+      const uint64_t off = p.row_at(t0 + (int)(mine >> 24), a.page_bytes, a.row_bytes) + (mine & 0xFFFFFFu);
       load_lds(to + j * Ge::kWaves * 1024, a.k + off);
       load_lds(to + j * Ge::kWaves * 1024 + co.vat, a.v + off);
     }
@@ -447,7 +437,7 @@ __device__ __forceinline__ void add_odd(const A& a, const Item& it, const Span& 
 // A wave holds all 16 RT rows of a row tile of its kv head and takes every turn-th tile of
 // them; the waves share nothing but the super tiles until the end.  The next super tile is on its
 // way while one is computed.
-template <int DP, int RT, bool kNarrow>
+template <int DP, int RT>
 __device__ __forceinline__ void run_few(const QuantAttn& a, const Item& it, const Span& span, QuantShared<DP>& sh) {
   using W = Wave<DP, RT>;
   constexpr int kWaves = Geo4<DP>::kWaves, kThreads = Geo4<DP>::kThreads;
@@ -504,7 +494,7 @@ __device__ __forceinline__ void run_few(const QuantAttn& a, const Item& it, cons
         const Pages pages{sh.list, b0, max(base * kTile, cur.lo), min(stop * kTile, cur.hi), a.shift, a.P - 1};
         const int limit = busy ? stop : 0, whole_lo = bad ? 0x7FFFFFFF : pages.lo;
         int slot = 0;
-        ld.template load<kNarrow>(a, co, pages, wave, base * kTile, lds);
+        ld.load(a, co, pages, wave, base * kTile, lds);
         // The queries are here before the loop: the compiler would wait for them in each step, and
         // with them for all loads under way.
 #pragma unroll
@@ -518,7 +508,7 @@ __device__ __forceinline__ void run_few(const QuantAttn& a, const Item& it, cons
           __builtin_amdgcn_s_barrier();  // the super tile is there, and the other stage has been read
           asm volatile("" ::: "memory");
           if (at + co.turn < stop)
-            ld.template load<kNarrow>(a, co, pages, wave, (at + co.turn) * kTile, lds + (slot ^ 1) * Geo4<DP>::kStage);
+            ld.load(a, co, pages, wave, (at + co.turn) * kTile, lds + (slot ^ 1) * Geo4<DP>::kStage);
           const int tile = at + mine;
           if (tile < limit) {
             const char* kt = sh.stage[slot] + mine * 512 * co.cpr;
@@ -717,7 +707,7 @@ struct Work {
   bool parts;
 };
 
-template <int DP, int RT, bool kNarrow>
+template <int DP, int RT>
 __global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(DP, RT) * Geo4<DP>::kWaves / 4) void k_quant_attention(
     QuantAttn a, int first, int end) {
   __shared__ QuantShared<DP> sh;
@@ -775,7 +765,7 @@ __global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(DP, RT) * Geo4<DP>::k
                                       : span_of(it.lo, it.hi, it.split, a.rest_splits, a.rest_least);
       wk.w += gridDim.x;
     }
-    if (go) run_few<DP, RT, kNarrow>(a, it, span, sh);
+    if (go) run_few<DP, RT>(a, it, span, sh);
     if (a.direct) {
       if (!it.ok) refuse(a, it);
     } else if (it.says) {
@@ -800,11 +790,10 @@ template <int DP>
 void launch(int mode, const QuantAttn& a, int64_t first, int64_t end, hipStream_t st) {
   if (end <= first) return;
   const int grid = (int)std::min<int64_t>(end - first, 1 << 22);
-#define GO(MODE, NARROW)                                                                             \
-  if (mode == MODE && (a.P < 16) == NARROW)                                                          \
-    k_quant_attention<DP, 1 + MODE, NARROW><<<grid, Geo4<DP>::kThreads, 0, st>>>(a, (int)first, (int)end);
-  GO(kRows16, false) GO(kRows16, true)
-  if constexpr (DP <= 128) { GO(kRows32, false) GO(kRows32, true) }
+#define GO(MODE) \
+  if (mode == MODE) k_quant_attention<DP, 1 + MODE><<<grid, Geo4<DP>::kThreads, 0, st>>>(a, (int)first, (int)end);
+  GO(kRows16)
+  if constexpr (DP <= 128) { GO(kRows32) }
 #undef GO
 }
 void launch(int dp, int mode, const QuantAttn& a, int64_t first, int64_t end, hipStream_t st) {
@@ -856,7 +845,7 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
   heads(1);
   p.direct = saved <= (int64_t)16 << 20 && tiles_in(x.max_len) <= kSteps * p.turn &&
-             (int64_t)x.n_seqs * p.rest_tiles * kv * tiles_in(x.max_len) <= 4 * waves * slots;
+             (int64_t)x.n_seqs * p.rest_tiles * kv * tiles_in(x.max_len) <= waves * slots;
   if (p.direct) {
     p.mode = p.rest_mode;
     p.rest_tiles = (int)std::min(most((int64_t)x.n_seqs * kv), (rows + rows_of(p.mode) - 1) / rows_of(p.mode));
@@ -873,7 +862,7 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   // Tiles of a split, at least `least`: so many that the items, were all of the greatest length,
   // are `slots` workgroups, and at most kMostSplits splits, whose sums the join reads.  A
   // workgroup's start and end take as long as kWorth super tiles.
-  constexpr int kMostSplits = 64, kWorth = 8;
+  constexpr int kMostSplits = 256, kWorth = 8;
   auto cut = [&](int64_t items, int64_t tiles, int64_t slots, int least, int& splits, int& per) {
     const int64_t n = std::max<int64_t>({(items * tiles + slots - 1) / std::max<int64_t>(1, slots),
                                          (tiles + kMostSplits - 1) / kMostSplits, least});
@@ -888,7 +877,8 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   p.pre_splits = 0;
   p.pre_least = kLeast;
   if (x.n_groups) cut(pre_items, shared ? tiles_in(x.max_prefix) : 0, pre_slots, kLeast, p.pre_splits, p.pre_least);
-  cut(items, tiles_in(own), slots - pre_slots, kWorth * p.turn, p.rest_splits, p.rest_least);
+  const int least = (int)std::min<int64_t>(kWorth, std::max<int64_t>(kLeast, items * tiles_in(own) / 256)) * p.turn;
+  cut(items, tiles_in(own), slots - pre_slots, least, p.rest_splits, p.rest_least);
   p.parts = 0;
   // the sums of tiles fit 31 bits
   const bool listed = x.n_seqs <= kMostListed && (int64_t)x.n_seqs * c.max_blocks * c.page_tokens < (int64_t)1 << 35;
@@ -896,7 +886,7 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
     // lengths that differ: equal parts of all of them
     p.parts = (int)std::max<int64_t>(1, (slots - pre_slots) / (columns * p.rest_tiles));
     p.rest_least = p.turn;
-    p.rest_splits = (int)std::max<int64_t>(2, std::min<int64_t>(130, 2 + 4 * ((p.parts + x.n_seqs - 1) / x.n_seqs)));
+    p.rest_splits = (int)std::max<int64_t>(2, std::min<int64_t>(kMostSplits + 2, 2 + 4 * ((p.parts + x.n_seqs - 1) / x.n_seqs)));
   }
   p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + x.n_q + 4;
   return p;
