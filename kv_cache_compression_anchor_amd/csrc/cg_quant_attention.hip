@@ -19,12 +19,13 @@ struct QuantAttn : Attn {
   uint32_t row_bytes, page_bytes;
   int pre_least, rest_least;  // tiles of a split, at least
   int turn;                   // tiles of a super tile
+  int pre_heads;              // kv heads of a workgroup of a shared prefix
   bool direct;                // one item has all of its queries' tokens and writes the outputs
   // not 0: the tiles of all sequences' own tokens, one sequence's behind the other's, are cut
   // into so many equal parts for each (row tile, kv heads), a workgroup each
   int parts;
 };
-__device__ __forceinline__ int prefix_heads(const QuantAttn& a) { return a.rest_heads; }
+__device__ __forceinline__ int prefix_heads(const QuantAttn& a) { return a.pre_heads; }
 
 // Tiles [from, to) of a stretch of tokens.
 struct Span {
@@ -631,8 +632,164 @@ __device__ __forceinline__ void run_few(const QuantAttn& a, const Item& it, cons
   }
 }
 
+// Many rows of one head: a wave holds 16 RT of the 16 RT kWaves, and all waves read the same
+// tiles, whose numbers they make once, as binary16 in the form that cg_attention.h's products
+// take.  Codes come to registers two tiles ahead, numbers are made one tile ahead of their products,
+// and one barrier a tile publishes them and frees the tile before.
+template <int DP, int RT>
+__device__ __forceinline__ void run_many(const QuantAttn& a, const Item& it, const Span& span, QuantShared<DP>& sh) {
+  using W = Wave<DP, RT>;
+  constexpr int kWaves = Geo4<DP>::kWaves, kThreads = Geo4<DP>::kThreads;
+  constexpr int CH = DP / 8, kWords = 64 * CH / kThreads;  // 8-channel words of a row, of K and V a thread
+  constexpr int kTileBytes = Geo<DP>::BYTES;
+  static_assert(sizeof(sh.stage) >= 4 * kTileBytes && kWords >= 1, "two tiles of K and V");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ranges = ranges_of(a, it);
+  const float c = log2_scale(a);
+  const int tile_rows = 16 * RT * kWaves, row_tiles = (it.rows + tile_rows - 1) / tile_rows;
+  const int list_tiles = (int)((int64_t)(kList - 1) * a.P / kTile) - 1;
+  if (!a.direct && span.from >= span.to) return;
+  char* tiles = sh.stage[0];  // K, V, K, V
+
+#pragma unroll 1
+  for (int rt = it.row_tile; rt < row_tiles; rt += it.row_tiles) {
+    const int row0 = rt * tile_rows + wave * 16 * RT;
+    const Nibbles nb;
+    const Places<DP> at_lane;
+    W w;
+    w.clear();
+    w.load_queries(a, it, it.head, row0, rare_lane());
+    if (threadIdx.x == 0) sh.odd = sh.bad = 0;
+#pragma unroll 1
+    for (int range = 0; range < ranges; range++) {
+      const Item cur = range_of(it, ranges, range);
+      const Span sp = a.direct ? span_of(cur.lo, cur.hi, 0, 1, 1) : span;
+      const int min_lim = row_lim(a, cur, rt * tile_rows);
+      const int end = min(sp.to, (row_lim(a, cur, (rt + 1) * tile_rows - 1) + kTile - 1) / kTile);
+#pragma unroll 1
+      for (int base = sp.from; base < end; base += list_tiles) {
+        const int stop = min(base + list_tiles, end);
+        const int b0 = max(base * kTile, cur.lo) >> a.shift, b1 = (min(stop * kTile, cur.hi) - 1) >> a.shift;
+        __syncthreads();  // the list and the tiles are free
+        for (int i = rare_thread(); i <= b1 - b0; i += kThreads) {
+          const int page = a.tables[(int64_t)cur.trow * a.B + b0 + i];
+          const bool ok = page >= 0 && page < a.N;
+          sh.list[i] = ok ? page : -1;
+          if (!ok) sh.bad = 1;
+        }
+        __syncthreads();
+        const bool bad = __builtin_amdgcn_readfirstlane(sh.bad) != 0;
+        const Pages pages{sh.list, b0, max(base * kTile, cur.lo), min(stop * kTile, cur.hi), a.shift, a.P - 1};
+        auto whole = [&](int tile) { return !bad && tile * kTile >= pages.lo && (tile + 1) * kTile <= pages.hi; };
+        uint32_t word[kWords];
+        uint16_t scale[kWords];
+        auto fetch = [&](int tile) {
+#pragma unroll
+          for (int i = 0; i < kWords; i++) {
+            const int id = (int)threadIdx.x + i * kThreads, chunk = id % CH;
+            const char* row = (id >= 32 * CH ? a.v : a.k) + pages.row_at(tile * kTile + id / CH % 32, a.page_bytes, a.row_bytes);
+            word[i] = *(const uint32_t*)(row + it.head * a.head_bytes + min(chunk * 4, a.head_bytes - 4));
+            scale[i] = *(const uint16_t*)(row + a.scales + 2 * (it.head * a.groups + min(chunk / 4, a.groups - 1)));
+          }
+        };
+        // all: every query sees every token of the tile
+        auto make = [&](int tile, bool all, int to) {
+          const uint32_t alive = whole(tile) ? 0xFFFFFFFFu : find(pages, tile * kTile);
+#pragma unroll
+          for (int i = 0; i < kWords; i++) {
+            const int id = (int)threadIdx.x + i * kThreads, chunk = id % CH, tok = id / CH % 32;
+            const bool v = id >= 32 * CH, there = ((alive >> tok) & 1) && chunk * 8 < a.d;
+            u4 x = __builtin_bit_cast(u4, nb.numbers(word[i], both(scale[i])));
+            if (!there) x = u4{0, 0, 0, 0};
+            if (!all && v) {
+              // a number that is not finite must not meet the zero weight of a query that does not see
+              // it: add_odd() gives it to those that do
+              bool odd = false;
+#pragma unroll
+              for (int j = 0; j < 4; j++) {
+                const uint32_t keep = ((x[j] & 0x7C00u) == 0x7C00u ? 0 : 0xFFFFu) | ((x[j] & 0x7C000000u) == 0x7C000000u ? 0 : 0xFFFF0000u);
+                odd |= keep != 0xFFFFFFFFu;
+                x[j] &= keep;
+              }
+              if (odd) sh.odd = 1;
+            }
+            *(u4*)(tiles + (2 * to + v) * kTileBytes + tok * DP * 2 + (chunk ^ swizzle<DP>(tok)) * 16) = x;
+          }
+        };
+        auto seen = [&](int tile) { return whole(tile) && (tile + 1) * kTile <= min_lim; };
+        int slot = 0;
+        fetch(base);
+        make(base, seen(base), 0);
+        if (base + 1 < stop) fetch(base + 1);
+#pragma unroll 1
+        for (int tile = base; tile < stop; tile++, slot ^= 1) {
+          wait_lds();
+          __builtin_amdgcn_s_barrier();  // the tile is there, and the other one has been read
+          asm volatile("" ::: "memory");
+          if (tile + 1 < stop) make(tile + 1, seen(tile + 1), slot ^ 1);
+          if (tile + 2 < stop) fetch(tile + 2);
+          if (row0 < it.rows) {
+            const char *kt = tiles + 2 * slot * kTileBytes, *vt = kt + kTileBytes;
+            f4 s[RT][2];
+            h8 p[RT];
+            float mx[RT];
+            w.scores(kt, at_lane.fresh(), s, [] {});
+            if (!seen(tile))
+              mask_scores<DP, RT>(a, cur, row0, s, tile * kTile, whole(tile) ? 0xFFFFFFFFu : find(pages, tile * kTile));
+            const bool raise = w.peaks(s, c, mx);
+            w.reference(raise, mx, c);
+            w.weights(s, c, p);
+            w.values(vt, at_lane.fresh(), p, [] {});
+          }
+          asm volatile("" ::: "memory");  // one end of the loop's body, not two loops
+        }
+      }
+    }
+    const int tid = rare_thread(), n = tid & 15, g = (tid & 63) >> 4;
+    __syncthreads();
+    if (sh.bad && tid == 0) atomicOr(a.status, kBadPage);
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+      const float l = w.sum(r);
+      const int row = row0 + r * 16 + n;
+      if (row >= it.rows) continue;
+      if (a.direct) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* to = out_at(a, it, it.head, row);
+#pragma unroll
+        for (int b = 0; b < W::NB; b++)
+          if (b * 16 + g * 4 < a.d) store_out(to + b * 16 + g * 4, quotient_of(w.o[r][b], inv));
+        if (g == 0) sh.m[wave][r * 16 + n] = inv;
+        if (g == 0 && a.lse) *lse_at(a, it, it.head, row) = lse_of(w.m[r], l);
+        continue;
+      }
+      const int64_t at = part_at(a, it, it.head, row);
+      if (g == 0) *(float2*)(a.ml + 2 * at) = float2{w.m[r], l};
+#pragma unroll
+      for (int b = 0; b < W::NB; b++)
+        if (b * 16 + g * 4 < a.d) *(f4*)(a.part + at * a.d + b * 16 + g * 4) = w.o[r][b];
+    }
+    __syncthreads();
+    if (sh.odd)
+      add_odd<kThreads>(a, it, span, ranges, rt * tile_rows, (rt + 1) * tile_rows, [&](int, int row) {
+        return sh.m[(row - rt * tile_rows) / (16 * RT)][row % (16 * RT)] == 0.0f;
+      });
+    __syncthreads();  // m, the list and the tiles are free
+  }
+}
+
+// How a workgroup holds rows: all of 16 or 32 in each wave, which share out heads and tokens; or
+// 16 or 32 in each wave of one head, all of whose waves go through the same tiles.
+enum { kFew16 = 0, kFew32 = 1, kMany16 = 2, kMany32 = 3 };
+__host__ __device__ constexpr bool is_many(int mode) { return mode >= kMany16; }
+__host__ __device__ constexpr int tiles_of_rows(int mode) { return 1 + (mode & 1); }  // of 16, of a wave
+__host__ __device__ constexpr int rows_in(int dp, int mode) {
+  return 16 * tiles_of_rows(mode) * (is_many(mode) ? dp == 256 ? 4 : 8 : 1);
+}
 // Workgroups on a compute unit, as LDS and registers allow.
-__host__ __device__ constexpr int resident4(int dp, int rt) { return dp == 128 && rt == 2 ? 1 : 2; }
+__host__ __device__ constexpr int resident4(int pre, int rest) {
+  return tiles_of_rows(pre) == 2 || tiles_of_rows(rest) == 2 ? 1 : 2;
+}
 
 // Tiles of sequence s's own tokens, 0 without queries.
 __device__ __forceinline__ int tiles_of(const QuantAttn& a, int s) {
@@ -707,11 +864,17 @@ struct Work {
   bool parts;
 };
 
-template <int DP, int RT>
-__global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(DP, RT) * Geo4<DP>::kWaves / 4) void k_quant_attention(
+template <int DP, int MODE>
+__device__ __forceinline__ void run_item(const QuantAttn& a, const Item& it, const Span& span, QuantShared<DP>& sh) {
+  if constexpr (is_many(MODE)) run_many<DP, tiles_of_rows(MODE)>(a, it, span, sh);
+  else run_few<DP, tiles_of_rows(MODE)>(a, it, span, sh);
+}
+
+template <int DP, int PRE, int REST>
+__global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(PRE, REST) * Geo4<DP>::kWaves / 4) void k_quant_attention(
     QuantAttn a, int first, int end) {
   __shared__ QuantShared<DP> sh;
-  const int columns = a.kv / a.rest_heads, pre_items = a.pre_groups * a.pre_splits * a.pre_tiles * columns;
+  const int columns = a.kv / a.rest_heads, pre_items = a.pre_groups * a.pre_splits * a.pre_tiles * (a.kv / a.pre_heads);
   Item it;
   Work wk{0, 1, 0, 0, 0, 0, first + (int)blockIdx.x, a.parts && first + (int)blockIdx.x >= pre_items};
   if (wk.parts) {
@@ -746,7 +909,7 @@ __global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(DP, RT) * Geo4<DP>::k
 #pragma unroll 1
   while (wk.parts ? wk.pos < wk.end : wk.w < end) {
     Span span{0, 0};
-    bool go;
+    bool go, prefix = false;
     int own = -1;  // splits of the sequence's own tokens
     if (wk.parts) {
       const int s = wk.s++, tiles = tiles_of(a, s);
@@ -761,11 +924,15 @@ __global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(DP, RT) * Geo4<DP>::k
       wk.base += tiles;
     } else {
       go = item_of(a, wk.w, it);
-      if (go) span = wk.w < pre_items ? span_of(0, it.hi, it.split, a.pre_splits, a.pre_least)
+      prefix = wk.w < pre_items;
+      if (go) span = prefix ? span_of(0, it.hi, it.split, a.pre_splits, a.pre_least)
                                       : span_of(it.lo, it.hi, it.split, a.rest_splits, a.rest_least);
       wk.w += gridDim.x;
     }
-    if (go) run_few<DP, RT>(a, it, span, sh);
+    if (go) {
+      if (PRE == REST || !prefix) run_item<DP, REST>(a, it, span, sh);
+      else run_item<DP, PRE>(a, it, span, sh);
+    }
     if (a.direct) {
       if (!it.ok) refuse(a, it);
     } else if (it.says) {
@@ -780,29 +947,36 @@ __global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(DP, RT) * Geo4<DP>::k
 // ---------------------------------------------------------------------------
 // How many splits and row tiles the launch has, from the call's numbers alone.
 struct Plan {
-  int dp, pre_splits, rest_splits, pre_least, rest_least, pre_tiles, rest_tiles, pre_mode, rest_mode, mode, pre_groups,
+  int dp, pre_splits, rest_splits, pre_least, rest_least, pre_tiles, rest_tiles, pre_mode, rest_mode, pre_groups, pre_heads,
       rest_heads, turn, parts;
   bool direct;
   size_t words;
 };
 
 template <int DP>
-void launch(int mode, const QuantAttn& a, int64_t first, int64_t end, hipStream_t st) {
-  if (end <= first) return;
-  const int grid = (int)std::min<int64_t>(end - first, 1 << 22);
-#define GO(MODE) \
-  if (mode == MODE) k_quant_attention<DP, 1 + MODE><<<grid, Geo4<DP>::kThreads, 0, st>>>(a, (int)first, (int)end);
-  GO(kRows16)
-  if constexpr (DP <= 128) { GO(kRows32) }
+void launch(int pre, int rest, const QuantAttn& a, int64_t items, hipStream_t st) {
+  if (items <= 0) return;
+  const int grid = (int)std::min<int64_t>(items, 1 << 22);
+#define GO(PRE, REST) \
+  if (pre == PRE && rest == REST) k_quant_attention<DP, PRE, REST><<<grid, Geo4<DP>::kThreads, 0, st>>>(a, 0, (int)items);
+  GO(kFew16, kFew16) GO(kMany16, kMany16) GO(kMany16, kFew16)
+  if constexpr (DP <= 128) {
+    GO(kFew32, kFew32) GO(kMany32, kMany32) GO(kMany16, kFew32) GO(kMany32, kFew16) GO(kMany32, kFew32)
+  }
 #undef GO
 }
-void launch(int dp, int mode, const QuantAttn& a, int64_t first, int64_t end, hipStream_t st) {
-  if (dp == 64) launch<64>(mode, a, first, end, st);
-  else if (dp == 128) launch<128>(mode, a, first, end, st);
-  else launch<256>(mode, a, first, end, st);
+void launch(int dp, int pre, int rest, const QuantAttn& a, int64_t items, hipStream_t st) {
+  if (dp == 64) launch<64>(pre, rest, a, items, st);
+  else if (dp == 128) launch<128>(pre, rest, a, items, st);
+  else launch<256>(pre, rest, a, items, st);
 }
 
-int mode_of(int64_t rows, int dp) { return rows <= 16 || dp == 256 ? kRows16 : kRows32; }
+// The smallest that holds `rows`.  Waves of 32 rows of 256 channels would not fit their registers.
+int mode_of(int64_t rows, int dp) {
+  if (rows <= 16) return kFew16;
+  if (dp == 256) return kMany16;
+  return rows <= 32 ? kFew32 : rows <= 128 ? kMany16 : kMany32;
+}
 
 Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention& x) {
   Plan p;
@@ -818,12 +992,18 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   // rows of an average group
   const int64_t pre_rows = std::max<int64_t>(1, x.n_groups ? (x.n_q + x.n_groups - 1) / x.n_groups : 1) * G;
   p.pre_mode = mode_of(pre_rows, p.dp);
-  // Prefixes and the rest are one launch, of the larger number of rows: two, one after the other,
-  // leave the chip half empty (64 requests on 9,216 shared and up to 600 own tokens: 40 + 38 us).
-  p.mode = shared ? std::max(p.pre_mode, p.rest_mode) : p.rest_mode;
-  p.rest_tiles = (int)std::min(most((int64_t)x.n_seqs * kv), (rows + rows_of(p.mode) - 1) / rows_of(p.mode));
-  p.pre_tiles = (int)std::min(most((int64_t)x.n_groups * kv), (pre_rows + rows_of(p.mode) - 1) / rows_of(p.mode));
-  const int64_t slots = 256 * resident4(p.dp, p.mode + 1);
+  // Prefixes and the rest are one launch: two, one after the other, leave the chip half empty (64
+  // requests on 9,216 shared and up to 600 own tokens: 40 + 38 us).  There are kernels for
+  // many rows of the one and few of the other; else both are held as the one with more.
+  if (!shared) p.pre_mode = p.rest_mode;
+  if (p.pre_mode != p.rest_mode && !(is_many(p.pre_mode) && !is_many(p.rest_mode)))
+    p.pre_mode = p.rest_mode = std::max(p.pre_mode, p.rest_mode);
+  auto row_tiles = [&](int64_t items, int64_t rows, int mode) {
+    return (int)std::min(most(items), (rows + rows_in(p.dp, mode) - 1) / rows_in(p.dp, mode));
+  };
+  p.rest_tiles = row_tiles((int64_t)x.n_seqs * kv, rows, p.rest_mode);
+  p.pre_tiles = row_tiles((int64_t)x.n_groups * kv, pre_rows, p.pre_mode);
+  const int64_t slots = 256 * resident4(p.pre_mode, p.rest_mode);
   const int64_t own = std::max(0, x.max_len - (shared ? x.max_prefix : 0));
   auto tiles_in = [](int64_t tokens) { return (tokens + kTile - 1) / kTile; };
   // kv heads of a workgroup, and tiles of a super tile: as many as waves are left for, and as LDS holds.
@@ -843,22 +1023,27 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   // (sequences - 1) times their reading: not for little.
   constexpr int kSteps = 6;  // super tiles that a workgroup takes rather than have sums joined
   const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
-  heads(1);
-  p.direct = saved <= (int64_t)16 << 20 && tiles_in(x.max_len) <= kSteps * p.turn &&
-             (int64_t)x.n_seqs * p.rest_tiles * kv * tiles_in(x.max_len) <= waves * slots;
-  if (p.direct) {
-    p.mode = p.rest_mode;
-    p.rest_tiles = (int)std::min(most((int64_t)x.n_seqs * kv), (rows + rows_of(p.mode) - 1) / rows_of(p.mode));
+  auto alone = [&] {
+    p.pre_mode = p.rest_mode;
     p.pre_groups = 0;
     p.pre_splits = 0;
+    p.pre_heads = 1;
     p.pre_least = p.rest_least = 1;
     p.rest_splits = 1;
     p.parts = 0;
     p.words = 4;
     return p;
-  }
+  };
+  heads(1);
+  if (is_many(p.rest_mode)) p.turn = 1;
+  const int64_t all = (int64_t)x.n_seqs * p.rest_tiles * kv;
+  p.direct = saved <= (int64_t)16 << 20 &&
+             (is_many(p.rest_mode) ? all >= slots / 2 || tiles_in(x.max_len) <= kSteps
+                                   : tiles_in(x.max_len) <= kSteps * p.turn && all * tiles_in(x.max_len) <= waves * slots);
+  if (p.direct) return alone();
   // Otherwise as many neighbours as there are waves, so that whole stretches of rows are read.
-  heads(waves);
+  if (!is_many(p.rest_mode)) heads(waves);
+  p.pre_heads = is_many(p.pre_mode) ? 1 : p.rest_heads;
   // Tiles of a split, at least `least`: so many that the items, were all of the greatest length,
   // are `slots` workgroups, and at most kMostSplits splits, whose sums the join reads.  A
   // workgroup's start and end take as long as kWorth super tiles.
@@ -870,14 +1055,17 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
     per = (int)std::min<int64_t>(n, 1 << 25);
   };
   const int64_t columns = kv / p.rest_heads, items = std::max(1, x.n_seqs) * p.rest_tiles * columns;
-  const int64_t pre_items = (int64_t)x.n_groups * columns * p.pre_tiles;
-  // prefixes and the rest get slots by their work; lengths are mostly below the greatest
-  const int64_t pre_work = shared ? pre_items * tiles_in(x.max_prefix) : 0, work = items * tiles_in(own) / 2;
+  const int64_t pre_items = (int64_t)x.n_groups * (kv / p.pre_heads) * p.pre_tiles;
+  // Prefixes and the rest get slots by their work; lengths are mostly below the greatest.  A tile
+  // takes a workgroup of many rows a third of the time of one of few rows of all heads.
+  const int64_t pre_work = !shared ? 0 : pre_items * tiles_in(x.max_prefix) / (is_many(p.pre_mode) && !is_many(p.rest_mode) ? 3 : 1);
+  const int64_t work = items * tiles_in(own) / 2;
   const int64_t pre_slots = pre_work ? std::min(std::max(slots * pre_work / (pre_work + work), slots / 8), slots * 7 / 8) : 0;
   p.pre_splits = 0;
   p.pre_least = kLeast;
-  if (x.n_groups) cut(pre_items, shared ? tiles_in(x.max_prefix) : 0, pre_slots, kLeast, p.pre_splits, p.pre_least);
-  const int least = (int)std::min<int64_t>(kWorth, std::max<int64_t>(kLeast, items * tiles_in(own) / 256)) * p.turn;
+  if (x.n_groups)
+    cut(pre_items, shared ? tiles_in(x.max_prefix) : 0, pre_slots, is_many(p.pre_mode) ? 2 * kWorth : kLeast, p.pre_splits, p.pre_least);
+  const int least = (int)std::min<int64_t>(kWorth, std::max<int64_t>(kLeast, items * tiles_in(own) / 256)) * (is_many(p.rest_mode) ? 2 : p.turn);
   cut(items, tiles_in(own), slots - pre_slots, least, p.rest_splits, p.rest_least);
   p.parts = 0;
   // the sums of tiles fit 31 bits
@@ -918,7 +1106,7 @@ int cg_quant_attention_async(const cg_paged_cache* c, const cg_quant_form* f, co
   const Plan p = plan_of(*c, *f, *a);
   const QuantRow r = quant_row(*f);
   QuantAttn v{view(*c, *a, f->channels), r.head, r.groups, r.scales, (uint32_t)r.row,
-              (uint32_t)r.row * (uint32_t)c->page_tokens, p.pre_least, p.rest_least, p.turn, p.direct, p.parts};
+              (uint32_t)r.row * (uint32_t)c->page_tokens, p.pre_least, p.rest_least, p.turn, p.pre_heads, p.direct, p.parts};
   const int64_t layer = (int64_t)a->layer * c->num_pages * v.page_bytes;
   v.k = (const char*)c->k_pool_dev + layer;
   v.v = (const char*)c->v_pool_dev + layer;
@@ -931,10 +1119,10 @@ int cg_quant_attention_async(const cg_paged_cache* c, const cg_quant_form* f, co
   v.part = (float*)workspace_dev;
   v.ml = v.part + (size_t)(p.pre_splits + p.rest_splits) * a->n_q * a->n_heads * a->head_dim;
   v.used = (int32_t*)(v.ml + (size_t)2 * (p.pre_splits + p.rest_splits) * a->n_q * a->n_heads);
-  const int64_t pre = (int64_t)p.pre_groups * p.pre_splits * p.pre_tiles * (v.kv / p.rest_heads);
+  const int64_t pre = (int64_t)p.pre_groups * p.pre_splits * p.pre_tiles * (v.kv / p.pre_heads);
   const int64_t rest = (int64_t)(p.parts ? p.parts : a->n_seqs * (int64_t)p.rest_splits) * p.rest_tiles * (v.kv / p.rest_heads);
   hipStream_t st = (hipStream_t)stream;
-  launch(p.dp, p.mode, v, 0, pre + rest, st);
+  launch(p.dp, p.pre_mode, p.rest_mode, v, pre + rest, st);
   if (!p.direct) {
     const int total = p.pre_splits + p.rest_splits;
     v.join = std::min(total <= 2 ? 1 : total <= 8 ? 2 : 8, kThreads / (v.d / 4));
