@@ -640,9 +640,10 @@ template <int DP, int RT>
 __device__ __forceinline__ void run_many(const QuantAttn& a, const Item& it, const Span& span, QuantShared<DP>& sh) {
   using W = Wave<DP, RT>;
   constexpr int kWaves = Geo4<DP>::kWaves, kThreads = Geo4<DP>::kThreads;
-  constexpr int CH = DP / 8, kWords = 64 * CH / kThreads;  // 8-channel words of a row, of K and V a thread
+  constexpr int CH = DP / 8;  // 8-channel words of a row
+  constexpr int kSides = DP == 64 ? 1 : 2, kTokens = 64 * CH / kThreads / kSides;
   constexpr int kTileBytes = Geo<DP>::BYTES;
-  static_assert(sizeof(sh.stage) >= 4 * kTileBytes && kWords >= 1, "two tiles of K and V");
+  static_assert(sizeof(sh.stage) >= 4 * kTileBytes && kTokens * kSides * kThreads == 64 * CH, "two tiles of K and V");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ranges = ranges_of(a, it);
   const float c = log2_scale(a);
@@ -650,6 +651,8 @@ __device__ __forceinline__ void run_many(const QuantAttn& a, const Item& it, con
   const int list_tiles = (int)((int64_t)(kList - 1) * a.P / kTile) - 1;
   if (!a.direct && span.from >= span.to) return;
   char* tiles = sh.stage[0];  // K, V, K, V
+  const int token0 = threadIdx.x / CH % 32;
+  const bool side0 = threadIdx.x >= 32 * CH;  // DP = 64: V
 
 #pragma unroll 1
   for (int rt = it.row_tile; rt < row_tiles; rt += it.row_tiles) {
@@ -681,40 +684,50 @@ __device__ __forceinline__ void run_many(const QuantAttn& a, const Item& it, con
         const bool bad = __builtin_amdgcn_readfirstlane(sh.bad) != 0;
         const Pages pages{sh.list, b0, max(base * kTile, cur.lo), min(stop * kTile, cur.hi), a.shift, a.P - 1};
         auto whole = [&](int tile) { return !bad && tile * kTile >= pages.lo && (tile + 1) * kTile <= pages.hi; };
-        uint32_t word[kWords];
-        uint16_t scale[kWords];
+        // This thread's words: of kTokens tokens, kThreads / CH apart, of K and of V (DP = 64: of one of them).
+        uint32_t word[kTokens][kSides];
+        uint16_t scale[kTokens][kSides];
         auto fetch = [&](int tile) {
+          const int chunk = threadIdx.x % CH;
+          const int code = it.head * a.head_bytes + min(chunk * 4, a.head_bytes - 4);
+          const int at = a.scales + 2 * (it.head * a.groups + min(chunk / 4, a.groups - 1));
 #pragma unroll
-          for (int i = 0; i < kWords; i++) {
-            const int id = (int)threadIdx.x + i * kThreads, chunk = id % CH;
-            const char* row = (id >= 32 * CH ? a.v : a.k) + pages.row_at(tile * kTile + id / CH % 32, a.page_bytes, a.row_bytes);
-            word[i] = *(const uint32_t*)(row + it.head * a.head_bytes + min(chunk * 4, a.head_bytes - 4));
-            scale[i] = *(const uint16_t*)(row + a.scales + 2 * (it.head * a.groups + min(chunk / 4, a.groups - 1)));
+          for (int i = 0; i < kTokens; i++) {
+            const uint64_t row = pages.row_at(tile * kTile + token0 + i * (kThreads / CH), a.page_bytes, a.row_bytes);
+#pragma unroll
+            for (int v = 0; v < kSides; v++) {
+              const char* p = (DP == 64 ? side0 : v != 0) ? a.v + row : a.k + row;
+              word[i][v] = *(const uint32_t*)(p + code);
+              scale[i][v] = *(const uint16_t*)(p + at);
+            }
           }
         };
         // all: every query sees every token of the tile
         auto make = [&](int tile, bool all, int to) {
           const uint32_t alive = whole(tile) ? 0xFFFFFFFFu : find(pages, tile * kTile);
+          const int chunk = threadIdx.x % CH;
 #pragma unroll
-          for (int i = 0; i < kWords; i++) {
-            const int id = (int)threadIdx.x + i * kThreads, chunk = id % CH, tok = id / CH % 32;
-            const bool v = id >= 32 * CH, there = ((alive >> tok) & 1) && chunk * 8 < a.d;
-            u4 x = __builtin_bit_cast(u4, nb.numbers(word[i], both(scale[i])));
-            if (!there) x = u4{0, 0, 0, 0};
-            if (!all && v) {
-              // a number that is not finite must not meet the zero weight of a query that does not see
-              // it: add_odd() gives it to those that do
-              bool odd = false;
+          for (int i = 0; i < kTokens; i++)
 #pragma unroll
-              for (int j = 0; j < 4; j++) {
-                const uint32_t keep = ((x[j] & 0x7C00u) == 0x7C00u ? 0 : 0xFFFFu) | ((x[j] & 0x7C000000u) == 0x7C000000u ? 0 : 0xFFFF0000u);
-                odd |= keep != 0xFFFFFFFFu;
-                x[j] &= keep;
+            for (int y = 0; y < kSides; y++) {
+              const int tok = token0 + i * (kThreads / CH);
+              const bool v = DP == 64 ? side0 : y != 0, there = ((alive >> tok) & 1) && chunk * 8 < a.d;
+              u4 x = __builtin_bit_cast(u4, nb.numbers(word[i][y], both(scale[i][y])));
+              if (!there) x = u4{0, 0, 0, 0};
+              if (!all && v) {
+                // a number that is not finite must not meet the zero weight of a query that does not see
+                // it: add_odd() gives it to those that do
+                bool odd = false;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                  const uint32_t keep = ((x[j] & 0x7C00u) == 0x7C00u ? 0 : 0xFFFFu) | ((x[j] & 0x7C000000u) == 0x7C000000u ? 0 : 0xFFFF0000u);
+                  odd |= keep != 0xFFFFFFFFu;
+                  x[j] &= keep;
+                }
+                if (odd) sh.odd = 1;
               }
-              if (odd) sh.odd = 1;
+              *(u4*)(tiles + (2 * to + v) * kTileBytes + tok * DP * 2 + (chunk ^ swizzle<DP>(tok)) * 16) = x;
             }
-            *(u4*)(tiles + (2 * to + v) * kTileBytes + tok * DP * 2 + (chunk ^ swizzle<DP>(tok)) * 16) = x;
-          }
         };
         auto seen = [&](int tile) { return whole(tile) && (tile + 1) * kTile <= min_lim; };
         int slot = 0;
@@ -1044,13 +1057,13 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   // Otherwise as many neighbours as there are waves, so that whole stretches of rows are read.
   if (!is_many(p.rest_mode)) heads(waves);
   p.pre_heads = is_many(p.pre_mode) ? 1 : p.rest_heads;
-  // Tiles of a split, at least `least`: so many that the items, were all of the greatest length,
-  // are `slots` workgroups, and at most kMostSplits splits, whose sums the join reads.  A
+  // Tiles of a split, at least `least`: so many that the items are `slots` workgroups at
+  // most, and at most kMostSplits splits, whose sums the join reads.  A
   // workgroup's start and end take as long as kWorth super tiles.
   constexpr int kMostSplits = 256, kWorth = 8;
   auto cut = [&](int64_t items, int64_t tiles, int64_t slots, int least, int& splits, int& per) {
-    const int64_t n = std::max<int64_t>({(items * tiles + slots - 1) / std::max<int64_t>(1, slots),
-                                         (tiles + kMostSplits - 1) / kMostSplits, least});
+    const int64_t by = std::min<int64_t>(std::max<int64_t>(1, slots / items), kMostSplits);
+    const int64_t n = std::max<int64_t>((tiles + by - 1) / by, least);
     splits = (int)std::max<int64_t>(1, (tiles + n - 1) / n);
     per = (int)std::min<int64_t>(n, 1 << 25);
   };
@@ -1061,10 +1074,6 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   const int64_t pre_work = !shared ? 0 : pre_items * tiles_in(x.max_prefix) / (is_many(p.pre_mode) && !is_many(p.rest_mode) ? 3 : 1);
   const int64_t work = items * tiles_in(own) / 2;
   const int64_t pre_slots = pre_work ? std::min(std::max(slots * pre_work / (pre_work + work), slots / 8), slots * 7 / 8) : 0;
-  p.pre_splits = 0;
-  p.pre_least = kLeast;
-  if (x.n_groups)
-    cut(pre_items, shared ? tiles_in(x.max_prefix) : 0, pre_slots, is_many(p.pre_mode) ? 2 * kWorth : kLeast, p.pre_splits, p.pre_least);
   const int least = (int)std::min<int64_t>(kWorth, std::max<int64_t>(kLeast, items * tiles_in(own) / 256)) * (is_many(p.rest_mode) ? 2 : p.turn);
   cut(items, tiles_in(own), slots - pre_slots, least, p.rest_splits, p.rest_least);
   p.parts = 0;
@@ -1076,6 +1085,11 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
     p.rest_least = p.turn;
     p.rest_splits = (int)std::max<int64_t>(2, std::min<int64_t>(kMostSplits + 2, 2 + 4 * ((p.parts + x.n_seqs - 1) / x.n_seqs)));
   }
+  p.pre_splits = 0;
+  p.pre_least = kLeast;
+  if (x.n_groups)  // the slots that the rest leaves
+    cut(pre_items, shared ? tiles_in(x.max_prefix) : 0, p.parts ? pre_slots : std::max(pre_slots, slots - items * p.rest_splits),
+        is_many(p.pre_mode) ? 2 * kWorth : kLeast, p.pre_splits, p.pre_least);
   p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + x.n_q + 4;
   return p;
 }
