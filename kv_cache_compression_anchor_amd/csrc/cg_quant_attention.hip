@@ -667,10 +667,10 @@ __device__ __forceinline__ void run_many(const QuantAttn& a, const Item& it, con
     for (int range = 0; range < ranges; range++) {
       const Item cur = range_of(it, ranges, range);
       const Span sp = a.direct ? span_of(cur.lo, cur.hi, 0, 1, 1) : span;
-      const int min_lim = row_lim(a, cur, rt * tile_rows);
-      const int end = min(sp.to, (row_lim(a, cur, (rt + 1) * tile_rows - 1) + kTile - 1) / kTile);
+      const int min_lim = __builtin_amdgcn_readfirstlane(row_lim(a, cur, rt * tile_rows));
+      const int end = __builtin_amdgcn_readfirstlane(min(sp.to, (row_lim(a, cur, (rt + 1) * tile_rows - 1) + kTile - 1) / kTile));
 #pragma unroll 1
-      for (int base = sp.from; base < end; base += list_tiles) {
+      for (int base = __builtin_amdgcn_readfirstlane(sp.from); base < end; base += list_tiles) {
         const int stop = min(base + list_tiles, end);
         const int b0 = max(base * kTile, cur.lo) >> a.shift, b1 = (min(stop * kTile, cur.hi) - 1) >> a.shift;
         __syncthreads();  // the list and the tiles are free
@@ -682,7 +682,7 @@ __device__ __forceinline__ void run_many(const QuantAttn& a, const Item& it, con
         }
         __syncthreads();
         const bool bad = __builtin_amdgcn_readfirstlane(sh.bad) != 0;
-        const Pages pages{sh.list, b0, max(base * kTile, cur.lo), min(stop * kTile, cur.hi), a.shift, a.P - 1};
+        const Pages pages{sh.list, b0, __builtin_amdgcn_readfirstlane(max(base * kTile, cur.lo)), __builtin_amdgcn_readfirstlane(min(stop * kTile, cur.hi)), a.shift, a.P - 1};
         auto whole = [&](int tile) { return !bad && tile * kTile >= pages.lo && (tile + 1) * kTile <= pages.hi; };
         // This thread's words: of kTokens tokens, kThreads / CH apart, of K and of V (DP = 64: of one of them).
         uint32_t word[kTokens][kSides];
@@ -883,13 +883,24 @@ __device__ __forceinline__ void run_item(const QuantAttn& a, const Item& it, con
   else run_few<DP, tiles_of_rows(MODE)>(a, it, span, sh);
 }
 
-template <int DP, int PRE, int REST>
+// How a launch cuts the sequences: splits, or parts, of what the join then adds up, or each sequence to one workgroup,
+// which writes the outputs (a.direct).  Known to the compiler, each needs fewer scalar registers
+// than there are, and half the code, which a workgroup of few tokens fetches for one use.
+enum { kSplits = 0, kParts = 1, kAlone = 2 };
+
+template <int DP, int PRE, int REST, int CUT>
 __global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(PRE, REST) * Geo4<DP>::kWaves / 4) void k_quant_attention(
-    QuantAttn a, int first, int end) {
+    QuantAttn a, int end) {
   __shared__ QuantShared<DP> sh;
+  a.direct = CUT == kAlone;
+  if constexpr (CUT != kParts) a.parts = 0;
+  if constexpr (CUT == kAlone) {
+    a.pre_groups = a.pre_splits = 0;
+    a.rest_splits = a.rest_heads = a.pre_heads = a.pre_least = a.rest_least = 1;
+  }
   const int columns = a.kv / a.rest_heads, pre_items = a.pre_groups * a.pre_splits * a.pre_tiles * (a.kv / a.pre_heads);
   Item it;
-  Work wk{0, 1, 0, 0, 0, 0, first + (int)blockIdx.x, a.parts && first + (int)blockIdx.x >= pre_items};
+  Work wk{0, 1, 0, 0, 0, 0, (int)blockIdx.x, CUT == kParts && (int)blockIdx.x >= pre_items};
   if (wk.parts) {
     static_assert(sizeof(sh.stage) >= (kMostListed + 1) * 4, "room for the sums of tiles");
     int* at = (int*)sh.stage;
@@ -969,13 +980,18 @@ struct Plan {
 template <int DP>
 void launch(int pre, int rest, const QuantAttn& a, int64_t items, hipStream_t st) {
   if (items <= 0) return;
-  const int grid = (int)std::min<int64_t>(items, 1 << 22);
-#define GO(PRE, REST) \
-  if (pre == PRE && rest == REST) k_quant_attention<DP, PRE, REST><<<grid, Geo4<DP>::kThreads, 0, st>>>(a, 0, (int)items);
-  GO(kFew16, kFew16) GO(kMany16, kMany16) GO(kMany16, kFew16)
+  const int grid = (int)std::min<int64_t>(items, 1 << 22), cut = a.direct ? kAlone : a.parts ? kParts : kSplits;
+#define GO(PRE, REST, CUT) \
+  if (pre == PRE && rest == REST && cut == CUT) \
+    k_quant_attention<DP, PRE, REST, CUT><<<grid, Geo4<DP>::kThreads, 0, st>>>(a, (int)items);
+#define GO_SAME(MODE) GO(MODE, MODE, kSplits) GO(MODE, MODE, kParts) GO(MODE, MODE, kAlone)
+#define GO_BOTH(PRE, REST) GO(PRE, REST, kSplits) GO(PRE, REST, kParts)
+  GO_SAME(kFew16) GO_SAME(kMany16) GO_BOTH(kMany16, kFew16)
   if constexpr (DP <= 128) {
-    GO(kFew32, kFew32) GO(kMany32, kMany32) GO(kMany16, kFew32) GO(kMany32, kFew16) GO(kMany32, kFew32)
+    GO_SAME(kFew32) GO_SAME(kMany32) GO_BOTH(kMany16, kFew32) GO_BOTH(kMany32, kFew16) GO_BOTH(kMany32, kFew32)
   }
+#undef GO_BOTH
+#undef GO_SAME
 #undef GO
 }
 void launch(int dp, int pre, int rest, const QuantAttn& a, int64_t items, hipStream_t st) {
