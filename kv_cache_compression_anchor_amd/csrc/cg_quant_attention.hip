@@ -1090,8 +1090,10 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   const int64_t pre_work = !shared ? 0 : pre_items * tiles_in(x.max_prefix) / (is_many(p.pre_mode) && !is_many(p.rest_mode) ? 3 : 1);
   const int64_t work = items * tiles_in(own) / 2;
   const int64_t pre_slots = pre_work ? std::min(std::max(slots * pre_work / (pre_work + work), slots / 8), slots * 7 / 8) : 0;
+  // whole splits of all sequences: the prefix, whose workgroups all take as long, gets what they leave
+  const int64_t rest_slots = pre_slots ? std::min((slots - pre_slots + items / 2) / items * items, slots * 7 / 8) : slots;
   const int least = (int)std::min<int64_t>(kWorth, std::max<int64_t>(kLeast, items * tiles_in(own) / 256)) * (is_many(p.rest_mode) ? 2 : p.turn);
-  cut(items, tiles_in(own), slots - pre_slots, least, p.rest_splits, p.rest_least);
+  cut(items, tiles_in(own), rest_slots, least, p.rest_splits, p.rest_least);
   p.parts = 0;
   // the sums of tiles fit 31 bits
   const bool listed = x.n_seqs <= kMostListed && (int64_t)x.n_seqs * c.max_blocks * c.page_tokens < (int64_t)1 << 35;
@@ -1104,7 +1106,7 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   p.pre_splits = 0;
   p.pre_least = kLeast;
   if (x.n_groups)  // the slots that the rest leaves
-    cut(pre_items, shared ? tiles_in(x.max_prefix) : 0, p.parts ? pre_slots : std::max(pre_slots, slots - items * p.rest_splits),
+    cut(pre_items, shared ? tiles_in(x.max_prefix) : 0, p.parts ? pre_slots : std::max(slots / 8, slots - items * p.rest_splits),
         is_many(p.pre_mode) ? 2 * kWorth : kLeast, p.pre_splits, p.pre_least);
   p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + x.n_q + 4;
   return p;
