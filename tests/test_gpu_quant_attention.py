@@ -69,9 +69,10 @@ def gpu_attention(x, layer, q, scale, rows, q_starts, group_starts=None, prefix_
 
 
 def hints_of(q_starts):
-    """The lengths'; a prefix shared, tokens split and joined; joined; one kernel."""
+    """The lengths'; a prefix shared, tokens in parts and joined; joined; one kernel; splits."""
     most = max(1, int(np.max(np.diff(q_starts), initial=0)))
-    return None, (most, 1 << 20, 1 << 21), (most, 0, 1 << 21), (most, 0, 0)
+    return (None, (most, 1 << 20, 1 << 21), (most, 0, 1 << 21), (most, 0, 0), (most, 1 << 20, (1 << 20) + 200),
+            (most, 0, 4000))
 
 
 def oracle(x, layer, q, scale, rows, q_starts, *groups):
