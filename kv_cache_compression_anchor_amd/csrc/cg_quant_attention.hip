@@ -387,7 +387,7 @@ struct QuantShared {
 };
 static_assert(sizeof(QuantShared<128>) <= 160 * 1024 / 2, "two workgroups a compute unit");
 
-// Half of channel ch of kv head `head` in the row at p.
+// The number of channel ch of kv head `head` in the row at p.
 __device__ __forceinline__ float number_at(const QuantAttn& a, const char* p, int head, int ch) {
   const uint32_t w = *(const uint32_t*)(p + head * a.head_bytes + ch / 8 * 4);
   const _Float16 s = __builtin_bit_cast(_Float16, *(const uint16_t*)(p + a.scales + 2 * (head * a.groups + ch / 32)));
@@ -931,7 +931,7 @@ __global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(PRE, REST) * Geo4<DP>
     wk.base = __builtin_amdgcn_readfirstlane(at[s]);  // the stages take the place of the sums from here
   }
 #pragma unroll 1
-  while (wk.parts ? wk.pos < wk.end : wk.w < end) {
+  while (wk.parts ? wk.pos < wk.end && wk.s < a.n_seqs : wk.w < end) {
     Span span{0, 0};
     bool go, prefix = false;
     int own = -1;  // splits of the sequence's own tokens
@@ -1011,9 +1011,9 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   Plan p;
   const int kv = f.channels / x.head_dim, G = x.n_heads / kv;
   p.dp = x.head_dim <= 64 ? 64 : x.head_dim <= 128 ? 128 : 256;
-  // row tiles with workgroups of their own: few enough that an item's number, over
-  // all heads, sequences and splits, fits 31 bits
-  auto most = [&](int64_t items) { return std::max<int64_t>(1, (1 << 22) / std::max<int64_t>(1, items)); };
+  // Row tiles with workgroups of their own: few enough that an item's number, over
+  // all heads, sequences and splits, fits 31 bits.
+  auto most = [&](int64_t items) { return std::max<int64_t>(1, (1 << 21) / std::max<int64_t>(1, items)); };
   const int64_t rows = (int64_t)std::max(1, std::min(x.max_q, x.n_q)) * G;
   p.rest_mode = mode_of(rows, p.dp);
   const bool shared = x.n_groups > 0 && x.max_prefix > 0;
@@ -1048,9 +1048,12 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
     while ((p.turn * 512 * cpr + 1023) / 1024 * 1024 > 37 * 1024 / 2) p.turn--;
   };
   // Few tokens: one head a workgroup, whose waves share the tokens, in one kernel that writes the
-  // outputs itself, without a join (5 us and the start of a kernel).  Sharing prefixes saves
-  // (sequences - 1) times their reading: not for little.
-  constexpr int kSteps = 6;  // super tiles that a workgroup takes rather than have sums joined
+  // outputs itself, without a join.  For 8 kv heads of 128 channels, that kernel and the other
+  // way: one sequence of 768 tokens 16 and 20 us, of 1,536 tokens 21 and 20; 8 of 1,000 19.5 and 20,
+  // of 1,536 24 and 20; 32 of 512 20 and 25, of 1,000 28 and 22; 64 of 256 20 and 28, of 512 29
+  // and 22.  Sharing prefixes saves (sequences - 1) times their reading, not for little: 64
+  // sequences with 128 tokens in common (32 MiB of binary16 numbers) 17 and 19 us, 16 with 512 17 and 17.
+  constexpr int kSteps = 4;  // super tiles that a workgroup takes rather than have sums joined
   const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
   auto alone = [&] {
     p.pre_mode = p.rest_mode;
@@ -1066,7 +1069,7 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   heads(1);
   if (is_many(p.rest_mode)) p.turn = 1;
   const int64_t all = (int64_t)x.n_seqs * p.rest_tiles * kv;
-  p.direct = saved <= (int64_t)16 << 20 &&
+  p.direct = saved <= (int64_t)32 << 20 &&
              (is_many(p.rest_mode) ? all >= slots / 2 || tiles_in(x.max_len) <= kSteps
                                    : tiles_in(x.max_len) <= kSteps * p.turn && all * tiles_in(x.max_len) <= waves * slots);
   if (p.direct) return alone();
@@ -1097,8 +1100,10 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   p.parts = 0;
   // the sums of tiles fit 31 bits
   const bool listed = x.n_seqs <= kMostListed && (int64_t)x.n_seqs * c.max_blocks * c.page_tokens < (int64_t)1 << 35;
-  if (x.n_seqs > 1 && listed && work >= kWorth * p.turn * (slots - pre_slots)) {
-    // lengths that differ: equal parts of all of them
+  // Lengths that differ: equal parts of all of them, where that is two or more for each row tile and
+  // its heads, and a launch has all items (2^22 at most) at once.
+  if (x.n_seqs > 1 && listed && work >= kWorth * p.turn * (slots - pre_slots) &&
+      slots - pre_slots >= 2 * columns * p.rest_tiles && pre_items <= 1 << 21) {
     p.parts = (int)std::max<int64_t>(1, (slots - pre_slots) / (columns * p.rest_tiles));
     p.rest_least = p.turn;
     p.rest_splits = (int)std::max<int64_t>(2, std::min<int64_t>(kMostSplits + 2, 2 + 4 * ((p.parts + x.n_seqs - 1) / x.n_seqs)));
