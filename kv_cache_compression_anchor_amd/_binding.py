@@ -628,7 +628,8 @@ class QuantCache(PagedCache):
 def _quant_rows(cache, a, b, names):
     """Strides (token, layer) of a pair of fp16 tensors [layers, tokens, channels]."""
     strides = _rows3(a, cache.f16, cache.index, cache.numbers, names[0])
-    if a.shape != b.shape or strides != _rows3(b, cache.f16, cache.index, cache.numbers, names[1]):
+    if a.shape != b.shape or ((b.stride() != a.stride() or b.dtype != a.dtype or b.get_device() != cache.index)
+                              and strides != _rows3(b, cache.f16, cache.index, cache.numbers, names[1])):
         raise ValueError(f"{names[0]} and {names[1]} must have the same shape and strides")
     return strides[1], strides[0]
 
