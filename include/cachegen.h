@@ -494,7 +494,8 @@ int cg_quant_row(const cg_quant_form* form, int32_t* cache_channels);
 
 /* cg_pages_write_async into a cache of this form: the same arguments, with token_stride >=
  * form->channels.  k_held_dev and v_held_dev, both or neither NULL, receive the numbers
- * that the cache holds, of every token, whatever its slot, with the strides held_token_stride and
+ * that the cache holds, of every token, whatever its slot (a slot named twice is left with parts of
+ * each of its tokens), with the strides held_token_stride and
  * held_layer_stride; they may be k_new_dev and v_new_dev themselves with the same strides,
  * but not overlap them otherwise. */
 int cg_quant_write_async(const cg_paged_cache* cache, const cg_quant_form* form, int32_t layer0,

