@@ -1092,14 +1092,16 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   if (!is_many(p.rest_mode)) heads(waves);
   p.pre_heads = is_many(p.pre_mode) ? 1 : p.rest_heads;
   // Tiles of a split, at least `least`: so many that the items are `slots` workgroups at
-  // most, and at most kMostSplits splits, whose sums the join reads.  A
-  // workgroup's start and end take as long as kWorth super tiles.
+  // most, and at most kMostSplits splits, whose sums the join reads.  A workgroup's start and
+  // end take as long as kWorth super tiles.  What is shorter than the call says is cut as often, down to kLeast
+  // tiles, as all these workgroups run at once (64 sequences on 9,216 shared tokens, said to be up to
+  // 147,456: 45 us, in splits as long as said 253).
   constexpr int kMostSplits = 256, kWorth = 8;
   auto cut = [&](int64_t items, int64_t tiles, int64_t slots, int least, int& splits, int& per) {
     const int64_t by = std::min<int64_t>(std::max<int64_t>(1, slots / items), kMostSplits);
     const int64_t n = std::max<int64_t>((tiles + by - 1) / by, least);
     splits = (int)std::max<int64_t>(1, (tiles + n - 1) / n);
-    per = (int)std::min<int64_t>(n, 1 << 25);
+    per = std::min(least, kLeast);
   };
   const int64_t columns = kv / p.rest_heads, items = std::max(1, x.n_seqs) * p.rest_tiles * columns;
   const int64_t pre_items = (int64_t)x.n_groups * (kv / p.pre_heads) * p.pre_tiles;
@@ -1120,14 +1122,14 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   if (x.n_seqs > 1 && listed && work >= kWorth * p.turn * (slots - pre_slots) &&
       slots - pre_slots >= 2 * columns * p.rest_tiles && pre_items <= 1 << 21) {
     p.parts = (int)std::max<int64_t>(1, (slots - pre_slots) / (columns * p.rest_tiles));
-    p.rest_least = p.turn;
+    p.rest_least = kWorth / 2 * p.turn;
     p.rest_splits = (int)std::max<int64_t>(2, std::min<int64_t>(kMostSplits + 2, 2 + 4 * ((p.parts + x.n_seqs - 1) / x.n_seqs)));
   }
   p.pre_splits = 0;
   p.pre_least = kLeast;
   if (x.n_groups)  // the slots that the rest leaves
     cut(pre_items, shared ? tiles_in(x.max_prefix) : 0, p.parts ? pre_slots : std::max(slots / 8, slots - items * p.rest_splits),
-        is_many(p.pre_mode) ? 2 * kWorth : kLeast, p.pre_splits, p.pre_least);
+        kLeast, p.pre_splits, p.pre_least);
   p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + x.n_q + 4;
   return p;
 }
