@@ -588,7 +588,20 @@ __device__ __forceinline__ void run_few(const QuantAttn& a, const Item& it, cons
           }
       }
     } else {
-      // the waves' sums together, against the largest reference exponent
+      // The waves' sums together, against the largest reference exponent.  Loops over the waves are
+      // unrolled, so that their reads are under way together.
+      constexpr int kQuads = DP / 4;  // of a row, rotated by row
+      static_assert(sizeof(sh.stage) >= (size_t)kWaves * 16 * kQuads * 16, "room for the sums");
+      f4* sums = (f4*)sh.stage;
+      auto put = [&](int r) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int ch = __shfl(hd.channel, 4 * g + i);
+#pragma unroll
+          for (int b = 0; b < W::NB; b += 4)
+            if (r * 16 + n < rows) sums[(wave * 16 + n) * kQuads + (((ch + b) / 4 + n) & (kQuads - 1))] = quad_of(r, b, i);
+        }
+      };
 #pragma unroll
       for (int r = 0; r < RT; r++) {
         const float l = w.sum(r);
@@ -597,44 +610,52 @@ __device__ __forceinline__ void run_few(const QuantAttn& a, const Item& it, cons
           sh.l[wave][r * 16 + n] = l;
         }
       }
+      put(0);
       __syncthreads();
-      const int waves = it.heads * co.turn;  // wave h + heads y has tile y of head h
+      auto wave_of = [&](int h, int y) { return h + it.heads * min(y, co.turn - 1); };  // that has tile y of head h
       if (tid < 16 * RT * it.heads) {
         const int x = tid % (16 * RT), h = tid / (16 * RT);
-        float m = -__builtin_inff(), l = 0.0f;
-        for (int y = h; y < waves; y += it.heads) m = fmaxf(m, sh.m[y][x]);
-        for (int y = h; y < waves; y += it.heads) {
+        float m = -__builtin_inff(), l = 0.0f, ms[kWaves], ls[kWaves];
+#pragma unroll
+        for (int y = 0; y < kWaves; y++) {
+          ms[y] = sh.m[wave_of(h, y)][x];
+          ls[y] = sh.l[wave_of(h, y)][x];
+        }
+#pragma unroll
+        for (int y = 0; y < kWaves; y++) m = fmaxf(m, ms[y]);
+#pragma unroll
+        for (int y = 0; y < kWaves; y++) {
           // a wave without a reference has weighed nothing, or only what is no number
-          const float my = sh.m[y][x], ly = sh.l[y][x];
-          const float f = my == m ? 1.0f : my == -__builtin_inff() && ly != 0.0f
-                              ? 1.0f : __builtin_amdgcn_exp2f(my - m);
-          sh.scale[y][x] = f;
-          l += f * ly;
+          const float f = ms[y] == m ? 1.0f : ms[y] == -__builtin_inff() && ls[y] != 0.0f
+                                 ? 1.0f : __builtin_amdgcn_exp2f(ms[y] - m);
+          sh.scale[wave_of(h, y)][x] = f;
+          l += y < co.turn ? f * ls[y] : 0.0f;
         }
         store_sums(h, x, m, l);
       }
-      constexpr int kQuads = DP / 4;  // of a row, rotated by row
-      static_assert(sizeof(sh.stage) >= (size_t)kWaves * 16 * kQuads * 16, "room for the sums");
-      f4* sums = (f4*)sh.stage;
 #pragma unroll 1
       for (int r = 0; r * 16 < rows; r++) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int ch = __shfl(hd.channel, 4 * g + i);
-#pragma unroll
-          for (int b = 0; b < W::NB; b += 4)
-            if (r * 16 + n < rows) sums[(wave * 16 + n) * kQuads + (((ch + b) / 4 + n) & (kQuads - 1))] = quad_of(r, b, i);
+        if (r) {
+          __syncthreads();
+          put(r);
         }
         __syncthreads();
-        const int here = min(rows - r * 16, 16);
+        const int here = rows - r * 16;
 #pragma unroll 1
-        for (int i = tid; i < it.heads * here * kQuads; i += kThreads) {
-          const int quad = i % kQuads, x = i / kQuads % here, h = i / (here * kQuads), row = r * 16 + x;
-          if (quad * 4 >= a.d) continue;
-          f4 sum{0, 0, 0, 0};
-          for (int y = h; y < waves; y += it.heads)
-            sum += sh.scale[y][row] * sums[(y * 16 + x) * kQuads + ((quad + x) & (kQuads - 1))];
+        for (int i = tid; i < it.heads * 16 * kQuads; i += kThreads) {
+          const int quad = i % kQuads, x = i / kQuads % 16, h = i / (16 * kQuads), row = r * 16 + x;
+          if (quad * 4 >= a.d || x >= here) continue;
+          f4 part[kWaves], sum{0, 0, 0, 0};
+          float f[kWaves];
+#pragma unroll
+          for (int y = 0; y < kWaves; y++) {
+            const int from = wave_of(h, y);
+            f[y] = sh.scale[from][row];
+            part[y] = sums[(from * 16 + x) * kQuads + ((quad + x) & (kQuads - 1))];
+          }
+#pragma unroll
+          for (int y = 0; y < kWaves; y++)
+            if (y < co.turn) sum += f[y] * part[y];
           store(h, row, quad * 4, sum);
         }
       }
