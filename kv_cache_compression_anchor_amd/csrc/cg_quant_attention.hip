@@ -1025,6 +1025,7 @@ void launch(int pre, int rest, const QuantAttn& a, int64_t items, hipStream_t st
   GO_SAME(kFew16) GO_SAME(kMany16) GO_BOTH(kMany16, kFew16)
   if constexpr (DP <= 128) {
     GO_SAME(kFew32) GO_SAME(kMany32) GO_BOTH(kMany16, kFew32) GO_BOTH(kMany32, kFew16) GO_BOTH(kMany32, kFew32)
+    GO_BOTH(kFew32, kFew16)
   }
 #undef GO_BOTH
 #undef GO_SAME
@@ -1058,10 +1059,11 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   const int64_t pre_rows = std::max<int64_t>(1, x.n_groups ? (x.n_q + x.n_groups - 1) / x.n_groups : 1) * G;
   p.pre_mode = mode_of(pre_rows, p.dp);
   // Prefixes and the rest are one launch: two, one after the other, leave the chip half empty (64
-  // requests on 9,216 shared and up to 600 own tokens: 40 + 38 us).  There are kernels for
-  // many rows of the one and few of the other; else both are held as the one with more.
+  // requests on 9,216 shared and up to 600 own tokens: 40 + 38 us).  A group's rows are as many as a
+  // sequence's or more (21 sequences of up to 5 rows on three prompts: 38 us, with 32 rows for
+  // both 43); where not, or both are many, both are held as the one with more.
   if (!shared) p.pre_mode = p.rest_mode;
-  if (p.pre_mode != p.rest_mode && !(is_many(p.pre_mode) && !is_many(p.rest_mode)))
+  if (p.pre_mode < p.rest_mode || (is_many(p.pre_mode) && is_many(p.rest_mode)))
     p.pre_mode = p.rest_mode = std::max(p.pre_mode, p.rest_mode);
   auto row_tiles = [&](int64_t items, int64_t rows, int mode) {
     return (int)std::min(most(items), (rows + rows_in(p.dp, mode) - 1) / rows_in(p.dp, mode));
