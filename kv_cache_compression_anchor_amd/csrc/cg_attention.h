@@ -396,6 +396,16 @@ struct Wave {
       for (int e = 0; e < 8; e++) p[r][e] = (_Float16)w[e];  // rounded to nearest
     }
   }
+  // What that rounding took from each.
+  __device__ __forceinline__ void rests(const f4 (&s)[RT][2], float c, const h8 (&p)[RT], h8 (&rest)[RT]) {
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+      const float mu = m[r] == -__builtin_inff() ? 0.0f : m[r];
+#pragma unroll
+      for (int e = 0; e < 8; e++)
+        rest[r][e] = (_Float16)(__builtin_amdgcn_exp2f(__builtin_fmaf(s[r][e >> 2][e & 3], c, -mu)) - (float)p[r][e]);
+    }
+  }
 
   // o += V^T P^T
   template <class F>

@@ -314,9 +314,10 @@ __device__ __forceinline__ bool clean_values(const A& a, const Columns& co, int 
 
 // o += V^T P^T.  Row n of block b of V^T is channel b of the lane's, so that a lane's
 // channels are neighbours in its word; its tokens come together two at a time.
+// two: P^T + rest^T.
 template <int DP, int RT>
 __device__ __forceinline__ void values(Wave<DP, RT>& w, const Head<DP>& hd, const Nibbles& nb, const char* vt,
-                                       const h8 (&p)[RT]) {
+                                       const h8 (&p)[RT], bool two, const h8 (&rest)[RT]) {
   constexpr int VW = DP == 256 ? 2 : 1, HALVES = DP == 64 ? 1 : 2;  // words of a lane, halves of a word
   uint32_t x[8][VW];
   union { s4 t[2]; h2 s[4]; uint16_t u[8]; } sc;  // scales of tokens 4 g .. + 3, 16 + 4 g .. + 3
@@ -363,6 +364,10 @@ __device__ __forceinline__ void values(Wave<DP, RT>& w, const Head<DP>& hd, cons
 #pragma unroll
       for (int r = 0; r < RT; r++)
         w.o[r][block] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[b].h, p[r], w.o[r][block], 0, 0, 0);
+      if (two)
+#pragma unroll
+        for (int r = 0; r < RT; r++)
+          w.o[r][block] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[b].h, rest[r], w.o[r][block], 0, 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -541,7 +546,11 @@ __device__ __forceinline__ void run_few(const QuantAttn& a, const Item& it, cons
             w.reference(raise, mx, c);
             w.weights(s, c, p);
             if (!all && clean_values<DP>(a, co, hh, vt, alive)) sh.odd = 1;
-            values(w, hd, nb, vt, p);
+            // A workgroup alone with a few tokens, whose weights' roundings do not average out and whose time
+            // is not in its products, gives the second product the weights in two parts.
+            h8 rest[RT];
+            if (a.direct) w.rests(s, c, p, rest);
+            values(w, hd, nb, vt, p, a.direct, rest);
           }
           asm volatile("" ::: "memory");  // one end of the loop's body, not two loops
         }
