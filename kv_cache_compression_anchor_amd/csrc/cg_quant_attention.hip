@@ -1096,10 +1096,10 @@ Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention
   };
   // Few tokens: one head a workgroup, whose waves share the tokens, in one kernel that writes the
   // outputs itself, without a join.  For 8 kv heads of 128 channels, that kernel and the other
-  // way: one sequence of 768 tokens 16 and 20 us, of 1,536 tokens 21 and 20; 8 of 1,000 19.5 and 20,
-  // of 1,536 24 and 20; 32 of 512 20 and 25, of 1,000 28 and 22; 64 of 256 20 and 28, of 512 29
+  // way: one sequence of 768 tokens 16 and 20 us, of 1,536 tokens 22 and 20; 8 of 1,000 20 and 20,
+  // of 1,536 24 and 21; 32 of 512 19 and 22, of 1,000 28 and 22; 64 of 256 20 and 22, of 512 29
   // and 22.  Sharing prefixes saves (sequences - 1) times their reading, not for little: 64
-  // sequences with 128 tokens in common (9 MB) 17.5 and 19 us, 16 with 512 (9 MB) 17 and 17.
+  // sequences with 128 tokens in common (9 MB) 17.6 and 18 to 19 us, 16 with 512 (9 MB) 17 and 17.
   constexpr int kSteps = 4;  // super tiles that a workgroup takes rather than have sums joined
   const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
   auto alone = [&] {
