@@ -465,7 +465,8 @@ int cg_pages_slots_async(const cg_paged_cache* cache, int32_t n, const int32_t* 
  * contexts that stay on the device.  Such a cache is a cg_paged_cache whose `channels`
  * count the 16-bit units of a row, as cg_quant_row gives them: reserve, fork, free, compact,
  * copy and slots work on it as they are.  K and V are written, read back and attended to
- * through the calls below.
+ * through the calls below; cg_pages_write_async and cg_attention_prefix_async would take the
+ * units as binary16 numbers, which the struct does not tell apart.
  *
  * A row holds one token's K (or V) of one layer: `channels` numbers, heads of head_dim
  * channels, each head in groups of 32 channels (the last may be shorter).  With a the

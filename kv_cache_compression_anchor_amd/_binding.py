@@ -426,6 +426,7 @@ class PagedCache:
     [layers, num_pages, page_tokens, channels], int32 tables [rows, max_blocks],
     int32 lens [rows], int32 refs [num_pages], int32 status [1].  Keeps the
     tensors and the struct that the cg_pages_* and cg_attention_* calls take."""
+    form = None  # of rows that are not fp16 numbers
 
     def __init__(self, k_pool, v_pool, tables, lens, refs, status):
         import torch
@@ -477,6 +478,18 @@ class PagedCache:
         return _stream(stream)
 
 
+def _need_numbers(cache, call):
+    """The struct of a cache held in 4 bits does not say so: its 16-bit units would be taken as
+    fp16 numbers."""
+    if cache.form is not None:
+        raise ValueError(f"{call} takes a cache of fp16 numbers, not one held in 4 bits")
+
+
+def _need_form(cache, call):
+    if cache.form is None:
+        raise ValueError(f"{call} takes a QuantCache")
+
+
 def cg_pages_workspace(cache: PagedCache) -> int:
     n = C.c_size_t(0)
     _check(cache.lib.cg_pages_workspace(cache.ref, C.byref(n)))
@@ -508,6 +521,7 @@ def cg_pages_reserve_async(cache: PagedCache, rows, starts, slots, workspace, n_
 def cg_pages_write_async(cache: PagedCache, layer0, slots, k_new, v_new, stream=None):
     """Writes k_new / v_new (fp16 [layers, tokens, channels], channels contiguous,
     both with the same strides) to `slots` in layers layer0 .."""
+    _need_numbers(cache, "cg_pages_write_async")
     strides = _rows3(k_new, cache.f16, cache.index, cache.channels, "k_new")
     if (k_new.shape != v_new.shape
             or strides != _rows3(v_new, cache.f16, cache.index, cache.channels, "v_new")):
@@ -547,6 +561,7 @@ def cg_pages_compact_async(cache: PagedCache, workspace, n_live=None, stream=Non
 def cg_attention_workspace(cache: PagedCache, n_q, n_heads, head_dim, n_seqs, n_groups, max_q,
                            max_prefix, max_len) -> int:
     """Bytes of workspace of a cg_attention_prefix_async call of these numbers."""
+    _need_numbers(cache, "cg_attention_workspace")
     a = cg_attention(0, n_heads, head_dim, 1.0, n_seqs, n_q, n_groups, max_q, max_prefix, max_len)
     n = C.c_size_t(0)
     _check(cache.lib.cg_attention_workspace(cache.ref, C.byref(a), C.byref(n)))
@@ -578,6 +593,7 @@ def cg_attention_prefix_async(cache: PagedCache, layer, q, out, scale, rows, q_s
     cache into out (the same shape) and lse (fp32 [tokens, heads], may be None).
     rows None: sequence s is row s.  group_starts / prefix_lens None: no shared
     prefixes.  q and out may have a longer stride between tokens."""
+    _need_numbers(cache, "cg_attention_prefix_async")
     a = _attention_call(cache, layer, q, out, scale, rows, q_starts, group_starts, prefix_lens, max_q,
                         max_prefix, max_len, lse)
     _check(cache.lib.cg_attention_prefix_async(cache.ref, C.byref(a),
@@ -607,7 +623,7 @@ def cg_quant_row(channels: int, head_dim: int) -> int:
 class QuantCache(PagedCache):
     """A paged cache held in 4 bits: pools uint8 [layers, num_pages, page_tokens,
     2 x cg_quant_row(channels, head_dim)], the rest as PagedCache has it.  The cg_pages_* calls
-    take it, and the cg_quant_* calls for what its rows stand for."""
+    but cg_pages_write_async take it, and the cg_quant_* calls for what its rows stand for."""
 
     def __init__(self, k_pool, v_pool, tables, lens, refs, status, channels, head_dim):
         import torch
@@ -639,6 +655,7 @@ def cg_quant_write_async(cache: QuantCache, layer0, slots, k_new, v_new, k_held=
     """Writes k_new / v_new (fp16 [layers, tokens, channels], channels contiguous, both with
     the same strides) in 4 bits to `slots` in layers layer0 ..; k_held / v_held (the same
     shape) receive what the cache holds, and may be k_new / v_new."""
+    _need_form(cache, "cg_quant_write_async")
     new = _quant_rows(cache, k_new, v_new, ("k_new", "v_new"))
     kh = vh = None
     held = (cache.numbers, 0)
@@ -659,6 +676,7 @@ def cg_quant_write_async(cache: QuantCache, layer0, slots, k_new, v_new, k_held=
 def cg_quant_read_async(cache: QuantCache, layer0, slots, k_out, v_out, stream=None):
     """What the cache holds at `slots` in layers layer0 .. into k_out / v_out (fp16 [layers,
     tokens, channels], channels contiguous, both with the same strides)."""
+    _need_form(cache, "cg_quant_read_async")
     strides = _quant_rows(cache, k_out, v_out, ("k_out", "v_out"))
     layers, n, _ = k_out.shape
     _check(cache.lib.cg_quant_read_async(cache.ref, cache.form_ref, layer0, layers, n,
@@ -669,6 +687,7 @@ def cg_quant_read_async(cache: QuantCache, layer0, slots, k_out, v_out, stream=N
 def cg_quant_attention_workspace(cache: QuantCache, n_q, n_heads, n_seqs, n_groups, max_q, max_prefix,
                                  max_len) -> int:
     """Bytes of workspace of a cg_quant_attention_async call of these numbers."""
+    _need_form(cache, "cg_quant_attention_workspace")
     a = cg_attention(0, n_heads, cache.form.head_dim, 1.0, n_seqs, n_q, n_groups, max_q, max_prefix, max_len)
     n = C.c_size_t(0)
     _check(cache.lib.cg_quant_attention_workspace(cache.ref, cache.form_ref, C.byref(a), C.byref(n)))
@@ -678,6 +697,7 @@ def cg_quant_attention_workspace(cache: QuantCache, n_q, n_heads, n_seqs, n_grou
 def cg_quant_attention_async(cache: QuantCache, layer, q, out, scale, rows, q_starts, group_starts,
                              prefix_lens, max_q, max_prefix, max_len, workspace, lse=None, stream=None):
     """cg_attention_prefix_async over a cache held in 4 bits."""
+    _need_form(cache, "cg_quant_attention_async")
     a = _attention_call(cache, layer, q, out, scale, rows, q_starts, group_starts, prefix_lens, max_q,
                         max_prefix, max_len, lse)
     _check(cache.lib.cg_quant_attention_async(cache.ref, cache.form_ref, C.byref(a),
