@@ -25,6 +25,7 @@
 
 #include "cg_attention.h"
 #include "cg_hostapi.h"
+#include "cg_quant_plan.h"
 
 namespace cg {
 namespace {
@@ -836,19 +837,6 @@ __device__ __forceinline__ void run_many(const QuantAttn& a, const Item& it, con
   }
 }
 
-// How a workgroup holds rows: all of 16 or 32 in each wave, which share out heads and tokens; or
-// 16 or 32 in each wave of one head, all of whose waves go through the same tiles.
-enum { kFew16 = 0, kFew32 = 1, kMany16 = 2, kMany32 = 3 };
-__host__ __device__ constexpr bool is_many(int mode) { return mode >= kMany16; }
-__host__ __device__ constexpr int tiles_of_rows(int mode) { return 1 + (mode & 1); }  // of 16, of a wave
-__host__ __device__ constexpr int rows_in(int dp, int mode) {
-  return 16 * tiles_of_rows(mode) * (is_many(mode) ? dp == 256 ? 4 : 8 : 1);
-}
-// Workgroups on a compute unit, as LDS and registers allow.
-__host__ __device__ constexpr int resident4(int pre, int rest) {
-  return tiles_of_rows(pre) == 2 || tiles_of_rows(rest) == 2 ? 1 : 2;
-}
-
 // Tiles of sequence s's own tokens, 0 without queries.
 __device__ __forceinline__ int tiles_of(const QuantAttn& a, int s) {
   const int row = row_of(a, s);
@@ -871,7 +859,6 @@ __device__ __forceinline__ int tiles_of(const QuantAttn& a, int s) {
 // (Cut into splits of one length the last of them run when most are done, and the chip's
 // dispatcher does not fill all slots evenly: 64 sequences of 1,000 to 9,216 tokens
 // took 123 to 136 us.)
-constexpr int kMostListed = 4096;  // sequences
 __device__ __forceinline__ int add_up(const QuantAttn& a, int* at, int* sums, int* most) {
   const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x / 64;
   const int mine = (a.n_seqs + blockDim.x - 1) / blockDim.x, s0 = min(tid * mine, a.n_seqs), s1 = min(s0 + mine, a.n_seqs);
@@ -927,11 +914,6 @@ __device__ __forceinline__ void run_item(const QuantAttn& a, const Item& it, con
   if constexpr (is_many(MODE)) run_many<DP, tiles_of_rows(MODE)>(a, it, span, sh);
   else run_few<DP, tiles_of_rows(MODE)>(a, it, span, sh);
 }
-
-// How a launch cuts the sequences: splits, or parts, of what the join then adds up, or each sequence to one workgroup,
-// which writes the outputs (a.direct).  Known to the compiler, each needs fewer scalar registers
-// than there are, and half the code, which a workgroup of few tokens fetches for one use.
-enum { kSplits = 0, kParts = 1, kAlone = 2 };
 
 template <int DP, int PRE, int REST, int CUT>
 __global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(PRE, REST) * Geo4<DP>::kWaves / 4) void k_quant_attention(
@@ -1014,156 +996,27 @@ __global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(PRE, REST) * Geo4<DP>
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-// How many splits and row tiles the launch has, from the call's numbers alone.
-struct Plan {
-  int dp, pre_splits, rest_splits, pre_least, rest_least, pre_tiles, rest_tiles, pre_mode, rest_mode, pre_groups, pre_heads,
-      rest_heads, turn, parts;
-  bool direct;
-  size_t words;
-};
-
-template <int DP>
-void launch(int pre, int rest, const QuantAttn& a, int64_t items, hipStream_t st) {
-  if (items <= 0) return;
-  const int grid = (int)std::min<int64_t>(items, 1 << 22), cut = a.direct ? kAlone : a.parts ? kParts : kSplits;
-#define GO(PRE, REST, CUT) \
-  if (pre == PRE && rest == REST && cut == CUT) \
-    k_quant_attention<DP, PRE, REST, CUT><<<grid, Geo4<DP>::kThreads, 0, st>>>(a, (int)items);
-#define GO_SAME(MODE) GO(MODE, MODE, kSplits) GO(MODE, MODE, kParts) GO(MODE, MODE, kAlone)
-#define GO_BOTH(PRE, REST) GO(PRE, REST, kSplits) GO(PRE, REST, kParts)
-  GO_SAME(kFew16) GO_SAME(kMany16) GO_BOTH(kMany16, kFew16)
-  if constexpr (DP <= 128) {
-    GO_SAME(kFew32) GO_SAME(kMany32) GO_BOTH(kMany16, kFew32) GO_BOTH(kMany32, kFew16) GO_BOTH(kMany32, kFew32)
-    GO_BOTH(kFew32, kFew16)
+// The kernel of the call's modes and cut, if it is built.
+template <int DP, int I = 0>
+bool launch(int pre, int rest, int cut, const QuantAttn& a, int64_t items, hipStream_t st) {
+  constexpr int PRE = I / kCuts / kModes, REST = I / kCuts % kModes, CUT = I % kCuts;
+  if constexpr (PRE == kModes) {
+    return false;
+  } else {
+    if constexpr (built(DP, PRE, REST, CUT)) {
+      if (pre == PRE && rest == REST && cut == CUT) {
+        const int grid = (int)std::min<int64_t>(items, 1 << 22);
+        if (items > 0) k_quant_attention<DP, PRE, REST, CUT><<<grid, Geo4<DP>::kThreads, 0, st>>>(a, (int)items);
+        return true;
+      }
+    }
+    return launch<DP, I + 1>(pre, rest, cut, a, items, st);
   }
-#undef GO_BOTH
-#undef GO_SAME
-#undef GO
 }
-void launch(int dp, int pre, int rest, const QuantAttn& a, int64_t items, hipStream_t st) {
-  if (dp == 64) launch<64>(pre, rest, a, items, st);
-  else if (dp == 128) launch<128>(pre, rest, a, items, st);
-  else launch<256>(pre, rest, a, items, st);
-}
-
-// The smallest that holds `rows`.  Waves of 32 rows of 256 channels would not fit their registers.
-int mode_of(int64_t rows, int dp) {
-  if (rows <= 16) return kFew16;
-  if (dp == 256) return kMany16;
-  return rows <= 32 ? kFew32 : rows <= 128 ? kMany16 : kMany32;
-}
-
-Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_attention& x) {
-  Plan p;
-  const int kv = f.channels / x.head_dim, G = x.n_heads / kv;
-  p.dp = x.head_dim <= 64 ? 64 : x.head_dim <= 128 ? 128 : 256;
-  // Row tiles with workgroups of their own: few enough that an item's number, over
-  // all heads, sequences and splits, fits 31 bits.
-  auto most = [&](int64_t items) { return std::max<int64_t>(1, (1 << 21) / std::max<int64_t>(1, items)); };
-  const int64_t rows = (int64_t)std::max(1, std::min(x.max_q, x.n_q)) * G;
-  p.rest_mode = mode_of(rows, p.dp);
-  const bool shared = x.n_groups > 0 && x.max_prefix > 0;
-  p.pre_groups = x.n_groups;
-  // rows of an average group
-  const int64_t pre_rows = std::max<int64_t>(1, x.n_groups ? (x.n_q + x.n_groups - 1) / x.n_groups : 1) * G;
-  p.pre_mode = mode_of(pre_rows, p.dp);
-  // Prefixes and the rest are one launch: two, one after the other, leave the chip half empty (64
-  // requests on 9,216 shared and up to 600 own tokens: 40 + 38 us).  A group's rows are as many as a
-  // sequence's or more (21 sequences of up to 5 rows on three prompts: 38 us, with 32 rows for
-  // both 43); where not, or both are many, both are held as the one with more.
-  if (!shared) p.pre_mode = p.rest_mode;
-  if (p.pre_mode < p.rest_mode || (is_many(p.pre_mode) && is_many(p.rest_mode)))
-    p.pre_mode = p.rest_mode = std::max(p.pre_mode, p.rest_mode);
-  auto row_tiles = [&](int64_t items, int64_t rows, int mode) {
-    return (int)std::min(most(items), (rows + rows_in(p.dp, mode) - 1) / rows_in(p.dp, mode));
-  };
-  p.rest_tiles = row_tiles((int64_t)x.n_seqs * kv, rows, p.rest_mode);
-  p.pre_tiles = row_tiles((int64_t)x.n_groups * kv, pre_rows, p.pre_mode);
-  const int64_t slots = 256 * resident4(p.pre_mode, p.rest_mode);
-  const int64_t own = std::max(0, x.max_len - (shared ? x.max_prefix : 0));
-  auto tiles_in = [](int64_t tokens) { return (tokens + kTile - 1) / kTile; };
-  // kv heads of a workgroup, and tiles of a super tile: as many as waves are left for, and as LDS holds.
-  const int waves = p.dp == 256 ? 4 : 8;
-  const QuantRow row = quant_row(f);
-  auto heads = [&](int n) {
-    while (kv % n) n--;
-    int cpr = 0;  // as the kernel has it, at most
-    for (int head = 0; head < kv && head < 8 * n; head += n)
-      cpr = std::max(cpr, n * row.head / 16 + ((row.scales + 2 * head * row.groups) % 16 + 2 * n * row.groups + 15) / 16);
-    p.rest_heads = n;
-    p.turn = waves / n;
-    while ((p.turn * 512 * cpr + 1023) / 1024 * 1024 > 37 * 1024 / 2) p.turn--;
-  };
-  // Few tokens: one head a workgroup, whose waves share the tokens, in one kernel that writes the
-  // outputs itself, without a join.  For 8 kv heads of 128 channels, that kernel and the other
-  // way: one sequence of 768 tokens 16 and 20 us, of 1,536 tokens 22 and 20; 8 of 1,000 20 and 20,
-  // of 1,536 24 and 21; 32 of 512 19 and 22, of 1,000 28 and 22; 64 of 256 20 and 22, of 512 29
-  // and 22.  Sharing prefixes saves (sequences - 1) times their reading, not for little: 64
-  // sequences with 128 tokens in common (9 MB) 17.6 and 18 to 19 us, 16 with 512 (9 MB) 17 and 17.
-  constexpr int kSteps = 4;  // super tiles that a workgroup takes rather than have sums joined
-  const int64_t saved = shared ? (int64_t)x.n_seqs * x.max_prefix * c.channels * 4 : 0;
-  auto alone = [&] {
-    p.pre_mode = p.rest_mode;
-    p.pre_groups = 0;
-    p.pre_splits = 0;
-    p.pre_heads = 1;
-    p.pre_least = p.rest_least = 1;
-    p.rest_splits = 1;
-    p.parts = 0;
-    p.words = 4;
-    return p;
-  };
-  heads(1);
-  if (is_many(p.rest_mode)) p.turn = 1;
-  const int64_t all = (int64_t)x.n_seqs * p.rest_tiles * kv, room = 256 * resident4(p.rest_mode, p.rest_mode);
-  p.direct = saved <= (int64_t)16 << 20 &&
-             (is_many(p.rest_mode) ? all >= room / 2 || tiles_in(x.max_len) <= kSteps
-                                   : tiles_in(x.max_len) <= kSteps * p.turn && all * tiles_in(x.max_len) <= waves * room);
-  if (p.direct) return alone();
-  // Otherwise as many neighbours as there are waves, so that whole stretches of rows are read.
-  if (!is_many(p.rest_mode)) heads(waves);
-  p.pre_heads = is_many(p.pre_mode) ? 1 : p.rest_heads;
-  // Tiles of a split, at least `least`: so many that the items are `slots` workgroups at
-  // most, and at most kMostSplits splits, whose sums the join reads.  A workgroup's start and
-  // end take as long as kWorth super tiles.  What is shorter than the call says is cut as often, down to kLeast
-  // tiles, as all these workgroups run at once (64 sequences on 9,216 shared tokens, said to be up to
-  // 147,456: 45 us, in splits as long as said 253).
-  constexpr int kMostSplits = 256, kWorth = 8;
-  auto cut = [&](int64_t items, int64_t tiles, int64_t slots, int least, int& splits, int& per) {
-    const int64_t by = std::min<int64_t>(std::max<int64_t>(1, slots / items), kMostSplits);
-    const int64_t n = std::max<int64_t>((tiles + by - 1) / by, least);
-    splits = (int)std::max<int64_t>(1, (tiles + n - 1) / n);
-    per = std::min(least, kLeast);
-  };
-  const int64_t columns = kv / p.rest_heads, items = std::max(1, x.n_seqs) * p.rest_tiles * columns;
-  const int64_t pre_items = (int64_t)x.n_groups * (kv / p.pre_heads) * p.pre_tiles;
-  // Prefixes and the rest get slots by their work; lengths are mostly below the greatest.  A tile
-  // takes a workgroup of many rows a third of the time of one of few rows of all heads.
-  const int64_t pre_work = !shared ? 0 : pre_items * tiles_in(x.max_prefix) / (is_many(p.pre_mode) && !is_many(p.rest_mode) ? 3 : 1);
-  const int64_t work = items * tiles_in(own) / 2;
-  const int64_t pre_slots = pre_work ? std::min(std::max(slots * pre_work / (pre_work + work), slots / 8), slots * 7 / 8) : 0;
-  // whole splits of all sequences: the prefix, whose workgroups all take as long, gets what they leave
-  const int64_t rest_slots = pre_slots ? std::min((slots - pre_slots + items / 2) / items * items, slots * 7 / 8) : slots;
-  const int least = (int)std::min<int64_t>(kWorth, std::max<int64_t>(kLeast, items * tiles_in(own) / 256)) * (is_many(p.rest_mode) ? 2 : p.turn);
-  cut(items, tiles_in(own), rest_slots, least, p.rest_splits, p.rest_least);
-  p.parts = 0;
-  // the sums of tiles fit 31 bits
-  const bool listed = x.n_seqs <= kMostListed && (int64_t)x.n_seqs * c.max_blocks * c.page_tokens < (int64_t)1 << 35;
-  // Lengths that differ: equal parts of all of them, where that is two or more for each row tile and
-  // its heads, and a launch has all items (2^22 at most) at once.
-  if (x.n_seqs > 1 && listed && work >= kWorth * p.turn * (slots - pre_slots) &&
-      slots - pre_slots >= 2 * columns * p.rest_tiles && pre_items <= 1 << 21) {
-    p.parts = (int)std::max<int64_t>(1, (slots - pre_slots) / (columns * p.rest_tiles));
-    p.rest_least = kWorth / 2 * p.turn;
-    p.rest_splits = (int)std::max<int64_t>(2, std::min<int64_t>(kMostSplits + 2, 2 + 4 * ((p.parts + x.n_seqs - 1) / x.n_seqs)));
-  }
-  p.pre_splits = 0;
-  p.pre_least = kLeast;
-  if (x.n_groups)  // the slots that the rest leaves
-    cut(pre_items, shared ? tiles_in(x.max_prefix) : 0, p.parts ? pre_slots : std::max(slots / 8, slots - items * p.rest_splits),
-        kLeast, p.pre_splits, p.pre_least);
-  p.words = (size_t)(p.pre_splits + p.rest_splits) * x.n_q * x.n_heads * (x.head_dim + 2) + x.n_q + 4;
-  return p;
+bool launch(const Plan& p, const QuantAttn& a, int64_t items, hipStream_t st) {
+  return p.dp == 64    ? launch<64>(p.pre_mode, p.rest_mode, p.cut(), a, items, st)
+         : p.dp == 128 ? launch<128>(p.pre_mode, p.rest_mode, p.cut(), a, items, st)
+                       : launch<256>(p.pre_mode, p.rest_mode, p.cut(), a, items, st);
 }
 
 }  // namespace
@@ -1208,7 +1061,7 @@ int cg_quant_attention_async(const cg_paged_cache* c, const cg_quant_form* f, co
   const int64_t pre = (int64_t)p.pre_groups * p.pre_splits * p.pre_tiles * (v.kv / p.pre_heads);
   const int64_t rest = (int64_t)(p.parts ? p.parts : a->n_seqs * (int64_t)p.rest_splits) * p.rest_tiles * (v.kv / p.rest_heads);
   hipStream_t st = (hipStream_t)stream;
-  launch(p.dp, p.pre_mode, p.rest_mode, v, pre + rest, st);
+  if (!launch(p, v, pre + rest, st)) return fail(CG_E_HIP, "attention over 4 bits: no kernel for the call's rows");
   if (!p.direct) {
     const int total = p.pre_splits + p.rest_splits;
     v.join = std::min(total <= 2 ? 1 : total <= 8 ? 2 : 8, kThreads / (v.d / 4));
