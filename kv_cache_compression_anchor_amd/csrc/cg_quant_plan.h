@@ -116,8 +116,18 @@ inline Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_at
   heads(1);
   if (is_many(p.rest_mode)) p.turn = 1;
   const int64_t all = (int64_t)x.n_seqs * p.rest_tiles * kv, room = 256 * resident4(p.rest_mode, p.rest_mode);
+  // More than 32 rows, whose join reads more: also long sequences whose workgroups fill the chip, and
+  // those that fill half of it up to kHalf tiles.  For 8 kv heads of 128 channels with 4 query heads each,
+  // this way and cut (us): 2, 3, 4 prompts of 512 queries on 9,216 tokens (128, 192, 256 workgroups on 256
+  // slots) 358 and 239, 359 and 336, 358 and 391; 16 of 64 queries (128) on 512 tokens 33 and 44, on 1,024 52
+  // and 73, on 81,920 3,086 and 1,690; 8 of 128 queries (128) on 2,048 90 and 93; one of 512 and one of a
+  // single query (128, 56 of them without rows) on 81,920 3,080 and 1,585, and eight of a single one (576)
+  // 5,459 and 6,110.  64 channels, 32 kv heads, 8 of 64 queries (256 on 512 slots) on 4,096 85 and 77.  32
+  // of 5 drafts, 8 query heads each, on 1,000 to 9,216 tokens (256 on 512) 225 and 130.
+  constexpr int kHalf = 64;
   p.direct = saved <= (int64_t)16 << 20 &&
-             (is_many(p.rest_mode) ? all >= room / 2 || tiles_in(x.max_len) <= kSteps
+             (is_many(p.rest_mode) ? all >= room || (all >= room / 2 && tiles_in(x.max_len) <= kHalf) ||
+                                         tiles_in(x.max_len) <= kSteps
                                    : tiles_in(x.max_len) <= kSteps * p.turn && all * tiles_in(x.max_len) <= waves * room);
   if (p.direct) return alone();
   // Otherwise as many neighbours as there are waves, so that whole stretches of rows are read.
