@@ -855,7 +855,7 @@ __device__ __forceinline__ int tiles_of(const QuantAttn& a, int s) {
 }
 
 // The tiles of each sequence's own tokens, added up: at[s] before sequence s, at[n_seqs] in all.  Returns
-// how many are a part: as equal as they come, no sequence in more than rest_splits of them.
+// how many are a part.
 // (Cut into splits of one length the last of them run when most are done, and the chip's
 // dispatcher does not fill all slots evenly: 64 sequences of 1,000 to 9,216 tokens
 // took 123 to 136 us.)
@@ -897,8 +897,7 @@ __device__ __forceinline__ int add_up(const QuantAttn& a, int* at, int* sums, in
   __syncthreads();
   all = __builtin_amdgcn_readfirstlane(all);
   top = __builtin_amdgcn_readfirstlane(top);
-  return max(max((int)(((uint32_t)all + a.parts - 1) / (uint32_t)a.parts),
-                 (int)(((uint32_t)top + a.rest_splits - 2) / (uint32_t)(a.rest_splits - 1))), a.rest_least);
+  return tiles_of_part(all, top, a.parts, a.rest_splits, a.rest_least);
 }
 
 // What a workgroup computes next: items of the launch, or its part of the sequences' own tokens,
@@ -965,11 +964,11 @@ __global__ __launch_bounds__(Geo4<DP>::kThreads, resident4(PRE, REST) * Geo4<DP>
     if (wk.parts) {
       const int s = wk.s++, tiles = tiles_of(a, s);
       if (tiles == 0) continue;
-      const int at = (uint32_t)wk.base / (uint32_t)wk.per;
+      const Parts in = parts_of(wk.base, tiles, wk.per);
       const int from = wk.pos - wk.base, n = min(tiles - from, wk.end - wk.pos);
-      it.split = wk.part - at;
+      it.split = wk.part - in.first;
       go = rest_item(a, s, it);
-      own = (int)((uint32_t)(wk.base + tiles - 1) / (uint32_t)wk.per) - at + 1;
+      own = in.used;
       if (go) span = Span{it.lo / kTile + from, it.lo / kTile + from + n};
       wk.pos += n;
       wk.base += tiles;

@@ -2,6 +2,8 @@
 // anything.  Plain C++: the attention's kernels use these, and so can a host program.
 #pragma once
 
+#include <stdint.h>
+
 namespace cg {
 
 constexpr int kTile = 32;  // tokens of a tile: the depth of one 16x16x32 product
@@ -31,6 +33,23 @@ constexpr Split split_of(int lo, int hi, int splits, int least = kLeast) {
   if (s.per < least) s.per = least;
   s.used = (s.tiles + s.per - 1) / s.per;
   return s;
+}
+
+// Tiles of a part, where the tiles of all sequences, one sequence's behind the other's, `all` of them
+// and at most `top` of one sequence, are cut into `parts` equal parts, of `least` tiles or more: as equal as
+// they come, and no sequence in more than `splits` (2 or more) of them, wherever in a part it begins.
+constexpr int tiles_of_part(int all, int top, int parts, int splits, int least) {
+  const int per = (int)(((uint32_t)all + parts - 1) / (uint32_t)parts);
+  const int one = (int)(((uint32_t)top + splits - 2) / (uint32_t)(splits - 1));
+  return per > one ? per > least ? per : least : one > least ? one : least;
+}
+// The parts that a sequence of `tiles` tiles (one or more), the first of which is number `base`, lies in.
+struct Parts {
+  int first, used;
+};
+constexpr Parts parts_of(int base, int tiles, int per) {
+  const int first = (int)((uint32_t)base / (uint32_t)per);
+  return {first, (int)((uint32_t)(base + tiles - 1) / (uint32_t)per) - first + 1};
 }
 
 }  // namespace cg

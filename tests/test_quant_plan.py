@@ -34,3 +34,8 @@ def test_long_contexts_are_cut_unless_their_workgroups_fill_the_chip():
         assert p.rest >= MANY16 and p.cut != ALONE and p.pieces > 1, (c, p)
     for c, p in zip(alone, plans(alone)):
         assert p.rest >= MANY16 and p.cut == ALONE, (c, p)
+
+
+def test_parts_hold_every_tile_once(tmp_path):
+    r = build_and_run(tmp_path, "parts_check")
+    assert r.returncode == 0 and "parts ok" in r.stdout, r.stdout[-2000:] + r.stderr[-4000:]
