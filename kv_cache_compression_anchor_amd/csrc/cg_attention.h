@@ -43,7 +43,7 @@ struct Attn {
   // the launch: splits of a prefix and of a sequence's rest, row tiles that have
   // workgroups of their own (there may be more)
   int pre_splits, rest_splits, pre_tiles, rest_tiles, pre_groups, join;
-  int rest_heads;  // kv heads of a workgroup that deals out the rest's tokens: 1, 2 or 4
+  int rest_heads;  // kv heads of a workgroup that deals out the rest's tokens: 1, 2 or 4; over 4 bits up to 8
   float* part;  // [pre_splits + rest_splits][n_q][H][d] sums, not divided
   float* ml;    // the same with [2]: reference exponent m, sum of weights l
   // [n_q]: splits of the prefix and (in the upper half) of the rest that the query's

@@ -8,8 +8,8 @@
 // below these and well above binary32's errors replaces exact quotients.
 //
 // What bounds it: memory.  4,666 tokens of 32 layers and 1,024 channels with the held numbers (1.40 GB)
-// are written in 289 us, 4.8 TB/s (a copy reaches 4.9); 9,216 tokens of them are read back in 265
-// us, 5.8 TB/s, as most of it is written.  A step's tokens of 64 requests (19 MB) take 6.8 us, four
+// are written in 290 us, 4.8 TB/s (a copy reaches 4.9); 9,216 tokens of them are read back in 270
+// us, 5.7 TB/s, as most of it is written.  A step's tokens of 64 requests (19 MB) take 6.8 us, four
 // tokens of a small model 2.3.
 #include <algorithm>
 

@@ -16,11 +16,12 @@
 // all waves take one head, whose numbers are made once, into LDS.
 //
 // What bounds it: 64 sequences of 1,000 to 9,216 tokens (32 heads, 8 of K and V, 128 channels, 345 MB)
-// take 92 us, 88 of them here (3.9 TB/s, 70.7 us at a copy's rate): vector instructions fill 75% of
+// take 93 us with the join, which takes 7 (70.7 at a copy's rate): vector instructions fill 75% of
 // the issue slots, 3.35 a lane for a number of the cache, 1.7 of them to make it.  Four of 81,920
-// tokens (378 MB) take 91 us.  64 on 9,216 shared tokens and up to 600 of their own take 44, 37 of
-// them here, at 1.3 us a tile of a workgroup (products and the numbers' making share the issue
-// slots, two waves to each) and 8 us of beginning and end; the join takes 7.
+// tokens (378 MB) take 92 us.  64 on 9,216 shared tokens and up to 600 of their own take 44 with the join (7), at
+// 1.3 us a tile of a workgroup (products and the numbers' making share the issue slots, two waves to
+// each, and all waves do the same at one time) and 8 us of beginning and end.  Four prompts of 512 queries on
+// 9,216 tokens take 360 us, 233 at the rate of a large product.
 #include <algorithm>
 
 #include "cg_attention.h"

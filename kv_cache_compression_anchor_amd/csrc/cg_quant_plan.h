@@ -24,8 +24,9 @@ constexpr int resident4(int pre, int rest) {
 }
 
 // How a launch cuts the sequences: splits, or parts, of what the join then adds up, or each sequence to one workgroup,
-// which writes the outputs (a.direct).  Known to the compiler, each needs fewer scalar registers
-// than there are, and half the code, which a workgroup of few tokens fetches for one use.
+// which writes the outputs (a.direct).  Known to the compiler, each needs fewer registers (100 to 345 scalar
+// values still wait in lanes of vector registers, and one of the 52 kernels, <128, kMany16, kFew16, kParts>,
+// spills 4 vector registers) and half the code, which a workgroup of few tokens fetches for one use.
 enum { kSplits = 0, kParts = 1, kAlone = 2, kCuts = 3 };
 
 // The kernels there are: rows held alike, or those of a prefix as more rows than the rest's, which are few;
@@ -152,7 +153,8 @@ inline Plan plan_of(const cg_paged_cache& c, const cg_quant_form& f, const cg_at
   const int64_t pre_work = !shared ? 0 : pre_items * tiles_in(x.max_prefix) / (is_many(p.pre_mode) && !is_many(p.rest_mode) ? 3 : 1);
   const int64_t work = items * tiles_in(own) / 2;
   const int64_t pre_slots = pre_work ? std::min(std::max(slots * pre_work / (pre_work + work), slots / 8), slots * 7 / 8) : 0;
-  // whole splits of all sequences: the prefix, whose workgroups all take as long, gets what they leave
+  // whole splits of all sequences: the prefix, whose workgroups all take as long, gets what they leave (0
+  // where there are more sequences than slots, each of which is one split then)
   const int64_t rest_slots = pre_slots ? std::min((slots - pre_slots + items / 2) / items * items, slots * 7 / 8) : slots;
   const int least = (int)std::min<int64_t>(kWorth, std::max<int64_t>(kLeast, items * tiles_in(own) / 256)) * (is_many(p.rest_mode) ? 2 : p.turn);
   cut(items, tiles_in(own), rest_slots, least, p.rest_splits, p.rest_least);
